@@ -40,7 +40,8 @@
  *     and workspaces waits for the kernels before it; the plain inputs do not.
  *     So q, k, v, k_new and v_new must not be the output (out, or a shard's
  *     state) of the immediately preceding decode call (tq_decode_attention,
- *     tq_decode_attention_noalloc, tq_decode_step, tq_decode_partials) on the
+ *     tq_decode_attention_noalloc, tq_decode_step, tq_decode_partials,
+ *     tq_kv8_attention) on the
  *     same stream: any other kernel or memory copy enqueued between the two
  *     calls (as a model's projections are) restores plain stream order.
  */
@@ -84,6 +85,7 @@ typedef enum {
 #define TQ_DEVERR_BLOCK 2u      /* block id outside [0, num_blocks)              */
 #define TQ_DEVERR_SEQLEN 4u     /* decode seq_len outside [q_len, capacity]      */
 #define TQ_DEVERR_TIMEOUT 8u    /* a bounded wait for a bulk copy ran out         */
+#define TQ_DEVERR_NONFINITE 16u /* tq_kv8_append met a NaN or an infinity          */
 
 /* ------------------------------------------------------------------ */
 /* Codecs                                                               */
@@ -651,6 +653,146 @@ tq_status tq_decode_attention_noalloc(const tq_codec *key_codec, const tq_codec 
                                       const int32_t *seq_lens, const int32_t *block_table,
                                       int max_blocks, int max_seq_len, float scale, float *out,
                                       tq_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* 8-bit cache                                                          */
+/* ------------------------------------------------------------------ */
+
+/*
+ * A paged cache with 8 bits per coordinate: the tier above the rotated codecs
+ * for layers, or parts of a sequence, that need more precision (the pages
+ * have no counterpart; block tables, lengths and KV-head grouping are those of
+ * the compressed cache, so that one block table can address both).
+ *
+ * Codes are [layer][block][KV head][token][head_dim] bytes, keys and values
+ * apart: e4m3 values, or two's-complement integers. Each (block, KV head) has
+ * one scale for its keys and one for its values, a power of two held as the
+ * byte x = e + 127 (scale 2^e; the E8M0 reading). A cached value is code * 2^e.
+ * The append writes e in [-63, 63], and attention takes no other.
+ */
+typedef enum { TQ_KV8_E4M3 = 0, TQ_KV8_INT8 = 1 } tq_kv8_format;
+
+typedef struct {
+    void *k_codes, *v_codes;      /* device, 16-byte aligned: layer 0                    */
+    void *k_scales, *v_scales;    /* device bytes [num_blocks][num_kv_heads] of layer 0  */
+    int64_t code_layer_stride;    /* bytes between consecutive layers' codes (mult. of 16) */
+    int64_t scale_layer_stride;   /* bytes between consecutive layers' scales            */
+    int num_layers;
+    int num_blocks;
+    int block_tokens;             /* power of two, 16..256                               */
+    int num_kv_heads;
+    int head_dim;                 /* 64, 128 or 256                                      */
+    int format;                   /* tq_kv8_format                                       */
+} tq_kv8_cache;
+
+/*
+ * Rows of heads in the caller's own layout: element (b, h, t, d) is at
+ * data + b*stride_batch + h*stride_head + t*stride_token + d (strides in
+ * elements, d contiguous), so that slices of a fused projection
+ * [batch][token][3][head][dim] and head-major tensors are read as they lie.
+ * data and the byte strides are multiples of 16.
+ */
+typedef struct {
+    void *data;
+    int64_t stride_batch, stride_head, stride_token;
+} tq_rows;
+
+/*
+ * Position rotation of the first rot_dim coordinates of a head (the others
+ * pass). Pair i of a vector at position p turns by p * inv_freq[i]:
+ *   (x1, x2) -> scale * (x1 cos - x2 sin, x2 cos + x1 sin),
+ * with (x1, x2) coordinates (i, i + rot_dim/2), or (2i, 2i + 1) with
+ * interleaved. The angle is reduced exactly (as turns, modulo 1, in 64-bit
+ * integers), so that far positions lose nothing.
+ */
+typedef struct {
+    const double *inv_freq;  /* device [rot_dim / 2], |inv_freq| < 1024          */
+    int rot_dim;             /* multiple of 16, at most head_dim                  */
+    int interleaved;
+    float scale;             /* 0 means 1                                         */
+} tq_rope;
+
+/*
+ * Append tokens to layer `layer` of an 8-bit cache: token i < new_lens[b] of
+ * sequence b goes to position seq_lens[b] + i, the keys rotated by `rope` on
+ * the way (NULL: as they are), each rounded once (to nearest even) to the
+ * 8-bit format at its block's scale.
+ *   k, v       [batch][num_kv_heads][n_new][head_dim], f32/bf16/f16 (one dtype)
+ *   seq_lens   device int32 [batch], tokens already cached (not modified)
+ *   new_lens   device int32 [batch] in [0, n_new], or NULL: n_new each
+ *   positions  device int32 [batch][n_new], rotation positions, or NULL: the
+ *              position in the cache
+ *   block_table, max_blocks: as tq_encode_append; no block may belong to two
+ *              of the batch's sequences at the places that are appended to
+ * Scale of a block and head: the smallest 2^e at which the largest magnitude
+ * of its tokens is at most the largest code (448 or 127). A block that holds
+ * earlier tokens keeps its scale, or takes the larger one that the new tokens
+ * need: then its earlier codes are rounded to it (for e4m3, exact but for the
+ * smallest codes). Bytes behind the last token stay as they were.
+ * A NaN is stored as 0 and an infinity as the largest code of its sign, and
+ * either sets TQ_DEVERR_NONFINITE: nothing in the cache poisons other rows.
+ * Tokens past a sequence's capacity or in a block id outside the pool are
+ * skipped and flagged (TQ_DEVERR_CAPACITY, TQ_DEVERR_BLOCK), a sequence with a
+ * negative length or a new_lens outside [0, n_new] too (TQ_DEVERR_SEQLEN).
+ * Errors: TQ_ERR_INVALID_ARG (pointers, sizes, alignment, layer),
+ * TQ_ERR_UNSUPPORTED (head_dim, block_tokens, format, rot_dim),
+ * TQ_ERR_CAPACITY as tq_encode_append.
+ */
+tq_status tq_kv8_append(const tq_kv8_cache *cache, int layer, const tq_rows *k, const tq_rows *v, tq_dtype dtype,
+                        int batch, int n_new, const int32_t *seq_lens, const int32_t *new_lens,
+                        const int32_t *block_table, int max_blocks, const tq_rope *rope, const int32_t *positions,
+                        tq_stream_t stream);
+
+/* How tq_kv8_attention scores and masks. All zero: plain causal attention. */
+typedef struct {
+    float scale;                /* 0 means 1/sqrt(head_dim)                                   */
+    float softcap;              /* > 0: score = softcap * tanh(score / softcap)               */
+    const float *slopes;        /* device [num_q_heads] or NULL: score -= slope * |p - t|     */
+    int window;                 /* > 0: a query at p sees keys t > p - window                 */
+    const int32_t *prefix_lens; /* device [batch] or NULL: every query sees keys t < prefix   */
+    const int32_t *doc_starts;  /* device [batch][q_len] or NULL: query l sees t >= doc_start */
+    const tq_rope *rope;        /* rotate the queries on the way in, or NULL                  */
+    const int32_t *positions;   /* device [batch][q_len], the queries' rotation positions, or *
+                                 * NULL: their positions in the cache                          */
+} tq_kv8_scores;
+
+/* Workspace (device bytes) tq_kv8_attention needs for these sizes on the current device. */
+tq_status tq_kv8_workspace_bytes(const tq_kv8_cache *cache, int batch, int num_q_heads, int q_len, int max_seq_len,
+                                 size_t *bytes);
+
+/*
+ * Attention over layer `layer` of an 8-bit cache, for single tokens and for
+ * chunks of any length. The q_lens[b] queries of sequence b are its newest
+ * tokens: query l is at position p = seq_lens[b] - q_lens[b] + l and sees key t
+ * of 0 <= t < seq_lens[b] where
+ *   (t <= p and t > p - window and t >= doc_start) or t < prefix,
+ *   score = scale * <q, k_t>, then the cap, then the bias (distances are those
+ *   of cache positions), out = softmax(score) V; a row that sees no key is 0.
+ *   q, out     [batch][num_q_heads][q_len][head_dim] in rows of one dtype, bf16
+ *              or f16; query head hq reads KV head hq / (num_q_heads/num_kv_heads).
+ *              Rows l >= q_lens[b] of out stay as they were. out may not overlap q.
+ *   seq_lens   device int32 [batch] in [0, min(max_seq_len, capacity)]: all
+ *              tokens, the queries' own among them; others count as 0 and set
+ *              TQ_DEVERR_SEQLEN
+ *   q_lens     device int32 [batch] in [0, q_len], or NULL: q_len each (others:
+ *              TQ_DEVERR_SEQLEN, and the nearest of them)
+ *   block_table, max_blocks: as tq_encode_append. Blocks that no query of the
+ *              sequence sees are not looked at (their entries may be anything);
+ *              an id outside the pool counts as a block that nobody sees and
+ *              sets TQ_DEVERR_BLOCK.
+ *   scores     NULL: plain causal attention
+ *   workspace  device, >= tq_kv8_workspace_bytes(...), 256-byte aligned (NULL
+ *              where that is 0); only this call uses it while it runs.
+ * Operands are fp16 (cached codes are exact in it; queries are scaled by a power
+ * of two per row, then rounded, where they were rotated; softmax weights are
+ * rounded), sums and softmax statistics fp32, the output is rounded once.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED as tq_kv8_append, also for f32
+ * queries; TQ_ERR_CAPACITY if the workspace is too small.
+ */
+tq_status tq_kv8_attention(const tq_kv8_cache *cache, int layer, const tq_rows *q, tq_dtype dtype, int batch,
+                           int num_q_heads, int q_len, const int32_t *seq_lens, const int32_t *q_lens,
+                           const int32_t *block_table, int max_blocks, int max_seq_len, const tq_kv8_scores *scores,
+                           const tq_rows *out, void *workspace, size_t workspace_bytes, tq_stream_t stream);
 
 /* ------------------------------------------------------------------ */
 /* Diagnostics                                                          */

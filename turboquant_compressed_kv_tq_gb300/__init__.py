@@ -13,9 +13,10 @@ from typing import Optional
 import numpy as np
 
 from . import _lib
-from ._lib import (TQ_BF16, TQ_DEVERR_BLOCK, TQ_DEVERR_CAPACITY, TQ_DEVERR_SEQLEN, TQ_ENCODE_AUTO,
-                   TQ_ENCODE_EXACT, TQ_F16, TQ_F32, TQ_MODE_GROUP, TQ_MODE_MSE, TQ_MODE_PROD, TQ_OK, TQError, check,
-                   lib, library_path, status_string, tq_batch, tq_cache_desc, tq_codec_info_t, tq_split_state)
+from ._lib import (TQ_BF16, TQ_DEVERR_BLOCK, TQ_DEVERR_CAPACITY, TQ_DEVERR_NONFINITE, TQ_DEVERR_SEQLEN, TQ_ENCODE_AUTO,
+                   TQ_ENCODE_EXACT, TQ_F16, TQ_F32, TQ_KV8_E4M3, TQ_KV8_INT8, TQ_MODE_GROUP, TQ_MODE_MSE, TQ_MODE_PROD,
+                   TQ_OK, TQError, check, lib, library_path, status_string, tq_batch, tq_cache_desc, tq_codec_info_t,
+                   tq_kv8_cache, tq_kv8_scores, tq_rope, tq_rows, tq_split_state)
 
 __all__ = [
     "tq_codec_create", "tq_codec_create_group", "tq_codec_destroy", "tq_codec_info",
@@ -27,10 +28,11 @@ __all__ = [
     "tq_decode_partials", "tq_decode_merge",
     "tq_encode_append_split", "tq_decode_workspace_bytes_split", "tq_decode_attention_split", "SplitCache",
     "tq_batch_filter", "tq_batch_extend", "tq_batch_merge", "tq_batch_extract", "Batch",
+    "tq_kv8_append", "tq_kv8_attention", "tq_kv8_workspace_bytes", "KV8Cache", "Rope",
     "tq_device_error", "tq_selftest_wait_timeout",
     "tq_launch_count", "tq_abi_version", "Codec", "CompressedKVCache", "TQError",
     "TQ_MODE_MSE", "TQ_MODE_PROD", "TQ_MODE_GROUP", "TQ_F32", "TQ_BF16", "TQ_F16",
-    "TQ_ENCODE_AUTO", "TQ_ENCODE_EXACT",
+    "TQ_ENCODE_AUTO", "TQ_ENCODE_EXACT", "TQ_KV8_E4M3", "TQ_KV8_INT8",
 ]
 
 
@@ -499,3 +501,213 @@ class CompressedKVCache:
         """Append the step's tokens at seq_lens (lengths before the step) and decode, in one call."""
         tq_decode_step(self.key.handle, self.value.handle, self.desc, layer, k_new, v_new, q, seq_lens,
                        block_table, max_blocks, max_seq_len, out, workspace, scale, stream)
+
+
+# ----------------------------------------------------------------- 8-bit cache
+
+_KV8_DTYPES = None
+
+
+def _kv8_dtype(dtype) -> int:
+    global _KV8_DTYPES
+    if _KV8_DTYPES is None:
+        torch = _torch()
+        _KV8_DTYPES = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
+    code = _KV8_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _rows(t, name, dtype, device, shape) -> tq_rows:
+    """A [batch, heads, tokens, head_dim] view, in whatever order its first three axes lie."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [batch, heads, tokens, head_dim] = {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}, not {t.dtype} on {t.device}")
+    sb, sh, st, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: the coordinates of a head must be contiguous")
+    # the stride of an axis of one element says nothing, whatever it is
+    return tq_rows(t.data_ptr(), sb if shape[0] > 1 else 0, sh if shape[1] > 1 else 0, st if shape[2] > 1 else 0)
+
+
+def _array(t, name, dtype, device, shape) -> Optional[int]:
+    """Pointer of a small contiguous argument (lengths, tables, slopes), or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+class Rope:
+    """Position rotation: pair i of a head's first ``2 * len(inv_freq)`` coordinates turns by position * inv_freq[i].
+
+    ``inv_freq`` is a float64 device tensor, kept by this object; pairs are coordinates (i, i + rot_dim / 2), or
+    (2i, 2i + 1) with ``interleaved``; ``scale`` multiplies the rotated coordinates.
+    """
+
+    def __init__(self, inv_freq, interleaved: bool = False, scale: float = 1.0):
+        torch = _torch()
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not inv_freq.is_cuda:
+            raise ValueError("inv_freq must be a contiguous one-dimensional float64 tensor on a CUDA device")
+        if not scale:
+            raise ValueError("scale must not be 0")
+        self.inv_freq = inv_freq
+        self.desc = tq_rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), scale)
+        self.ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def of_base(cls, rot_dim: int, base: float = 10000.0, device="cuda", interleaved: bool = False, scale: float = 1.0):
+        """inv_freq[i] = base ** (-2 i / rot_dim)."""
+        torch = _torch()
+        i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+        return cls(base ** (-i / rot_dim), interleaved, scale)
+
+
+def tq_kv8_append(cache: "KV8Cache", layer, k, v, seq_lens, block_table=None, max_blocks=0, new_lens=None, rope=None,
+                  positions=None, stream=None):
+    """Append k, v [batch, kv heads, n_new, head_dim] (views in any order of the first three axes) at seq_lens."""
+    torch = _torch()
+    device = cache.device
+    if k.dim() != 4:
+        raise ValueError("k must be [batch, heads, tokens, head_dim]")
+    batch, n_new = k.shape[0], k.shape[2]
+    shape = torch.Size((batch, cache.num_kv_heads, n_new, cache.head_dim))
+    kr = _rows(k, "k", k.dtype, device, shape)
+    vr = _rows(v, "v", k.dtype, device, shape)
+    i32, per = torch.int32, torch.Size((batch,))
+    if rope is not None and rope.inv_freq.device != device:
+        raise ValueError(f"rope must be on {device}")
+    args = (_array(seq_lens, "seq_lens", i32, device, per), _array(new_lens, "new_lens", i32, device, per),
+            _array(block_table, "block_table", i32, device, torch.Size((batch, max_blocks))), max_blocks,
+            rope.ref if rope is not None else None,
+            _array(positions, "positions", i32, device, torch.Size((batch, n_new))))
+    with cache.on_device():
+        check(lib().tq_kv8_append(cache.ref, layer, ctypes.byref(kr), ctypes.byref(vr), _kv8_dtype(k.dtype), batch, n_new,
+                                  *args, _stream(stream)), "tq_kv8_append")
+
+
+def tq_kv8_workspace_bytes(cache: "KV8Cache", batch, num_q_heads, q_len, max_seq_len) -> int:
+    n = ctypes.c_size_t()
+    with cache.on_device():
+        check(lib().tq_kv8_workspace_bytes(cache.ref, batch, num_q_heads, q_len, max_seq_len, ctypes.byref(n)),
+              "tq_kv8_workspace_bytes")
+    return n.value
+
+
+def tq_kv8_attention(cache: "KV8Cache", layer, q, seq_lens, block_table=None, max_blocks=0, max_seq_len=0, out=None,
+                     workspace=None, q_lens=None, scale=0.0, softcap=0.0, slopes=None, window=0, prefix_lens=None,
+                     doc_starts=None, rope=None, positions=None, stream=None):
+    """Attention of q [batch, query heads, q_len, head_dim] over the cache; returns out (like q if None).
+
+    Without `out`, rows behind q_lens are zero. Without `workspace`, one is taken from torch's allocator on the
+    current stream, so give one where `stream` is another.
+    """
+    torch = _torch()
+    device = cache.device
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, heads, tokens, head_dim]")
+    batch, heads, q_len, _ = q.shape
+    shape = torch.Size((batch, heads, q_len, cache.head_dim))
+    qr = _rows(q, "q", q.dtype, device, shape)
+    dtype = _kv8_dtype(q.dtype)
+    if out is None:
+        out = torch.empty_like(q) if q_lens is None else torch.zeros_like(q)
+    orow = _rows(out, "out", q.dtype, device, shape)
+    i32, per = torch.int32, torch.Size((batch,))
+    each = torch.Size((batch, q_len))
+    if rope is not None and rope.inv_freq.device != device:
+        raise ValueError(f"rope must be on {device}")
+    sc = None
+    if scale or softcap or window or rope is not None or slopes is not None or prefix_lens is not None or doc_starts is not None:
+        sc = ctypes.byref(tq_kv8_scores(
+            scale, softcap, _array(slopes, "slopes", torch.float32, device, torch.Size((heads,))), window,
+            _array(prefix_lens, "prefix_lens", i32, device, per), _array(doc_starts, "doc_starts", i32, device, each),
+            ctypes.pointer(rope.desc) if rope is not None else None, _array(positions, "positions", i32, device, each)))
+    args = (_array(seq_lens, "seq_lens", i32, device, per), _array(q_lens, "q_lens", i32, device, per),
+            _array(block_table, "block_table", i32, device, torch.Size((batch, max_blocks))), max_blocks, max_seq_len)
+    with cache.on_device():
+        if workspace is None:
+            n = tq_kv8_workspace_bytes(cache, batch, heads, q_len, max_seq_len)
+            workspace = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+        elif workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {device}")
+        check(lib().tq_kv8_attention(cache.ref, layer, ctypes.byref(qr), dtype, batch, heads, q_len, *args, sc,
+                                     ctypes.byref(orow), workspace.data_ptr() if workspace is not None else None,
+                                     workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                     _stream(stream)), "tq_kv8_attention")
+    return out
+
+
+class _Here:
+    """Nothing to switch: the cache's device is the current one."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *_):
+        return False
+
+
+_HERE = _Here()
+
+
+class KV8Cache:
+    """A paged 8-bit cache: codes [layer, block, kv head, token, head_dim], scale bytes [layer, block, kv head]."""
+
+    def __init__(self, num_layers: int, num_blocks: int, block_tokens: int, num_kv_heads: int, head_dim: int,
+                 format: int = TQ_KV8_E4M3, device="cuda"):
+        torch = _torch()
+        codes = (num_layers, num_blocks, num_kv_heads, block_tokens, head_dim)
+        self._set(*(torch.zeros(codes, dtype=torch.uint8, device=device) for _ in "kv"),
+                  *(torch.full(codes[:3], 127, dtype=torch.uint8, device=device) for _ in "kv"), format)
+
+    @classmethod
+    def wrap(cls, k_codes, v_codes, k_scales, v_scales, format: int = TQ_KV8_E4M3) -> "KV8Cache":
+        """A cache over tensors of the caller's (uint8; without the layer axis: one layer). Scale bytes in [64, 190]."""
+        self = cls.__new__(cls)
+        if k_codes.dim() == 4:
+            k_codes, v_codes, k_scales, v_scales = (t.unsqueeze(0) for t in (k_codes, v_codes, k_scales, v_scales))
+        self._set(k_codes, v_codes, k_scales, v_scales, format)
+        return self
+
+    def _set(self, k_codes, v_codes, k_scales, v_scales, format):
+        torch = _torch()
+        if k_codes.dim() != 5 or v_codes.shape != k_codes.shape or k_scales.shape != k_codes.shape[:3] \
+                or v_scales.shape != k_scales.shape:
+            raise ValueError("codes must be [layers, blocks, kv heads, tokens, head_dim], scales [layers, blocks, kv heads]")
+        for t in (k_codes, v_codes, k_scales, v_scales):
+            if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != k_codes.device or not t.is_cuda:
+                raise ValueError("codes and scales must be contiguous uint8 tensors on one CUDA device")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.num_layers, self.num_blocks, self.num_kv_heads, self.block_tokens, self.head_dim = k_codes.shape
+        self.format = format
+        self.device = k_codes.device
+        self.desc = tq_kv8_cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                                 k_codes.stride(0), k_scales.stride(0), self.num_layers, self.num_blocks,
+                                 self.block_tokens, self.num_kv_heads, self.head_dim, format)
+        self.ref = ctypes.byref(self.desc)
+
+    def on_device(self):
+        torch = _torch()
+        return _HERE if torch.cuda.current_device() == self.device.index else torch.cuda.device(self.device)
+
+    @property
+    def nbytes(self) -> int:
+        return 2 * (self.k_codes.numel() + self.k_scales.numel())
+
+    def append(self, layer, k, v, seq_lens, block_table=None, max_blocks=0, new_lens=None, rope=None, positions=None,
+               stream=None):
+        tq_kv8_append(self, layer, k, v, seq_lens, block_table, max_blocks, new_lens, rope, positions, stream)
+
+    def workspace_bytes(self, batch, num_q_heads, q_len, max_seq_len):
+        return tq_kv8_workspace_bytes(self, batch, num_q_heads, q_len, max_seq_len)
+
+    def attention(self, layer, q, seq_lens, block_table=None, max_blocks=0, max_seq_len=0, out=None, workspace=None,
+                  q_lens=None, scale=0.0, softcap=0.0, slopes=None, window=0, prefix_lens=None, doc_starts=None,
+                  rope=None, positions=None, stream=None):
+        return tq_kv8_attention(self, layer, q, seq_lens, block_table, max_blocks, max_seq_len, out, workspace, q_lens,
+                                scale, softcap, slopes, window, prefix_lens, doc_starts, rope, positions, stream)

@@ -36,6 +36,10 @@ TQ_DEVERR_CAPACITY = 1
 TQ_DEVERR_BLOCK = 2
 TQ_DEVERR_SEQLEN = 4
 TQ_DEVERR_TIMEOUT = 8
+TQ_DEVERR_NONFINITE = 16
+
+TQ_KV8_E4M3 = 0
+TQ_KV8_INT8 = 1
 
 TQ_NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -82,6 +86,30 @@ class tq_split_state(ctypes.Structure):
     _fields_ = [("key_low", ctypes.c_void_p), ("value_low", ctypes.c_void_p), ("key_high", ctypes.c_void_p),
                 ("value_high", ctypes.c_void_p), ("low", ctypes.POINTER(tq_cache_desc)),
                 ("high", ctypes.POINTER(tq_cache_desc))]
+
+
+class tq_kv8_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("code_layer_stride", ctypes.c_int64),
+                ("scale_layer_stride", ctypes.c_int64), ("num_layers", ctypes.c_int), ("num_blocks", ctypes.c_int),
+                ("block_tokens", ctypes.c_int), ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("format", ctypes.c_int)]
+
+
+class tq_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64)]
+
+
+class tq_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class tq_kv8_scores(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("window", ctypes.c_int), ("prefix_lens", ctypes.c_void_p), ("doc_starts", ctypes.c_void_p),
+                ("rope", ctypes.POINTER(tq_rope)), ("positions", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -136,6 +164,11 @@ SIGNATURES = {
     "tq_batch_extend": (_ST, [ctypes.POINTER(tq_batch), ctypes.POINTER(tq_batch), _P, _I, _P, _P]),
     "tq_batch_merge": (_ST, [ctypes.POINTER(tq_batch), ctypes.POINTER(tq_batch), _I, _P, _I, _P, _P]),
     "tq_batch_extract": (_ST, [ctypes.POINTER(tq_batch), _I, ctypes.POINTER(tq_batch), _P, _I, _P, _P]),
+    "tq_kv8_append": (_ST, [ctypes.POINTER(tq_kv8_cache), _I, ctypes.POINTER(tq_rows), ctypes.POINTER(tq_rows), _I, _I,
+                            _I, _P, _P, _P, _I, ctypes.POINTER(tq_rope), _P, _P]),
+    "tq_kv8_workspace_bytes": (_ST, [ctypes.POINTER(tq_kv8_cache), _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "tq_kv8_attention": (_ST, [ctypes.POINTER(tq_kv8_cache), _I, ctypes.POINTER(tq_rows), _I, _I, _I, _I, _P, _P, _P,
+                               _I, _I, ctypes.POINTER(tq_kv8_scores), ctypes.POINTER(tq_rows), _P, _SZ, _P]),
     "tq_device_error": (_ST, [ctypes.POINTER(ctypes.c_uint32)]),
     "tq_selftest_wait_timeout": (_ST, [ctypes.c_double, _P]),
 }

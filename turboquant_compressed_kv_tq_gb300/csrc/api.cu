@@ -23,6 +23,8 @@ unsigned* g_err_ptr[kMaxDevices] = {};
 int g_num_sms[kMaxDevices] = {};
 std::mutex g_dev_mu;
 
+}  // namespace
+
 tq_status device_state(unsigned** err, int* num_sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TQ_ERR_CUDA;
@@ -42,6 +44,8 @@ tq_status device_state(unsigned** err, int* num_sms) {
     if (num_sms) *num_sms = g_num_sms[dev];
     return TQ_OK;
 }
+
+namespace {
 
 // The bounded-wait error path, on its own: one thread waits on an mbarrier
 // that nothing arrives on (mbarrier.try_wait.parity in a loop, as the kernels

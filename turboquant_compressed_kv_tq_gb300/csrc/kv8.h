@@ -1,0 +1,76 @@
+// Internal declarations of the 8-bit cache's kernels (kv8_api.cu checks the
+// arguments and launches; kv8_append.cu, kv8_decode.cu and kv8_prefill.cu hold
+// the kernels).
+#pragma once
+
+#include "tq_internal.h"
+
+namespace tq {
+namespace kv8 {
+
+// One layer of an 8-bit cache and the block table over it.
+struct Pool {
+    uint8_t *kc, *vc;   // codes [block][head][token][dim]
+    uint8_t *kx, *vx;   // scale bytes [block][head]
+    const int32_t* table;
+    int max_blocks, num_blocks, H, BT, bt_shift;
+};
+
+struct Rows {
+    void* data;
+    int64_t sb, sh, st;   // strides in elements
+};
+
+struct Rope {
+    const double* inv_freq;
+    int rot, inter;
+    float scale;
+    const int32_t* positions;   // [batch][n] or null
+};
+
+struct AppendArgs {
+    Pool pool;
+    Rows k, v;
+    Rope rope;
+    int batch, n_new;
+    const int32_t *seq, *news;
+    unsigned* err;
+};
+
+struct AttendArgs {
+    Pool pool;
+    Rows q, out;
+    Rope rope;
+    int batch, Hq, G, L;
+    const int32_t *seq, *qlens;
+    int max_seq;
+    float scale, cap;
+    const float* slopes;
+    int window;
+    const int32_t *prefix, *docs;
+    // split partials: [batch][H][row groups][splits][rows of a group] x (reference, sum) and x D
+    float *part_ml, *part_o;
+    int splits, split_tiles;   // token splits per row group, and the tiles of each
+    int groups;                // row groups per (sequence, KV head)
+    unsigned* err;
+};
+
+// The launch shape of an attention call, shared by workspace sizing and the launch.
+struct AttendPlan {
+    int chunk;         // 1: the tensor-memory kernel (many rows), 0: the split kernel (few rows)
+    int group_rows;    // query rows of a group
+    int groups;        // ceil(G q_len / group_rows)
+    int splits, split_tiles;
+    size_t ml_bytes, total;
+};
+
+AttendPlan attend_plan(int D, int batch, int H, int G, int L, int max_seq, int num_sms);
+
+#ifdef __CUDACC__
+cudaError_t launch_append(const AppendArgs& a, int D, int format, int dtype, cudaStream_t s);
+cudaError_t launch_decode(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s);
+cudaError_t launch_prefill(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s);
+#endif
+
+}  // namespace kv8
+}  // namespace tq

@@ -1,0 +1,527 @@
+// Attention over the 8-bit cache for few query rows: single tokens, a few
+// speculative ones.
+//
+// The rows of one KV head (r = l G + g: query l, head g of the group) are taken
+// kRows = 8 NT at a time; the tokens are split over CTAs, and each warp of a CTA
+// walks tiles of 16 tokens of its own. Per tile (mma.sync m16n8k16, fp16 in, fp32
+// out; tokens and coordinates on M, query rows on N, so that 8 rows waste
+// nothing):
+//   S^T = K Q^T      A = the tile's key codes, B = the queries (registers)
+//   u   = log2(e) score + log2(value scale)   masks, cap and bias on the way
+//   p   = 2^(u - M)  M: the row's reference, moved only when u passes it by 8
+//   l  += p / value scale
+//   O^T += V^T P     A = the tile's value codes, B = p (two 8x8 transposes)
+// Codes become fp16 exactly; block scales are powers of two and stay out of the
+// operands: the keys' is a factor of the scores, the values' moves the softmax's
+// reference (p <= 2^8 whatever the scales are) and is divided out of the sum.
+//
+// Layout. The coordinates (and for values the token pairs) that an MMA operand
+// wants in one lane are whatever order both operands share, so each lane takes
+// 16 consecutive bytes: of keys, lane (g, c) reads tokens g and g + 8 at bytes
+// 64 i + 16 c; of values, tokens 2c, 2c + 1, 2c + 8, 2c + 9 at bytes 128 i + 16 g.
+// Every load is 16 bytes a lane, straight from global memory to the operand's
+// registers, a tile ahead of its use: no shared memory, no barrier in the loop.
+//
+// Bound: memory, 2 D bytes a token.
+#include <climits>
+
+#include "kv8_device.cuh"
+#include "tc_ptx.cuh"
+
+namespace tq {
+namespace kv8 {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -1e30f;    // reference of a row that has seen nothing
+constexpr float kGap = 8.0f;       // how far scores may pass the reference (log2 units)
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+    return r;
+}
+
+template <int W>
+struct Words {   // W 32-bit words of one lane's load
+    uint32_t w[W];
+};
+template <int W>
+__device__ __forceinline__ void load_words(Words<W>& d, const uint8_t* p) {
+    if constexpr (W == 4) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+        d.w[0] = u.x, d.w[1] = u.y, d.w[2] = u.z, d.w[3] = u.w;
+    } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        d.w[0] = u.x, d.w[1] = u.y;
+    }
+}
+
+// Warps of a CTA: as many as fit next to the registers a warp needs.
+template <int D, int NT>
+struct Shape {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kWarps = D * NT >= 256 ? 8 : 8;
+    static constexpr int kCtas = D * NT >= 256 ? 1 : 2;   // per SM
+    static constexpr int kKL = D / 64;                 // key loads per token
+    static constexpr int kVW = D >= 128 ? 4 : 2;       // words of a value load
+    static constexpr int kVL = D / (32 * kVW);         // value loads per token
+    static constexpr int kMT = D / 16;                 // value MMAs
+};
+
+// What the rows of a group see, as tiles: [0, n1) and then [first, first + n2).
+struct Tiles {
+    int n1, first, n2;
+    __device__ __forceinline__ int at(int i) const { return i < n1 ? i : first + (i - n1); }
+    __device__ __forceinline__ int count() const { return n1 + n2; }
+};
+
+template <typename T, int D, int NT, bool I8>
+__global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas) decode_kernel(const __grid_constant__ AttendArgs A) {
+    using S = Shape<D, NT>;
+    constexpr int kRows = S::kRows, kThreads = 32 * S::kWarps;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __half* s_q = reinterpret_cast<__half*>(smem);   // [kRows][D], then the warps' outputs
+    __shared__ uint64_t s_turns[D / 2];
+    __shared__ float s_fac[kRows], s_m[S::kWarps][kRows], s_l[S::kWarps][kRows];
+    __shared__ Sight s_sight[kRows];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const Pool& P = A.pool;
+    const int grp = blockIdx.x % A.groups, split = blockIdx.x / A.groups, h = blockIdx.y, b = blockIdx.z;
+    const int rows = min(A.G * A.L - grp * kRows, kRows);
+
+    int N = A.seq[b], nq = A.qlens ? A.qlens[b] : A.L;
+    const bool bad_n = N < 0 || N > A.max_seq || (N + P.BT - 1) >> P.bt_shift > P.max_blocks, bad_q = nq < 0 || nq > A.L;
+    if (bad_n) N = 0;
+    if (bad_q) nq = nq < 0 ? 0 : A.L;
+    if ((bad_n || bad_q) && tid == 0 && blockIdx.x == 0 && h == 0) atomicOr(A.err, TQ_DEVERR_SEQLEN);
+    const int l_first = grp * kRows / A.G, l_last = min((grp * kRows + rows - 1) / A.G, nq - 1);
+    if (l_first >= nq) return;   // only rows behind the sequence's queries
+
+    // ---------------- what each row sees, and the tiles that any row sees
+    const int pre = A.prefix ? min(max(A.prefix[b], 0), N) : 0;
+    auto sight_of = [&](int l) {
+        Sight s;
+        s.p = N - nq + l;
+        s.lo = 0;
+        if (A.window > 0) s.lo = max(s.lo, s.p - A.window + 1);
+        if (A.docs) s.lo = max(s.lo, A.docs[static_cast<int64_t>(b) * A.L + l]);
+        s.prefix = pre;
+        return s;
+    };
+    int lo_min = INT_MAX, lo_max = 0;
+    for (int l = l_first; l <= l_last; ++l) {
+        const Sight s = sight_of(l);
+        lo_min = min(lo_min, s.lo);
+        lo_max = max(lo_max, s.lo);
+    }
+    const int p_min = N - nq + l_first, p_max = N - nq + l_last;
+    Tiles tiles;
+    tiles.n1 = (pre + 15) >> 4;
+    tiles.first = max(tiles.n1, lo_min >> 4);
+    tiles.n2 = max(0, ((p_max + 16) >> 4) - tiles.first);   // p_max >= -A.L
+    if (lo_min > p_max) tiles.n2 = 0;
+    const int i_begin = split * A.split_tiles, i_end = min(i_begin + A.split_tiles, tiles.count());
+    const int per = (max(i_end - i_begin, 0) + S::kWarps - 1) / S::kWarps;   // tiles of a warp, consecutive
+    const int w_begin = min(i_begin + warp * per, i_end), w_end = min(w_begin + per, i_end);
+
+    const int64_t unit = (static_cast<int64_t>(b) * P.H + h) * A.groups + grp;
+    if (i_begin >= i_end && A.splits > 1) {   // nothing here: the join skips it
+        if (tid < rows) *reinterpret_cast<float2*>(A.part_ml + 2 * ((unit * A.splits + split) * kRows + tid)) = make_float2(kNone, 0.0f);
+        return;
+    }
+
+    // ---------------- the queries: rotated, scaled by a power of two, fp16
+    if (i_begin < i_end) {
+        if (A.rope.rot > 0) {
+            for (int i = tid; i < A.rope.rot / 2; i += kThreads) s_turns[i] = turns_of(A.rope.inv_freq[i]);
+            __syncthreads();
+        }
+        constexpr int J = D / 16;   // chunk pairs of a row: J consecutive lanes
+        for (int it = tid; it < kRows * J; it += kThreads) {
+            const int r = it / J, j = it % J;
+            const int rr = grp * kRows + r, l = rr / A.G;
+            float xa[8] = {}, xb[8] = {};
+            int a0, b0;
+            chunk_pair(j, A.rope.rot, A.rope.inter, a0, b0);
+            if (r < rows && l < nq) {
+                const T* q = static_cast<const T*>(A.q.data) + b * A.q.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.q.sh + l * A.q.st;
+                load8(q + a0, xa);
+                load8(q + b0, xb);
+                if (A.rope.rot > 0)
+                    rotate_pair(xa, xb, j, A.rope, s_turns, A.rope.positions ? A.rope.positions[static_cast<int64_t>(b) * A.L + l] : N - nq + l);
+            }
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(xa[i]), fabsf(xb[i])));
+#pragma unroll
+            for (int o = J / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // to [1, 2): fp16 then keeps 11 bits down to 2^-14 of the row's largest
+            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126), 126);
+            const float f = exp2i(-e);
+            uint32_t* d = reinterpret_cast<uint32_t*>(s_q + r * D);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                d[a0 / 2 + i] = pack_out<__half>(xa[2 * i] * f, xa[2 * i + 1] * f);
+                d[b0 / 2 + i] = pack_out<__half>(xb[2 * i] * f, xb[2 * i + 1] * f);
+            }
+            if (j == 0) s_fac[r] = A.scale * exp2i(e);
+        }
+    }
+    if (tid < kRows) {
+        const int l = min((grp * kRows + tid) / A.G, l_last);
+        s_sight[tid] = sight_of(max(l, l_first));
+    }
+    __syncthreads();
+
+    float acc[NT][S::kMT][4];
+    float m[NT][2], l_sum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < S::kMT; ++j) acc[nt][j][0] = acc[nt][j][1] = acc[nt][j][2] = acc[nt][j][3] = 0.0f;
+        m[nt][0] = m[nt][1] = kNone;
+        l_sum[nt][0] = l_sum[nt][1] = 0.0f;
+    }
+    if (w_begin < w_end) {
+        uint32_t qf[NT][D / 16][2];
+        float fac[NT][2], slope[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(s_q + (8 * nt + g) * D);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {   // step 4 i + s: coordinates 64 i + 16 c + 4 s ..
+                const int d = 64 * (ks >> 2) + 16 * c + 4 * (ks & 3);
+                qf[nt][ks][0] = q[d / 2];
+                qf[nt][ks][1] = q[d / 2 + 1];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * nt + 2 * c + e;
+                fac[nt][e] = s_fac[r];
+                const int rr = grp * kRows + r;
+                slope[nt][e] = A.slopes && r < rows ? A.slopes[h * A.G + rr % A.G] * kLog2e : 0.0f;
+            }
+        }
+        const bool plain = A.cap <= 0.0f && !A.slopes;
+        const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
+        const int64_t unit_bytes = static_cast<int64_t>(P.BT) * D;
+
+        // lane k holds the block and scales of the warp's tile base + k
+        int base = w_begin, my_id = -1, my_kx = 0, my_vx = 0;
+        auto look_up = [&](int from) {
+            my_id = -1;
+            my_kx = my_vx = 0;
+            const int i = from + lane;
+            if (i < w_end) {
+                const int lb = (tiles.at(i) << 4) >> P.bt_shift;
+                const int64_t id = P.table ? P.table[b * static_cast<int64_t>(P.max_blocks) + lb] : b * static_cast<int64_t>(P.max_blocks) + lb;
+                if (id >= 0 && id < P.num_blocks) {
+                    my_id = static_cast<int>(id);
+                    my_kx = P.kx[id * P.H + h];
+                    my_vx = P.vx[id * P.H + h];
+                } else {
+                    atomicOr(A.err, TQ_DEVERR_BLOCK);
+                }
+            }
+        };
+        look_up(base);
+        Words<4> kw[2][S::kKL];
+        Words<S::kVW> vw[4][S::kVL];
+        // offset of tile i's codes in the pool, or -1
+        auto offset_of = [&](int i) -> int64_t {
+            const int id = __shfl_sync(0xffffffffu, my_id, i - base);
+            return id < 0 ? -1 : (static_cast<int64_t>(id) * P.H + h) * unit_bytes + static_cast<int64_t>((tiles.at(i) << 4) & (P.BT - 1)) * D;
+        };
+        auto load_k = [&](int64_t off) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < S::kKL; ++i) load_words(kw[t][i], P.kc + (off < 0 ? 0 : off) + (g + 8 * t) * D + 64 * i + 16 * c);
+        };
+        auto load_v = [&](int64_t off) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < S::kVL; ++i)
+                    load_words(vw[t][i], P.vc + (off < 0 ? 0 : off) + (2 * c + (t & 1) + 8 * (t >> 1)) * D + 32 * S::kVW * i + 4 * S::kVW * g);
+        };
+        int64_t off = offset_of(w_begin);
+        load_k(off);
+        load_v(off);
+        for (int i = w_begin; i < w_end; ++i) {
+            const int t0 = tiles.at(i) << 4;
+            const int kx = __shfl_sync(0xffffffffu, my_kx, i - base), vx = __shfl_sync(0xffffffffu, my_vx, i - base);
+            const bool here = off >= 0;
+            int64_t next = -1;
+            const bool more = i + 1 < w_end;
+            if (more) {
+                if (i + 1 - base == 32) {
+                    base = i + 1;
+                    look_up(base);
+                }
+                next = offset_of(i + 1);
+            }
+            // ---------------- scores
+            float sc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t a0, a1, a2, a3;
+                codes_f16<I8>(kw[0][ks >> 2].w[ks & 3], a0, a2);
+                codes_f16<I8>(kw[1][ks >> 2].w[ks & 3], a1, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+            }
+            if (more) load_k(next);
+            // ---------------- u = log2(e) score + log2(value scale), masked
+            const float ks2 = exp2i(kx == 0 ? -126 : kx - 127), lv = static_cast<float>(vx - 127);
+            const bool open = here && t0 + 15 <= p_min && t0 >= lo_max;
+            float u[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {   // e: token g + 8 (e >> 1), row 2c + (e & 1)
+                    const float s = sc[nt][e] * (fac[nt][e & 1] * ks2);
+                    if (plain) {
+                        u[nt][e] = fmaf(s, kLog2e, lv);
+                    } else {
+                        float y = s * kLog2e;
+                        if (A.cap > 0.0f) y = cap2 - 2.0f * cap2 * __frcp_rn(1.0f + ex2(s * cap_in));
+                        if (A.slopes) {
+                            const int p = s_sight[8 * nt + 2 * c + (e & 1)].p;
+                            y -= slope[nt][e & 1] * fabsf(static_cast<float>(p - (t0 + g + 8 * (e >> 1))));
+                        }
+                        u[nt][e] = y + lv;
+                    }
+                }
+            if (!open) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = t0 + g + 8 * (e >> 1);
+                        if (!(here && t < N && s_sight[8 * nt + 2 * c + (e & 1)].sees(t))) u[nt][e] = -INFINITY;
+                    }
+                // codes behind the sequence's end, or of no block, may be anything:
+                // their weight is 0, so they only have to be finite
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (!here || t0 + 2 * c + (t & 1) + 8 * (t >> 1) >= N)
+#pragma unroll
+                        for (int k = 0; k < S::kVL; ++k)
+#pragma unroll
+                            for (int w = 0; w < S::kVW; ++w) vw[t][k].w[w] = 0;
+            }
+            // ---------------- the reference moves only when a score passes it by the gap
+            bool pass = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pass |= u[nt][e] > m[nt][e & 1] + kGap;
+            if (__any_sync(0xffffffffu, pass)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = fmaxf(u[nt][e], u[nt][e + 2]);
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        x = fmaxf(x, m[nt][e]);
+                        const float alpha = ex2(m[nt][e] - x);
+                        m[nt][e] = x;
+                        l_sum[nt][e] *= alpha;
+#pragma unroll
+                        for (int j = 0; j < S::kMT; ++j) {
+                            acc[nt][j][e] *= alpha;
+                            acc[nt][j][e + 2] *= alpha;
+                        }
+                    }
+            }
+            // ---------------- p, its sum, and p as the second operand (rows on N)
+            const float iv = exp2i(127 - vx < -126 ? -126 : min(127 - vx, 126));
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = ex2(u[nt][e] - m[nt][e & 1]);
+                    l_sum[nt][e & 1] = fmaf(p[e], iv, l_sum[nt][e & 1]);
+                }
+                pb[nt][0] = transpose8x8(pack_out<__half>(p[0], p[1]));
+                pb[nt][1] = transpose8x8(pack_out<__half>(p[2], p[3]));
+            }
+            // ---------------- O^T += V^T P
+#pragma unroll
+            for (int k = 0; k < S::kVL; ++k)
+#pragma unroll
+                for (int w = 0; w < S::kVW; ++w) {
+                    uint32_t x[2][4];   // [token pair][coordinate]: fp16 pairs of two tokens
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t a = vw[2 * t][k].w[w], d = vw[2 * t + 1][k].w[w];
+                        codes_f16<I8>(__byte_perm(a, d, 0x5140), x[t][0], x[t][1]);
+                        codes_f16<I8>(__byte_perm(a, d, 0x7362), x[t][2], x[t][3]);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816(acc[nt][(k * S::kVW + w) * 2], x[0][0], x[0][1], x[1][0], x[1][1], pb[nt][0], pb[nt][1]);
+                        mma16816(acc[nt][(k * S::kVW + w) * 2 + 1], x[0][2], x[0][3], x[1][2], x[1][3], pb[nt][0], pb[nt][1]);
+                    }
+                }
+            if (more) load_v(next);
+            off = next;
+        }
+    }
+
+    // ---------------- the CTA's state of each row: the warps' states at their largest reference
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float x = l_sum[nt][e];
+            x += __shfl_xor_sync(0xffffffffu, x, 4);
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            if (g == 0) {
+                s_m[warp][8 * nt + 2 * c + e] = m[nt][e];
+                s_l[warp][8 * nt + 2 * c + e] = x;
+            }
+        }
+    __syncthreads();   // and the queries in shared memory are done with
+    float* s_o = reinterpret_cast<float*>(smem);   // [warps][kRows][D]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * nt + 2 * c + e;
+            float top = s_m[0][r];
+            for (int w = 1; w < S::kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+            const float f = ex2(m[nt][e] - top);
+            float* o = s_o + (warp * kRows + r) * D;
+#pragma unroll
+            for (int k = 0; k < S::kVL; ++k)
+#pragma unroll
+                for (int w = 0; w < S::kVW; ++w) {
+                    const int j = (k * S::kVW + w) * 2;
+                    const int d = 32 * S::kVW * k + 4 * S::kVW * g + 4 * w;
+                    *reinterpret_cast<float4*>(o + d) =
+                        make_float4(acc[nt][j][e] * f, acc[nt][j][e + 2] * f, acc[nt][j + 1][e] * f, acc[nt][j + 1][e + 2] * f);
+                }
+        }
+    __syncthreads();
+    for (int it = tid; it < rows * (D / 4); it += kThreads) {
+        const int r = it / (D / 4), d = 4 * (it % (D / 4));
+        const int rr = grp * kRows + r, l = rr / A.G;
+        if (l >= nq) continue;
+        float top = s_m[0][r];
+        for (int w = 1; w < S::kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float sum = 0.0f;
+        for (int w = 0; w < S::kWarps; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kRows + r) * D + d);
+            o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+            sum = fmaf(s_l[w][r], ex2(s_m[w][r] - top), sum);
+        }
+        if (A.splits == 1) {
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.out.sh + l * A.out.st + d;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_out<T>(o.x * inv, o.y * inv), pack_out<T>(o.z * inv, o.w * inv));
+        } else {
+            const int64_t at = (unit * A.splits + split) * kRows + r;
+            *reinterpret_cast<float4*>(A.part_o + at * D + d) = o;
+            if (d == 0) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(top, sum);
+        }
+    }
+    tc::grid_release_dependents();
+}
+
+// Joins the splits of a row: out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i.
+// One warp per row and 128 coordinates; splits that no tile reached hold l = 0
+// at the reference kNone.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendArgs A, int group_rows) {
+    tc::grid_wait_prior();
+    constexpr int kLanes = D / 4 < 32 ? D / 4 : 32;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);   // over batch, H, rows
+    const int lane = threadIdx.x & 31;
+    const int R = A.G * A.L;
+    if (row >= static_cast<int64_t>(A.batch) * A.pool.H * R) return;
+    const int rr = static_cast<int>(row % R), h = static_cast<int>(row / R % A.pool.H), b = static_cast<int>(row / R / A.pool.H);
+    const int l = rr / A.G;
+    int nq = A.qlens ? A.qlens[b] : A.L;
+    if (l >= min(nq, A.L)) return;
+    const int64_t unit = (static_cast<int64_t>(b) * A.pool.H + h) * A.groups + rr / group_rows;
+    const int64_t at = unit * A.splits * group_rows + rr % group_rows;
+    float top = kNone;
+    for (int i = lane; i < A.splits; i += 32) top = fmaxf(top, A.part_ml[2 * (at + static_cast<int64_t>(i) * group_rows)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.0f;
+    float4 o[D / 128 > 0 ? D / 128 : 1] = {};
+    for (int i = 0; i < A.splits; ++i) {
+        const int64_t a = at + static_cast<int64_t>(i) * group_rows;
+        const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + 2 * a);
+        if (ml.y == 0.0f) continue;   // nothing seen: its output is not looked at
+        const float f = ex2(ml.x - top);
+        sum = fmaf(ml.y, f, sum);
+        if (lane < kLanes)
+#pragma unroll
+            for (int k = 0; k < (D / 128 > 0 ? D / 128 : 1); ++k) {
+                const float4 x = *reinterpret_cast<const float4*>(A.part_o + a * D + 128 * k + 4 * lane);
+                o[k].x = fmaf(x.x, f, o[k].x), o[k].y = fmaf(x.y, f, o[k].y), o[k].z = fmaf(x.z, f, o[k].z), o[k].w = fmaf(x.w, f, o[k].w);
+            }
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.out.sh + l * A.out.st;
+    if (lane < kLanes)
+#pragma unroll
+        for (int k = 0; k < (D / 128 > 0 ? D / 128 : 1); ++k)
+            *reinterpret_cast<uint2*>(dst + 128 * k + 4 * lane) =
+                make_uint2(pack_out<T>(o[k].x * inv, o[k].y * inv), pack_out<T>(o[k].z * inv, o[k].w * inv));
+}
+
+template <typename T, int D, int NT, bool I8>
+cudaError_t launch_t(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+    using S = Shape<D, NT>;
+    const int smem = S::kWarps * S::kRows * D * 4;
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, NT, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    decode_kernel<T, D, NT, I8><<<dim3(p.groups * p.splits, a.pool.H, a.batch), 32 * S::kWarps, smem, s>>>(a);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const int64_t rows = static_cast<int64_t>(a.batch) * a.pool.H * a.G * a.L;
+    e = launch_overlapped(join_kernel<T, D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, a, p.group_rows);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return e;
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const AttendArgs& a, const AttendPlan& p, int format, cudaStream_t s) {
+    if (format == TQ_KV8_INT8) return p.group_rows == 8 ? launch_t<T, D, 1, true>(a, p, s) : launch_t<T, D, 2, true>(a, p, s);
+    return p.group_rows == 8 ? launch_t<T, D, 1, false>(a, p, s) : launch_t<T, D, 2, false>(a, p, s);
+}
+
+template <typename T>
+cudaError_t launch_dtype(const AttendArgs& a, const AttendPlan& p, int D, int format, cudaStream_t s) {
+    return D == 64 ? launch_d<T, 64>(a, p, format, s) : D == 128 ? launch_d<T, 128>(a, p, format, s) : launch_d<T, 256>(a, p, format, s);
+}
+
+}  // namespace
+
+cudaError_t launch_decode(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s) {
+    return dtype == TQ_F16 ? launch_dtype<__half>(a, p, D, format, s) : launch_dtype<__nv_bfloat16>(a, p, D, format, s);
+}
+
+}  // namespace kv8
+}  // namespace tq
