@@ -69,6 +69,8 @@ AttendPlan attend_plan(int D, int batch, int H, int G, int L, int max_seq, int n
 #ifdef __CUDACC__
 cudaError_t launch_append(const AppendArgs& a, int D, int format, int dtype, cudaStream_t s);
 cudaError_t launch_decode(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s);
+// Joins the splits of an attention call (part_ml, part_o) into its output.
+cudaError_t launch_join(const AttendArgs& a, const AttendPlan& p, int D, int dtype, cudaStream_t s);
 cudaError_t launch_prefill(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s);
 #endif
 

@@ -89,6 +89,14 @@ tq_status check_sizes(const tq_kv8_cache* c, int batch, int Hq, int L, int max_s
 AttendPlan attend_plan(int D, int batch, int H, int G, int L, int max_seq, int num_sms) {
     AttendPlan p{};
     const int rows = G * L;
+    if (rows > 32) {   // the tensor-memory kernel
+        p.chunk = 1;
+        p.group_rows = D == 256 ? 128 : 256;
+        p.groups = (rows + p.group_rows - 1) / p.group_rows;
+        p.splits = 1;
+        p.split_tiles = kMaxTokens;
+        return p;
+    }
     p.group_rows = rows <= 8 ? 8 : 16;
     p.groups = (rows + p.group_rows - 1) / p.group_rows;
     const int64_t units = static_cast<int64_t>(batch) * H * p.groups;
@@ -208,9 +216,10 @@ tq_status tq_kv8_attention(const tq_kv8_cache* cache, int layer, const tq_rows* 
     a.splits = p.splits;
     a.split_tiles = p.split_tiles;
     a.groups = p.groups;
-    return launch_decode(a, p, cache->head_dim, cache->format, dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? TQ_OK
-               : TQ_ERR_CUDA;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = p.chunk ? launch_prefill(a, p, cache->head_dim, cache->format, dtype, s)
+                                  : launch_decode(a, p, cache->head_dim, cache->format, dtype, s);
+    return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
                         u[nt][e] = fmaf(s, kLog2e, lv);
                     } else {
                         float y = s * kLog2e;
-                        if (A.cap > 0.0f) y = cap2 - 2.0f * cap2 * __frcp_rn(1.0f + ex2(s * cap_in));
+                        if (A.cap > 0.0f) y = fmaf(-2.0f * cap2, rcp(1.0f + ex2(s * cap_in)), cap2);   // cap tanh(s / cap)
                         if (A.slopes) {
                             const int p = s_sight[8 * nt + 2 * c + (e & 1)].p;
                             y -= slope[nt][e & 1] * fabsf(static_cast<float>(p - (t0 + g + 8 * (e >> 1))));
@@ -498,12 +498,7 @@ cudaError_t launch_t(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     decode_kernel<T, D, NT, I8><<<dim3(p.groups * p.splits, a.pool.H, a.batch), 32 * S::kWarps, smem, s>>>(a);
     g_launches.fetch_add(1, std::memory_order_relaxed);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || p.splits == 1) return e;
-    const int64_t rows = static_cast<int64_t>(a.batch) * a.pool.H * a.G * a.L;
-    e = launch_overlapped(join_kernel<T, D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, a, p.group_rows);
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return e;
+    return cudaGetLastError();
 }
 
 template <typename T, int D>
@@ -520,7 +515,18 @@ cudaError_t launch_dtype(const AttendArgs& a, const AttendPlan& p, int D, int fo
 }  // namespace
 
 cudaError_t launch_decode(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s) {
-    return dtype == TQ_F16 ? launch_dtype<__half>(a, p, D, format, s) : launch_dtype<__nv_bfloat16>(a, p, D, format, s);
+    const cudaError_t e = dtype == TQ_F16 ? launch_dtype<__half>(a, p, D, format, s) : launch_dtype<__nv_bfloat16>(a, p, D, format, s);
+    return e != cudaSuccess || p.splits == 1 ? e : launch_join(a, p, D, dtype, s);
+}
+
+cudaError_t launch_join(const AttendArgs& a, const AttendPlan& p, int D, int dtype, cudaStream_t s) {
+    auto kernel = dtype == TQ_F16 ? (D == 64 ? join_kernel<__half, 64> : D == 128 ? join_kernel<__half, 128> : join_kernel<__half, 256>)
+                                  : (D == 64 ? join_kernel<__nv_bfloat16, 64>
+                                             : D == 128 ? join_kernel<__nv_bfloat16, 128> : join_kernel<__nv_bfloat16, 256>);
+    const int64_t rows = static_cast<int64_t>(a.batch) * a.pool.H * a.G * a.L;
+    const cudaError_t e = launch_overlapped(kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, a, p.group_rows);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return e;
 }
 
 }  // namespace kv8

@@ -205,6 +205,12 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // ------------------------------------------------------------------ what a query sees
 
 // The visible keys of one query: [lo, p] and [0, prefix), below the sequence's end.

@@ -1,0 +1,643 @@
+// Attention over the 8-bit cache for many query rows (chunks of a prompt), on
+// the 5th-generation tensor cores.
+//
+// A CTA owns kHalves x 128 query rows of one KV head (row r = l G + g: query l,
+// head g of the group, so that neighbouring rows see nearly the same keys) and
+// walks tiles of kT tokens (flash attention: one pass, running reference M and
+// sum l per row). Four kinds of warps:
+//   convert  4 warps: codes from global memory to registers (16 bytes a lane, a
+//            tile ahead), to fp16, to the operands in shared memory: keys and values alike as
+//            [8 tokens x 8 coordinates] core matrices, which are K-major for S = Q K^T and
+//            MN-major for O += P V, so nothing is transposed
+//   mma      1 thread: S = Q K^T (operands in shared memory, S in TMEM), O += P V (P in TMEM)
+//   softmax  4 warps a half, one row a thread: S from TMEM, masks, p = 2^(u - M)
+//            to TMEM as fp16, the row's sum; O is rescaled in TMEM only when a score passes
+//            the reference by 8 (log2 units)
+// With two halves one's softmax runs while the tensor cores work for the other;
+// with one (head_dim 256, whose O fills half of TMEM) the scores of the next tile
+// are computed ahead into a second buffer.
+//
+// Block scales are powers of two. Within a tile the codes are brought to the
+// tile's largest scale in fp16 (exact down to 2^-24 of it); that one scale is a
+// factor of the row's scores, and for values moves the softmax's reference:
+// u = log2(e) score + log2(scale), p = 2^(u - M), l += p / scale.
+//
+// Bound: softmax and conversion instructions next to the tensor cores' 4 D
+// flops per row and key.
+#include <climits>
+
+#include "kv8_device.cuh"
+#include "tc_ptx.cuh"
+#include "tc_tmem_wide.cuh"
+
+namespace tq {
+namespace kv8 {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -1e30f;
+constexpr float kGap = 8.0f;
+// 8 softmax warps, 4 converting ones, 1 for the MMAs: 152 registers a thread, which hold a row of 128 scores
+constexpr int kConvThreads = 128, kThreads = 416;
+
+template <int D>
+struct Shape {
+    static constexpr int kHalves = D == 256 ? 1 : 2;
+    static constexpr int kRows = 128 * kHalves;
+    static constexpr int kT = D == 256 ? 64 : 128;         // tokens of a tile
+    static constexpr int kOperand = kT * D * 2;            // bytes of a tile's keys or values as fp16
+    static constexpr int kVOff = 0, kKOff = 2 * kOperand, kQOff = 4 * kOperand;
+    static constexpr int kSmem = kQOff + kRows * D * 2;
+    // TMEM columns: O, S and P of half (or tile parity) x
+    static constexpr int kO = 0, kS = kHalves * D, kSStep = kT;
+    // P over the scores it comes from where TMEM is full (D 128), else apart
+    static constexpr bool kPOver = D == 128;
+    static constexpr int kP = kPOver ? kS : kS + 2 * kSStep, kPStep = kPOver ? kSStep : kT / 2;
+    static_assert((kPOver ? kS + 2 * kSStep : kP + 2 * kPStep) <= 512, "TMEM columns");
+    static constexpr int kGroups = kT / 8;                 // groups of 8 tokens
+    static constexpr int kUnits = kT * (D / 16) / kConvThreads;   // 16-byte loads of a converter a tile
+};
+
+// Byte offset of (row, d) in an operand of core matrices: 8 rows x 16 bytes.
+template <int D>
+__device__ __forceinline__ int core(int row, int d) {
+    return ((row >> 3) * (D / 8) + (d >> 3)) * 128 + (row & 7) * 16;
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+struct Tiles {
+    int n1, first, n2;
+    __device__ __forceinline__ int at(int i) const { return i < n1 ? i : first + (i - n1); }
+    __device__ __forceinline__ int count() const { return n1 + n2; }
+};
+
+// What the converters say about a tile.
+struct TileInfo {
+    int kref, vref;    // its scales' exponents
+    unsigned gone;     // groups of 8 tokens that belong to no block
+};
+
+template <typename T, int D, bool I8, bool MOD>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ AttendArgs A) {
+    using S = Shape<D>;
+    constexpr int kT = S::kT, kH = S::kHalves;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ uint64_t s_turns[D / 2];
+    __shared__ __align__(8) uint64_t s_bar[14];
+    __shared__ float s_fac[S::kRows];
+    __shared__ TileInfo s_info[4];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_fail;
+    uint64_t *k_full = s_bar, *k_free = s_bar + 2, *v_full = s_bar + 4, *v_free = s_bar + 6;
+    uint64_t *s_ready = s_bar + 8, *p_ready = s_bar + 10, *o_done = s_bar + 12;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Pool& P = A.pool;
+    // the longest rows first: the last wave then holds short ones
+    const int grp = A.groups - 1 - blockIdx.x / A.splits, split = blockIdx.x % A.splits, h = blockIdx.y, b = blockIdx.z;
+    const int rows = min(A.G * A.L - grp * S::kRows, S::kRows);
+
+    int N = A.seq[b], nq = A.qlens ? A.qlens[b] : A.L;
+    const bool bad_n = N < 0 || N > A.max_seq || (N + P.BT - 1) >> P.bt_shift > P.max_blocks, bad_q = nq < 0 || nq > A.L;
+    if (bad_n) N = 0;
+    if (bad_q) nq = nq < 0 ? 0 : A.L;
+    if ((bad_n || bad_q) && tid == 0 && blockIdx.x == 0 && h == 0) atomicOr(A.err, TQ_DEVERR_SEQLEN);
+    const int l_first = grp * S::kRows / A.G, l_last = min((grp * S::kRows + rows - 1) / A.G, nq - 1);
+    if (l_first >= nq) return;   // only rows behind the sequence's queries
+
+    const int pre = A.prefix ? min(max(A.prefix[b], 0), N) : 0;
+    auto sight_of = [&](int l) {
+        Sight s;
+        s.p = N - nq + l;
+        s.lo = 0;
+        if (A.window > 0) s.lo = max(s.lo, s.p - A.window + 1);
+        if (A.docs) s.lo = max(s.lo, A.docs[static_cast<int64_t>(b) * A.L + l]);
+        s.prefix = pre;
+        return s;
+    };
+    // the smallest first key of any row (each warp for itself)
+    int lo_min = INT_MAX;
+    if (A.docs) {
+        for (int l = l_first + lane; l <= l_last; l += 32) lo_min = min(lo_min, sight_of(l).lo);
+        lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+    } else {
+        lo_min = sight_of(l_first).lo;
+    }
+    const int p_max = N - nq + l_last;
+    Tiles tiles;
+    tiles.n1 = (pre + kT - 1) / kT;
+    tiles.first = max(tiles.n1, lo_min / kT);
+    tiles.n2 = p_max < 0 || lo_min > p_max ? 0 : max(0, p_max / kT + 1 - tiles.first);
+    const int i_begin = split * A.split_tiles, n_tiles = max(0, min(A.split_tiles, tiles.count() - i_begin));
+    const int64_t unit = (static_cast<int64_t>(b) * P.H + h) * A.groups + grp;
+
+    // ---------------- set up: TMEM, barriers, the queries (rotated, scaled by a power of two, fp16)
+    if (warp == 12) {
+        tc::tmem_alloc(&s_tmem, 512);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&k_full[s], kConvThreads / 32);
+            tc::mbar_init(&v_full[s], kConvThreads / 32);
+            tc::mbar_init(&k_free[s], 1);
+            tc::mbar_init(&v_free[s], 1);
+            tc::mbar_init(&s_ready[s], 1);
+            tc::mbar_init(&p_ready[s], 4);
+            tc::mbar_init(&o_done[s], 1);
+        }
+        tc::mbar_fence_init();
+        s_fail = 0;
+    }
+    if (A.rope.rot > 0)
+        for (int i = tid; i < A.rope.rot / 2; i += kThreads) s_turns[i] = turns_of(A.rope.inv_freq[i]);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    if (n_tiles > 0) {
+        constexpr int J = D / 16;   // chunk pairs of a row: J consecutive lanes
+        const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
+        for (int it = tid; it < S::kRows * J; it += kThreads) {
+            const int r = it / J, j = it % J;
+            const int rr = grp * S::kRows + r, l = rr / A.G;
+            float xa[8] = {}, xb[8] = {};
+            int a0, b0;
+            chunk_pair(j, A.rope.rot, A.rope.inter, a0, b0);
+            if (r < rows && l < nq) {
+                const T* q = static_cast<const T*>(A.q.data) + b * A.q.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.q.sh + l * A.q.st;
+                load8(q + a0, xa);
+                load8(q + b0, xb);
+                if (A.rope.rot > 0)
+                    rotate_pair(xa, xb, j, A.rope, s_turns, A.rope.positions ? A.rope.positions[static_cast<int64_t>(b) * A.L + l] : N - nq + l);
+            }
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(xa[i]), fabsf(xb[i])));
+#pragma unroll
+            for (int o = J / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126), 126);
+            const float f = sign * exp2i(-e);
+            uint4 va, vb;
+            va.x = pack_out<__half>(xa[0] * f, xa[1] * f), va.y = pack_out<__half>(xa[2] * f, xa[3] * f);
+            va.z = pack_out<__half>(xa[4] * f, xa[5] * f), va.w = pack_out<__half>(xa[6] * f, xa[7] * f);
+            vb.x = pack_out<__half>(xb[0] * f, xb[1] * f), vb.y = pack_out<__half>(xb[2] * f, xb[3] * f);
+            vb.z = pack_out<__half>(xb[4] * f, xb[5] * f), vb.w = pack_out<__half>(xb[6] * f, xb[7] * f);
+            *reinterpret_cast<uint4*>(smem + S::kQOff + core<D>(r, a0)) = va;
+            *reinterpret_cast<uint4*>(smem + S::kQOff + core<D>(r, b0)) = vb;
+            if (j == 0) s_fac[r] = fabsf(A.scale) * exp2i(e);
+        }
+    }
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const bool two = kH == 2 && rows > 128;   // the second half has rows
+
+    if (warp < 8) {
+        // ================================================= softmax
+        const int half = warp >> 2;
+        const int row = 128 * half + 32 * (warp & 3) + lane;
+        const bool mine = kH == 1 ? half == 0 : (half == 0 || two);
+        const uint32_t t_row = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        const uint32_t t_o = t_row + S::kO + (kH == 2 ? half * D : 0);
+        float m = kNone, l_sum = 0.0f;
+        bool ok = true;
+        const int rr = grp * S::kRows + min(row, rows - 1);
+        const int l_row = min(rr / A.G, nq - 1);
+        if (mine && n_tiles > 0) {
+            const Sight sight = sight_of(l_row);
+            const int p_min = __reduce_min_sync(0xffffffffu, sight.p), lo_max = __reduce_max_sync(0xffffffffu, sight.lo);
+            const float fac = s_fac[min(row, S::kRows - 1)];
+            const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
+            const float slope = MOD && A.slopes ? A.slopes[h * A.G + rr % A.G] * kLog2e : 0.0f;
+            for (int i = 0; i < n_tiles; ++i) {
+                const int t0 = tiles.at(i_begin + i) * kT;
+                const int sb = kH == 2 ? half : i & 1;                    // buffer of S and P
+                ok = tc::mbar_wait(&s_ready[sb], kH == 2 ? i & 1 : (i >> 1) & 1);
+                if (!ok) break;
+                tc::tc_fence_after();
+                const TileInfo info = s_info[i & 3];
+                const float kf = fac * exp2i(info.kref), lv = static_cast<float>(info.vref);
+                const float f = MOD ? 1.0f : fmaxf(kf * kLog2e, FLT_MIN);
+                const bool open = info.gone == 0 && ((t0 + kT - 1 <= p_min && t0 >= lo_max) || t0 + kT <= pre);
+                // 64 columns of the row's scores, k a multiple of 64: cap and bias applied, unseen ones -inf
+                auto finish = [&](uint32_t (&sr)[64], int k) {
+                    if constexpr (MOD) {
+                        const float from = static_cast<float>(t0 + k - sight.p);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) {
+                            const float s = __uint_as_float(sr[e]) * kf;
+                            float y = s * kLog2e;
+                            if (A.cap > 0.0f) y = fmaf(-2.0f * cap2, rcp(1.0f + ex2(s * cap_in)), cap2);
+                            if (A.slopes) y -= slope * fabsf(from + static_cast<float>(e));
+                            sr[e] = __float_as_uint(y);
+                        }
+                    }
+                    if (!open) {
+                        // the seen columns as bits, 32 at a time
+                        auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+#pragma unroll
+                        for (int n = 0; n < 64; n += 32) {
+                            const int at = t0 + k + n;
+                            uint32_t see = (below(sight.p - at + 1) & ~below(sight.lo - at)) | below(sight.prefix - at);
+                            if (info.gone) {
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+                                    if ((info.gone >> ((k + n) / 8 + g)) & 1u) see &= ~(0xFFu << (8 * g));
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) sr[n + e] = (see >> e) & 1u ? sr[n + e] : 0xFF800000u;
+                        }
+                    }
+                };
+                auto largest = [&](const uint32_t (&sr)[64]) {
+                    float x0 = __uint_as_float(sr[0]), x1 = __uint_as_float(sr[1]);
+#pragma unroll
+                    for (int e = 2; e < 64; e += 2) {
+                        x0 = fmaxf(x0, __uint_as_float(sr[e]));
+                        x1 = fmaxf(x1, __uint_as_float(sr[e + 1]));
+                    }
+                    return fmaxf(x0, x1);
+                };
+                // 128 scores are more registers than a thread has: the upper 64 are
+                // looked at for the maximum, and read again once the lower are done
+                const uint32_t t_s = t_row + S::kS + sb * S::kSStep;
+                uint32_t sr[64];
+                float top = -INFINITY;
+                if constexpr (kT == 128) {
+                    tc::tmem_ld(t_s + 64, sr);
+                    if (MOD || !open) {
+                        finish(sr, 64);
+                        tc::tmem_st(t_s + 64, sr);
+                    }
+                    top = largest(sr);
+                }
+                tc::tmem_ld(t_s, sr);
+                finish(sr, 0);
+                top = fmaf(fmaxf(top, largest(sr)), f, lv);
+                const bool pass = top > m + kGap;
+                if (__any_sync(0xffffffffu, pass)) {
+                    const float x = fmaxf(top, m);
+                    const float alpha = ex2(m - x);
+                    m = x;
+                    l_sum *= alpha;
+                    if (i > 0) {
+                        if (kH == 1) {
+                            ok = tc::mbar_wait(&o_done[0], (i - 1) & 1);
+                            if (!ok) break;
+                            tc::tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t v[32];
+                            tc::tmem_ld(t_o + 32 * c, v);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                            tc::tmem_st(t_o + 32 * c, v);
+                        }
+                    }
+                }
+                const uint64_t f2 = pack2(f, f), o2 = pack2(lv - m, lv - m);
+                uint64_t sum0 = 0, sum1 = 0;
+                auto weights = [&](int k) {   // of the 64 scores in sr
+#pragma unroll
+                    for (int n = 0; n < 64; n += 32) {
+                        uint32_t pr[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            float a, c, d, g;
+                            unpack2(fma2(pack2(__uint_as_float(sr[n + e]), __uint_as_float(sr[n + e + 1])), f2, o2), a, c);
+                            unpack2(fma2(pack2(__uint_as_float(sr[n + e + 2]), __uint_as_float(sr[n + e + 3])), f2, o2), d, g);
+                            a = ex2(a), c = ex2(c), d = ex2(d), g = ex2(g);
+                            sum0 = add2(sum0, pack2(a, c));
+                            sum1 = add2(sum1, pack2(d, g));
+                            pr[e / 2] = pack_out<__half>(a, c);
+                            pr[e / 2 + 1] = pack_out<__half>(d, g);
+                        }
+                        tc::tmem_st16u(t_row + S::kP + sb * S::kPStep + (k + n) / 2, pr);
+                    }
+                };
+                weights(0);
+                if constexpr (kT == 128) {
+                    tc::tmem_ld(t_s + 64, sr);
+                    weights(64);
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&p_ready[sb]);
+                float a, c, d, g;
+                unpack2(sum0, a, c);
+                unpack2(sum1, d, g);
+                l_sum = fmaf((a + c) + (d + g), exp2i(-info.vref), l_sum);
+            }
+            if (ok) ok = tc::mbar_wait(&o_done[kH == 2 ? half : 0], kH == 2 ? 0 : (n_tiles - 1) & 1);
+            if (!ok) {
+                s_fail = 1;
+                atomicOr(A.err, TQ_DEVERR_TIMEOUT);
+            }
+            tc::tc_fence_after();
+        }
+        // ---------------- the rows out, once every copy of s_fail is in
+        asm volatile("bar.sync 1, 256;\n" ::: "memory");
+        const bool failed = *const_cast<volatile int*>(&s_fail) != 0;
+        if (mine) {
+            const bool real = row < rows && rr / A.G < nq;
+            if (A.splits == 1) {
+                const float inv = !failed && l_sum > 0.0f ? 1.0f / l_sum : 0.0f;
+                T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.out.sh + (rr / A.G) * A.out.st;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float v[32];
+                    if (n_tiles > 0) tc::tmem_ld32(t_o + 32 * c, v);
+                    if (real) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 w = make_uint4(0, 0, 0, 0);
+                            if (inv > 0.0f) {
+                                w.x = pack_out<T>(v[e] * inv, v[e + 1] * inv), w.y = pack_out<T>(v[e + 2] * inv, v[e + 3] * inv);
+                                w.z = pack_out<T>(v[e + 4] * inv, v[e + 5] * inv), w.w = pack_out<T>(v[e + 6] * inv, v[e + 7] * inv);
+                            }
+                            *reinterpret_cast<uint4*>(dst + 32 * c + e) = w;
+                        }
+                    }
+                }
+            } else {
+                const int64_t at = (unit * A.splits + split) * S::kRows + row;
+                const bool some = !failed && l_sum > 0.0f;
+                if (real) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(some ? m : kNone, some ? l_sum : 0.0f);
+                if (n_tiles > 0)
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        float v[32];
+                        tc::tmem_ld32(t_o + 32 * c, v);
+                        if (real && some)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4*>(A.part_o + at * D + 32 * c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    }
+            }
+        }
+    } else if (warp < 12) {
+        // ================================================= convert
+        const int w = warp - 8;
+        constexpr int CQ = D / 64;               // quarters of 64 coordinates: a unit is a lane's 16 bytes of one
+        constexpr int TG = S::kUnits / CQ;       // token groups of a warp
+        const int64_t unit_bytes = static_cast<int64_t>(P.BT) * D;
+        const int tok = lane & 7, ch = lane >> 3;
+        // lane g < kGroups holds the block and scales of the tile's group g
+        int id = -1, kx = -64, vx = -64;
+        auto look_up = [&](int i) {
+            id = -1;
+            kx = vx = -64;
+            const int t = tiles.at(i_begin + i) * kT + 8 * lane;
+            if (lane < S::kGroups && t < N && (t <= p_max || t < pre)) {
+                const int lb = t >> P.bt_shift;
+                const bool seen = ((lb << P.bt_shift) + P.BT > lo_min) || (lb << P.bt_shift) < pre;
+                if (seen) {
+                    const int64_t x = P.table ? P.table[b * static_cast<int64_t>(P.max_blocks) + lb] : b * static_cast<int64_t>(P.max_blocks) + lb;
+                    if (x >= 0 && x < P.num_blocks) {
+                        id = static_cast<int>(x);
+                        kx = static_cast<int>(P.kx[x * P.H + h]) - 127;
+                        vx = static_cast<int>(P.vx[x * P.H + h]) - 127;
+                    } else {
+                        atomicOr(A.err, TQ_DEVERR_BLOCK);
+                    }
+                }
+            }
+        };
+        // unit k of a warp: group w + 4 (k / CQ), bytes 64 (k % CQ) + 16 ch of token tok
+        auto load = [&](uint4 (&x)[S::kUnits], const uint8_t* codes, int i) {
+            const int t0 = tiles.at(i_begin + i) * kT;
+#pragma unroll
+            for (int q = 0; q < TG; ++q) {
+                const int g = w + 4 * q, t = t0 + 8 * g + tok;
+                const int gid = __shfl_sync(0xffffffffu, id, g);
+                const uint8_t* p = codes + (static_cast<int64_t>(max(gid, 0)) * P.H + h) * unit_bytes + static_cast<int64_t>(t & (P.BT - 1)) * D + 16 * ch;
+#pragma unroll
+                for (int c = 0; c < CQ; ++c)
+                    x[q * CQ + c] = gid >= 0 && t < N ? __ldg(reinterpret_cast<const uint4*>(p + 64 * c)) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        // the codes times 2^(their group's exponent - ref), as fp16
+        auto convert = [&](const uint4 (&x)[S::kUnits], int ex, int ref, unsigned char* dst) {
+#pragma unroll
+            for (int q = 0; q < TG; ++q) {
+                const int g = w + 4 * q;
+                const int down = max(__shfl_sync(0xffffffffu, ex, g) - ref, -25);
+                const __half mul = __float2half_rn(down < -24 ? 0.0f : exp2i(down));
+                const __half2 mul2 = __half2(mul, mul);
+#pragma unroll
+                for (int c = 0; c < CQ; ++c) {
+                    const uint32_t in[4] = {x[q * CQ + c].x, x[q * CQ + c].y, x[q * CQ + c].z, x[q * CQ + c].w};
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        codes_f16<I8>(in[e], y[2 * e], y[2 * e + 1]);
+                        __half2 a = __hmul2(*reinterpret_cast<__half2*>(&y[2 * e]), mul2), d = __hmul2(*reinterpret_cast<__half2*>(&y[2 * e + 1]), mul2);
+                        y[2 * e] = *reinterpret_cast<uint32_t*>(&a);
+                        y[2 * e + 1] = *reinterpret_cast<uint32_t*>(&d);
+                    }
+                    unsigned char* o = dst + core<D>(8 * g + tok, 64 * c + 16 * ch);
+                    *reinterpret_cast<uint4*>(o) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4*>(o + 128) = make_uint4(y[4], y[5], y[6], y[7]);
+                }
+            }
+        };
+        bool ok = true;
+        if (n_tiles > 0) {
+            uint4 kr[S::kUnits], vr[S::kUnits];
+            look_up(0);
+            load(kr, P.kc, 0);
+            for (int i = 0; i < n_tiles; ++i) {
+                const int st = i & 1;
+                load(vr, P.vc, i);
+                const int kref = __reduce_max_sync(0xffffffffu, kx), vref = __reduce_max_sync(0xffffffffu, vx);
+                const int t0 = tiles.at(i_begin + i) * kT;
+                // groups of no block among those that have tokens
+                const unsigned gone = __ballot_sync(0xffffffffu, lane < S::kGroups && id < 0 && t0 + 8 * lane < N);
+                const int vx_now = vx;
+                if (i >= 2) ok = tc::mbar_wait(&k_free[st], ((i >> 1) - 1) & 1);
+                if (!ok) break;
+                if (w == 0 && lane == 0) s_info[i & 3] = TileInfo{kref, vref, gone};
+                convert(kr, kx, kref, smem + S::kKOff + st * S::kOperand);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&k_full[st]);
+                if (i + 1 < n_tiles) {
+                    look_up(i + 1);
+                    load(kr, P.kc, i + 1);
+                }
+                if (i >= 2) ok = tc::mbar_wait(&v_free[st], ((i >> 1) - 1) & 1);
+                if (!ok) break;
+                convert(vr, vx_now, vref, smem + S::kVOff + st * S::kOperand);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&v_full[st]);
+            }
+            if (!ok) {
+                s_fail = 1;
+                atomicOr(A.err, TQ_DEVERR_TIMEOUT);
+            }
+        }
+    } else {
+        // ================================================= mma
+        if (warp == 12 && lane == 0 && n_tiles > 0) {
+            constexpr uint32_t id_s = tc::idesc_f16_f32(128, kT);
+            constexpr uint32_t id_o = tc::idesc_f16_f32(128, D) | (1u << 16);   // B is MN-major: coordinates contiguous
+            constexpr uint32_t kRowStep = (D / 8) * 128;                        // bytes between groups of 8 rows
+            const uint32_t base = tc::smem_addr(smem);
+            const uint64_t dq = tc::smem_desc(base + S::kQOff, 128, kRowStep);
+            const uint64_t dk = tc::smem_desc(base + S::kKOff, 128, kRowStep);
+            const uint64_t dv = tc::smem_desc(base + S::kVOff, kRowStep, 128);
+            auto scores = [&](int x, int buf, int st) {   // half x's rows with stage st's keys into buffer buf
+                const uint64_t q = dq + static_cast<uint64_t>(x * 128 * D * 2 >> 4), k = dk + static_cast<uint64_t>(st * S::kOperand >> 4);
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) tc::mma_f16(tmem + S::kS + buf * S::kSStep, q + 16 * s, k + 16 * s, id_s, s > 0);
+            };
+            auto values = [&](int x, int buf, int st, bool more) {
+                const uint64_t v = dv + static_cast<uint64_t>(st * S::kOperand >> 4);
+                const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
+                const uint32_t o = tmem + S::kO + x * D, p = tmem + S::kP + buf * S::kPStep;
+#pragma unroll
+                for (int s = 0; s < kT / 16; ++s) {
+                    if (s == 0 && !more) tc::mma_f16_ta_w<false>(o, p, lo, hi, id_o);
+                    else tc::mma_f16_ta_w<true>(o, p + 8 * s, lo + s * (2 * kRowStep >> 4), hi, id_o);
+                }
+            };
+            bool ok = tc::mbar_wait(&k_full[0], 0);
+            int s_commits[2] = {0, 0}, o_commits[2] = {0, 0};
+            tc::tc_fence_after();
+            if constexpr (kH == 2) {
+                const int nh = two ? 2 : 1;
+                if (ok) {
+                    for (int x = 0; x < nh; ++x) {
+                        scores(x, x, 0);
+                        tc::mma_commit(&s_ready[x]);
+                        ++s_commits[x];
+                    }
+                    tc::mma_commit(&k_free[0]);
+                }
+                for (int i = 0; i < n_tiles && ok; ++i) {
+                    const int st = i & 1, sn = st ^ 1;
+                    for (int x = 0; x < nh && ok; ++x) {
+                        if (x == 0) ok = tc::mbar_wait(&v_full[st], (i >> 1) & 1);
+                        if (ok) ok = tc::mbar_wait(&p_ready[x], i & 1);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        values(x, x, st, i > 0);
+                        if (x == nh - 1) tc::mma_commit(&v_free[st]);
+                        if (i + 1 == n_tiles) {
+                            tc::mma_commit(&o_done[x]);
+                            ++o_commits[x];
+                        } else {
+                            if (x == 0) ok = tc::mbar_wait(&k_full[sn], ((i + 1) >> 1) & 1);
+                            if (!ok) break;
+                            tc::tc_fence_after();
+                            scores(x, x, sn);
+                            tc::mma_commit(&s_ready[x]);
+                            ++s_commits[x];
+                            if (x == nh - 1) tc::mma_commit(&k_free[sn]);
+                        }
+                    }
+                }
+            } else {
+                if (ok) {
+                    scores(0, 0, 0);
+                    tc::mma_commit(&s_ready[0]);
+                    ++s_commits[0];
+                    tc::mma_commit(&k_free[0]);
+                }
+                for (int i = 0; i < n_tiles && ok; ++i) {
+                    const int st = i & 1, sn = st ^ 1;
+                    if (i + 1 < n_tiles) {
+                        ok = tc::mbar_wait(&k_full[sn], ((i + 1) >> 1) & 1);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        scores(0, sn, sn);
+                        tc::mma_commit(&s_ready[sn]);
+                        ++s_commits[sn];
+                        tc::mma_commit(&k_free[sn]);
+                    }
+                    ok = tc::mbar_wait(&v_full[st], (i >> 1) & 1);
+                    if (ok) ok = tc::mbar_wait(&p_ready[st], (i >> 1) & 1);   // one a buffer: the next tile's may be there too
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    values(0, st, st, i > 0);
+                    tc::mma_commit(&v_free[st]);
+                    tc::mma_commit(&o_done[0]);
+                    ++o_commits[0];
+                }
+            }
+            if (!ok) {
+                s_fail = 1;
+                atomicOr(A.err, TQ_DEVERR_TIMEOUT);
+            }
+            // nothing is in flight when the CTA ends: the last phases of the commits
+            for (int x = 0; x < 2; ++x) {
+                if (s_commits[x]) (void)tc::mbar_wait(&s_ready[x], (s_commits[x] - 1) & 1);
+                if (o_commits[x]) (void)tc::mbar_wait(&o_done[x], (o_commits[x] - 1) & 1);
+            }
+        }
+        __syncwarp();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0)
+        for (int s = 0; s < 14; ++s) tc::mbar_inval(&s_bar[s]);
+    tc::grid_release_dependents();
+}
+
+template <typename T, int D, bool I8, bool MOD>
+cudaError_t launch_m(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+    using S = Shape<D>;
+    static_assert(S::kSmem <= 227 * 1024 - 4096, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<T, D, I8, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    prefill_kernel<T, D, I8, MOD><<<dim3(p.groups * p.splits, a.pool.H, a.batch), kThreads, S::kSmem, s>>>(a);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const AttendArgs& a, const AttendPlan& p, int format, cudaStream_t s) {
+    const bool mod = a.cap > 0.0f || a.slopes;
+    cudaError_t e;
+    if (format == TQ_KV8_INT8) e = mod ? launch_m<T, D, true, true>(a, p, s) : launch_m<T, D, true, false>(a, p, s);
+    else e = mod ? launch_m<T, D, false, true>(a, p, s) : launch_m<T, D, false, false>(a, p, s);
+    return e;
+}
+
+template <typename T>
+cudaError_t launch_dtype(const AttendArgs& a, const AttendPlan& p, int D, int format, cudaStream_t s) {
+    return D == 64 ? launch_d<T, 64>(a, p, format, s) : D == 128 ? launch_d<T, 128>(a, p, format, s) : launch_d<T, 256>(a, p, format, s);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s) {
+    const cudaError_t e = dtype == TQ_F16 ? launch_dtype<__half>(a, p, D, format, s) : launch_dtype<__nv_bfloat16>(a, p, D, format, s);
+    return e != cudaSuccess || p.splits == 1 ? e : launch_join(a, p, D, dtype, s);
+}
+
+}  // namespace kv8
+}  // namespace tq
