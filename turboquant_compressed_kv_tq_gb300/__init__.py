@@ -8,6 +8,7 @@ library's CUDA kernels. PyTorch provides device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import numpy as np
@@ -519,25 +520,30 @@ def _kv8_dtype(dtype) -> int:
     return code
 
 
-def _rows(t, name, dtype, device, shape) -> tq_rows:
-    """A [batch, heads, tokens, head_dim] view, in whatever order its first three axes lie."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must be [batch, heads, tokens, head_dim] = {tuple(shape)}, not {tuple(t.shape)}")
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} on {device}, not {t.dtype} on {t.device}")
+def _rows(t, name, dtype, device, batch, heads, tokens, dim) -> bytes:
+    """tq_rows of a [batch, heads, tokens, head_dim] view, in whatever order its first three axes lie."""
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != batch or shape[1] != heads or shape[2] != tokens or shape[3] != dim:
+        raise ValueError(f"{name} must be [batch, heads, tokens, head_dim] = {(batch, heads, tokens, dim)}, not {tuple(shape)}")
+    if t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} on cuda:{device}, not {t.dtype} on {t.device}")
     sb, sh, st, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}: the coordinates of a head must be contiguous")
     # the stride of an axis of one element says nothing, whatever it is
-    return tq_rows(t.data_ptr(), sb if shape[0] > 1 else 0, sh if shape[1] > 1 else 0, st if shape[2] > 1 else 0)
+    return _pack_rows(t.data_ptr(), sb if batch > 1 else 0, sh if heads > 1 else 0, st if tokens > 1 else 0)
 
 
-def _array(t, name, dtype, device, shape) -> Optional[int]:
+_pack_rows = struct.Struct("@Pqqq").pack                 # tq_rows
+_pack_scores = struct.Struct("@ffPiPPPP").pack           # tq_kv8_scores
+
+
+def _array(t, name, dtype, device, *shape) -> Optional[int]:
     """Pointer of a small contiguous argument (lengths, tables, slopes), or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, "
+    if t.dtype != dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on cuda:{device}, "
                          f"not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -556,8 +562,9 @@ class Rope:
         if not scale:
             raise ValueError("scale must not be 0")
         self.inv_freq = inv_freq
+        self.device = inv_freq.get_device()
         self.desc = tq_rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), scale)
-        self.ref = ctypes.byref(self.desc)
+        self.address = ctypes.addressof(self.desc)
 
     @classmethod
     def of_base(cls, rot_dim: int, base: float = 10000.0, device="cuda", interleaved: bool = False, scale: float = 1.0):
@@ -570,24 +577,22 @@ class Rope:
 def tq_kv8_append(cache: "KV8Cache", layer, k, v, seq_lens, block_table=None, max_blocks=0, new_lens=None, rope=None,
                   positions=None, stream=None):
     """Append k, v [batch, kv heads, n_new, head_dim] (views in any order of the first three axes) at seq_lens."""
-    torch = _torch()
-    device = cache.device
+    device, i32 = cache.index, _torch().int32
     if k.dim() != 4:
         raise ValueError("k must be [batch, heads, tokens, head_dim]")
-    batch, n_new = k.shape[0], k.shape[2]
-    shape = torch.Size((batch, cache.num_kv_heads, n_new, cache.head_dim))
-    kr = _rows(k, "k", k.dtype, device, shape)
-    vr = _rows(v, "v", k.dtype, device, shape)
-    i32, per = torch.int32, torch.Size((batch,))
-    if rope is not None and rope.inv_freq.device != device:
-        raise ValueError(f"rope must be on {device}")
-    args = (_array(seq_lens, "seq_lens", i32, device, per), _array(new_lens, "new_lens", i32, device, per),
-            _array(block_table, "block_table", i32, device, torch.Size((batch, max_blocks))), max_blocks,
-            rope.ref if rope is not None else None,
-            _array(positions, "positions", i32, device, torch.Size((batch, n_new))))
+    batch, _, n_new, _ = k.shape
+    dtype = k.dtype
+    heads, dim = cache.num_kv_heads, cache.head_dim
+    if rope is not None and rope.device != device:
+        raise ValueError(f"rope must be on cuda:{device}")
     with cache.on_device():
-        check(lib().tq_kv8_append(cache.ref, layer, ctypes.byref(kr), ctypes.byref(vr), _kv8_dtype(k.dtype), batch, n_new,
-                                  *args, _stream(stream)), "tq_kv8_append")
+        check(lib().tq_kv8_append(
+            cache.ref, layer, _rows(k, "k", dtype, device, batch, heads, n_new, dim),
+            _rows(v, "v", dtype, device, batch, heads, n_new, dim), _kv8_dtype(dtype), batch, n_new,
+            _array(seq_lens, "seq_lens", i32, device, batch), _array(new_lens, "new_lens", i32, device, batch),
+            _array(block_table, "block_table", i32, device, batch, max_blocks), max_blocks,
+            rope.address if rope is not None else None, _array(positions, "positions", i32, device, batch, n_new),
+            _stream(stream)), "tq_kv8_append")
 
 
 def tq_kv8_workspace_bytes(cache: "KV8Cache", batch, num_q_heads, q_len, max_seq_len) -> int:
@@ -607,38 +612,38 @@ def tq_kv8_attention(cache: "KV8Cache", layer, q, seq_lens, block_table=None, ma
     current stream, so give one where `stream` is another.
     """
     torch = _torch()
-    device = cache.device
+    device, i32 = cache.index, torch.int32
     if q.dim() != 4:
         raise ValueError("q must be [batch, heads, tokens, head_dim]")
     batch, heads, q_len, _ = q.shape
-    shape = torch.Size((batch, heads, q_len, cache.head_dim))
-    qr = _rows(q, "q", q.dtype, device, shape)
-    dtype = _kv8_dtype(q.dtype)
+    dtype, dim = q.dtype, cache.head_dim
+    qr = _rows(q, "q", dtype, device, batch, heads, q_len, dim)
+    code = _kv8_dtype(dtype)
     if out is None:
         out = torch.empty_like(q) if q_lens is None else torch.zeros_like(q)
-    orow = _rows(out, "out", q.dtype, device, shape)
-    i32, per = torch.int32, torch.Size((batch,))
-    each = torch.Size((batch, q_len))
-    if rope is not None and rope.inv_freq.device != device:
-        raise ValueError(f"rope must be on {device}")
+    if rope is not None and rope.device != device:
+        raise ValueError(f"rope must be on cuda:{device}")
     sc = None
     if scale or softcap or window or rope is not None or slopes is not None or prefix_lens is not None or doc_starts is not None:
-        sc = ctypes.byref(tq_kv8_scores(
-            scale, softcap, _array(slopes, "slopes", torch.float32, device, torch.Size((heads,))), window,
-            _array(prefix_lens, "prefix_lens", i32, device, per), _array(doc_starts, "doc_starts", i32, device, each),
-            ctypes.pointer(rope.desc) if rope is not None else None, _array(positions, "positions", i32, device, each)))
-    args = (_array(seq_lens, "seq_lens", i32, device, per), _array(q_lens, "q_lens", i32, device, per),
-            _array(block_table, "block_table", i32, device, torch.Size((batch, max_blocks))), max_blocks, max_seq_len)
+        sc = _pack_scores(scale, softcap, _array(slopes, "slopes", torch.float32, device, heads) or 0, window,
+                          _array(prefix_lens, "prefix_lens", i32, device, batch) or 0,
+                          _array(doc_starts, "doc_starts", i32, device, batch, q_len) or 0,
+                          rope.address if rope is not None else 0,
+                          _array(positions, "positions", i32, device, batch, q_len) or 0)
     with cache.on_device():
         if workspace is None:
             n = tq_kv8_workspace_bytes(cache, batch, heads, q_len, max_seq_len)
-            workspace = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-        elif workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {device}")
-        check(lib().tq_kv8_attention(cache.ref, layer, ctypes.byref(qr), dtype, batch, heads, q_len, *args, sc,
-                                     ctypes.byref(orow), workspace.data_ptr() if workspace is not None else None,
-                                     workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                     _stream(stream)), "tq_kv8_attention")
+            workspace = torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+        elif workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on cuda:{device}")
+        check(lib().tq_kv8_attention(
+            cache.ref, layer, qr, code, batch, heads, q_len, _array(seq_lens, "seq_lens", i32, device, batch),
+            _array(q_lens, "q_lens", i32, device, batch),
+            _array(block_table, "block_table", i32, device, batch, max_blocks), max_blocks, max_seq_len, sc,
+            _rows(out, "out", dtype, device, batch, heads, q_len, dim),
+            workspace.data_ptr() if workspace is not None else None,
+            workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)),
+            "tq_kv8_attention")
     return out
 
 
@@ -685,7 +690,7 @@ class KV8Cache:
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.num_layers, self.num_blocks, self.num_kv_heads, self.block_tokens, self.head_dim = k_codes.shape
         self.format = format
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
         self.desc = tq_kv8_cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                  k_codes.stride(0), k_scales.stride(0), self.num_layers, self.num_blocks,
                                  self.block_tokens, self.num_kv_heads, self.head_dim, format)
@@ -693,7 +698,7 @@ class KV8Cache:
 
     def on_device(self):
         torch = _torch()
-        return _HERE if torch.cuda.current_device() == self.device.index else torch.cuda.device(self.device)
+        return _HERE if torch.cuda.current_device() == self.index else torch.cuda.device(self.device)
 
     @property
     def nbytes(self) -> int:

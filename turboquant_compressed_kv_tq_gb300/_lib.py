@@ -164,11 +164,10 @@ SIGNATURES = {
     "tq_batch_extend": (_ST, [ctypes.POINTER(tq_batch), ctypes.POINTER(tq_batch), _P, _I, _P, _P]),
     "tq_batch_merge": (_ST, [ctypes.POINTER(tq_batch), ctypes.POINTER(tq_batch), _I, _P, _I, _P, _P]),
     "tq_batch_extract": (_ST, [ctypes.POINTER(tq_batch), _I, ctypes.POINTER(tq_batch), _P, _I, _P, _P]),
-    "tq_kv8_append": (_ST, [ctypes.POINTER(tq_kv8_cache), _I, ctypes.POINTER(tq_rows), ctypes.POINTER(tq_rows), _I, _I,
-                            _I, _P, _P, _P, _I, ctypes.POINTER(tq_rope), _P, _P]),
-    "tq_kv8_workspace_bytes": (_ST, [ctypes.POINTER(tq_kv8_cache), _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
-    "tq_kv8_attention": (_ST, [ctypes.POINTER(tq_kv8_cache), _I, ctypes.POINTER(tq_rows), _I, _I, _I, _I, _P, _P, _P,
-                               _I, _I, ctypes.POINTER(tq_kv8_scores), ctypes.POINTER(tq_rows), _P, _SZ, _P]),
+    # the small structs of these two go as their bytes (see _rows): building ctypes structures costs more than the calls
+    "tq_kv8_append": (_ST, [_P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P]),
+    "tq_kv8_workspace_bytes": (_ST, [_P, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "tq_kv8_attention": (_ST, [_P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]),
     "tq_device_error": (_ST, [ctypes.POINTER(ctypes.c_uint32)]),
     "tq_selftest_wait_timeout": (_ST, [ctypes.c_double, _P]),
 }

@@ -19,10 +19,12 @@
 // wants in one lane are whatever order both operands share, so each lane takes
 // 16 consecutive bytes: of keys, lane (g, c) reads tokens g and g + 8 at bytes
 // 64 i + 16 c; of values, tokens 2c, 2c + 1, 2c + 8, 2c + 9 at bytes 128 i + 16 g.
-// Every load is 16 bytes a lane, straight from global memory to the operand's
-// registers, a tile ahead of its use: no shared memory, no barrier in the loop.
+// Every copy is 16 bytes a lane, and each lane copies what it will use itself:
+// shared memory holds a queue of tiles for each lane (cp.async, kStages deep),
+// which needs no barrier, no other lane's copies, and has no bank conflicts.
 //
-// Bound: memory, 2 D bytes a token.
+// Bound: memory, 2 D bytes a token. The queue is there for that: 48 to 192 KB on
+// their way to each SM, where registers alone could hold 32 to 64.
 #include <climits>
 
 #include "kv8_device.cuh"
@@ -48,18 +50,23 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return r;
 }
 
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, bool here, bool wide) {
+    // nothing is read where there is no block: the destination is zeroed
+    if (wide) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(here ? 16 : 0) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(here ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+
 template <int W>
-struct Words {   // W 32-bit words of one lane's load
-    uint32_t w[W];
-};
-template <int W>
-__device__ __forceinline__ void load_words(Words<W>& d, const uint8_t* p) {
+__device__ __forceinline__ void load_words(uint32_t (&w)[W], const unsigned char* p) {
     if constexpr (W == 4) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-        d.w[0] = u.x, d.w[1] = u.y, d.w[2] = u.z, d.w[3] = u.w;
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
     } else {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-        d.w[0] = u.x, d.w[1] = u.y;
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        w[0] = u.x, w[1] = u.y;
     }
 }
 
@@ -67,12 +74,18 @@ __device__ __forceinline__ void load_words(Words<W>& d, const uint8_t* p) {
 template <int D, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kWarps = D * NT >= 256 ? 8 : 8;
+    static constexpr int kWarps = 8;
     static constexpr int kCtas = D * NT >= 256 ? 1 : 2;   // per SM
     static constexpr int kKL = D / 64;                 // key loads per token
     static constexpr int kVW = D >= 128 ? 4 : 2;       // words of a value load
     static constexpr int kVL = D / (32 * kVW);         // value loads per token
     static constexpr int kMT = D / 16;                 // value MMAs
+    static constexpr int kCopies = 2 * kKL + 4 * kVL;  // a lane's copies of a tile
+    static constexpr int kTileBytes = 32 * D;          // keys and values of 16 tokens
+    static constexpr int kStages = (kCtas == 2 ? 96 : 192) * 1024 / (kWarps * kTileBytes);
+    static constexpr int kRing = kStages * kWarps * kTileBytes;
+    static constexpr int kOut = kWarps * kRows * D * 4;          // the warps' outputs, over the queues
+    static constexpr int kSmem = kRing > kOut ? kRing : kOut;    // and the queries, at the end
 };
 
 // What the rows of a group see, as tiles: [0, n1) and then [first, first + n2).
@@ -87,7 +100,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
     using S = Shape<D, NT>;
     constexpr int kRows = S::kRows, kThreads = 32 * S::kWarps;
     extern __shared__ __align__(16) unsigned char smem[];
-    __half* s_q = reinterpret_cast<__half*>(smem);   // [kRows][D], then the warps' outputs
+    __half* s_q = reinterpret_cast<__half*>(smem + S::kSmem);   // [kRows][D]
     __shared__ uint64_t s_turns[D / 2];
     __shared__ float s_fac[kRows], s_m[S::kWarps][kRows], s_l[S::kWarps][kRows];
     __shared__ Sight s_sight[kRows];
@@ -213,74 +226,94 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
         const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
         const int64_t unit_bytes = static_cast<int64_t>(P.BT) * D;
 
-        // lane k holds the block and scales of the warp's tile base + k
-        int base = w_begin, my_id = -1, my_kx = 0, my_vx = 0;
-        auto look_up = [&](int from) {
-            my_id = -1;
-            my_kx = my_vx = 0;
+        // lane k holds the block and scales of the warp's tile base + k, and of the 32 after those
+        int base = w_begin;
+        int64_t id = -1, id_next = -1;
+        uint32_t meta = 0, meta_next = 0;   // scale bytes, and whether there is a block
+        auto look_up = [&](int from, int64_t& x, uint32_t& sc) {
+            x = -1;
+            sc = 0;
             const int i = from + lane;
             if (i < w_end) {
                 const int lb = (tiles.at(i) << 4) >> P.bt_shift;
-                const int64_t id = P.table ? P.table[b * static_cast<int64_t>(P.max_blocks) + lb] : b * static_cast<int64_t>(P.max_blocks) + lb;
-                if (id >= 0 && id < P.num_blocks) {
-                    my_id = static_cast<int>(id);
-                    my_kx = P.kx[id * P.H + h];
-                    my_vx = P.vx[id * P.H + h];
+                const int64_t at = P.table ? P.table[b * static_cast<int64_t>(P.max_blocks) + lb] : b * static_cast<int64_t>(P.max_blocks) + lb;
+                if (at >= 0 && at < P.num_blocks) {
+                    x = at * P.H + h;
+                    sc = P.kx[x] | (P.vx[x] << 8) | 0x10000u;
                 } else {
                     atomicOr(A.err, TQ_DEVERR_BLOCK);
                 }
             }
         };
-        look_up(base);
-        Words<4> kw[2][S::kKL];
-        Words<S::kVW> vw[4][S::kVL];
-        // offset of tile i's codes in the pool, or -1
-        auto offset_of = [&](int i) -> int64_t {
-            const int id = __shfl_sync(0xffffffffu, my_id, i - base);
-            return id < 0 ? -1 : (static_cast<int64_t>(id) * P.H + h) * unit_bytes + static_cast<int64_t>((tiles.at(i) << 4) & (P.BT - 1)) * D;
+        look_up(base, id, meta);
+        look_up(base + 32, id_next, meta_next);
+        unsigned char* ring = smem + warp * S::kTileBytes + 16 * lane;   // a copy of the lane: 512 bytes apart
+        const uint32_t ring_at = tc::smem_addr(ring);
+        constexpr int kStep = S::kWarps * S::kTileBytes;
+        uint32_t ahead[S::kStages - 1];   // meta of the tiles on their way
+        int put = 0, get = 0;             // stages
+        // start tile i's copies (none behind the warp's last tile); its meta
+        auto fetch = [&](int i) -> uint32_t {
+            uint32_t mt = 0;
+            if (i < w_end) {
+                if (i - base == 32) {
+                    base = i;
+                    id = id_next;
+                    meta = meta_next;
+                    look_up(base + 32, id_next, meta_next);
+                }
+                const int64_t x = __shfl_sync(0xffffffffu, id, i - base);
+                mt = __shfl_sync(0xffffffffu, meta, i - base);
+                const bool here = x >= 0;
+                const int64_t off = (here ? x : 0) * unit_bytes + static_cast<int64_t>((tiles.at(i) << 4) & (P.BT - 1)) * D;
+                const uint8_t *kp = P.kc + off + g * D + 16 * c, *vp = P.vc + off + 2 * c * D + 4 * S::kVW * g;
+                const uint32_t dst = ring_at + put * kStep;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int k = 0; k < S::kKL; ++k) copy_async(dst + (t * S::kKL + k) * 512, kp + 8 * t * D + 64 * k, here, true);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int k = 0; k < S::kVL; ++k)
+                        copy_async(dst + 2 * S::kKL * 512 + (S::kVW == 4 ? (t * S::kVL + k) * 512 : (t >> 1) * 512 + (t & 1) * 8),
+                                   vp + ((t & 1) + 8 * (t >> 1)) * D + 32 * S::kVW * k, here, S::kVW == 4);
+                put = put + 1 == S::kStages ? 0 : put + 1;
+            }
+            copies_close();
+            return mt;
         };
-        auto load_k = [&](int64_t off) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < S::kKL; ++i) load_words(kw[t][i], P.kc + (off < 0 ? 0 : off) + (g + 8 * t) * D + 64 * i + 16 * c);
-        };
-        auto load_v = [&](int64_t off) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int i = 0; i < S::kVL; ++i)
-                    load_words(vw[t][i], P.vc + (off < 0 ? 0 : off) + (2 * c + (t & 1) + 8 * (t >> 1)) * D + 32 * S::kVW * i + 4 * S::kVW * g);
-        };
-        int64_t off = offset_of(w_begin);
-        load_k(off);
-        load_v(off);
+        for (int k = 0; k < S::kStages - 1; ++k) ahead[k] = fetch(w_begin + k);
         for (int i = w_begin; i < w_end; ++i) {
             const int t0 = tiles.at(i) << 4;
-            const int kx = __shfl_sync(0xffffffffu, my_kx, i - base), vx = __shfl_sync(0xffffffffu, my_vx, i - base);
-            const bool here = off >= 0;
-            int64_t next = -1;
-            const bool more = i + 1 < w_end;
-            if (more) {
-                if (i + 1 - base == 32) {
-                    base = i + 1;
-                    look_up(base);
-                }
-                next = offset_of(i + 1);
-            }
+            const uint32_t mt = ahead[0];
+#pragma unroll
+            for (int k = 0; k < S::kStages - 2; ++k) ahead[k] = ahead[k + 1];
+            ahead[S::kStages - 2] = fetch(i + S::kStages - 1);
+            copies_wait<S::kStages - 1>();
+            const int kx = mt & 0xFF, vx = (mt >> 8) & 0xFF;
+            const bool here = mt >> 16;
+            const unsigned char* src = ring + get * kStep;
+            get = get + 1 == S::kStages ? 0 : get + 1;
             // ---------------- scores
             float sc[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                uint32_t a0, a1, a2, a3;
-                codes_f16<I8>(kw[0][ks >> 2].w[ks & 3], a0, a2);
-                codes_f16<I8>(kw[1][ks >> 2].w[ks & 3], a1, a3);
+            for (int k = 0; k < S::kKL; ++k) {
+                uint32_t w0[4], w1[4];
+                load_words(w0, src + k * 512);
+                load_words(w1, src + (S::kKL + k) * 512);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t a0, a1, a2, a3;
+                    codes_f16<I8>(w0[w], a0, a2);
+                    codes_f16<I8>(w1[w], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], a0, a1, a2, a3, qf[nt][4 * k + w][0], qf[nt][4 * k + w][1]);
+                }
             }
-            if (more) load_k(next);
             // ---------------- u = log2(e) score + log2(value scale), masked
             const float ks2 = exp2i(kx == 0 ? -126 : kx - 127), lv = static_cast<float>(vx - 127);
             const bool open = here && t0 + 15 <= p_min && t0 >= lo_max;
@@ -310,15 +343,6 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
                         const int t = t0 + g + 8 * (e >> 1);
                         if (!(here && t < N && s_sight[8 * nt + 2 * c + (e & 1)].sees(t))) u[nt][e] = -INFINITY;
                     }
-                // codes behind the sequence's end, or of no block, may be anything:
-                // their weight is 0, so they only have to be finite
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    if (!here || t0 + 2 * c + (t & 1) + 8 * (t >> 1) >= N)
-#pragma unroll
-                        for (int k = 0; k < S::kVL; ++k)
-#pragma unroll
-                            for (int w = 0; w < S::kVW; ++w) vw[t][k].w[w] = 0;
             }
             // ---------------- the reference moves only when a score passes it by the gap
             bool pass = false;
@@ -361,14 +385,34 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
                 pb[nt][1] = transpose8x8(pack_out<__half>(p[2], p[3]));
             }
             // ---------------- O^T += V^T P
+            const bool whole = t0 + 16 <= N;
 #pragma unroll
-            for (int k = 0; k < S::kVL; ++k)
+            for (int k = 0; k < S::kVL; ++k) {
+                uint32_t vw[4][S::kVW];
+                if constexpr (S::kVW == 4) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) load_words(vw[t], src + (2 * S::kKL + t * S::kVL + k) * 512);
+                } else {   // 8 bytes of two tokens side by side
+#pragma unroll
+                    for (int t = 0; t < 4; t += 2) {
+                        uint32_t both[4];
+                        load_words(both, src + (2 * S::kKL + t / 2) * 512);
+                        vw[t][0] = both[0], vw[t][1] = both[1], vw[t + 1][0] = both[2], vw[t + 1][1] = both[3];
+                    }
+                }
+                if (!whole) {   // codes behind the sequence's end may be anything: their weight is 0, so they have to be finite
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (t0 + 2 * c + (t & 1) + 8 * (t >> 1) >= N)
+#pragma unroll
+                            for (int w = 0; w < S::kVW; ++w) vw[t][w] = 0;
+                }
 #pragma unroll
                 for (int w = 0; w < S::kVW; ++w) {
                     uint32_t x[2][4];   // [token pair][coordinate]: fp16 pairs of two tokens
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const uint32_t a = vw[2 * t][k].w[w], d = vw[2 * t + 1][k].w[w];
+                        const uint32_t a = vw[2 * t][w], d = vw[2 * t + 1][w];
                         codes_f16<I8>(__byte_perm(a, d, 0x5140), x[t][0], x[t][1]);
                         codes_f16<I8>(__byte_perm(a, d, 0x7362), x[t][2], x[t][3]);
                     }
@@ -378,8 +422,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
                         mma16816(acc[nt][(k * S::kVW + w) * 2 + 1], x[0][2], x[0][3], x[1][2], x[1][3], pb[nt][0], pb[nt][1]);
                     }
                 }
-            if (more) load_v(next);
-            off = next;
+            }
         }
     }
 
@@ -493,7 +536,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
 template <typename T, int D, int NT, bool I8>
 cudaError_t launch_t(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
     using S = Shape<D, NT>;
-    const int smem = S::kWarps * S::kRows * D * 4;
+    const int smem = S::kSmem + S::kRows * D * 2;
     cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, NT, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     decode_kernel<T, D, NT, I8><<<dim3(p.groups * p.splits, a.pool.H, a.batch), 32 * S::kWarps, smem, s>>>(a);

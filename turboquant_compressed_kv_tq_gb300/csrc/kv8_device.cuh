@@ -79,23 +79,30 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
 }
 
 // cos and sin of the angle `t` / 2^64 of a turn: to the nearest quarter turn
-// (exact), then the Taylor series in the remainder, |y| <= pi/4: the first
-// terms left out are y^11/11! and y^12/12!, below 2e-9 and 2e-10.
+// (exact), then the Taylor series in the remainder y, |y| <= pi/4 (the first
+// terms left out are y^11/11! and y^12/12!, below 2e-9 and 2e-10), with what
+// fp32 leaves out of y added to first order: within about 2^-24.
 __device__ __forceinline__ void turn_cos_sin(uint64_t t, float& co, float& si) {
+    constexpr float kHi = 1.462918120e-09f, kLo = -4.070940433e-17f;   // 2 pi / 2^32
     const uint32_t h = static_cast<uint32_t>(t >> 32);
     const uint32_t quad = (h + 0x20000000u) >> 30;
     const int32_t r = static_cast<int32_t>(h - (quad << 30));   // [-2^29, 2^29] / 2^32 of a turn
-    const float y = static_cast<float>(r) * 1.46291807926715968e-9f;   // 2 pi / 2^32
+    const float rf = static_cast<float>(r), rl = static_cast<float>(r - static_cast<int32_t>(rf));
+    const float y = rf * kHi;
+    const float dy = fmaf(rl, kHi, fmaf(rf, kLo, fmaf(rf, kHi, -y)));
     const float z = y * y;
     float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
     s = fmaf(z, s, 8.3333333e-3f);
     s = fmaf(z, s, -1.6666667e-1f);
-    s = fmaf(y * z, s, y);
     float c = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
     c = fmaf(z, c, -1.3888889e-3f);
     c = fmaf(z, c, 4.1666667e-2f);
     c = fmaf(z, c, -0.5f);
-    c = fmaf(z, c, 1.0f);
+    const float c1 = fmaf(z, c, 1.0f);
+    s = fmaf(y * z, s, dy * c1);
+    c = fmaf(z, c, -dy * y);
+    s += y;
+    c += 1.0f;
     const float a = (quad & 1) ? s : c, b = (quad & 1) ? c : s;
     co = ((quad + 1) & 2) ? -a : a;
     si = (quad & 2) ? -b : b;

@@ -58,6 +58,21 @@ struct Shape {
     static constexpr int kUnits = kT * (D / 16) / kConvThreads;   // 16-byte loads of a converter a tile
 };
 
+// Wait for the phase with this parity; false after about a second.
+__device__ __forceinline__ bool arrived(uint64_t* bar, unsigned parity) {
+    const uint32_t a = tc::smem_addr(bar);
+    for (unsigned it = 0; it < (1u << 18); ++it) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+
 // Byte offset of (row, d) in an operand of core matrices: 8 rows x 16 bytes.
 template <int D>
 __device__ __forceinline__ int core(int row, int d) {
@@ -99,13 +114,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     constexpr int kT = S::kT, kH = S::kHalves;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint64_t s_turns[D / 2];
-    __shared__ __align__(8) uint64_t s_bar[14];
+    __shared__ __align__(8) uint64_t s_bar[15];
     __shared__ float s_fac[S::kRows];
     __shared__ TileInfo s_info[4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     uint64_t *k_full = s_bar, *k_free = s_bar + 2, *v_full = s_bar + 4, *v_free = s_bar + 6;
-    uint64_t *s_ready = s_bar + 8, *p_ready = s_bar + 10, *o_done = s_bar + 12;
+    uint64_t *s_ready = s_bar + 8, *p_ready = s_bar + 10, *o_done = s_bar + 12, *drained = s_bar + 14;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Pool& P = A.pool;
     // the longest rows first: the last wave then holds short ones
@@ -161,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             tc::mbar_init(&p_ready[s], 4);
             tc::mbar_init(&o_done[s], 1);
         }
+        tc::mbar_init(drained, 1);
         tc::mbar_fence_init();
         s_fail = 0;
     }
@@ -229,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             for (int i = 0; i < n_tiles; ++i) {
                 const int t0 = tiles.at(i_begin + i) * kT;
                 const int sb = kH == 2 ? half : i & 1;                    // buffer of S and P
-                ok = tc::mbar_wait(&s_ready[sb], kH == 2 ? i & 1 : (i >> 1) & 1);
+                ok = arrived(&s_ready[sb], kH == 2 ? i & 1 : (i >> 1) & 1);
                 if (!ok) break;
                 tc::tc_fence_after();
                 const TileInfo info = s_info[i & 3];
@@ -292,17 +308,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 finish(sr, 0);
                 top = fmaf(fmaxf(top, largest(sr)), f, lv);
                 const bool pass = top > m + kGap;
+                if (kH == 1 && i > 0) {   // every phase in its turn: a wait by parity tells neighbouring phases apart, no others
+                    ok = arrived(&o_done[0], (i - 1) & 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                }
                 if (__any_sync(0xffffffffu, pass)) {
                     const float x = fmaxf(top, m);
                     const float alpha = ex2(m - x);
                     m = x;
                     l_sum *= alpha;
                     if (i > 0) {
-                        if (kH == 1) {
-                            ok = tc::mbar_wait(&o_done[0], (i - 1) & 1);
-                            if (!ok) break;
-                            tc::tc_fence_after();
-                        }
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t v[32];
@@ -346,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 unpack2(sum1, d, g);
                 l_sum = fmaf((a + c) + (d + g), exp2i(-info.vref), l_sum);
             }
-            if (ok) ok = tc::mbar_wait(&o_done[kH == 2 ? half : 0], kH == 2 ? 0 : (n_tiles - 1) & 1);
+            if (ok) ok = arrived(&o_done[kH == 2 ? half : 0], kH == 2 ? 0 : (n_tiles - 1) & 1);
             if (!ok) {
                 s_fail = 1;
                 atomicOr(A.err, TQ_DEVERR_TIMEOUT);
@@ -472,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 // groups of no block among those that have tokens
                 const unsigned gone = __ballot_sync(0xffffffffu, lane < S::kGroups && id < 0 && t0 + 8 * lane < N);
                 const int vx_now = vx;
-                if (i >= 2) ok = tc::mbar_wait(&k_free[st], ((i >> 1) - 1) & 1);
+                if (i >= 2) ok = arrived(&k_free[st], ((i >> 1) - 1) & 1);
                 if (!ok) break;
                 if (w == 0 && lane == 0) s_info[i & 3] = TileInfo{kref, vref, gone};
                 convert(kr, kx, kref, smem + S::kKOff + st * S::kOperand);
@@ -483,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     look_up(i + 1);
                     load(kr, P.kc, i + 1);
                 }
-                if (i >= 2) ok = tc::mbar_wait(&v_free[st], ((i >> 1) - 1) & 1);
+                if (i >= 2) ok = arrived(&v_free[st], ((i >> 1) - 1) & 1);
                 if (!ok) break;
                 convert(vr, vx_now, vref, smem + S::kVOff + st * S::kOperand);
                 tc::fence_proxy_async_smem();
@@ -520,8 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     else tc::mma_f16_ta_w<true>(o, p + 8 * s, lo + s * (2 * kRowStep >> 4), hi, id_o);
                 }
             };
-            bool ok = tc::mbar_wait(&k_full[0], 0);
-            int s_commits[2] = {0, 0}, o_commits[2] = {0, 0};
+            bool ok = arrived(&k_full[0], 0);
             tc::tc_fence_after();
             if constexpr (kH == 2) {
                 const int nh = two ? 2 : 1;
@@ -529,29 +544,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     for (int x = 0; x < nh; ++x) {
                         scores(x, x, 0);
                         tc::mma_commit(&s_ready[x]);
-                        ++s_commits[x];
                     }
                     tc::mma_commit(&k_free[0]);
                 }
                 for (int i = 0; i < n_tiles && ok; ++i) {
                     const int st = i & 1, sn = st ^ 1;
                     for (int x = 0; x < nh && ok; ++x) {
-                        if (x == 0) ok = tc::mbar_wait(&v_full[st], (i >> 1) & 1);
-                        if (ok) ok = tc::mbar_wait(&p_ready[x], i & 1);
+                        if (x == 0) ok = arrived(&v_full[st], (i >> 1) & 1);
+                        if (ok) ok = arrived(&p_ready[x], i & 1);
                         if (!ok) break;
                         tc::tc_fence_after();
                         values(x, x, st, i > 0);
                         if (x == nh - 1) tc::mma_commit(&v_free[st]);
                         if (i + 1 == n_tiles) {
                             tc::mma_commit(&o_done[x]);
-                            ++o_commits[x];
                         } else {
-                            if (x == 0) ok = tc::mbar_wait(&k_full[sn], ((i + 1) >> 1) & 1);
+                            if (x == 0) ok = arrived(&k_full[sn], ((i + 1) >> 1) & 1);
                             if (!ok) break;
                             tc::tc_fence_after();
                             scores(x, x, sn);
                             tc::mma_commit(&s_ready[x]);
-                            ++s_commits[x];
                             if (x == nh - 1) tc::mma_commit(&k_free[sn]);
                         }
                     }
@@ -560,39 +572,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 if (ok) {
                     scores(0, 0, 0);
                     tc::mma_commit(&s_ready[0]);
-                    ++s_commits[0];
                     tc::mma_commit(&k_free[0]);
                 }
                 for (int i = 0; i < n_tiles && ok; ++i) {
                     const int st = i & 1, sn = st ^ 1;
                     if (i + 1 < n_tiles) {
-                        ok = tc::mbar_wait(&k_full[sn], ((i + 1) >> 1) & 1);
+                        ok = arrived(&k_full[sn], ((i + 1) >> 1) & 1);
                         if (!ok) break;
                         tc::tc_fence_after();
                         scores(0, sn, sn);
                         tc::mma_commit(&s_ready[sn]);
-                        ++s_commits[sn];
                         tc::mma_commit(&k_free[sn]);
                     }
-                    ok = tc::mbar_wait(&v_full[st], (i >> 1) & 1);
-                    if (ok) ok = tc::mbar_wait(&p_ready[st], (i >> 1) & 1);   // one a buffer: the next tile's may be there too
+                    ok = arrived(&v_full[st], (i >> 1) & 1);
+                    if (ok) ok = arrived(&p_ready[st], (i >> 1) & 1);   // one a buffer: the next tile's may be there too
                     if (!ok) break;
                     tc::tc_fence_after();
                     values(0, st, st, i > 0);
                     tc::mma_commit(&v_free[st]);
                     tc::mma_commit(&o_done[0]);
-                    ++o_commits[0];
                 }
             }
             if (!ok) {
                 s_fail = 1;
                 atomicOr(A.err, TQ_DEVERR_TIMEOUT);
             }
-            // nothing is in flight when the CTA ends: the last phases of the commits
-            for (int x = 0; x < 2; ++x) {
-                if (s_commits[x]) (void)tc::mbar_wait(&s_ready[x], (s_commits[x] - 1) & 1);
-                if (o_commits[x]) (void)tc::mbar_wait(&o_done[x], (o_commits[x] - 1) & 1);
-            }
+            // nothing is in flight when the CTA ends
+            tc::mma_commit(drained);
+            (void)arrived(drained, 0);
         }
         __syncwarp();
     }
@@ -603,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         tc::tmem_dealloc(tmem, 512);
     }
     if (tid == 0)
-        for (int s = 0; s < 14; ++s) tc::mbar_inval(&s_bar[s]);
+        for (int s = 0; s < 15; ++s) tc::mbar_inval(&s_bar[s]);
     tc::grid_release_dependents();
 }
 
