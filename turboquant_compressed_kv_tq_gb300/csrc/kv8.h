@@ -48,10 +48,11 @@ struct AttendArgs {
     const float* slopes;
     int window;
     const int32_t *prefix, *docs;
-    // split partials: [batch][H][row groups][splits][rows of a group] x (reference, sum) and x D
-    float *part_ml, *part_o;
-    int splits, split_tiles;   // token splits per row group, and the tiles of each
     int groups;                // row groups per (sequence, KV head)
+    // few rows: states of units that lie in several CTAs' shares, [CTA][2][rows of a group] x (reference, sum)
+    // and x D, and the first and last such CTA of each unit [batch][groups][H]
+    float *part_ml, *part_o;
+    int* unit_shares;
     unsigned* err;
 };
 
@@ -60,8 +61,8 @@ struct AttendPlan {
     int chunk;         // 1: the tensor-memory kernel (many rows), 0: the split kernel (few rows)
     int group_rows;    // query rows of a group
     int groups;        // ceil(G q_len / group_rows)
-    int splits, split_tiles;
-    size_t ml_bytes, total;
+    int ctas;          // of the split kernel
+    size_t ml_bytes, unit_bytes, total;
 };
 
 AttendPlan attend_plan(int D, int batch, int H, int G, int L, int max_seq, int num_sms);
@@ -69,8 +70,6 @@ AttendPlan attend_plan(int D, int batch, int H, int G, int L, int max_seq, int n
 #ifdef __CUDACC__
 cudaError_t launch_append(const AppendArgs& a, int D, int format, int dtype, cudaStream_t s);
 cudaError_t launch_decode(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s);
-// Joins the splits of an attention call (part_ml, part_o) into its output.
-cudaError_t launch_join(const AttendArgs& a, const AttendPlan& p, int D, int dtype, cudaStream_t s);
 cudaError_t launch_prefill(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s);
 #endif
 

@@ -93,27 +93,19 @@ AttendPlan attend_plan(int D, int batch, int H, int G, int L, int max_seq, int n
         p.chunk = 1;
         p.group_rows = D == 256 ? 128 : 256;
         p.groups = (rows + p.group_rows - 1) / p.group_rows;
-        p.splits = 1;
-        p.split_tiles = kMaxTokens;
         return p;
     }
     p.group_rows = rows <= 8 ? 8 : 16;
     p.groups = (rows + p.group_rows - 1) / p.group_rows;
+    // one share of the tiles for each SM, at least a tile for each of its CTA's warps (eight or more)
     const int64_t units = static_cast<int64_t>(batch) * H * p.groups;
-    const int tiles = std::max(1, (max_seq + 15) / 16);
-    // four rounds of CTAs level out sequences of different lengths; a split
-    // keeps 64 tiles (eight for each warp) unless the SMs would stay empty
-    const int per_sm = D * (p.group_rows / 8) >= 256 ? 1 : 2;
-    const int64_t slots = static_cast<int64_t>(num_sms) * per_sm;
-    int64_t splits = std::max<int64_t>(1, 4 * slots / std::max<int64_t>(1, units));
-    splits = std::min<int64_t>(splits, std::max<int64_t>((tiles + 63) / 64, slots / std::max<int64_t>(1, units)));
-    splits = std::max<int64_t>(1, std::min<int64_t>(splits, (tiles + 7) / 8));
-    p.split_tiles = static_cast<int>((tiles + splits - 1) / splits);
-    p.splits = (tiles + p.split_tiles - 1) / p.split_tiles;
-    if (p.splits > 1) {
-        const size_t n = static_cast<size_t>(units) * p.splits * p.group_rows;
+    const int64_t tiles = units * std::max(1, (max_seq + 15) / 16);
+    p.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms, (tiles + 7) / 8)));
+    if (p.ctas > 1) {
+        const size_t n = static_cast<size_t>(2) * p.ctas * p.group_rows;
         p.ml_bytes = (n * 8 + 255) / 256 * 256;
-        p.total = p.ml_bytes + n * D * 4;
+        p.unit_bytes = (static_cast<size_t>(units) * 8 + 255) / 256 * 256;
+        p.total = p.ml_bytes + p.unit_bytes + n * D * 4;
     }
     return p;
 }
@@ -211,10 +203,10 @@ tq_status tq_kv8_attention(const tq_kv8_cache* cache, int layer, const tq_rows* 
     a.window = sc.window;
     a.prefix = sc.prefix_lens;
     a.docs = sc.doc_starts;
-    a.part_ml = static_cast<float*>(workspace);
-    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_bytes);
-    a.splits = p.splits;
-    a.split_tiles = p.split_tiles;
+    char* ws = static_cast<char*>(workspace);
+    a.part_ml = reinterpret_cast<float*>(ws);
+    a.unit_shares = reinterpret_cast<int*>(ws + p.ml_bytes);
+    a.part_o = reinterpret_cast<float*>(ws + p.ml_bytes + p.unit_bytes);
     a.groups = p.groups;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = p.chunk ? launch_prefill(a, p, cache->head_dim, cache->format, dtype, s)

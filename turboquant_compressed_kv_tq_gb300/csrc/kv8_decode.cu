@@ -2,8 +2,13 @@
 // speculative ones.
 //
 // The rows of one KV head (r = l G + g: query l, head g of the group) are taken
-// kRows = 8 NT at a time; the tokens are split over CTAs, and each warp of a CTA
-// walks tiles of 16 tokens of its own. Per tile (mma.sync m16n8k16, fp16 in, fp32
+// kRows = 8 NT at a time; such a group of rows is a unit, and its keys come in
+// tiles of 16 tokens. One CTA to an SM; the tiles of all units, one
+// after another, are dealt out to them in equal shares, by lengths that only the
+// device knows: sequences of any lengths keep every SM busy to the end. A unit
+// that lies in one share is finished there; of the others each share leaves a
+// state (at most two a CTA), which a second kernel joins. Within a share each
+// warp walks tiles of its own. Per tile (mma.sync m16n8k16, fp16 in, fp32
 // out; tokens and coordinates on M, query rows on N, so that 8 rows waste
 // nothing):
 //   S^T = K Q^T      A = the tile's key codes, B = the queries (registers)
@@ -26,6 +31,7 @@
 // Bound: memory, 2 D bytes a token. The queue is there for that: 48 to 192 KB on
 // their way to each SM, where registers alone could hold 32 to 64.
 #include <climits>
+#include <type_traits>
 
 #include "kv8_device.cuh"
 #include "tc_ptx.cuh"
@@ -70,92 +76,170 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[W], const unsigned char
     }
 }
 
-// Warps of a CTA: as many as fit next to the registers a warp needs.
 template <int D, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kWarps = 8;
-    static constexpr int kCtas = D * NT >= 256 ? 1 : 2;   // per SM
+    // warps by the registers that a warp needs, one CTA to an SM
+    static constexpr int kWarps = D * NT >= 256 ? 8 : D * NT == 128 ? 12 : 16;
+    static constexpr int kU = D == 256 ? 1 : 2;        // tiles taken together: two chains of dependent instructions
     static constexpr int kKL = D / 64;                 // key loads per token
     static constexpr int kVW = D >= 128 ? 4 : 2;       // words of a value load
     static constexpr int kVL = D / (32 * kVW);         // value loads per token
     static constexpr int kMT = D / 16;                 // value MMAs
-    static constexpr int kCopies = 2 * kKL + 4 * kVL;  // a lane's copies of a tile
     static constexpr int kTileBytes = 32 * D;          // keys and values of 16 tokens
-    static constexpr int kStages = (kCtas == 2 ? 96 : 192) * 1024 / (kWarps * kTileBytes);
-    static constexpr int kRing = kStages * kWarps * kTileBytes;
+    static constexpr int kStages = 192 * 1024 / (kWarps * kTileBytes * kU);   // of kU tiles
+    static constexpr int kRing = kStages * kWarps * kTileBytes * kU;
     static constexpr int kOut = kWarps * kRows * D * 4;          // the warps' outputs, over the queues
     static constexpr int kSmem = kRing > kOut ? kRing : kOut;    // and the queries, at the end
+    static_assert(kStages >= 2, "a stage to use and one on its way");
 };
+
+// A sequence's lengths, checked.
+struct Seq {
+    int N, nq, pre;
+    bool bad;
+    __device__ __forceinline__ Seq(const AttendArgs& A, int b) {
+        N = A.seq[b];
+        nq = A.qlens ? A.qlens[b] : A.L;
+        const bool bad_n = N < 0 || N > A.max_seq || (N + A.pool.BT - 1) >> A.pool.bt_shift > A.pool.max_blocks, bad_q = nq < 0 || nq > A.L;
+        if (bad_n) N = 0;
+        if (bad_q) nq = nq < 0 ? 0 : A.L;
+        bad = bad_n || bad_q;
+        pre = A.prefix ? min(max(A.prefix[b], 0), N) : 0;
+    }
+};
+
+__device__ __forceinline__ Sight sight_of(const AttendArgs& A, const Seq& q, int b, int l) {
+    Sight s;
+    s.p = q.N - q.nq + l;
+    s.lo = 0;
+    if (A.window > 0) s.lo = max(s.lo, s.p - A.window + 1);
+    if (A.docs) s.lo = max(s.lo, A.docs[static_cast<int64_t>(b) * A.L + l]);
+    s.prefix = q.pre;
+    return s;
+}
 
 // What the rows of a group see, as tiles: [0, n1) and then [first, first + n2).
 struct Tiles {
+    int l_first, l_last, rows;     // the group's queries and rows
+    int lo_max;                    // the largest first key of a row
     int n1, first, n2;
+    __device__ __forceinline__ Tiles(const AttendArgs& A, const Seq& q, int b, int grp, int group_rows) {
+        rows = min(A.G * A.L - grp * group_rows, group_rows);
+        l_first = grp * group_rows / A.G;
+        l_last = min((grp * group_rows + rows - 1) / A.G, q.nq - 1);
+        int lo_min = INT_MAX;
+        lo_max = 0;
+        for (int l = l_first; l <= l_last; ++l) {
+            const int lo = sight_of(A, q, b, l).lo;
+            lo_min = min(lo_min, lo);
+            lo_max = max(lo_max, lo);
+        }
+        const int p_max = q.N - q.nq + l_last;
+        n1 = (q.pre + 15) >> 4;
+        first = max(n1, lo_min >> 4);
+        n2 = p_max < 0 || lo_min > p_max ? 0 : max(0, (p_max >> 4) + 1 - first);
+    }
+    __device__ __forceinline__ bool none() const { return l_last < l_first; }   // only rows behind the sequence's queries
     __device__ __forceinline__ int at(int i) const { return i < n1 ? i : first + (i - n1); }
-    __device__ __forceinline__ int count() const { return n1 + n2; }
+    // a unit that sees nothing is a tile of its own: its rows are written too
+    __device__ __forceinline__ int count() const { return none() ? 0 : max(1, n1 + n2); }
 };
 
 template <typename T, int D, int NT, bool I8>
-__global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas) decode_kernel(const __grid_constant__ AttendArgs A) {
+__global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(const __grid_constant__ AttendArgs A) {
     using S = Shape<D, NT>;
     constexpr int kRows = S::kRows, kThreads = 32 * S::kWarps;
     extern __shared__ __align__(16) unsigned char smem[];
-    __half* s_q = reinterpret_cast<__half*>(smem + S::kSmem);   // [kRows][D]
+    // the queries as operand fragments, one uint2 (4 coordinates) a lane: coordinates 64 i + 16 c + 4 s .. of
+    // row 8 nt + g at step 4 i + s, lane 4 g + c; with fp16 queries a second set holds what the first rounded off
+    constexpr bool kFine = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
+    auto s_frag = [&](int part, int r, int d) {
+        const int ks = 4 * (d >> 6) + ((d >> 2) & 3), ln = 4 * (r & 7) + ((d >> 4) & 3);
+        return reinterpret_cast<uint2*>(smem + S::kSmem) + ((part * NT + (r >> 3)) * (D / 16) + ks) * 32 + ln;
+    };
+    auto split = [](float x0, float x1, float x2, float x3, uint2& lo) {
+        const __half2 a = __floats2half2_rn(x0, x1), d = __floats2half2_rn(x2, x3);
+        const float2 fa = __half22float2(a), fd = __half22float2(d);
+        lo = make_uint2(pack_out<__half>(x0 - fa.x, x1 - fa.y), pack_out<__half>(x2 - fd.x, x3 - fd.y));
+        return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&d));
+    };
     __shared__ uint64_t s_turns[D / 2];
     __shared__ float s_fac[kRows], s_m[S::kWarps][kRows], s_l[S::kWarps][kRows];
     __shared__ Sight s_sight[kRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const Pool& P = A.pool;
-    const int grp = blockIdx.x % A.groups, split = blockIdx.x / A.groups, h = blockIdx.y, b = blockIdx.z;
-    const int rows = min(A.G * A.L - grp * kRows, kRows);
 
-    int N = A.seq[b], nq = A.qlens ? A.qlens[b] : A.L;
-    const bool bad_n = N < 0 || N > A.max_seq || (N + P.BT - 1) >> P.bt_shift > P.max_blocks, bad_q = nq < 0 || nq > A.L;
-    if (bad_n) N = 0;
-    if (bad_q) nq = nq < 0 ? 0 : A.L;
-    if ((bad_n || bad_q) && tid == 0 && blockIdx.x == 0 && h == 0) atomicOr(A.err, TQ_DEVERR_SEQLEN);
-    const int l_first = grp * kRows / A.G, l_last = min((grp * kRows + rows - 1) / A.G, nq - 1);
-    if (l_first >= nq) return;   // only rows behind the sequence's queries
-
-    // ---------------- what each row sees, and the tiles that any row sees
-    const int pre = A.prefix ? min(max(A.prefix[b], 0), N) : 0;
-    auto sight_of = [&](int l) {
-        Sight s;
-        s.p = N - nq + l;
-        s.lo = 0;
-        if (A.window > 0) s.lo = max(s.lo, s.p - A.window + 1);
-        if (A.docs) s.lo = max(s.lo, A.docs[static_cast<int64_t>(b) * A.L + l]);
-        s.prefix = pre;
-        return s;
-    };
-    int lo_min = INT_MAX, lo_max = 0;
-    for (int l = l_first; l <= l_last; ++l) {
-        const Sight s = sight_of(l);
-        lo_min = min(lo_min, s.lo);
-        lo_max = max(lo_max, s.lo);
+    // ---------------- this CTA's share of the tiles of all units. A pair (sequence, row group) has the
+    // tiles of its P.H units, one head after another
+    __shared__ long long s_scan[S::kWarps], s_at;
+    __shared__ int s_pair;
+    const int pairs = A.batch * A.groups, each = (pairs + kThreads - 1) / kThreads;
+    long long sum = 0;
+    for (int p = tid * each; p < min((tid + 1) * each, pairs); ++p) {
+        const int b = p / A.groups;
+        const Seq q(A, b);
+        if (q.bad && blockIdx.x == 0) atomicOr(A.err, TQ_DEVERR_SEQLEN);
+        sum += static_cast<long long>(Tiles(A, q, b, p % A.groups, kRows).count()) * P.H;
     }
-    const int p_min = N - nq + l_first, p_max = N - nq + l_last;
-    Tiles tiles;
-    tiles.n1 = (pre + 15) >> 4;
-    tiles.first = max(tiles.n1, lo_min >> 4);
-    tiles.n2 = max(0, ((p_max + 16) >> 4) - tiles.first);   // p_max >= -A.L
-    if (lo_min > p_max) tiles.n2 = 0;
-    const int i_begin = split * A.split_tiles, i_end = min(i_begin + A.split_tiles, tiles.count());
+    long long upto = sum;   // inclusive over the threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) s_scan[warp] = upto;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < S::kWarps; ++w) {
+        if (w < warp) upto += s_scan[w];
+        total += s_scan[w];
+    }
+    const long long share = max(static_cast<long long>(S::kWarps), (total + gridDim.x - 1) / gridDim.x);
+    const long long begin = blockIdx.x * share, end = min(begin + share, total);
+    if (begin >= end) return;
+    if (upto - sum <= begin && begin < upto) {
+        long long at = upto - sum;
+        for (int p = tid * each;; ++p) {
+            const int b = p / A.groups;
+            const long long n = static_cast<long long>(Tiles(A, Seq(A, b), b, p % A.groups, kRows).count()) * P.H;
+            if (begin < at + n) {
+                s_pair = p;
+                s_at = at;
+                break;
+            }
+            at += n;
+        }
+    }
+    if (A.rope.rot > 0)
+        for (int i = tid; i < A.rope.rot / 2; i += kThreads) s_turns[i] = turns_of(A.rope.inv_freq[i]);
+    __syncthreads();
+
+    int pair = s_pair;
+    long long pair_at = s_at;
+    for (long long from = begin; from < end;) {
+    const int b = pair / A.groups, grp = pair % A.groups;
+    const Seq seq(A, b);
+    const Tiles tiles(A, seq, b, grp, kRows);
+    const int N = seq.N, nq = seq.nq, rows = tiles.rows, lo_max = tiles.lo_max, p_min = N - nq + tiles.l_first;
+    const int unit_tiles = tiles.count();
+    if (unit_tiles == 0) {
+        ++pair;
+        continue;
+    }
+    const int h = static_cast<int>((from - pair_at) / unit_tiles);
+    const int i_begin = static_cast<int>((from - pair_at) % unit_tiles);
+    const int i_all = static_cast<int>(min(static_cast<long long>(unit_tiles - i_begin), end - from));   // tiles of this segment
+    const int i_end = min(i_begin + i_all, tiles.n1 + tiles.n2);                                        // without the one that is none
     const int per = (max(i_end - i_begin, 0) + S::kWarps - 1) / S::kWarps;   // tiles of a warp, consecutive
     const int w_begin = min(i_begin + warp * per, i_end), w_end = min(w_begin + per, i_end);
-
-    const int64_t unit = (static_cast<int64_t>(b) * P.H + h) * A.groups + grp;
-    if (i_begin >= i_end && A.splits > 1) {   // nothing here: the join skips it
-        if (tid < rows) *reinterpret_cast<float2*>(A.part_ml + 2 * ((unit * A.splits + split) * kRows + tid)) = make_float2(kNone, 0.0f);
-        return;
-    }
+    const int64_t unit = static_cast<int64_t>(pair) * P.H + h;
+    if (tid == 0 && i_begin == 0 && gridDim.x > 1)   // the shares that the unit lies in
+        *reinterpret_cast<int2*>(A.unit_shares + 2 * unit) =
+            make_int2(blockIdx.x, static_cast<int>((pair_at + static_cast<long long>(h + 1) * unit_tiles - 1) / share));
 
     // ---------------- the queries: rotated, scaled by a power of two, fp16
     if (i_begin < i_end) {
-        if (A.rope.rot > 0) {
-            for (int i = tid; i < A.rope.rot / 2; i += kThreads) s_turns[i] = turns_of(A.rope.inv_freq[i]);
-            __syncthreads();
-        }
         constexpr int J = D / 16;   // chunk pairs of a row: J consecutive lanes
         for (int it = tid; it < kRows * J; it += kThreads) {
             const int r = it / J, j = it % J;
@@ -178,19 +262,18 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
             // to [1, 2): fp16 then keeps 11 bits down to 2^-14 of the row's largest
             const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126), 126);
             const float f = exp2i(-e);
-            uint32_t* d = reinterpret_cast<uint32_t*>(s_q + r * D);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                d[a0 / 2 + i] = pack_out<__half>(xa[2 * i] * f, xa[2 * i + 1] * f);
-                d[b0 / 2 + i] = pack_out<__half>(xb[2 * i] * f, xb[2 * i + 1] * f);
+            for (int i = 0; i < 8; i += 4) {
+                uint2 lo;
+                *s_frag(0, r, a0 + i) = split(xa[i] * f, xa[i + 1] * f, xa[i + 2] * f, xa[i + 3] * f, lo);
+                if constexpr (kFine) *s_frag(1, r, a0 + i) = lo;
+                *s_frag(0, r, b0 + i) = split(xb[i] * f, xb[i + 1] * f, xb[i + 2] * f, xb[i + 3] * f, lo);
+                if constexpr (kFine) *s_frag(1, r, b0 + i) = lo;
             }
             if (j == 0) s_fac[r] = A.scale * exp2i(e);
         }
     }
-    if (tid < kRows) {
-        const int l = min((grp * kRows + tid) / A.G, l_last);
-        s_sight[tid] = sight_of(max(l, l_first));
-    }
+    if (tid < kRows) s_sight[tid] = sight_of(A, seq, b, min((grp * kRows + tid) / A.G, tiles.l_last));
     __syncthreads();
 
     float acc[NT][S::kMT][4];
@@ -207,12 +290,11 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
         float fac[NT][2], slope[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(s_q + (8 * nt + g) * D);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {   // step 4 i + s: coordinates 64 i + 16 c + 4 s ..
-                const int d = 64 * (ks >> 2) + 16 * c + 4 * (ks & 3);
-                qf[nt][ks][0] = q[d / 2];
-                qf[nt][ks][1] = q[d / 2 + 1];
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint2 f = reinterpret_cast<const uint2*>(smem + S::kSmem)[(nt * (D / 16) + ks) * 32 + lane];
+                qf[nt][ks][0] = f.x;
+                qf[nt][ks][1] = f.y;
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -247,27 +329,29 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
         };
         look_up(base, id, meta);
         look_up(base + 32, id_next, meta_next);
-        unsigned char* ring = smem + warp * S::kTileBytes + 16 * lane;   // a copy of the lane: 512 bytes apart
+        unsigned char* ring = smem + warp * S::kTileBytes * S::kU + 16 * lane;   // a copy of the lane: 512 bytes apart
         const uint32_t ring_at = tc::smem_addr(ring);
-        constexpr int kStep = S::kWarps * S::kTileBytes;
-        uint32_t ahead[S::kStages - 1];   // meta of the tiles on their way
-        int put = 0, get = 0;             // stages
-        // start tile i's copies (none behind the warp's last tile); its meta
-        auto fetch = [&](int i) -> uint32_t {
-            uint32_t mt = 0;
-            if (i < w_end) {
-                if (i - base == 32) {
-                    base = i;
+        constexpr int kStep = S::kWarps * S::kTileBytes * S::kU, kU = S::kU;
+        uint32_t ahead[S::kStages - 1][kU];   // meta of the tiles on their way
+        int put = 0, get = 0;                 // stages
+        // start the copies of the kU tiles from i (none behind the warp's last tile); their metas
+        auto fetch = [&](int i, uint32_t (&mt)[kU]) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                mt[u] = 0;
+                if (i + u >= w_end) continue;
+                if (i + u - base == 32) {
+                    base = i + u;
                     id = id_next;
                     meta = meta_next;
                     look_up(base + 32, id_next, meta_next);
                 }
-                const int64_t x = __shfl_sync(0xffffffffu, id, i - base);
-                mt = __shfl_sync(0xffffffffu, meta, i - base);
+                const int64_t x = __shfl_sync(0xffffffffu, id, i + u - base);
+                mt[u] = __shfl_sync(0xffffffffu, meta, i + u - base);
                 const bool here = x >= 0;
-                const int64_t off = (here ? x : 0) * unit_bytes + static_cast<int64_t>((tiles.at(i) << 4) & (P.BT - 1)) * D;
+                const int64_t off = (here ? x : 0) * unit_bytes + static_cast<int64_t>((tiles.at(i + u) << 4) & (P.BT - 1)) * D;
                 const uint8_t *kp = P.kc + off + g * D + 16 * c, *vp = P.vc + off + 2 * c * D + 4 * S::kVW * g;
-                const uint32_t dst = ring_at + put * kStep;
+                const uint32_t dst = ring_at + put * kStep + u * S::kTileBytes;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -278,84 +362,107 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
                     for (int k = 0; k < S::kVL; ++k)
                         copy_async(dst + 2 * S::kKL * 512 + (S::kVW == 4 ? (t * S::kVL + k) * 512 : (t >> 1) * 512 + (t & 1) * 8),
                                    vp + ((t & 1) + 8 * (t >> 1)) * D + 32 * S::kVW * k, here, S::kVW == 4);
-                put = put + 1 == S::kStages ? 0 : put + 1;
             }
+            put = put + 1 == S::kStages ? 0 : put + 1;
             copies_close();
-            return mt;
         };
 #pragma unroll
-        for (int k = 0; k < S::kStages - 1; ++k) ahead[k] = fetch(w_begin + k);
-        for (int i = w_begin; i < w_end; ++i) {
-            const int t0 = tiles.at(i) << 4;
-            const uint32_t mt = ahead[0];
+        for (int k = 0; k < S::kStages - 1; ++k) fetch(w_begin + k * kU, ahead[k]);
+        for (int i = w_begin; i < w_end; i += kU) {
+            uint32_t mt[kU];
+            int t0[kU];   // a tile behind the warp's last one: behind the sequence's end
 #pragma unroll
-            for (int k = 0; k < S::kStages - 2; ++k) ahead[k] = ahead[k + 1];
-            ahead[S::kStages - 2] = fetch(i + S::kStages - 1);
+            for (int u = 0; u < kU; ++u) {
+                mt[u] = ahead[0][u];
+                t0[u] = i + u < w_end ? tiles.at(i + u) << 4 : N;
+#pragma unroll
+                for (int k = 0; k < S::kStages - 2; ++k) ahead[k][u] = ahead[k + 1][u];
+            }
+            fetch(i + (S::kStages - 1) * kU, ahead[S::kStages - 2]);
             copies_wait<S::kStages - 1>();
-            const int kx = mt & 0xFF, vx = (mt >> 8) & 0xFF;
-            const bool here = mt >> 16;
             const unsigned char* src = ring + get * kStep;
             get = get + 1 == S::kStages ? 0 : get + 1;
             // ---------------- scores
-            float sc[NT][4];
+            float sc[kU][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+            for (int u = 0; u < kU; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) sc[u][nt][0] = sc[u][nt][1] = sc[u][nt][2] = sc[u][nt][3] = 0.0f;
 #pragma unroll
             for (int k = 0; k < S::kKL; ++k) {
-                uint32_t w0[4], w1[4];
-                load_words(w0, src + k * 512);
-                load_words(w1, src + (S::kKL + k) * 512);
+                uint32_t w0[kU][4], w1[kU][4];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    load_words(w0[u], src + u * S::kTileBytes + k * 512);
+                    load_words(w1[u], src + u * S::kTileBytes + (S::kKL + k) * 512);
+                }
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    uint32_t a0, a1, a2, a3;
-                    codes_f16<I8>(w0[w], a0, a2);
-                    codes_f16<I8>(w1[w], a1, a3);
+                    uint2 fine[NT];
+                    if constexpr (kFine)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], a0, a1, a2, a3, qf[nt][4 * k + w][0], qf[nt][4 * k + w][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+                            fine[nt] = reinterpret_cast<const uint2*>(smem + S::kSmem)[((NT + nt) * (D / 16) + 4 * k + w) * 32 + lane];
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) {
+                        uint32_t a0, a1, a2, a3;
+                        codes_f16<I8>(w0[u][w], a0, a2);
+                        codes_f16<I8>(w1[u][w], a1, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816(sc[u][nt], a0, a1, a2, a3, qf[nt][4 * k + w][0], qf[nt][4 * k + w][1]);
+                            if constexpr (kFine) mma16816(sc[u][nt], a0, a1, a2, a3, fine[nt].x, fine[nt].y);
+                        }
+                    }
                 }
             }
             // ---------------- u = log2(e) score + log2(value scale), masked
-            const float ks2 = exp2i(kx == 0 ? -126 : kx - 127), lv = static_cast<float>(vx - 127);
-            const bool open = here && t0 + 15 <= p_min && t0 >= lo_max;
-            float u[NT][4];
+            float lg[kU][NT][4];
+            bool pass = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {   // e: token g + 8 (e >> 1), row 2c + (e & 1)
-                    const float s = sc[nt][e] * (fac[nt][e & 1] * ks2);
-                    if (plain) {
-                        u[nt][e] = fmaf(s, kLog2e, lv);
-                    } else {
-                        float y = s * kLog2e;
-                        if (A.cap > 0.0f) y = fmaf(-2.0f * cap2, rcp(1.0f + ex2(s * cap_in)), cap2);   // cap tanh(s / cap)
-                        if (A.slopes) {
-                            const int p = s_sight[8 * nt + 2 * c + (e & 1)].p;
-                            y -= slope[nt][e & 1] * fabsf(static_cast<float>(p - (t0 + g + 8 * (e >> 1))));
-                        }
-                        u[nt][e] = y + lv;
-                    }
-                }
-            if (!open) {
+            for (int u = 0; u < kU; ++u) {
+                const int kx = mt[u] & 0xFF, vx = (mt[u] >> 8) & 0xFF;
+                const bool here = mt[u] >> 16;
+                const float ks2 = exp2i(kx == 0 ? -126 : kx - 127), lv = static_cast<float>(vx - 127);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = t0 + g + 8 * (e >> 1);
-                        if (!(here && t < N && s_sight[8 * nt + 2 * c + (e & 1)].sees(t))) u[nt][e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e) {   // e: token g + 8 (e >> 1), row 2c + (e & 1)
+                        const float s = sc[u][nt][e] * (fac[nt][e & 1] * ks2);
+                        if (plain) {
+                            lg[u][nt][e] = fmaf(s, kLog2e, lv);
+                        } else {
+                            float y = s * kLog2e;
+                            if (A.cap > 0.0f) y = fmaf(-2.0f * cap2, rcp(1.0f + ex2(s * cap_in)), cap2);   // cap tanh(s / cap)
+                            if (A.slopes) {
+                                const int p = s_sight[8 * nt + 2 * c + (e & 1)].p;
+                                y -= slope[nt][e & 1] * fabsf(static_cast<float>(p - (t0[u] + g + 8 * (e >> 1))));
+                            }
+                            lg[u][nt][e] = y + lv;
+                        }
                     }
+                if (!(here && t0[u] + 15 <= p_min && t0[u] >= lo_max)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = t0[u] + g + 8 * (e >> 1);
+                            if (!(here && t < N && s_sight[8 * nt + 2 * c + (e & 1)].sees(t))) lg[u][nt][e] = -INFINITY;
+                        }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) pass |= lg[u][nt][e] > m[nt][e & 1] + kGap;
             }
             // ---------------- the reference moves only when a score passes it by the gap
-            bool pass = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) pass |= u[nt][e] > m[nt][e & 1] + kGap;
             if (__any_sync(0xffffffffu, pass)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(u[nt][e], u[nt][e + 2]);
+                        float x = fmaxf(lg[0][nt][e], lg[0][nt][e + 2]);
+                        if constexpr (kU == 2) x = fmaxf(x, fmaxf(lg[1][nt][e], lg[1][nt][e + 2]));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -371,58 +478,64 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
                     }
             }
             // ---------------- p, its sum, and p as the second operand (rows on N)
-            const float iv = exp2i(127 - vx < -126 ? -126 : min(127 - vx, 126));
-            uint32_t pb[NT][2];
+            uint32_t pb[kU][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
+            for (int u = 0; u < kU; ++u) {
+                const int vx = (mt[u] >> 8) & 0xFF;
+                const float iv = exp2i(127 - vx < -126 ? -126 : min(127 - vx, 126));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[e] = ex2(u[nt][e] - m[nt][e & 1]);
-                    l_sum[nt][e & 1] = fmaf(p[e], iv, l_sum[nt][e & 1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = ex2(lg[u][nt][e] - m[nt][e & 1]);
+                        l_sum[nt][e & 1] = fmaf(p[e], iv, l_sum[nt][e & 1]);
+                    }
+                    pb[u][nt][0] = transpose8x8(pack_out<__half>(p[0], p[1]));
+                    pb[u][nt][1] = transpose8x8(pack_out<__half>(p[2], p[3]));
                 }
-                pb[nt][0] = transpose8x8(pack_out<__half>(p[0], p[1]));
-                pb[nt][1] = transpose8x8(pack_out<__half>(p[2], p[3]));
             }
             // ---------------- O^T += V^T P
-            const bool whole = t0 + 16 <= N;
 #pragma unroll
-            for (int k = 0; k < S::kVL; ++k) {
-                uint32_t vw[4][S::kVW];
-                if constexpr (S::kVW == 4) {
+            for (int u = 0; u < kU; ++u)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) load_words(vw[t], src + (2 * S::kKL + t * S::kVL + k) * 512);
-                } else {   // 8 bytes of two tokens side by side
+                for (int k = 0; k < S::kVL; ++k) {
+                    const unsigned char* from_v = src + u * S::kTileBytes + 2 * S::kKL * 512;
+                    uint32_t vw[4][S::kVW];
+                    if constexpr (S::kVW == 4) {
 #pragma unroll
-                    for (int t = 0; t < 4; t += 2) {
-                        uint32_t both[4];
-                        load_words(both, src + (2 * S::kKL + t / 2) * 512);
-                        vw[t][0] = both[0], vw[t][1] = both[1], vw[t + 1][0] = both[2], vw[t + 1][1] = both[3];
+                        for (int t = 0; t < 4; ++t) load_words(vw[t], from_v + (t * S::kVL + k) * 512);
+                    } else {   // 8 bytes of two tokens side by side
+#pragma unroll
+                        for (int t = 0; t < 4; t += 2) {
+                            uint32_t both[4];
+                            load_words(both, from_v + (t / 2) * 512);
+                            vw[t][0] = both[0], vw[t][1] = both[1], vw[t + 1][0] = both[2], vw[t + 1][1] = both[3];
+                        }
                     }
-                }
-                if (!whole) {   // codes behind the sequence's end may be anything: their weight is 0, so they have to be finite
+                    if (t0[u] + 16 > N) {   // codes behind the sequence's end may be anything: their weight is 0, so they have to be finite
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        if (t0 + 2 * c + (t & 1) + 8 * (t >> 1) >= N)
+                        for (int t = 0; t < 4; ++t)
+                            if (t0[u] + 2 * c + (t & 1) + 8 * (t >> 1) >= N)
 #pragma unroll
-                            for (int w = 0; w < S::kVW; ++w) vw[t][w] = 0;
-                }
-#pragma unroll
-                for (int w = 0; w < S::kVW; ++w) {
-                    uint32_t x[2][4];   // [token pair][coordinate]: fp16 pairs of two tokens
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const uint32_t a = vw[2 * t][w], d = vw[2 * t + 1][w];
-                        codes_f16<I8>(__byte_perm(a, d, 0x5140), x[t][0], x[t][1]);
-                        codes_f16<I8>(__byte_perm(a, d, 0x7362), x[t][2], x[t][3]);
+                                for (int w = 0; w < S::kVW; ++w) vw[t][w] = 0;
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma16816(acc[nt][(k * S::kVW + w) * 2], x[0][0], x[0][1], x[1][0], x[1][1], pb[nt][0], pb[nt][1]);
-                        mma16816(acc[nt][(k * S::kVW + w) * 2 + 1], x[0][2], x[0][3], x[1][2], x[1][3], pb[nt][0], pb[nt][1]);
+                    for (int w = 0; w < S::kVW; ++w) {
+                        uint32_t x[2][4];   // [token pair][coordinate]: fp16 pairs of two tokens
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const uint32_t a = vw[2 * t][w], d = vw[2 * t + 1][w];
+                            codes_f16<I8>(__byte_perm(a, d, 0x5140), x[t][0], x[t][1]);
+                            codes_f16<I8>(__byte_perm(a, d, 0x7362), x[t][2], x[t][3]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816(acc[nt][(k * S::kVW + w) * 2], x[0][0], x[0][1], x[1][0], x[1][1], pb[u][nt][0], pb[u][nt][1]);
+                            mma16816(acc[nt][(k * S::kVW + w) * 2 + 1], x[0][2], x[0][3], x[1][2], x[1][3], pb[u][nt][0], pb[u][nt][1]);
+                        }
                     }
                 }
-            }
         }
     }
 
@@ -475,51 +588,60 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, Shape<D, NT>::kCtas
             o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
             sum = fmaf(s_l[w][r], ex2(s_m[w][r] - top), sum);
         }
-        if (A.splits == 1) {
+        if (i_all == unit_tiles) {
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
             T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.out.sh + l * A.out.st + d;
             *reinterpret_cast<uint2*>(dst) = make_uint2(pack_out<T>(o.x * inv, o.y * inv), pack_out<T>(o.z * inv, o.w * inv));
         } else {
-            const int64_t at = (unit * A.splits + split) * kRows + r;
+            // the unit goes on behind this share (state 1 of the CTA), or began before it (state 0)
+            const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + (i_begin == 0 ? 1 : 0)) * kRows + r;
             *reinterpret_cast<float4*>(A.part_o + at * D + d) = o;
             if (d == 0) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(top, sum);
         }
     }
+    from += i_all;
+    if (from == pair_at + static_cast<long long>(unit_tiles) * P.H) {
+        pair_at = from;
+        ++pair;
+    }
+    __syncthreads();   // before the next segment's queries and copies
+    }
     tc::grid_release_dependents();
 }
 
-// Joins the splits of a row: out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i.
-// One warp per row and 128 coordinates; splits that no tile reached hold l = 0
-// at the reference kNone.
+// Joins the states of the units that lie in several shares:
+// out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i. One warp a row.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendArgs A, int group_rows) {
     tc::grid_wait_prior();
-    constexpr int kLanes = D / 4 < 32 ? D / 4 : 32;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);   // over batch, H, rows
-    const int lane = threadIdx.x & 31;
-    const int R = A.G * A.L;
-    if (row >= static_cast<int64_t>(A.batch) * A.pool.H * R) return;
-    const int rr = static_cast<int>(row % R), h = static_cast<int>(row / R % A.pool.H), b = static_cast<int>(row / R / A.pool.H);
-    const int l = rr / A.G;
-    int nq = A.qlens ? A.qlens[b] : A.L;
-    if (l >= min(nq, A.L)) return;
-    const int64_t unit = (static_cast<int64_t>(b) * A.pool.H + h) * A.groups + rr / group_rows;
-    const int64_t at = unit * A.splits * group_rows + rr % group_rows;
+    constexpr int kLanes = D / 4 < 32 ? D / 4 : 32, kV = D / 128 > 0 ? D / 128 : 1;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);   // over batch, row groups, H, rows of a group
+    const int lane = threadIdx.x & 31, H = A.pool.H;
+    const int64_t unit = row / group_rows;
+    const int r = static_cast<int>(row % group_rows);
+    if (unit >= static_cast<int64_t>(A.batch) * A.groups * H) return;
+    const int h = static_cast<int>(unit % H), grp = static_cast<int>(unit / H % A.groups), b = static_cast<int>(unit / H / A.groups);
+    const int rr = grp * group_rows + r, l = rr / A.G;
+    const int nq = A.qlens ? min(A.qlens[b], A.L) : A.L;
+    if (rr >= A.G * A.L || l >= nq || grp * group_rows / A.G >= nq) return;
+    const int2 sh = *reinterpret_cast<const int2*>(A.unit_shares + 2 * unit);
+    if (sh.x == sh.y) return;   // finished by its CTA
+    auto state = [&](int i) { return (2 * static_cast<int64_t>(i) + (i == sh.x ? 1 : 0)) * group_rows + r; };
     float top = kNone;
-    for (int i = lane; i < A.splits; i += 32) top = fmaxf(top, A.part_ml[2 * (at + static_cast<int64_t>(i) * group_rows)]);
+    for (int i = sh.x + lane; i <= sh.y; i += 32) top = fmaxf(top, A.part_ml[2 * state(i)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float sum = 0.0f;
-    float4 o[D / 128 > 0 ? D / 128 : 1] = {};
-    for (int i = 0; i < A.splits; ++i) {
-        const int64_t a = at + static_cast<int64_t>(i) * group_rows;
+    float4 o[kV] = {};
+#pragma unroll 4
+    for (int i = sh.x; i <= sh.y; ++i) {
+        const int64_t a = state(i);
         const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + 2 * a);
-        if (ml.y == 0.0f) continue;   // nothing seen: its output is not looked at
         const float f = ex2(ml.x - top);
         sum = fmaf(ml.y, f, sum);
         if (lane < kLanes)
 #pragma unroll
-            for (int k = 0; k < (D / 128 > 0 ? D / 128 : 1); ++k) {
+            for (int k = 0; k < kV; ++k) {
                 const float4 x = *reinterpret_cast<const float4*>(A.part_o + a * D + 128 * k + 4 * lane);
                 o[k].x = fmaf(x.x, f, o[k].x), o[k].y = fmaf(x.y, f, o[k].y), o[k].z = fmaf(x.z, f, o[k].z), o[k].w = fmaf(x.w, f, o[k].w);
             }
@@ -528,7 +650,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
     T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.out.sh + l * A.out.st;
     if (lane < kLanes)
 #pragma unroll
-        for (int k = 0; k < (D / 128 > 0 ? D / 128 : 1); ++k)
+        for (int k = 0; k < kV; ++k)
             *reinterpret_cast<uint2*>(dst + 128 * k + 4 * lane) =
                 make_uint2(pack_out<T>(o[k].x * inv, o[k].y * inv), pack_out<T>(o[k].z * inv, o[k].w * inv));
 }
@@ -536,12 +658,18 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
 template <typename T, int D, int NT, bool I8>
 cudaError_t launch_t(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
     using S = Shape<D, NT>;
-    const int smem = S::kSmem + S::kRows * D * 2;
+    constexpr bool kFine = !std::is_same<T, __nv_bfloat16>::value;
+    const int smem = S::kSmem + S::kRows * D * 2 * (kFine ? 2 : 1);
     cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, NT, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    decode_kernel<T, D, NT, I8><<<dim3(p.groups * p.splits, a.pool.H, a.batch), 32 * S::kWarps, smem, s>>>(a);
+    decode_kernel<T, D, NT, I8><<<p.ctas, 32 * S::kWarps, smem, s>>>(a);
     g_launches.fetch_add(1, std::memory_order_relaxed);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.ctas == 1) return e;
+    const int64_t rows = static_cast<int64_t>(a.batch) * a.groups * a.pool.H * p.group_rows;
+    e = launch_overlapped(join_kernel<T, D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, a, p.group_rows);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return e;
 }
 
 template <typename T, int D>
@@ -558,18 +686,7 @@ cudaError_t launch_dtype(const AttendArgs& a, const AttendPlan& p, int D, int fo
 }  // namespace
 
 cudaError_t launch_decode(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s) {
-    const cudaError_t e = dtype == TQ_F16 ? launch_dtype<__half>(a, p, D, format, s) : launch_dtype<__nv_bfloat16>(a, p, D, format, s);
-    return e != cudaSuccess || p.splits == 1 ? e : launch_join(a, p, D, dtype, s);
-}
-
-cudaError_t launch_join(const AttendArgs& a, const AttendPlan& p, int D, int dtype, cudaStream_t s) {
-    auto kernel = dtype == TQ_F16 ? (D == 64 ? join_kernel<__half, 64> : D == 128 ? join_kernel<__half, 128> : join_kernel<__half, 256>)
-                                  : (D == 64 ? join_kernel<__nv_bfloat16, 64>
-                                             : D == 128 ? join_kernel<__nv_bfloat16, 128> : join_kernel<__nv_bfloat16, 256>);
-    const int64_t rows = static_cast<int64_t>(a.batch) * a.pool.H * a.G * a.L;
-    const cudaError_t e = launch_overlapped(kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, a, p.group_rows);
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return e;
+    return dtype == TQ_F16 ? launch_dtype<__half>(a, p, D, format, s) : launch_dtype<__nv_bfloat16>(a, p, D, format, s);
 }
 
 }  // namespace kv8

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Pool& P = A.pool;
     // the longest rows first: the last wave then holds short ones
-    const int grp = A.groups - 1 - blockIdx.x / A.splits, split = blockIdx.x % A.splits, h = blockIdx.y, b = blockIdx.z;
+    const int grp = A.groups - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int rows = min(A.G * A.L - grp * S::kRows, S::kRows);
 
     int N = A.seq[b], nq = A.qlens ? A.qlens[b] : A.L;
@@ -158,8 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     tiles.n1 = (pre + kT - 1) / kT;
     tiles.first = max(tiles.n1, lo_min / kT);
     tiles.n2 = p_max < 0 || lo_min > p_max ? 0 : max(0, p_max / kT + 1 - tiles.first);
-    const int i_begin = split * A.split_tiles, n_tiles = max(0, min(A.split_tiles, tiles.count() - i_begin));
-    const int64_t unit = (static_cast<int64_t>(b) * P.H + h) * A.groups + grp;
+    const int n_tiles = tiles.count();
 
     // ---------------- set up: TMEM, barriers, the queries (rotated, scaled by a power of two, fp16)
     if (warp == 12) {
@@ -243,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
             const float slope = MOD && A.slopes ? A.slopes[h * A.G + rr % A.G] * kLog2e : 0.0f;
             for (int i = 0; i < n_tiles; ++i) {
-                const int t0 = tiles.at(i_begin + i) * kT;
+                const int t0 = tiles.at(i) * kT;
                 const int sb = kH == 2 ? half : i & 1;                    // buffer of S and P
                 ok = arrived(&s_ready[sb], kH == 2 ? i & 1 : (i >> 1) & 1);
                 if (!ok) break;
@@ -374,39 +373,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const bool failed = *const_cast<volatile int*>(&s_fail) != 0;
         if (mine) {
             const bool real = row < rows && rr / A.G < nq;
-            if (A.splits == 1) {
-                const float inv = !failed && l_sum > 0.0f ? 1.0f / l_sum : 0.0f;
-                T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.out.sh + (rr / A.G) * A.out.st;
+            const float inv = !failed && l_sum > 0.0f ? 1.0f / l_sum : 0.0f;
+            T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.out.sh + (rr / A.G) * A.out.st;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    float v[32];
-                    if (n_tiles > 0) tc::tmem_ld32(t_o + 32 * c, v);
-                    if (real) {
+            for (int c = 0; c < D / 32; ++c) {
+                float v[32];
+                if (n_tiles > 0) tc::tmem_ld32(t_o + 32 * c, v);
+                if (real) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 w = make_uint4(0, 0, 0, 0);
-                            if (inv > 0.0f) {
-                                w.x = pack_out<T>(v[e] * inv, v[e + 1] * inv), w.y = pack_out<T>(v[e + 2] * inv, v[e + 3] * inv);
-                                w.z = pack_out<T>(v[e + 4] * inv, v[e + 5] * inv), w.w = pack_out<T>(v[e + 6] * inv, v[e + 7] * inv);
-                            }
-                            *reinterpret_cast<uint4*>(dst + 32 * c + e) = w;
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        if (inv > 0.0f) {
+                            w.x = pack_out<T>(v[e] * inv, v[e + 1] * inv), w.y = pack_out<T>(v[e + 2] * inv, v[e + 3] * inv);
+                            w.z = pack_out<T>(v[e + 4] * inv, v[e + 5] * inv), w.w = pack_out<T>(v[e + 6] * inv, v[e + 7] * inv);
                         }
+                        *reinterpret_cast<uint4*>(dst + 32 * c + e) = w;
                     }
                 }
-            } else {
-                const int64_t at = (unit * A.splits + split) * S::kRows + row;
-                const bool some = !failed && l_sum > 0.0f;
-                if (real) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(some ? m : kNone, some ? l_sum : 0.0f);
-                if (n_tiles > 0)
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        float v[32];
-                        tc::tmem_ld32(t_o + 32 * c, v);
-                        if (real && some)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4*>(A.part_o + at * D + 32 * c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                    }
             }
         }
     } else if (warp < 12) {
@@ -421,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         auto look_up = [&](int i) {
             id = -1;
             kx = vx = -64;
-            const int t = tiles.at(i_begin + i) * kT + 8 * lane;
+            const int t = tiles.at(i) * kT + 8 * lane;
             if (lane < S::kGroups && t < N && (t <= p_max || t < pre)) {
                 const int lb = t >> P.bt_shift;
                 const bool seen = ((lb << P.bt_shift) + P.BT > lo_min) || (lb << P.bt_shift) < pre;
@@ -439,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         };
         // unit k of a warp: group w + 4 (k / CQ), bytes 64 (k % CQ) + 16 ch of token tok
         auto load = [&](uint4 (&x)[S::kUnits], const uint8_t* codes, int i) {
-            const int t0 = tiles.at(i_begin + i) * kT;
+            const int t0 = tiles.at(i) * kT;
 #pragma unroll
             for (int q = 0; q < TG; ++q) {
                 const int g = w + 4 * q, t = t0 + 8 * g + tok;
@@ -484,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int st = i & 1;
                 load(vr, P.vc, i);
                 const int kref = __reduce_max_sync(0xffffffffu, kx), vref = __reduce_max_sync(0xffffffffu, vx);
-                const int t0 = tiles.at(i_begin + i) * kT;
+                const int t0 = tiles.at(i) * kT;
                 // groups of no block among those that have tokens
                 const unsigned gone = __ballot_sync(0xffffffffu, lane < S::kGroups && id < 0 && t0 + 8 * lane < N);
                 const int vx_now = vx;
@@ -611,7 +594,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     if (tid == 0)
         for (int s = 0; s < 15; ++s) tc::mbar_inval(&s_bar[s]);
-    tc::grid_release_dependents();
 }
 
 template <typename T, int D, bool I8, bool MOD>
@@ -620,7 +602,7 @@ cudaError_t launch_m(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
     static_assert(S::kSmem <= 227 * 1024 - 4096, "shared memory");
     const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<T, D, I8, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    prefill_kernel<T, D, I8, MOD><<<dim3(p.groups * p.splits, a.pool.H, a.batch), kThreads, S::kSmem, s>>>(a);
+    prefill_kernel<T, D, I8, MOD><<<dim3(p.groups, a.pool.H, a.batch), kThreads, S::kSmem, s>>>(a);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cudaGetLastError();
 }
@@ -642,8 +624,7 @@ cudaError_t launch_dtype(const AttendArgs& a, const AttendPlan& p, int D, int fo
 }  // namespace
 
 cudaError_t launch_prefill(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s) {
-    const cudaError_t e = dtype == TQ_F16 ? launch_dtype<__half>(a, p, D, format, s) : launch_dtype<__nv_bfloat16>(a, p, D, format, s);
-    return e != cudaSuccess || p.splits == 1 ? e : launch_join(a, p, D, dtype, s);
+    return dtype == TQ_F16 ? launch_dtype<__half>(a, p, D, format, s) : launch_dtype<__nv_bfloat16>(a, p, D, format, s);
 }
 
 }  // namespace kv8
