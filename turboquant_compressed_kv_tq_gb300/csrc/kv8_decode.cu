@@ -24,12 +24,10 @@
 // wants in one lane are whatever order both operands share, so each lane takes
 // 16 consecutive bytes: of keys, lane (g, c) reads tokens g and g + 8 at bytes
 // 64 i + 16 c; of values, tokens 2c, 2c + 1, 2c + 8, 2c + 9 at bytes 128 i + 16 g.
-// Every copy is 16 bytes a lane, and each lane copies what it will use itself:
-// shared memory holds a queue of tiles for each lane (cp.async, kStages deep),
-// which needs no barrier, no other lane's copies, and has no bank conflicts.
+// A tile's keys and values are 16 D contiguous bytes each: one bulk copy into the
+// warp's own queue of stages in shared memory.
 //
-// Bound: memory, 2 D bytes a token. The queue is there for that: 48 to 192 KB on
-// their way to each SM, where registers alone could hold 32 to 64.
+// Bound: memory, 2 D bytes a token.
 #include <climits>
 #include <type_traits>
 
@@ -56,14 +54,20 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return r;
 }
 
-__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, bool here, bool wide) {
-    // nothing is read where there is no block: the destination is zeroed
-    if (wide) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(here ? 16 : 0) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(here ? 8 : 0) : "memory");
+// Wait for the phase with this parity; false after about a second.
+__device__ __forceinline__ bool arrived(uint64_t* bar, unsigned parity) {
+    const uint32_t a = tc::smem_addr(bar);
+    for (unsigned it = 0; it < (1u << 18); ++it) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (done) return true;
+    }
+    return false;
 }
-__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
 template <int W>
 __device__ __forceinline__ void load_words(uint32_t (&w)[W], const unsigned char* p) {
@@ -151,11 +155,11 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
     using S = Shape<D, NT>;
     constexpr int kRows = S::kRows, kThreads = 32 * S::kWarps;
     extern __shared__ __align__(16) unsigned char smem[];
-    // the queries as operand fragments, one uint2 (4 coordinates) a lane: coordinates 64 i + 16 c + 4 s .. of
+    // the queries as operand fragments, one uint2 (4 coordinates) a lane: coordinates 16 (kKL c + i) + 4 s .. of
     // row 8 nt + g at step 4 i + s, lane 4 g + c; with fp16 queries a second set holds what the first rounded off
     constexpr bool kFine = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
     auto s_frag = [&](int part, int r, int d) {
-        const int ks = 4 * (d >> 6) + ((d >> 2) & 3), ln = 4 * (r & 7) + ((d >> 4) & 3);
+        const int ks = 4 * ((d >> 4) % S::kKL) + ((d >> 2) & 3), ln = 4 * (r & 7) + (d >> 4) / S::kKL;
         return reinterpret_cast<uint2*>(smem + S::kSmem) + ((part * NT + (r >> 3)) * (D / 16) + ks) * 32 + ln;
     };
     auto split = [](float x0, float x1, float x2, float x3, uint2& lo) {
@@ -173,6 +177,11 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
     // ---------------- this CTA's share of the tiles of all units. A pair (sequence, row group) has the
     // tiles of its P.H units, one head after another
     __shared__ long long s_scan[S::kWarps], s_at;
+    __shared__ __align__(8) uint64_t s_bar[S::kWarps * S::kStages];
+    if (lane == 0) {
+        for (int k = 0; k < S::kStages; ++k) tc::mbar_init(&s_bar[warp * S::kStages + k], 1);
+        tc::mbar_fence_init();
+    }
     __shared__ int s_pair;
     const int pairs = A.batch * A.groups, each = (pairs + kThreads - 1) / kThreads;
     long long sum = 0;
@@ -215,6 +224,9 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         for (int i = tid; i < A.rope.rot / 2; i += kThreads) s_turns[i] = turns_of(A.rope.inv_freq[i]);
     __syncthreads();
 
+    uint64_t* bars = s_bar + warp * S::kStages;
+    unsigned puts = 0, gets = 0;   // of the warp's stages, over all its segments
+    bool dead = false;             // a copy did not come: nothing more is started
     int pair = s_pair;
     long long pair_at = s_at;
     for (long long from = begin; from < end;) {
@@ -285,7 +297,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         m[nt][0] = m[nt][1] = kNone;
         l_sum[nt][0] = l_sum[nt][1] = 0.0f;
     }
-    if (w_begin < w_end) {
+    if (w_begin < w_end && !dead) {
         uint32_t qf[NT][D / 16][2];
         float fac[NT][2], slope[NT][2];
 #pragma unroll
@@ -329,13 +341,16 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         };
         look_up(base, id, meta);
         look_up(base + 32, id_next, meta_next);
-        unsigned char* ring = smem + warp * S::kTileBytes * S::kU + 16 * lane;   // a copy of the lane: 512 bytes apart
-        const uint32_t ring_at = tc::smem_addr(ring);
-        constexpr int kStep = S::kWarps * S::kTileBytes * S::kU, kU = S::kU;
+        constexpr int kStep = S::kTileBytes * S::kU, kU = S::kU;
+        unsigned char* ring = smem + warp * S::kStages * kStep;
         uint32_t ahead[S::kStages - 1][kU];   // meta of the tiles on their way
-        int put = 0, get = 0;                 // stages
         // start the copies of the kU tiles from i (none behind the warp's last tile); their metas
         auto fetch = [&](int i, uint32_t (&mt)[kU]) {
+            const unsigned st = puts % S::kStages;
+            if (i < w_end) {
+                if (lane == 0) tc::mbar_expect_tx(&bars[st], i + kU <= w_end ? kStep : S::kTileBytes);
+                ++puts;
+            }
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
                 mt[u] = 0;
@@ -348,23 +363,13 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
                 }
                 const int64_t x = __shfl_sync(0xffffffffu, id, i + u - base);
                 mt[u] = __shfl_sync(0xffffffffu, meta, i + u - base);
-                const bool here = x >= 0;
-                const int64_t off = (here ? x : 0) * unit_bytes + static_cast<int64_t>((tiles.at(i + u) << 4) & (P.BT - 1)) * D;
-                const uint8_t *kp = P.kc + off + g * D + 16 * c, *vp = P.vc + off + 2 * c * D + 4 * S::kVW * g;
-                const uint32_t dst = ring_at + put * kStep + u * S::kTileBytes;
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int k = 0; k < S::kKL; ++k) copy_async(dst + (t * S::kKL + k) * 512, kp + 8 * t * D + 64 * k, here, true);
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int k = 0; k < S::kVL; ++k)
-                        copy_async(dst + 2 * S::kKL * 512 + (S::kVW == 4 ? (t * S::kVL + k) * 512 : (t >> 1) * 512 + (t & 1) * 8),
-                                   vp + ((t & 1) + 8 * (t >> 1)) * D + 32 * S::kVW * k, here, S::kVW == 4);
+                if (lane == 0) {   // where there is no block: any block, which nobody sees
+                    const int64_t off = (x < 0 ? 0 : x) * unit_bytes + static_cast<int64_t>((tiles.at(i + u) << 4) & (P.BT - 1)) * D;
+                    unsigned char* dst = ring + st * kStep + u * S::kTileBytes;
+                    tc::bulk_g2s(dst, P.kc + off, 16 * D, &bars[st]);
+                    tc::bulk_g2s(dst + 16 * D, P.vc + off, 16 * D, &bars[st]);
+                }
             }
-            put = put + 1 == S::kStages ? 0 : put + 1;
-            copies_close();
         };
 #pragma unroll
         for (int k = 0; k < S::kStages - 1; ++k) fetch(w_begin + k * kU, ahead[k]);
@@ -378,10 +383,16 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
 #pragma unroll
                 for (int k = 0; k < S::kStages - 2; ++k) ahead[k][u] = ahead[k + 1][u];
             }
+            __syncwarp();   // every lane has read the stage that is filled now
             fetch(i + (S::kStages - 1) * kU, ahead[S::kStages - 2]);
-            copies_wait<S::kStages - 1>();
-            const unsigned char* src = ring + get * kStep;
-            get = get + 1 == S::kStages ? 0 : get + 1;
+            const unsigned st = gets % S::kStages;
+            dead = !arrived(&bars[st], (gets / S::kStages) & 1);
+            if (__any_sync(0xffffffffu, dead)) {
+                dead = true;
+                break;
+            }
+            ++gets;
+            const unsigned char* src = ring + st * kStep;
             // ---------------- scores
             float sc[kU][NT][4];
 #pragma unroll
@@ -393,8 +404,8 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
                 uint32_t w0[kU][4], w1[kU][4];
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
-                    load_words(w0[u], src + u * S::kTileBytes + k * 512);
-                    load_words(w1[u], src + u * S::kTileBytes + (S::kKL + k) * 512);
+                    load_words(w0[u], src + u * S::kTileBytes + g * D + 16 * (S::kKL * c + k));
+                    load_words(w1[u], src + u * S::kTileBytes + (g + 8) * D + 16 * (S::kKL * c + k));
                 }
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -500,23 +511,15 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
             for (int u = 0; u < kU; ++u)
 #pragma unroll
                 for (int k = 0; k < S::kVL; ++k) {
-                    const unsigned char* from_v = src + u * S::kTileBytes + 2 * S::kKL * 512;
+                    const unsigned char* from_v = src + u * S::kTileBytes + 16 * D + 32 * S::kVW * k + 4 * S::kVW * g;
                     uint32_t vw[4][S::kVW];
-                    if constexpr (S::kVW == 4) {
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) load_words(vw[t], from_v + (t * S::kVL + k) * 512);
-                    } else {   // 8 bytes of two tokens side by side
-#pragma unroll
-                        for (int t = 0; t < 4; t += 2) {
-                            uint32_t both[4];
-                            load_words(both, from_v + (t / 2) * 512);
-                            vw[t][0] = both[0], vw[t][1] = both[1], vw[t + 1][0] = both[2], vw[t + 1][1] = both[3];
-                        }
-                    }
-                    if (t0[u] + 16 > N) {   // codes behind the sequence's end may be anything: their weight is 0, so they have to be finite
+                    for (int t = 0; t < 4; ++t) load_words(vw[t], from_v + (2 * c + (t & 1) + 8 * (t >> 1)) * D);
+                    // codes behind the sequence's end, or of no block, may be anything: their weight is 0, so they have to be finite
+                    if (t0[u] + 16 > N || !(mt[u] >> 16)) {
 #pragma unroll
                         for (int t = 0; t < 4; ++t)
-                            if (t0[u] + 2 * c + (t & 1) + 8 * (t >> 1) >= N)
+                            if (t0[u] + 2 * c + (t & 1) + 8 * (t >> 1) >= N || !(mt[u] >> 16))
 #pragma unroll
                                 for (int w = 0; w < S::kVW; ++w) vw[t][w] = 0;
                     }
@@ -539,6 +542,10 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         }
     }
 
+    if (dead) {   // what is in flight ends (or is given up) before its shared memory is used for anything else
+        if (lane == 0) atomicOr(A.err, TQ_DEVERR_TIMEOUT);
+        for (; gets < puts; ++gets) (void)arrived(&bars[gets % S::kStages], (gets / S::kStages) & 1);
+    }
     // ---------------- the CTA's state of each row: the warps' states at their largest reference
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -604,6 +611,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         pair_at = from;
         ++pair;
     }
+    tc::fence_proxy_async_smem();
     __syncthreads();   // before the next segment's queries and copies
     }
     tc::grid_release_dependents();
