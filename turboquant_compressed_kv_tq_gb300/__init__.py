@@ -506,25 +506,42 @@ class CompressedKVCache:
 
 # ----------------------------------------------------------------- 8-bit cache
 
-_KV8_DTYPES = None
+class _KV8:
+    """What the two calls below need of torch and the library, looked up once (they are short: every lookup counts)."""
 
-
-def _kv8_dtype(dtype) -> int:
-    global _KV8_DTYPES
-    if _KV8_DTYPES is None:
+    def __init__(self):
         torch = _torch()
-        _KV8_DTYPES = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
-    code = _KV8_DTYPES.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return code
+        self.codes = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
+        self.i32, self.f32 = torch.int32, torch.float32
+        self.device = torch._C._cuda_getDevice                # of torch.cuda.current_device
+        self.stream = torch._C._cuda_getCurrentRawStream      # of torch.cuda.current_stream(device).cuda_stream
+        self.append, self.attention = lib().tq_kv8_append, lib().tq_kv8_attention
+
+
+_kv8_found = None
+
+
+def _kv8() -> _KV8:
+    global _kv8_found
+    if _kv8_found is None:
+        _kv8_found = _KV8()
+    return _kv8_found
+
+
+def _raw_stream(t, stream, device) -> int:
+    if stream is None:
+        return t.stream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+_pack_rows = struct.Struct("@Pqqq").pack                 # tq_rows
+_pack_scores = struct.Struct("@ffPiPPPP").pack           # tq_kv8_scores
 
 
 def _rows(t, name, dtype, device, batch, heads, tokens, dim) -> bytes:
     """tq_rows of a [batch, heads, tokens, head_dim] view, in whatever order its first three axes lie."""
-    shape = t.shape
-    if len(shape) != 4 or shape[0] != batch or shape[1] != heads or shape[2] != tokens or shape[3] != dim:
-        raise ValueError(f"{name} must be [batch, heads, tokens, head_dim] = {(batch, heads, tokens, dim)}, not {tuple(shape)}")
+    if t.shape != (batch, heads, tokens, dim):
+        raise ValueError(f"{name} must be [batch, heads, tokens, head_dim] = {(batch, heads, tokens, dim)}, not {tuple(t.shape)}")
     if t.dtype != dtype or t.get_device() != device:
         raise ValueError(f"{name} must be {dtype} on cuda:{device}, not {t.dtype} on {t.device}")
     sb, sh, st, sd = t.stride()
@@ -534,11 +551,7 @@ def _rows(t, name, dtype, device, batch, heads, tokens, dim) -> bytes:
     return _pack_rows(t.data_ptr(), sb if batch > 1 else 0, sh if heads > 1 else 0, st if tokens > 1 else 0)
 
 
-_pack_rows = struct.Struct("@Pqqq").pack                 # tq_rows
-_pack_scores = struct.Struct("@ffPiPPPP").pack           # tq_kv8_scores
-
-
-def _array(t, name, dtype, device, *shape) -> Optional[int]:
+def _array(t, name, dtype, device, shape) -> Optional[int]:
     """Pointer of a small contiguous argument (lengths, tables, slopes), or None."""
     if t is None:
         return None
@@ -577,27 +590,34 @@ class Rope:
 def tq_kv8_append(cache: "KV8Cache", layer, k, v, seq_lens, block_table=None, max_blocks=0, new_lens=None, rope=None,
                   positions=None, stream=None):
     """Append k, v [batch, kv heads, n_new, head_dim] (views in any order of the first three axes) at seq_lens."""
-    device, i32 = cache.index, _torch().int32
+    t, device = _kv8(), cache.index
+    if t.device() != device:
+        with _torch().cuda.device(device):
+            return tq_kv8_append(cache, layer, k, v, seq_lens, block_table, max_blocks, new_lens, rope, positions, stream)
     if k.dim() != 4:
         raise ValueError("k must be [batch, heads, tokens, head_dim]")
     batch, _, n_new, _ = k.shape
-    dtype = k.dtype
-    heads, dim = cache.num_kv_heads, cache.head_dim
+    dtype, i32, heads, dim = k.dtype, t.i32, cache.num_kv_heads, cache.head_dim
+    code = t.codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
     if rope is not None and rope.device != device:
         raise ValueError(f"rope must be on cuda:{device}")
-    with cache.on_device():
-        check(lib().tq_kv8_append(
-            cache.ref, layer, _rows(k, "k", dtype, device, batch, heads, n_new, dim),
-            _rows(v, "v", dtype, device, batch, heads, n_new, dim), _kv8_dtype(dtype), batch, n_new,
-            _array(seq_lens, "seq_lens", i32, device, batch), _array(new_lens, "new_lens", i32, device, batch),
-            _array(block_table, "block_table", i32, device, batch, max_blocks), max_blocks,
-            rope.address if rope is not None else None, _array(positions, "positions", i32, device, batch, n_new),
-            _stream(stream)), "tq_kv8_append")
+    per = (batch,)
+    status = t.append(
+        cache.ref, layer, _rows(k, "k", dtype, device, batch, heads, n_new, dim),
+        _rows(v, "v", dtype, device, batch, heads, n_new, dim), code, batch, n_new,
+        _array(seq_lens, "seq_lens", i32, device, per), _array(new_lens, "new_lens", i32, device, per),
+        _array(block_table, "block_table", i32, device, (batch, max_blocks)), max_blocks,
+        rope.address if rope is not None else None, _array(positions, "positions", i32, device, (batch, n_new)),
+        _raw_stream(t, stream, device))
+    if status:
+        check(status, "tq_kv8_append")
 
 
 def tq_kv8_workspace_bytes(cache: "KV8Cache", batch, num_q_heads, q_len, max_seq_len) -> int:
     n = ctypes.c_size_t()
-    with cache.on_device():
+    with _torch().cuda.device(cache.index):
         check(lib().tq_kv8_workspace_bytes(cache.ref, batch, num_q_heads, q_len, max_seq_len, ctypes.byref(n)),
               "tq_kv8_workspace_bytes")
     return n.value
@@ -611,53 +631,46 @@ def tq_kv8_attention(cache: "KV8Cache", layer, q, seq_lens, block_table=None, ma
     Without `out`, rows behind q_lens are zero. Without `workspace`, one is taken from torch's allocator on the
     current stream, so give one where `stream` is another.
     """
-    torch = _torch()
-    device, i32 = cache.index, torch.int32
+    t, device = _kv8(), cache.index
+    if t.device() != device:
+        with _torch().cuda.device(device):
+            return tq_kv8_attention(cache, layer, q, seq_lens, block_table, max_blocks, max_seq_len, out, workspace,
+                                    q_lens, scale, softcap, slopes, window, prefix_lens, doc_starts, rope, positions,
+                                    stream)
     if q.dim() != 4:
         raise ValueError("q must be [batch, heads, tokens, head_dim]")
     batch, heads, q_len, _ = q.shape
-    dtype, dim = q.dtype, cache.head_dim
+    dtype, i32, dim = q.dtype, t.i32, cache.head_dim
+    code = t.codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
     qr = _rows(q, "q", dtype, device, batch, heads, q_len, dim)
-    code = _kv8_dtype(dtype)
     if out is None:
-        out = torch.empty_like(q) if q_lens is None else torch.zeros_like(q)
+        out = _torch().empty_like(q) if q_lens is None else _torch().zeros_like(q)
     if rope is not None and rope.device != device:
         raise ValueError(f"rope must be on cuda:{device}")
-    sc = None
-    if scale or softcap or window or rope is not None or slopes is not None or prefix_lens is not None or doc_starts is not None:
-        sc = _pack_scores(scale, softcap, _array(slopes, "slopes", torch.float32, device, heads) or 0, window,
-                          _array(prefix_lens, "prefix_lens", i32, device, batch) or 0,
-                          _array(doc_starts, "doc_starts", i32, device, batch, q_len) or 0,
+    per, each, sc = (batch,), (batch, q_len), None
+    if rope is not None or scale or softcap or window or slopes is not None or prefix_lens is not None or doc_starts is not None:
+        sc = _pack_scores(scale, softcap, _array(slopes, "slopes", t.f32, device, (heads,)) or 0, window,
+                          _array(prefix_lens, "prefix_lens", i32, device, per) or 0,
+                          _array(doc_starts, "doc_starts", i32, device, each) or 0,
                           rope.address if rope is not None else 0,
-                          _array(positions, "positions", i32, device, batch, q_len) or 0)
-    with cache.on_device():
-        if workspace is None:
-            n = tq_kv8_workspace_bytes(cache, batch, heads, q_len, max_seq_len)
-            workspace = torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
-        elif workspace.get_device() != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on cuda:{device}")
-        check(lib().tq_kv8_attention(
-            cache.ref, layer, qr, code, batch, heads, q_len, _array(seq_lens, "seq_lens", i32, device, batch),
-            _array(q_lens, "q_lens", i32, device, batch),
-            _array(block_table, "block_table", i32, device, batch, max_blocks), max_blocks, max_seq_len, sc,
-            _rows(out, "out", dtype, device, batch, heads, q_len, dim),
-            workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)),
-            "tq_kv8_attention")
+                          _array(positions, "positions", i32, device, each) or 0)
+    if workspace is None:
+        n = tq_kv8_workspace_bytes(cache, batch, heads, q_len, max_seq_len)
+        workspace = _torch().empty(n, dtype=_torch().uint8, device=cache.device) if n else None
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{device}")
+    status = t.attention(
+        cache.ref, layer, qr, code, batch, heads, q_len, _array(seq_lens, "seq_lens", i32, device, per),
+        _array(q_lens, "q_lens", i32, device, per),
+        _array(block_table, "block_table", i32, device, (batch, max_blocks)), max_blocks, max_seq_len, sc,
+        _rows(out, "out", dtype, device, batch, heads, q_len, dim),
+        workspace.data_ptr() if workspace is not None else None, workspace.nbytes if workspace is not None else 0,
+        _raw_stream(t, stream, device))
+    if status:
+        check(status, "tq_kv8_attention")
     return out
-
-
-class _Here:
-    """Nothing to switch: the cache's device is the current one."""
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *_):
-        return False
-
-
-_HERE = _Here()
 
 
 class KV8Cache:
@@ -695,10 +708,6 @@ class KV8Cache:
                                  k_codes.stride(0), k_scales.stride(0), self.num_layers, self.num_blocks,
                                  self.block_tokens, self.num_kv_heads, self.head_dim, format)
         self.ref = ctypes.byref(self.desc)
-
-    def on_device(self):
-        torch = _torch()
-        return _HERE if torch.cuda.current_device() == self.index else torch.cuda.device(self.device)
 
     @property
     def nbytes(self) -> int:

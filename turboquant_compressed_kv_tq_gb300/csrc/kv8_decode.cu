@@ -668,7 +668,8 @@ cudaError_t launch_t(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
     using S = Shape<D, NT>;
     constexpr bool kFine = !std::is_same<T, __nv_bfloat16>::value;
     const int smem = S::kSmem + S::kRows * D * 2 * (kFine ? 2 : 1);
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, NT, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(decode_kernel<T, D, NT, I8>, smem, allowed);
     if (e != cudaSuccess) return e;
     decode_kernel<T, D, NT, I8><<<p.ctas, 32 * S::kWarps, smem, s>>>(a);
     g_launches.fetch_add(1, std::memory_order_relaxed);

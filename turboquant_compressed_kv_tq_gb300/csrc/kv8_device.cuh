@@ -12,6 +12,20 @@
 namespace tq {
 namespace kv8 {
 
+// Let `kernel` (this one instance of it) have `smem` bytes of dynamic shared
+// memory, once on each device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int smem, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 // ------------------------------------------------------------------ inputs
 
 // 8 consecutive elements (16-byte aligned) as fp32.

@@ -600,7 +600,8 @@ template <typename T, int D, bool I8, bool MOD>
 cudaError_t launch_m(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
     using S = Shape<D>;
     static_assert(S::kSmem <= 227 * 1024 - 4096, "shared memory");
-    const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<T, D, I8, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(prefill_kernel<T, D, I8, MOD>, S::kSmem, allowed);
     if (e != cudaSuccess) return e;
     prefill_kernel<T, D, I8, MOD><<<dim3(p.groups, a.pool.H, a.batch), kThreads, S::kSmem, s>>>(a);
     g_launches.fetch_add(1, std::memory_order_relaxed);
