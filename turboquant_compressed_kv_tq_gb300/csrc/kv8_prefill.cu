@@ -4,15 +4,16 @@
 // A CTA owns kHalves x 128 query rows of one KV head (row r = l G + g: query l,
 // head g of the group, so that neighbouring rows see nearly the same keys) and
 // walks tiles of kT tokens (flash attention: one pass, running reference M and
-// sum l per row). Four kinds of warps:
-//   convert  4 warps: codes from global memory to registers (16 bytes a lane, a
-//            tile ahead), to fp16, to the operands in shared memory: keys and values alike as
+// sum l per row). Two kinds of warps, twelve of them, so that a thread has 168
+// registers and a row of scores fits:
+//   convert  4 warps: codes from global memory (cp.async into a place of each lane's own,
+//            a tile ahead) to fp16, to the operands in shared memory: keys and values alike as
 //            [8 tokens x 8 coordinates] core matrices, which are K-major for S = Q K^T and
 //            MN-major for O += P V, so nothing is transposed
-//   mma      1 thread: S = Q K^T (operands in shared memory, S in TMEM), O += P V (P in TMEM)
 //   softmax  4 warps a half, one row a thread: S from TMEM, masks, p = 2^(u - M)
 //            to TMEM as fp16, the row's sum; O is rescaled in TMEM only when a score passes
-//            the reference by 8 (log2 units)
+//            the reference by 8 (log2 units). One thread of each half issues its MMAs where it
+//            would wait for them: O += P V (P in TMEM), then the next S = Q K^T
 // With two halves one's softmax runs while the tensor cores work for the other;
 // with one (head_dim 256, whose O fills half of TMEM) the scores of the next tile
 // are computed ahead into a second buffer.
@@ -37,8 +38,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -1e30f;
 constexpr float kGap = 8.0f;
-// 8 softmax warps, 4 converting ones, 1 for the MMAs: 152 registers a thread, which hold a row of 128 scores
-constexpr int kConvThreads = 128, kThreads = 416;
+constexpr int kConvThreads = 128, kThreads = 256 + kConvThreads;
 
 template <int D>
 struct Shape {
@@ -47,7 +47,8 @@ struct Shape {
     static constexpr int kT = D == 256 ? 64 : 128;         // tokens of a tile
     static constexpr int kOperand = kT * D * 2;            // bytes of a tile's keys or values as fp16
     static constexpr int kVOff = 0, kKOff = 2 * kOperand, kQOff = 4 * kOperand;
-    static constexpr int kSmem = kQOff + kRows * D * 2;
+    static constexpr int kRawOff = kQOff + kRows * D * 2, kRaw = kT * D;   // a tile's codes, keys then values
+    static constexpr int kSmem = kRawOff + 2 * kRaw;
     // TMEM columns: O, S and P of half (or tile parity) x
     static constexpr int kO = 0, kS = kHalves * D, kSStep = kT;
     // P over the scores it comes from where TMEM is full (D 128), else apart
@@ -96,6 +97,21 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
+}
+
+// 16 bytes to shared memory, not by way of the L1 cache: next to 200 KB of shared
+// memory it has too few lines for what is on its way.
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int K>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(K) : "memory"); }
+
 struct Tiles {
     int n1, first, n2;
     __device__ __forceinline__ int at(int i) const { return i < n1 ? i : first + (i - n1); }
@@ -114,13 +130,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     constexpr int kT = S::kT, kH = S::kHalves;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint64_t s_turns[D / 2];
-    __shared__ __align__(8) uint64_t s_bar[15];
+    __shared__ __align__(8) uint64_t s_bar[17];
     __shared__ float s_fac[S::kRows];
     __shared__ TileInfo s_info[4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     uint64_t *k_full = s_bar, *k_free = s_bar + 2, *v_full = s_bar + 4, *v_free = s_bar + 6;
-    uint64_t *s_ready = s_bar + 8, *p_ready = s_bar + 10, *o_done = s_bar + 12, *drained = s_bar + 14;
+    uint64_t *s_ready = s_bar + 8, *p_ready = s_bar + 10, *o_done = s_bar + 12, *drained = s_bar + 14, *turn = s_bar + 15;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Pool& P = A.pool;
     // the longest rows first: the last wave then holds short ones
@@ -160,8 +176,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     tiles.n2 = p_max < 0 || lo_min > p_max ? 0 : max(0, p_max / kT + 1 - tiles.first);
     const int n_tiles = tiles.count();
 
+    const bool two = kH == 2 && rows > 128;   // the second half has rows
+
     // ---------------- set up: TMEM, barriers, the queries (rotated, scaled by a power of two, fp16)
-    if (warp == 12) {
+    if (warp == 8) {
         tc::tmem_alloc(&s_tmem, 512);
         tc::tmem_relinquish();
     }
@@ -169,13 +187,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&k_full[s], kConvThreads / 32);
             tc::mbar_init(&v_full[s], kConvThreads / 32);
-            tc::mbar_init(&k_free[s], 1);
-            tc::mbar_init(&v_free[s], 1);
+            tc::mbar_init(&k_free[s], two ? 2 : 1);   // one for each half
+            tc::mbar_init(&v_free[s], two ? 2 : 1);
             tc::mbar_init(&s_ready[s], 1);
             tc::mbar_init(&p_ready[s], 4);
             tc::mbar_init(&o_done[s], 1);
+            tc::mbar_init(&turn[s], 1);
         }
-        tc::mbar_init(drained, 1);
+        tc::mbar_init(drained, two ? 2 : 1);
         tc::mbar_fence_init();
         s_fail = 0;
     }
@@ -222,8 +241,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const bool two = kH == 2 && rows > 128;   // the second half has rows
-
     if (warp < 8) {
         // ================================================= softmax
         const int half = warp >> 2;
@@ -236,12 +253,61 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const int rr = grp * S::kRows + min(row, rows - 1);
         const int l_row = min(rr / A.G, nq - 1);
         if (mine && n_tiles > 0) {
+            // the half's MMAs, issued by its first thread
+            constexpr uint32_t id_s = tc::idesc_f16_f32(128, kT);
+            constexpr uint32_t id_o = tc::idesc_f16_f32(128, D) | (1u << 16);   // B is MN-major: coordinates contiguous
+            constexpr uint32_t kRowStep = (D / 8) * 128;                        // bytes between groups of 8 rows
+            const bool issuer = (warp & 3) == 0 && lane == 0;
+            const uint32_t base = tc::smem_addr(smem);
+            const int x = kH == 2 ? half : 0;
+            // S of tile j into its buffer
+            auto scores = [&](int j) {
+                const int st = j & 1, buf = kH == 2 ? half : st;
+                if (!arrived(&k_full[st], (j >> 1) & 1)) return false;
+                tc::tc_fence_after();
+                const uint64_t q = tc::smem_desc(base + S::kQOff + x * 128 * D * 2, 128, kRowStep);
+                const uint64_t k = tc::smem_desc(base + S::kKOff + st * S::kOperand, 128, kRowStep);
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) tc::mma_f16(tmem + S::kS + buf * S::kSStep, q + 16 * s, k + 16 * s, id_s, s > 0);
+                tc::mma_commit(&s_ready[buf]);
+                tc::mma_commit(&k_free[st]);
+                return true;
+            };
+            // O += P V of tile j
+            auto values = [&](int j) {
+                const int st = j & 1, buf = kH == 2 ? half : st;
+                if (!arrived(&v_full[st], (j >> 1) & 1)) return false;
+                // kH == 1: one barrier a buffer, as the next tile's P may be there too
+                if (!arrived(&p_ready[buf], kH == 2 ? j & 1 : (j >> 1) & 1)) return false;
+                tc::tc_fence_after();
+                const uint64_t v = tc::smem_desc(base + S::kVOff + st * S::kOperand, kRowStep, 128);
+                const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
+                const uint32_t o = tmem + S::kO + x * D, p = tmem + S::kP + buf * S::kPStep;
+                if (j == 0) tc::mma_f16_ta_w<false>(o, p, lo, hi, id_o);
+                else tc::mma_f16_ta_w<true>(o, p, lo, hi, id_o);
+#pragma unroll
+                for (int s = 1; s < kT / 16; ++s) tc::mma_f16_ta_w<true>(o, p + 8 * s, lo + s * (2 * kRowStep >> 4), hi, id_o);
+                tc::mma_commit(&v_free[st]);
+                if (kH == 1 || j + 1 == n_tiles) tc::mma_commit(&o_done[x]);
+                return true;
+            };
+            // the halves take turns, so that one's softmax runs while the tensor cores work for the other
+            auto my_turn = [&](int j) { return !two || (half == 0 ? j == 0 || arrived(&turn[0], (j - 1) & 1) : arrived(&turn[1], j & 1)); };
+            auto pass_on = [&]() {
+                if (two) tc::mbar_arrive(&turn[half ^ 1]);
+            };
+            if (issuer) {
+                ok = my_turn(0) && scores(0);
+                pass_on();
+                if (kH == 1 && ok && n_tiles > 1) ok = scores(1);
+            }
+            ok = __all_sync(0xffffffffu, ok);
             const Sight sight = sight_of(l_row);
             const int p_min = __reduce_min_sync(0xffffffffu, sight.p), lo_max = __reduce_max_sync(0xffffffffu, sight.lo);
             const float fac = s_fac[min(row, S::kRows - 1)];
             const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
             const float slope = MOD && A.slopes ? A.slopes[h * A.G + rr % A.G] * kLog2e : 0.0f;
-            for (int i = 0; i < n_tiles; ++i) {
+            for (int i = 0; i < n_tiles && ok; ++i) {
                 const int t0 = tiles.at(i) * kT;
                 const int sb = kH == 2 ? half : i & 1;                    // buffer of S and P
                 ok = arrived(&s_ready[sb], kH == 2 ? i & 1 : (i >> 1) & 1);
@@ -254,14 +320,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 // 64 columns of the row's scores, k a multiple of 64: cap and bias applied, unseen ones -inf
                 auto finish = [&](uint32_t (&sr)[64], int k) {
                     if constexpr (MOD) {
-                        const float from = static_cast<float>(t0 + k - sight.p);
+                        if (A.cap > 0.0f) {   // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+                            const float k2 = kf * cap_in;
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) {
-                            const float s = __uint_as_float(sr[e]) * kf;
-                            float y = s * kLog2e;
-                            if (A.cap > 0.0f) y = fmaf(-2.0f * cap2, rcp(1.0f + ex2(s * cap_in)), cap2);
-                            if (A.slopes) y -= slope * fabsf(from + static_cast<float>(e));
-                            sr[e] = __float_as_uint(y);
+                            for (int e = 0; e < 64; ++e)
+                                sr[e] = __float_as_uint(fmaf(-2.0f * cap2, rcp(1.0f + ex2(__uint_as_float(sr[e]) * k2)), cap2));
+                        } else {
+                            const float k2 = kf * kLog2e;
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) sr[e] = __float_as_uint(__uint_as_float(sr[e]) * k2);
+                        }
+                        if (A.slopes) {
+                            const float from = static_cast<float>(t0 + k - sight.p);
+#pragma unroll
+                            for (int e = 0; e < 64; ++e)
+                                sr[e] = __float_as_uint(fmaf(-slope, fabsf(from + static_cast<float>(e)), __uint_as_float(sr[e])));
                         }
                     }
                     if (!open) {
@@ -282,30 +355,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     }
                 };
                 auto largest = [&](const uint32_t (&sr)[64]) {
-                    float x0 = __uint_as_float(sr[0]), x1 = __uint_as_float(sr[1]);
+                    float x[4];
 #pragma unroll
-                    for (int e = 2; e < 64; e += 2) {
-                        x0 = fmaxf(x0, __uint_as_float(sr[e]));
-                        x1 = fmaxf(x1, __uint_as_float(sr[e + 1]));
+                    for (int q = 0; q < 4; ++q) {
+                        x[q] = max3(sr[16 * q], sr[16 * q + 1], sr[16 * q + 2]);
+#pragma unroll
+                        for (int e = 3; e < 15; e += 2) x[q] = max3(__float_as_uint(x[q]), sr[16 * q + e], sr[16 * q + e + 1]);
                     }
-                    return fmaxf(x0, x1);
+                    x[0] = max3(__float_as_uint(x[0]), sr[15], sr[31]);
+                    x[1] = max3(__float_as_uint(x[1]), sr[47], sr[63]);
+                    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                 };
-                // 128 scores are more registers than a thread has: the upper 64 are
-                // looked at for the maximum, and read again once the lower are done
+                // a row at once would be 128 registers: the upper 64 scores are looked at
+                // for the maximum, and read again once the lower are done
                 const uint32_t t_s = t_row + S::kS + sb * S::kSStep;
                 uint32_t sr[64];
                 float top = -INFINITY;
-                if constexpr (kT == 128) {
-                    tc::tmem_ld(t_s + 64, sr);
-                    if (MOD || !open) {
-                        finish(sr, 64);
-                        tc::tmem_st(t_s + 64, sr);
-                    }
-                    top = largest(sr);
+#pragma unroll 1   // (unrolled, the two halves' registers would live side by side)
+                for (int k = kT - 64; k >= 0; k -= 64) {
+                    tc::tmem_ld(t_s + k, sr);
+                    finish(sr, k);
+                    if (k > 0 && (MOD || !open)) tc::tmem_st(t_s + k, sr);
+                    top = fmaxf(top, largest(sr));
                 }
-                tc::tmem_ld(t_s, sr);
-                finish(sr, 0);
-                top = fmaf(fmaxf(top, largest(sr)), f, lv);
+                top = fmaf(top, f, lv);
                 const bool pass = top > m + kGap;
                 if (kH == 1 && i > 0) {   // every phase in its turn: a wait by parity tells neighbouring phases apart, no others
                     ok = arrived(&o_done[0], (i - 1) & 1);
@@ -319,18 +392,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     l_sum *= alpha;
                     if (i > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t v[32];
-                            tc::tmem_ld(t_o + 32 * c, v);
+                        for (int c = 0; c < D / 16; ++c) {
+                            float v[16];
+                            tc::tmem_ld16(t_o + 16 * c, v);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-                            tc::tmem_st(t_o + 32 * c, v);
+                            for (int e = 0; e < 16; ++e) v[e] *= alpha;
+                            tc::tmem_st16(t_o + 16 * c, v);
                         }
                     }
                 }
                 const uint64_t f2 = pack2(f, f), o2 = pack2(lv - m, lv - m);
                 uint64_t sum0 = 0, sum1 = 0;
-                auto weights = [&](int k) {   // of the 64 scores in sr
+#pragma unroll 1
+                for (int k = 0; k < kT / 64; ++k) {
+                    if (k == 1) tc::tmem_ld(t_s + 64, sr);
 #pragma unroll
                     for (int n = 0; n < 64; n += 32) {
                         uint32_t pr[16];
@@ -345,17 +420,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             pr[e / 2] = pack_out<__half>(a, c);
                             pr[e / 2 + 1] = pack_out<__half>(d, g);
                         }
-                        tc::tmem_st16u(t_row + S::kP + sb * S::kPStep + (k + n) / 2, pr);
+                        tc::tmem_st16u(t_row + S::kP + sb * S::kPStep + (64 * k + n) / 2, pr);
                     }
-                };
-                weights(0);
-                if constexpr (kT == 128) {
-                    tc::tmem_ld(t_s + 64, sr);
-                    weights(64);
                 }
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&p_ready[sb]);
+                if (issuer) {
+                    ok = my_turn(i + 1) && values(i);
+                    const int next = kH == 2 ? i + 1 : i + 2;
+                    if (ok && next < n_tiles) ok = scores(next);
+                    pass_on();
+                }
+                ok = __all_sync(0xffffffffu, ok);
                 float a, c, d, g;
                 unpack2(sum0, a, c);
                 unpack2(sum1, d, g);
@@ -366,6 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 s_fail = 1;
                 atomicOr(A.err, TQ_DEVERR_TIMEOUT);
             }
+            if (issuer) {   // nothing is in flight when the CTA ends
+                tc::mma_commit(drained);
+                (void)arrived(drained, 0);
+            }
+            __syncwarp();
             tc::tc_fence_after();
         }
         // ---------------- the rows out, once every copy of s_fail is in
@@ -392,58 +474,73 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 }
             }
         }
-    } else if (warp < 12) {
+    } else {
         // ================================================= convert
         const int w = warp - 8;
         constexpr int CQ = D / 64;               // quarters of 64 coordinates: a unit is a lane's 16 bytes of one
         constexpr int TG = S::kUnits / CQ;       // token groups of a warp
         const int64_t unit_bytes = static_cast<int64_t>(P.BT) * D;
         const int tok = lane & 7, ch = lane >> 3;
-        // lane g < kGroups holds the block and scales of the tile's group g
-        int id = -1, kx = -64, vx = -64;
-        auto look_up = [&](int i) {
-            id = -1;
-            kx = vx = -64;
-            const int t = tiles.at(i) * kT + 8 * lane;
-            if (lane < S::kGroups && t < N && (t <= p_max || t < pre)) {
-                const int lb = t >> P.bt_shift;
-                const bool seen = ((lb << P.bt_shift) + P.BT > lo_min) || (lb << P.bt_shift) < pre;
-                if (seen) {
-                    const int64_t x = P.table ? P.table[b * static_cast<int64_t>(P.max_blocks) + lb] : b * static_cast<int64_t>(P.max_blocks) + lb;
-                    if (x >= 0 && x < P.num_blocks) {
-                        id = static_cast<int>(x);
-                        kx = static_cast<int>(P.kx[x * P.H + h]) - 127;
-                        vx = static_cast<int>(P.vx[x * P.H + h]) - 127;
-                    } else {
-                        atomicOr(A.err, TQ_DEVERR_BLOCK);
-                    }
+        // lane g < kGroups holds the block and scale bytes of the tile's group g. Looked up in two steps, each
+        // a tile before what needs it: the block table's entry, then the scales
+        struct Found {
+            int id, kx, vx;
+        };
+        auto seen = [&](int i) {
+            if (i >= n_tiles || lane >= S::kGroups) return false;
+            const int t = tiles.at(i) * kT + 8 * lane, first = t & ~(P.BT - 1);
+            return t < N && (t <= p_max || t < pre) && (first + P.BT > lo_min || first < pre);
+        };
+        auto entry = [&](int i) {
+            const int lb = seen(i) ? (tiles.at(i) * kT + 8 * lane) >> P.bt_shift : 0;
+            const int64_t at = b * static_cast<int64_t>(P.max_blocks) + lb;
+            return P.table ? P.table[at] : static_cast<int>(at);
+        };
+        auto look_up = [&](int i, int e) {
+            Found f{-1, 0, 0};
+            if (seen(i)) {
+                if (e >= 0 && e < P.num_blocks) {
+                    f.id = e;
+                    f.kx = P.kx[static_cast<int64_t>(e) * P.H + h];
+                    f.vx = P.vx[static_cast<int64_t>(e) * P.H + h];
+                } else {
+                    atomicOr(A.err, TQ_DEVERR_BLOCK);
                 }
             }
+            return f;
         };
-        // unit k of a warp: group w + 4 (k / CQ), bytes 64 (k % CQ) + 16 ch of token tok
-        auto load = [&](uint4 (&x)[S::kUnits], const uint8_t* codes, int i) {
+        // unit k of a warp: group w + 4 (k / CQ), bytes 64 (k % CQ) + 16 ch of token tok (of the block's own memory
+        // behind the sequence's end, and of block 0 where there is no block: zeroed below)
+        unsigned char* raw = smem + S::kRawOff + 16 * (32 * w + lane);   // this lane's units, 2 KB apart
+        auto load = [&](int v, const uint8_t* codes, int i, int id) {
             const int t0 = tiles.at(i) * kT;
-#pragma unroll
-            for (int q = 0; q < TG; ++q) {
-                const int g = w + 4 * q, t = t0 + 8 * g + tok;
-                const int gid = __shfl_sync(0xffffffffu, id, g);
-                const uint8_t* p = codes + (static_cast<int64_t>(max(gid, 0)) * P.H + h) * unit_bytes + static_cast<int64_t>(t & (P.BT - 1)) * D + 16 * ch;
-#pragma unroll
-                for (int c = 0; c < CQ; ++c)
-                    x[q * CQ + c] = gid >= 0 && t < N ? __ldg(reinterpret_cast<const uint4*>(p + 64 * c)) : make_uint4(0, 0, 0, 0);
-            }
-        };
-        // the codes times 2^(their group's exponent - ref), as fp16
-        auto convert = [&](const uint4 (&x)[S::kUnits], int ex, int ref, unsigned char* dst) {
+            const uint32_t dst = tc::smem_addr(raw) + v * S::kRaw;
 #pragma unroll
             for (int q = 0; q < TG; ++q) {
                 const int g = w + 4 * q;
+                const int gid = max(__shfl_sync(0xffffffffu, id, g), 0);
+                const uint8_t* p = codes + (static_cast<int64_t>(gid) * P.H + h) * unit_bytes + ((t0 + 8 * g + tok) & (P.BT - 1)) * D + 16 * ch;
+#pragma unroll
+                for (int c = 0; c < CQ; ++c) copy_async(dst + (q * CQ + c) * 2048, p + 64 * c);
+            }
+            copies_close();
+        };
+        // the codes times 2^(their group's exponent - ref), as fp16 (`left`: tokens that the sequence still has from
+        // the tile's first on; `id`: the groups' blocks)
+        auto convert = [&](int v, int ex, int ref, int id, int left, unsigned char* dst) {
+            const bool clean = left >= kT && __all_sync(0xffffffffu, lane >= S::kGroups || id >= 0);
+#pragma unroll
+            for (int q = 0; q < TG; ++q) {
+                const int g = w + 4 * q;
+                const bool here = clean || (__shfl_sync(0xffffffffu, id, g) >= 0 && 8 * g + tok < left);
                 const int down = max(__shfl_sync(0xffffffffu, ex, g) - ref, -25);
                 const __half mul = __float2half_rn(down < -24 ? 0.0f : exp2i(down));
                 const __half2 mul2 = __half2(mul, mul);
 #pragma unroll
                 for (int c = 0; c < CQ; ++c) {
-                    const uint32_t in[4] = {x[q * CQ + c].x, x[q * CQ + c].y, x[q * CQ + c].z, x[q * CQ + c].w};
+                    uint4 x = *reinterpret_cast<const uint4*>(raw + v * S::kRaw + (q * CQ + c) * 2048);
+                    if (!here) x = make_uint4(0, 0, 0, 0);
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
                     uint32_t y[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -460,146 +557,61 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         };
         bool ok = true;
         if (n_tiles > 0) {
-            uint4 kr[S::kUnits], vr[S::kUnits];
-            look_up(0);
-            load(kr, P.kc, 0);
+            const int e0 = entry(0), e1 = entry(1);
+            int e2 = entry(2);
+            Found now = look_up(0, e0), next = look_up(1, e1);
+            load(0, P.kc, 0, now.id);
+            load(1, P.vc, 0, now.id);
             for (int i = 0; i < n_tiles; ++i) {
-                const int st = i & 1;
-                load(vr, P.vc, i);
+                const int st = i & 1, t0 = tiles.at(i) * kT;
+                const Found after = look_up(i + 2, e2);
+                e2 = entry(i + 3);
+                const int kx = now.id < 0 ? -64 : now.kx - 127, vx = now.id < 0 ? -64 : now.vx - 127;
                 const int kref = __reduce_max_sync(0xffffffffu, kx), vref = __reduce_max_sync(0xffffffffu, vx);
-                const int t0 = tiles.at(i) * kT;
                 // groups of no block among those that have tokens
-                const unsigned gone = __ballot_sync(0xffffffffu, lane < S::kGroups && id < 0 && t0 + 8 * lane < N);
-                const int vx_now = vx;
+                const unsigned gone = __ballot_sync(0xffffffffu, lane < S::kGroups && now.id < 0 && t0 + 8 * lane < N);
+                copies_wait<1>();
                 if (i >= 2) ok = arrived(&k_free[st], ((i >> 1) - 1) & 1);
                 if (!ok) break;
                 if (w == 0 && lane == 0) s_info[i & 3] = TileInfo{kref, vref, gone};
-                convert(kr, kx, kref, smem + S::kKOff + st * S::kOperand);
+                convert(0, kx, kref, now.id, N - t0, smem + S::kKOff + st * S::kOperand);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&k_full[st]);
-                if (i + 1 < n_tiles) {
-                    look_up(i + 1);
-                    load(kr, P.kc, i + 1);
-                }
+                if (i + 1 < n_tiles) load(0, P.kc, i + 1, next.id);
+                else copies_close();
+                copies_wait<1>();
                 if (i >= 2) ok = arrived(&v_free[st], ((i >> 1) - 1) & 1);
                 if (!ok) break;
-                convert(vr, vx_now, vref, smem + S::kVOff + st * S::kOperand);
+                convert(1, vx, vref, now.id, N - t0, smem + S::kVOff + st * S::kOperand);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&v_full[st]);
+                if (i + 1 < n_tiles) load(1, P.vc, i + 1, next.id);
+                now = next;
+                next = after;
             }
+            copies_wait<0>();
             if (!ok) {
                 s_fail = 1;
                 atomicOr(A.err, TQ_DEVERR_TIMEOUT);
             }
         }
-    } else {
-        // ================================================= mma
-        if (warp == 12 && lane == 0 && n_tiles > 0) {
-            constexpr uint32_t id_s = tc::idesc_f16_f32(128, kT);
-            constexpr uint32_t id_o = tc::idesc_f16_f32(128, D) | (1u << 16);   // B is MN-major: coordinates contiguous
-            constexpr uint32_t kRowStep = (D / 8) * 128;                        // bytes between groups of 8 rows
-            const uint32_t base = tc::smem_addr(smem);
-            const uint64_t dq = tc::smem_desc(base + S::kQOff, 128, kRowStep);
-            const uint64_t dk = tc::smem_desc(base + S::kKOff, 128, kRowStep);
-            const uint64_t dv = tc::smem_desc(base + S::kVOff, kRowStep, 128);
-            auto scores = [&](int x, int buf, int st) {   // half x's rows with stage st's keys into buffer buf
-                const uint64_t q = dq + static_cast<uint64_t>(x * 128 * D * 2 >> 4), k = dk + static_cast<uint64_t>(st * S::kOperand >> 4);
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) tc::mma_f16(tmem + S::kS + buf * S::kSStep, q + 16 * s, k + 16 * s, id_s, s > 0);
-            };
-            auto values = [&](int x, int buf, int st, bool more) {
-                const uint64_t v = dv + static_cast<uint64_t>(st * S::kOperand >> 4);
-                const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
-                const uint32_t o = tmem + S::kO + x * D, p = tmem + S::kP + buf * S::kPStep;
-#pragma unroll
-                for (int s = 0; s < kT / 16; ++s) {
-                    if (s == 0 && !more) tc::mma_f16_ta_w<false>(o, p, lo, hi, id_o);
-                    else tc::mma_f16_ta_w<true>(o, p + 8 * s, lo + s * (2 * kRowStep >> 4), hi, id_o);
-                }
-            };
-            bool ok = arrived(&k_full[0], 0);
-            tc::tc_fence_after();
-            if constexpr (kH == 2) {
-                const int nh = two ? 2 : 1;
-                if (ok) {
-                    for (int x = 0; x < nh; ++x) {
-                        scores(x, x, 0);
-                        tc::mma_commit(&s_ready[x]);
-                    }
-                    tc::mma_commit(&k_free[0]);
-                }
-                for (int i = 0; i < n_tiles && ok; ++i) {
-                    const int st = i & 1, sn = st ^ 1;
-                    for (int x = 0; x < nh && ok; ++x) {
-                        if (x == 0) ok = arrived(&v_full[st], (i >> 1) & 1);
-                        if (ok) ok = arrived(&p_ready[x], i & 1);
-                        if (!ok) break;
-                        tc::tc_fence_after();
-                        values(x, x, st, i > 0);
-                        if (x == nh - 1) tc::mma_commit(&v_free[st]);
-                        if (i + 1 == n_tiles) {
-                            tc::mma_commit(&o_done[x]);
-                        } else {
-                            if (x == 0) ok = arrived(&k_full[sn], ((i + 1) >> 1) & 1);
-                            if (!ok) break;
-                            tc::tc_fence_after();
-                            scores(x, x, sn);
-                            tc::mma_commit(&s_ready[x]);
-                            if (x == nh - 1) tc::mma_commit(&k_free[sn]);
-                        }
-                    }
-                }
-            } else {
-                if (ok) {
-                    scores(0, 0, 0);
-                    tc::mma_commit(&s_ready[0]);
-                    tc::mma_commit(&k_free[0]);
-                }
-                for (int i = 0; i < n_tiles && ok; ++i) {
-                    const int st = i & 1, sn = st ^ 1;
-                    if (i + 1 < n_tiles) {
-                        ok = arrived(&k_full[sn], ((i + 1) >> 1) & 1);
-                        if (!ok) break;
-                        tc::tc_fence_after();
-                        scores(0, sn, sn);
-                        tc::mma_commit(&s_ready[sn]);
-                        tc::mma_commit(&k_free[sn]);
-                    }
-                    ok = arrived(&v_full[st], (i >> 1) & 1);
-                    if (ok) ok = arrived(&p_ready[st], (i >> 1) & 1);   // one a buffer: the next tile's may be there too
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    values(0, st, st, i > 0);
-                    tc::mma_commit(&v_free[st]);
-                    tc::mma_commit(&o_done[0]);
-                }
-            }
-            if (!ok) {
-                s_fail = 1;
-                atomicOr(A.err, TQ_DEVERR_TIMEOUT);
-            }
-            // nothing is in flight when the CTA ends
-            tc::mma_commit(drained);
-            (void)arrived(drained, 0);
-        }
-        __syncwarp();
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 8) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
     if (tid == 0)
-        for (int s = 0; s < 15; ++s) tc::mbar_inval(&s_bar[s]);
+        for (int s = 0; s < 17; ++s) tc::mbar_inval(&s_bar[s]);
 }
 
 template <typename T, int D, bool I8, bool MOD>
 cudaError_t launch_m(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
     using S = Shape<D>;
-    static_assert(S::kSmem <= 227 * 1024 - 4096, "shared memory");
+    static_assert(S::kSmem <= 227 * 1024 - 2560, "shared memory");
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(prefill_kernel<T, D, I8, MOD>, S::kSmem, allowed);
     if (e != cudaSuccess) return e;
