@@ -4,16 +4,15 @@
 // A CTA owns kHalves x 128 query rows of one KV head (row r = l G + g: query l,
 // head g of the group, so that neighbouring rows see nearly the same keys) and
 // walks tiles of kT tokens (flash attention: one pass, running reference M and
-// sum l per row). Two kinds of warps, twelve of them, so that a thread has 168
-// registers and a row of scores fits:
-//   convert  4 warps: codes from global memory (cp.async into a place of each lane's own,
-//            a tile ahead) to fp16, to the operands in shared memory: keys and values alike as
+// sum l per row). Sixteen warps:
+//   convert  4 for keys, 3 for values: codes from global memory (cp.async into a place of each
+//            lane's own, a tile ahead) to fp16, to the operands in shared memory: both as
 //            [8 tokens x 8 coordinates] core matrices, which are K-major for S = Q K^T and
 //            MN-major for O += P V, so nothing is transposed
-//   softmax  4 warps a half, one row a thread: S from TMEM, masks, p = 2^(u - M)
-//            to TMEM as fp16, the row's sum; O is rescaled in TMEM only when a score passes
-//            the reference by 8 (log2 units). One thread of each half issues its MMAs where it
-//            would wait for them: O += P V (P in TMEM), then the next S = Q K^T
+//   mma      1 thread: S = Q K^T (operands in shared memory, S in TMEM), O += P V (P in TMEM)
+//   softmax  4 a half, one row a thread: S from TMEM, masks, p = 2^(u - M) to TMEM as fp16,
+//            64 columns at a time so that P V begins on the first, the row's sum; O is rescaled
+//            in TMEM only when a score passes the reference by 8 (log2 units)
 // With two halves one's softmax runs while the tensor cores work for the other;
 // with one (head_dim 256, whose O fills half of TMEM) the scores of the next tile
 // are computed ahead into a second buffer.
@@ -38,7 +37,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -1e30f;
 constexpr float kGap = 8.0f;
-constexpr int kConvThreads = 128, kThreads = 256 + kConvThreads;
+constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 15, kThreads = 32 * (kMmaWarp + 1);
 
 template <int D>
 struct Shape {
@@ -56,7 +55,6 @@ struct Shape {
     static constexpr int kP = kPOver ? kS : kS + 2 * kSStep, kPStep = kPOver ? kSStep : kT / 2;
     static_assert((kPOver ? kS + 2 * kSStep : kP + 2 * kPStep) <= 512, "TMEM columns");
     static constexpr int kGroups = kT / 8;                 // groups of 8 tokens
-    static constexpr int kUnits = kT * (D / 16) / kConvThreads;   // 16-byte loads of a converter a tile
 };
 
 // Wait for the phase with this parity; false after about a second.
@@ -136,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     uint64_t *k_full = s_bar, *k_free = s_bar + 2, *v_full = s_bar + 4, *v_free = s_bar + 6;
-    uint64_t *s_ready = s_bar + 8, *p_ready = s_bar + 10, *o_done = s_bar + 12, *drained = s_bar + 14, *turn = s_bar + 15;
+    uint64_t *s_ready = s_bar + 8, *p_ready = s_bar + 10, *o_done = s_bar + 12, *drained = s_bar + 14, *p_second = s_bar + 15;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Pool& P = A.pool;
     // the longest rows first: the last wave then holds short ones
@@ -179,22 +177,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const bool two = kH == 2 && rows > 128;   // the second half has rows
 
     // ---------------- set up: TMEM, barriers, the queries (rotated, scaled by a power of two, fp16)
-    if (warp == 8) {
+    if (warp == kMmaWarp) {
         tc::tmem_alloc(&s_tmem, 512);
         tc::tmem_relinquish();
     }
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            tc::mbar_init(&k_full[s], kConvThreads / 32);
-            tc::mbar_init(&v_full[s], kConvThreads / 32);
-            tc::mbar_init(&k_free[s], two ? 2 : 1);   // one for each half
-            tc::mbar_init(&v_free[s], two ? 2 : 1);
+            tc::mbar_init(&k_full[s], kVWarp - kKWarp);
+            tc::mbar_init(&v_full[s], kMmaWarp - kVWarp);
+            tc::mbar_init(&k_free[s], 1);
+            tc::mbar_init(&v_free[s], 1);
             tc::mbar_init(&s_ready[s], 1);
             tc::mbar_init(&p_ready[s], 4);
+            tc::mbar_init(&p_second[s], 4);
             tc::mbar_init(&o_done[s], 1);
-            tc::mbar_init(&turn[s], 1);
         }
-        tc::mbar_init(drained, two ? 2 : 1);
+        tc::mbar_init(drained, 1);
         tc::mbar_fence_init();
         s_fail = 0;
     }
@@ -253,55 +251,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const int rr = grp * S::kRows + min(row, rows - 1);
         const int l_row = min(rr / A.G, nq - 1);
         if (mine && n_tiles > 0) {
-            // the half's MMAs, issued by its first thread
-            constexpr uint32_t id_s = tc::idesc_f16_f32(128, kT);
-            constexpr uint32_t id_o = tc::idesc_f16_f32(128, D) | (1u << 16);   // B is MN-major: coordinates contiguous
-            constexpr uint32_t kRowStep = (D / 8) * 128;                        // bytes between groups of 8 rows
-            const bool issuer = (warp & 3) == 0 && lane == 0;
-            const uint32_t base = tc::smem_addr(smem);
-            const int x = kH == 2 ? half : 0;
-            // S of tile j into its buffer
-            auto scores = [&](int j) {
-                const int st = j & 1, buf = kH == 2 ? half : st;
-                if (!arrived(&k_full[st], (j >> 1) & 1)) return false;
-                tc::tc_fence_after();
-                const uint64_t q = tc::smem_desc(base + S::kQOff + x * 128 * D * 2, 128, kRowStep);
-                const uint64_t k = tc::smem_desc(base + S::kKOff + st * S::kOperand, 128, kRowStep);
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) tc::mma_f16(tmem + S::kS + buf * S::kSStep, q + 16 * s, k + 16 * s, id_s, s > 0);
-                tc::mma_commit(&s_ready[buf]);
-                tc::mma_commit(&k_free[st]);
-                return true;
-            };
-            // O += P V of tile j
-            auto values = [&](int j) {
-                const int st = j & 1, buf = kH == 2 ? half : st;
-                if (!arrived(&v_full[st], (j >> 1) & 1)) return false;
-                // kH == 1: one barrier a buffer, as the next tile's P may be there too
-                if (!arrived(&p_ready[buf], kH == 2 ? j & 1 : (j >> 1) & 1)) return false;
-                tc::tc_fence_after();
-                const uint64_t v = tc::smem_desc(base + S::kVOff + st * S::kOperand, kRowStep, 128);
-                const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
-                const uint32_t o = tmem + S::kO + x * D, p = tmem + S::kP + buf * S::kPStep;
-                if (j == 0) tc::mma_f16_ta_w<false>(o, p, lo, hi, id_o);
-                else tc::mma_f16_ta_w<true>(o, p, lo, hi, id_o);
-#pragma unroll
-                for (int s = 1; s < kT / 16; ++s) tc::mma_f16_ta_w<true>(o, p + 8 * s, lo + s * (2 * kRowStep >> 4), hi, id_o);
-                tc::mma_commit(&v_free[st]);
-                if (kH == 1 || j + 1 == n_tiles) tc::mma_commit(&o_done[x]);
-                return true;
-            };
-            // the halves take turns, so that one's softmax runs while the tensor cores work for the other
-            auto my_turn = [&](int j) { return !two || (half == 0 ? j == 0 || arrived(&turn[0], (j - 1) & 1) : arrived(&turn[1], j & 1)); };
-            auto pass_on = [&]() {
-                if (two) tc::mbar_arrive(&turn[half ^ 1]);
-            };
-            if (issuer) {
-                ok = my_turn(0) && scores(0);
-                pass_on();
-                if (kH == 1 && ok && n_tiles > 1) ok = scores(1);
-            }
-            ok = __all_sync(0xffffffffu, ok);
             const Sight sight = sight_of(l_row);
             const int p_min = __reduce_min_sync(0xffffffffu, sight.p), lo_max = __reduce_max_sync(0xffffffffu, sight.lo);
             const float fac = s_fac[min(row, S::kRows - 1)];
@@ -422,17 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         }
                         tc::tmem_st16u(t_row + S::kP + sb * S::kPStep + (64 * k + n) / 2, pr);
                     }
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(k == 0 ? &p_ready[sb] : &p_second[sb]);
                 }
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&p_ready[sb]);
-                if (issuer) {
-                    ok = my_turn(i + 1) && values(i);
-                    const int next = kH == 2 ? i + 1 : i + 2;
-                    if (ok && next < n_tiles) ok = scores(next);
-                    pass_on();
-                }
-                ok = __all_sync(0xffffffffu, ok);
                 float a, c, d, g;
                 unpack2(sum0, a, c);
                 unpack2(sum1, d, g);
@@ -443,11 +385,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 s_fail = 1;
                 atomicOr(A.err, TQ_DEVERR_TIMEOUT);
             }
-            if (issuer) {   // nothing is in flight when the CTA ends
-                tc::mma_commit(drained);
-                (void)arrived(drained, 0);
-            }
-            __syncwarp();
             tc::tc_fence_after();
         }
         // ---------------- the rows out, once every copy of s_fail is in
@@ -474,11 +411,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 }
             }
         }
-    } else {
+    } else if (warp < kMmaWarp) {
         // ================================================= convert
-        const int w = warp - 8;
+        const bool is_v = warp >= kVWarp;
+        const int w = warp - (is_v ? kVWarp : kKWarp), nw = is_v ? kMmaWarp - kVWarp : kVWarp - kKWarp;
+        uint64_t *full = is_v ? v_full : k_full, *free = is_v ? v_free : k_free;
+        const uint8_t* codes = is_v ? P.vc : P.kc;
+        unsigned char* operand = smem + (is_v ? S::kVOff : S::kKOff);
         constexpr int CQ = D / 64;               // quarters of 64 coordinates: a unit is a lane's 16 bytes of one
-        constexpr int TG = S::kUnits / CQ;       // token groups of a warp
+        constexpr int TG = (S::kGroups + 2) / 3;   // token groups of a warp, at most: w, w + nw, ..
         const int64_t unit_bytes = static_cast<int64_t>(P.BT) * D;
         const int tok = lane & 7, ch = lane >> 3;
         // lane g < kGroups holds the block and scale bytes of the tile's group g. Looked up in two steps, each
@@ -509,36 +450,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             }
             return f;
         };
-        // unit k of a warp: group w + 4 (k / CQ), bytes 64 (k % CQ) + 16 ch of token tok (of the block's own memory
-        // behind the sequence's end, and of block 0 where there is no block: zeroed below)
-        unsigned char* raw = smem + S::kRawOff + 16 * (32 * w + lane);   // this lane's units, 2 KB apart
-        auto load = [&](int v, const uint8_t* codes, int i, int id) {
+        // a unit: bytes 64 c + 16 ch of token tok of a group (of the block's own memory behind the sequence's end, and of
+        // block 0 where there is no block: zeroed below)
+        unsigned char* raw = smem + S::kRawOff + (is_v ? S::kRaw : 0) + 16 * lane;   // this lane's units, 512 bytes apart
+        auto load = [&](int i, int id) {
             const int t0 = tiles.at(i) * kT;
-            const uint32_t dst = tc::smem_addr(raw) + v * S::kRaw;
+            const uint32_t dst = tc::smem_addr(raw);
 #pragma unroll
             for (int q = 0; q < TG; ++q) {
-                const int g = w + 4 * q;
+                const int g = w + nw * q;
+                if (g >= S::kGroups) break;
                 const int gid = max(__shfl_sync(0xffffffffu, id, g), 0);
                 const uint8_t* p = codes + (static_cast<int64_t>(gid) * P.H + h) * unit_bytes + ((t0 + 8 * g + tok) & (P.BT - 1)) * D + 16 * ch;
 #pragma unroll
-                for (int c = 0; c < CQ; ++c) copy_async(dst + (q * CQ + c) * 2048, p + 64 * c);
+                for (int c = 0; c < CQ; ++c) copy_async(dst + (g * CQ + c) * 512, p + 64 * c);
             }
             copies_close();
         };
         // the codes times 2^(their group's exponent - ref), as fp16 (`left`: tokens that the sequence still has from
         // the tile's first on; `id`: the groups' blocks)
-        auto convert = [&](int v, int ex, int ref, int id, int left, unsigned char* dst) {
+        auto convert = [&](int ex, int ref, int id, int left, unsigned char* dst) {
             const bool clean = left >= kT && __all_sync(0xffffffffu, lane >= S::kGroups || id >= 0);
 #pragma unroll
             for (int q = 0; q < TG; ++q) {
-                const int g = w + 4 * q;
+                const int g = w + nw * q;
+                if (g >= S::kGroups) break;
                 const bool here = clean || (__shfl_sync(0xffffffffu, id, g) >= 0 && 8 * g + tok < left);
                 const int down = max(__shfl_sync(0xffffffffu, ex, g) - ref, -25);
                 const __half mul = __float2half_rn(down < -24 ? 0.0f : exp2i(down));
                 const __half2 mul2 = __half2(mul, mul);
 #pragma unroll
                 for (int c = 0; c < CQ; ++c) {
-                    uint4 x = *reinterpret_cast<const uint4*>(raw + v * S::kRaw + (q * CQ + c) * 2048);
+                    uint4 x = *reinterpret_cast<const uint4*>(raw + (g * CQ + c) * 512);
                     if (!here) x = make_uint4(0, 0, 0, 0);
                     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
                     uint32_t y[8];
@@ -560,8 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             const int e0 = entry(0), e1 = entry(1);
             int e2 = entry(2);
             Found now = look_up(0, e0), next = look_up(1, e1);
-            load(0, P.kc, 0, now.id);
-            load(1, P.vc, 0, now.id);
+            load(0, now.id);
             for (int i = 0; i < n_tiles; ++i) {
                 const int st = i & 1, t0 = tiles.at(i) * kT;
                 const Found after = look_up(i + 2, e2);
@@ -570,24 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int kref = __reduce_max_sync(0xffffffffu, kx), vref = __reduce_max_sync(0xffffffffu, vx);
                 // groups of no block among those that have tokens
                 const unsigned gone = __ballot_sync(0xffffffffu, lane < S::kGroups && now.id < 0 && t0 + 8 * lane < N);
-                copies_wait<1>();
-                if (i >= 2) ok = arrived(&k_free[st], ((i >> 1) - 1) & 1);
+                copies_wait<0>();
+                if (i >= 2) ok = arrived(&free[st], ((i >> 1) - 1) & 1);
                 if (!ok) break;
-                if (w == 0 && lane == 0) s_info[i & 3] = TileInfo{kref, vref, gone};
-                convert(0, kx, kref, now.id, N - t0, smem + S::kKOff + st * S::kOperand);
+                if (warp == kKWarp && lane == 0) s_info[i & 3] = TileInfo{kref, vref, gone};
+                convert(is_v ? vx : kx, is_v ? vref : kref, now.id, N - t0, operand + st * S::kOperand);
+                if (i + 1 < n_tiles) load(i + 1, next.id);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&k_full[st]);
-                if (i + 1 < n_tiles) load(0, P.kc, i + 1, next.id);
-                else copies_close();
-                copies_wait<1>();
-                if (i >= 2) ok = arrived(&v_free[st], ((i >> 1) - 1) & 1);
-                if (!ok) break;
-                convert(1, vx, vref, now.id, N - t0, smem + S::kVOff + st * S::kOperand);
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&v_full[st]);
-                if (i + 1 < n_tiles) load(1, P.vc, i + 1, next.id);
+                if (lane == 0) tc::mbar_arrive(&full[st]);
                 now = next;
                 next = after;
             }
@@ -597,10 +530,100 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 atomicOr(A.err, TQ_DEVERR_TIMEOUT);
             }
         }
+    } else {
+        // ================================================= mma
+        if (lane == 0 && n_tiles > 0) {
+            constexpr uint32_t id_s = tc::idesc_f16_f32(128, kT);
+            constexpr uint32_t id_o = tc::idesc_f16_f32(128, D) | (1u << 16);   // B is MN-major: coordinates contiguous
+            constexpr uint32_t kRowStep = (D / 8) * 128;                        // bytes between groups of 8 rows
+            const uint32_t base = tc::smem_addr(smem);
+            const uint64_t dq = tc::smem_desc(base + S::kQOff, 128, kRowStep);
+            const uint64_t dk = tc::smem_desc(base + S::kKOff, 128, kRowStep);
+            const uint64_t dv = tc::smem_desc(base + S::kVOff, kRowStep, 128);
+            auto scores = [&](int x, int buf, int st) {   // half x's rows with stage st's keys into buffer buf
+                const uint64_t q = dq + static_cast<uint64_t>(x * 128 * D * 2 >> 4), k = dk + static_cast<uint64_t>(st * S::kOperand >> 4);
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) tc::mma_f16(tmem + S::kS + buf * S::kSStep, q + 16 * s, k + 16 * s, id_s, s > 0);
+                tc::mma_commit(&s_ready[buf]);
+            };
+            // O += P V of 64 tokens, from step `from` on
+            auto values = [&](int x, int buf, int st, int from, bool first) {
+                const uint64_t v = dv + static_cast<uint64_t>(st * S::kOperand >> 4);
+                const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
+                const uint32_t o = tmem + S::kO + x * D, p = tmem + S::kP + buf * S::kPStep;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    if (s == 0 && first) tc::mma_f16_ta_w<false>(o, p, lo, hi, id_o);
+                    else tc::mma_f16_ta_w<true>(o, p + 8 * (from + s), lo + (from + s) * (2 * kRowStep >> 4), hi, id_o);
+                }
+            };
+            bool ok = arrived(&k_full[0], 0);
+            tc::tc_fence_after();
+            if constexpr (kH == 2) {
+                const int nh = two ? 2 : 1;
+                if (ok) {
+                    for (int x = 0; x < nh; ++x) scores(x, x, 0);
+                    tc::mma_commit(&k_free[0]);
+                }
+                for (int i = 0; i < n_tiles && ok; ++i) {
+                    const int st = i & 1, sn = st ^ 1;
+                    for (int x = 0; x < nh && ok; ++x) {
+                        ok = (x > 0 || arrived(&v_full[st], (i >> 1) & 1)) && arrived(&p_ready[x], i & 1);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        values(x, x, st, 0, i == 0);
+                        ok = arrived(&p_second[x], i & 1);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        values(x, x, st, 4, false);
+                        if (x == nh - 1) tc::mma_commit(&v_free[st]);
+                        if (i + 1 == n_tiles) {
+                            tc::mma_commit(&o_done[x]);
+                        } else {
+                            ok = x > 0 || arrived(&k_full[sn], ((i + 1) >> 1) & 1);
+                            if (!ok) break;
+                            tc::tc_fence_after();
+                            scores(x, x, sn);
+                            if (x == nh - 1) tc::mma_commit(&k_free[sn]);
+                        }
+                    }
+                }
+            } else {
+                if (ok) {
+                    scores(0, 0, 0);
+                    tc::mma_commit(&k_free[0]);
+                }
+                for (int i = 0; i < n_tiles && ok; ++i) {
+                    const int st = i & 1, sn = st ^ 1;
+                    if (i + 1 < n_tiles) {
+                        ok = arrived(&k_full[sn], ((i + 1) >> 1) & 1);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        scores(0, sn, sn);
+                        tc::mma_commit(&k_free[sn]);
+                    }
+                    // (one barrier a buffer: the next tile's P may be there too)
+                    ok = arrived(&v_full[st], (i >> 1) & 1) && arrived(&p_ready[st], (i >> 1) & 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    values(0, st, st, 0, i == 0);
+                    tc::mma_commit(&v_free[st]);
+                    tc::mma_commit(&o_done[0]);
+                }
+            }
+            if (!ok) {
+                s_fail = 1;
+                atomicOr(A.err, TQ_DEVERR_TIMEOUT);
+            }
+            // nothing is in flight when the CTA ends
+            tc::mma_commit(drained);
+            (void)arrived(drained, 0);
+        }
+        __syncwarp();
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kMmaWarp) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
