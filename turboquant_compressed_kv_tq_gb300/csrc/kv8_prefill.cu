@@ -422,24 +422,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         constexpr int TG = (S::kGroups + 2) / 3;   // token groups of a warp, at most: w, w + nw, ..
         const int64_t unit_bytes = static_cast<int64_t>(P.BT) * D;
         const int tok = lane & 7, ch = lane >> 3;
-        // lane g < kGroups holds the block and scale bytes of the tile's group g. Looked up in two steps, each
-        // a tile before what needs it: the block table's entry, then the scales
+        // a batch of kPer tiles: lane kGroups j + g holds the block and scale bytes of tile j's group g. Looked up in
+        // two steps, each a batch before what needs it: the block table's entry, then the scales
+        constexpr int kPer = 32 / S::kGroups;
+        const int my_tile = lane / S::kGroups, my_group = lane % S::kGroups;
         struct Found {
             int id, kx, vx;
         };
         auto seen = [&](int i) {
-            if (i >= n_tiles || lane >= S::kGroups) return false;
-            const int t = tiles.at(i) * kT + 8 * lane, first = t & ~(P.BT - 1);
+            if (i >= n_tiles) return false;
+            const int t = tiles.at(i) * kT + 8 * my_group, first = t & ~(P.BT - 1);
             return t < N && (t <= p_max || t < pre) && (first + P.BT > lo_min || first < pre);
         };
-        auto entry = [&](int i) {
-            const int lb = seen(i) ? (tiles.at(i) * kT + 8 * lane) >> P.bt_shift : 0;
+        auto entry = [&](int batch) {
+            const int i = kPer * batch + my_tile;
+            const int lb = seen(i) ? (tiles.at(i) * kT + 8 * my_group) >> P.bt_shift : 0;
             const int64_t at = b * static_cast<int64_t>(P.max_blocks) + lb;
             return P.table ? P.table[at] : static_cast<int>(at);
         };
-        auto look_up = [&](int i, int e) {
+        auto look_up = [&](int batch, int e) {
             Found f{-1, 0, 0};
-            if (seen(i)) {
+            if (seen(kPer * batch + my_tile)) {
                 if (e >= 0 && e < P.num_blocks) {
                     f.id = e;
                     f.kx = P.kx[static_cast<int64_t>(e) * P.H + h];
@@ -454,13 +457,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         // block 0 where there is no block: zeroed below)
         unsigned char* raw = smem + S::kRawOff + (is_v ? S::kRaw : 0) + 16 * lane;   // this lane's units, 512 bytes apart
         auto load = [&](int i, int id) {
-            const int t0 = tiles.at(i) * kT;
+            const int t0 = tiles.at(i) * kT, from = i % kPer * S::kGroups;
             const uint32_t dst = tc::smem_addr(raw);
 #pragma unroll
             for (int q = 0; q < TG; ++q) {
                 const int g = w + nw * q;
                 if (g >= S::kGroups) break;
-                const int gid = max(__shfl_sync(0xffffffffu, id, g), 0);
+                const int gid = max(__shfl_sync(0xffffffffu, id, from + g), 0);
                 const uint8_t* p = codes + (static_cast<int64_t>(gid) * P.H + h) * unit_bytes + ((t0 + 8 * g + tok) & (P.BT - 1)) * D + 16 * ch;
 #pragma unroll
                 for (int c = 0; c < CQ; ++c) copy_async(dst + (g * CQ + c) * 512, p + 64 * c);
@@ -469,14 +472,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         };
         // the codes times 2^(their group's exponent - ref), as fp16 (`left`: tokens that the sequence still has from
         // the tile's first on; `id`: the groups' blocks)
-        auto convert = [&](int ex, int ref, int id, int left, unsigned char* dst) {
-            const bool clean = left >= kT && __all_sync(0xffffffffu, lane >= S::kGroups || id >= 0);
+        auto convert = [&](int ex, int ref, int id, int from, int left, unsigned char* dst) {
+            const bool clean = left >= kT && __all_sync(0xffffffffu, lane - from < 0 || lane - from >= S::kGroups || id >= 0);
 #pragma unroll
             for (int q = 0; q < TG; ++q) {
                 const int g = w + nw * q;
                 if (g >= S::kGroups) break;
-                const bool here = clean || (__shfl_sync(0xffffffffu, id, g) >= 0 && 8 * g + tok < left);
-                const int down = max(__shfl_sync(0xffffffffu, ex, g) - ref, -25);
+                const bool here = clean || (__shfl_sync(0xffffffffu, id, from + g) >= 0 && 8 * g + tok < left);
+                const int down = max(__shfl_sync(0xffffffffu, ex, from + g) - ref, -25);
                 const __half mul = __float2half_rn(down < -24 ? 0.0f : exp2i(down));
                 const __half2 mul2 = __half2(mul, mul);
 #pragma unroll
@@ -501,28 +504,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         bool ok = true;
         if (n_tiles > 0) {
             const int e0 = entry(0), e1 = entry(1);
-            int e2 = entry(2);
+            int e_next = entry(2);
             Found now = look_up(0, e0), next = look_up(1, e1);
             load(0, now.id);
             for (int i = 0; i < n_tiles; ++i) {
-                const int st = i & 1, t0 = tiles.at(i) * kT;
-                const Found after = look_up(i + 2, e2);
-                e2 = entry(i + 3);
+                const int st = i & 1, t0 = tiles.at(i) * kT, from = i % kPer * S::kGroups;
+                const bool mine = lane >= from && lane < from + S::kGroups;
                 const int kx = now.id < 0 ? -64 : now.kx - 127, vx = now.id < 0 ? -64 : now.vx - 127;
-                const int kref = __reduce_max_sync(0xffffffffu, kx), vref = __reduce_max_sync(0xffffffffu, vx);
+                const int kref = __reduce_max_sync(0xffffffffu, mine ? kx : -64), vref = __reduce_max_sync(0xffffffffu, mine ? vx : -64);
                 // groups of no block among those that have tokens
-                const unsigned gone = __ballot_sync(0xffffffffu, lane < S::kGroups && now.id < 0 && t0 + 8 * lane < N);
+                const unsigned gone = __ballot_sync(0xffffffffu, mine && now.id < 0 && t0 + 8 * my_group < N) >> from;
                 copies_wait<0>();
                 if (i >= 2) ok = arrived(&free[st], ((i >> 1) - 1) & 1);
                 if (!ok) break;
                 if (warp == kKWarp && lane == 0) s_info[i & 3] = TileInfo{kref, vref, gone};
-                convert(is_v ? vx : kx, is_v ? vref : kref, now.id, N - t0, operand + st * S::kOperand);
-                if (i + 1 < n_tiles) load(i + 1, next.id);
+                convert(is_v ? vx : kx, is_v ? vref : kref, now.id, from, N - t0, operand + st * S::kOperand);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&full[st]);
-                now = next;
-                next = after;
+                if ((i + 1) % kPer == 0) {
+                    now = next;
+                    const int batch = (i + 1) / kPer;
+                    next = look_up(batch + 1, e_next);
+                    e_next = entry(batch + 2);
+                }
+                if (i + 1 < n_tiles) load(i + 1, now.id);
             }
             copies_wait<0>();
             if (!ok) {
