@@ -134,22 +134,16 @@ __device__ __forceinline__ void chunk_pair(int j, int rot, int inter, int& a, in
     }
 }
 
-// Rotate chunk pair j of a vector at position p; `turns`: the frequencies
-// (shared memory). Products and differences are rounded one by one, as
-// elementwise operations round them.
-__device__ __forceinline__ void rotate_pair(float (&xa)[8], float (&xb)[8], int j, const Rope& r, const uint64_t* turns,
-                                            int p) {
-    if (16 * j >= r.rot) return;
-    const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p));
+// Rotate chunk pair j by `angle(i)`, cos and sin of its pair i < 8. Products and
+// differences are rounded one by one, as elementwise operations round them.
+template <typename F>
+__device__ __forceinline__ void rotate_by(float (&xa)[8], float (&xb)[8], int inter, F&& angle) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float co, si;
-        turn_cos_sin(pos * turns[8 * j + i], co, si);
-        co *= r.scale;
-        si *= r.scale;
+        const float2 cs = angle(i);
         float* u;
         float* w;
-        if (r.inter) {
+        if (inter) {
             u = i < 4 ? &xa[(2 * i) & 7] : &xb[(2 * i) & 7];
             w = i < 4 ? &xa[(2 * i + 1) & 7] : &xb[(2 * i + 1) & 7];
         } else {
@@ -157,9 +151,23 @@ __device__ __forceinline__ void rotate_pair(float (&xa)[8], float (&xb)[8], int 
             w = &xb[i];
         }
         const float x = *u, y = *w;
-        *u = __fsub_rn(__fmul_rn(x, co), __fmul_rn(y, si));
-        *w = __fadd_rn(__fmul_rn(y, co), __fmul_rn(x, si));
+        *u = __fsub_rn(__fmul_rn(x, cs.x), __fmul_rn(y, cs.y));
+        *w = __fadd_rn(__fmul_rn(y, cs.x), __fmul_rn(x, cs.y));
     }
+}
+
+// cos and sin (times the rotation's scale) of frequency `turns` at position p.
+__device__ __forceinline__ float2 angle_at(const Rope& r, uint64_t turns, int p) {
+    float co, si;
+    turn_cos_sin(static_cast<uint64_t>(static_cast<int64_t>(p)) * turns, co, si);
+    return make_float2(co * r.scale, si * r.scale);
+}
+
+// Rotate chunk pair j of a vector at position p; `turns`: the frequencies (shared memory).
+__device__ __forceinline__ void rotate_pair(float (&xa)[8], float (&xb)[8], int j, const Rope& r, const uint64_t* turns,
+                                            int p) {
+    if (16 * j >= r.rot) return;
+    rotate_by(xa, xb, r.inter, [&](int i) { return angle_at(r, turns[8 * j + i], p); });
 }
 
 // ------------------------------------------------------------------ codes

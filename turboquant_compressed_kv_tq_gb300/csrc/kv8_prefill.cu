@@ -128,13 +128,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     constexpr int kT = S::kT, kH = S::kHalves;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint64_t s_turns[D / 2];
-    __shared__ __align__(8) uint64_t s_bar[17];
+    __shared__ __align__(8) uint64_t s_bar[18];
     __shared__ float s_fac[S::kRows];
     __shared__ TileInfo s_info[4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     uint64_t *k_full = s_bar, *k_free = s_bar + 2, *v_full = s_bar + 4, *v_free = s_bar + 6;
-    uint64_t *s_ready = s_bar + 8, *p_ready = s_bar + 10, *o_done = s_bar + 12, *drained = s_bar + 14, *p_second = s_bar + 15;
+    uint64_t *s_ready = s_bar + 8, *p_ready = s_bar + 10, *o_done = s_bar + 12, *drained = s_bar + 14, *p_second = s_bar + 15, *q_ready = s_bar + 17;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Pool& P = A.pool;
     // the longest rows first: the last wave then holds short ones
@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             tc::mbar_init(&o_done[s], 1);
         }
         tc::mbar_init(drained, 1);
+        tc::mbar_init(q_ready, 8);
         tc::mbar_fence_init();
         s_fail = 0;
     }
@@ -202,44 +203,62 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
-    if (n_tiles > 0) {
-        constexpr int J = D / 16;   // chunk pairs of a row: J consecutive lanes
-        const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
-        for (int it = tid; it < S::kRows * J; it += kThreads) {
-            const int r = it / J, j = it % J;
-            const int rr = grp * S::kRows + r, l = rr / A.G;
-            float xa[8] = {}, xb[8] = {};
-            int a0, b0;
-            chunk_pair(j, A.rope.rot, A.rope.inter, a0, b0);
-            if (r < rows && l < nq) {
-                const T* q = static_cast<const T*>(A.q.data) + b * A.q.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.q.sh + l * A.q.st;
-                load8(q + a0, xa);
-                load8(q + b0, xb);
-                if (A.rope.rot > 0)
-                    rotate_pair(xa, xb, j, A.rope, s_turns, A.rope.positions ? A.rope.positions[static_cast<int64_t>(b) * A.L + l] : N - nq + l);
-            }
-            float top = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(xa[i]), fabsf(xb[i])));
-#pragma unroll
-            for (int o = J / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126), 126);
-            const float f = sign * exp2i(-e);
-            uint4 va, vb;
-            va.x = pack_out<__half>(xa[0] * f, xa[1] * f), va.y = pack_out<__half>(xa[2] * f, xa[3] * f);
-            va.z = pack_out<__half>(xa[4] * f, xa[5] * f), va.w = pack_out<__half>(xa[6] * f, xa[7] * f);
-            vb.x = pack_out<__half>(xb[0] * f, xb[1] * f), vb.y = pack_out<__half>(xb[2] * f, xb[3] * f);
-            vb.z = pack_out<__half>(xb[4] * f, xb[5] * f), vb.w = pack_out<__half>(xb[6] * f, xb[7] * f);
-            *reinterpret_cast<uint4*>(smem + S::kQOff + core<D>(r, a0)) = va;
-            *reinterpret_cast<uint4*>(smem + S::kQOff + core<D>(r, b0)) = vb;
-            if (j == 0) s_fac[r] = fabsf(A.scale) * exp2i(e);
-        }
-    }
-    tc::fence_proxy_async_smem();
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
     if (warp < 8) {
+        // ================================================= the queries: rotated, scaled by a power of two, fp16
+        if (n_tiles > 0) {
+            // The heads of a query turn by the same angles: cos and sin of each (query, pair) once, in the operands'
+            // second stages (values, then keys), which the converters enter when the queries are done. With one head
+            // to a group (or so many pairs that they do not fit) each row computes its own.
+            constexpr int kHalf = S::kOperand / 8;
+            const int pairs = A.rope.rot / 2, angles = (l_last - l_first + 1) * pairs;
+            const bool shared = angles > 0 && angles <= 2 * kHalf && A.G > 1;
+            auto position = [&](int l) { return A.rope.positions ? A.rope.positions[static_cast<int64_t>(b) * A.L + l] : N - nq + l; };
+            auto place = [&](int e) {
+                return reinterpret_cast<float2*>(smem + (e < kHalf ? S::kVOff : S::kKOff - S::kOperand) + S::kOperand) + e;
+            };
+            if (shared) {
+                for (int e = tid; e < angles; e += 256) *place(e) = angle_at(A.rope, s_turns[e % pairs], position(l_first + e / pairs));
+                asm volatile("bar.sync 2, 256;\n" ::: "memory");
+            }
+            constexpr int J = D / 16;   // chunk pairs of a row: J consecutive lanes
+            const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
+            for (int it = tid; it < S::kRows * J; it += 256) {
+                const int r = it / J, j = it % J;
+                const int rr = grp * S::kRows + r, l = rr / A.G;
+                float xa[8] = {}, xb[8] = {};
+                int a0, b0;
+                chunk_pair(j, A.rope.rot, A.rope.inter, a0, b0);
+                if (r < rows && l < nq) {
+                    const T* q = static_cast<const T*>(A.q.data) + b * A.q.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.q.sh + l * A.q.st;
+                    load8(q + a0, xa);
+                    load8(q + b0, xb);
+                    if (shared) {
+                        const int e = (l - l_first) * pairs + 8 * j;
+                        if (16 * j < A.rope.rot) rotate_by(xa, xb, A.rope.inter, [&](int i) { return *place(e + i); });
+                    } else if (A.rope.rot > 0) {
+                        rotate_pair(xa, xb, j, A.rope, s_turns, position(l));
+                    }
+                }
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(xa[i]), fabsf(xb[i])));
+#pragma unroll
+                for (int o = J / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126), 126);
+                const float f = sign * exp2i(-e);
+                uint4 va, vb;
+                va.x = pack_out<__half>(xa[0] * f, xa[1] * f), va.y = pack_out<__half>(xa[2] * f, xa[3] * f);
+                va.z = pack_out<__half>(xa[4] * f, xa[5] * f), va.w = pack_out<__half>(xa[6] * f, xa[7] * f);
+                vb.x = pack_out<__half>(xb[0] * f, xb[1] * f), vb.y = pack_out<__half>(xb[2] * f, xb[3] * f);
+                vb.z = pack_out<__half>(xb[4] * f, xb[5] * f), vb.w = pack_out<__half>(xb[6] * f, xb[7] * f);
+                *reinterpret_cast<uint4*>(smem + S::kQOff + core<D>(r, a0)) = va;
+                *reinterpret_cast<uint4*>(smem + S::kQOff + core<D>(r, b0)) = vb;
+                if (j == 0) s_fac[r] = fabsf(A.scale) * exp2i(e);
+            }
+            tc::fence_proxy_async_smem();
+            asm volatile("bar.sync 2, 256;\n" ::: "memory");   // s_fac, for the softmax
+            if (lane == 0) tc::mbar_arrive(q_ready);
+        }
         // ================================================= softmax
         const int half = warp >> 2;
         const int row = 128 * half + 32 * (warp & 3) + lane;
@@ -391,23 +410,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         asm volatile("bar.sync 1, 256;\n" ::: "memory");
         const bool failed = *const_cast<volatile int*>(&s_fail) != 0;
         if (mine) {
-            const bool real = row < rows && rr / A.G < nq;
+            // by way of the rows' own place among the queries (nothing reads it any more), so that a row's bytes
+            // are stored together; 16-byte chunks trade places by their row, free of bank conflicts
             const float inv = !failed && l_sum > 0.0f ? 1.0f / l_sum : 0.0f;
-            T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.out.sh + (rr / A.G) * A.out.st;
+            constexpr int kChunks = D / 8;
+            unsigned char* stage = smem + S::kQOff + (128 * half + 32 * (warp & 3)) * D * 2;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 float v[32];
                 if (n_tiles > 0) tc::tmem_ld32(t_o + 32 * c, v);
-                if (real) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (inv > 0.0f) {
-                            w.x = pack_out<T>(v[e] * inv, v[e + 1] * inv), w.y = pack_out<T>(v[e + 2] * inv, v[e + 3] * inv);
-                            w.z = pack_out<T>(v[e + 4] * inv, v[e + 5] * inv), w.w = pack_out<T>(v[e + 6] * inv, v[e + 7] * inv);
-                        }
-                        *reinterpret_cast<uint4*>(dst + 32 * c + e) = w;
+                for (int e = 0; e < 4; ++e) {
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (inv > 0.0f) {
+                        w.x = pack_out<T>(v[8 * e] * inv, v[8 * e + 1] * inv), w.y = pack_out<T>(v[8 * e + 2] * inv, v[8 * e + 3] * inv);
+                        w.z = pack_out<T>(v[8 * e + 4] * inv, v[8 * e + 5] * inv), w.w = pack_out<T>(v[8 * e + 6] * inv, v[8 * e + 7] * inv);
                     }
+                    *reinterpret_cast<uint4*>(stage + lane * D * 2 + (((4 * c + e) ^ (lane & 7)) * 16)) = w;
+                }
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int k = lane; k < 32 * kChunks; k += 32) {
+                const int r = k / kChunks, c = k % kChunks;
+                const int at = 128 * half + 32 * (warp & 3) + r, ro = grp * S::kRows + at, l = ro / A.G;
+                if (at < rows && l < nq) {
+                    T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + ro % A.G) * A.out.sh + l * A.out.st;
+                    *reinterpret_cast<uint4*>(dst + 8 * c) = *reinterpret_cast<const uint4*>(stage + r * D * 2 + ((c ^ (r & 7)) * 16));
                 }
             }
         }
@@ -516,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const unsigned gone = __ballot_sync(0xffffffffu, mine && now.id < 0 && t0 + 8 * my_group < N) >> from;
                 copies_wait<0>();
                 if (i >= 2) ok = arrived(&free[st], ((i >> 1) - 1) & 1);
+                else if (i == 1) ok = arrived(q_ready, 0);   // whose angles are in the second stages
                 if (!ok) break;
                 if (warp == kKWarp && lane == 0) s_info[i & 3] = TileInfo{kref, vref, gone};
                 convert(is_v ? vx : kx, is_v ? vref : kref, now.id, from, N - t0, operand + st * S::kOperand);
@@ -563,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     else tc::mma_f16_ta_w<true>(o, p + 8 * (from + s), lo + (from + s) * (2 * kRowStep >> 4), hi, id_o);
                 }
             };
-            bool ok = arrived(&k_full[0], 0);
+            bool ok = arrived(q_ready, 0) && arrived(&k_full[0], 0);
             tc::tc_fence_after();
             if constexpr (kH == 2) {
                 const int nh = two ? 2 : 1;
@@ -634,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         tc::tmem_dealloc(tmem, 512);
     }
     if (tid == 0)
-        for (int s = 0; s < 17; ++s) tc::mbar_inval(&s_bar[s]);
+        for (int s = 0; s < 18; ++s) tc::mbar_inval(&s_bar[s]);
 }
 
 template <typename T, int D, bool I8, bool MOD>
