@@ -34,6 +34,7 @@ struct AppendArgs {
     Rope rope;
     int batch, n_new;
     const int32_t *seq, *news;
+    int angle_smem;   // bytes for the angles of a block's tokens, or 0 (set by the launch)
     unsigned* err;
 };
 
@@ -68,7 +69,7 @@ struct AttendPlan {
 AttendPlan attend_plan(int D, int batch, int H, int G, int L, int max_seq, int num_sms);
 
 #ifdef __CUDACC__
-cudaError_t launch_append(const AppendArgs& a, int D, int format, int dtype, cudaStream_t s);
+cudaError_t launch_append(const AppendArgs& a, int D, int format, int dtype, int sms, cudaStream_t s);
 cudaError_t launch_decode(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s);
 cudaError_t launch_prefill(const AttendArgs& a, const AttendPlan& p, int D, int format, int dtype, cudaStream_t s);
 #endif

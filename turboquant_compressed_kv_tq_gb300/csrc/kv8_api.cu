@@ -135,7 +135,8 @@ tq_status tq_kv8_append(const tq_kv8_cache* cache, int layer, const tq_rows* k, 
     const int elem = dtype == TQ_F32 ? 4 : 2;
     if ((st = check_rows(k, elem)) != TQ_OK || (st = check_rows(v, elem)) != TQ_OK) return st;
     if (!seq_lens) return TQ_ERR_INVALID_ARG;
-    if (device_state(&a.err, nullptr) != TQ_OK) return TQ_ERR_CUDA;
+    int sms = 0;
+    if (device_state(&a.err, &sms) != TQ_OK) return TQ_ERR_CUDA;
     a.pool = make_pool(cache, layer, block_table, max_blocks);
     a.k = make_rows(k);
     a.v = make_rows(v);
@@ -143,7 +144,7 @@ tq_status tq_kv8_append(const tq_kv8_cache* cache, int layer, const tq_rows* k, 
     a.n_new = n_new;
     a.seq = seq_lens;
     a.news = new_lens;
-    return launch_append(a, cache->head_dim, cache->format, dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch_append(a, cache->head_dim, cache->format, dtype, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? TQ_OK
                : TQ_ERR_CUDA;
 }

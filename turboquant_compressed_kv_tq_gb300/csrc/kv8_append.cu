@@ -1,12 +1,18 @@
 // Appending keys and values to the 8-bit cache, the keys rotated on the way.
 //
-// One CTA owns the new tokens of one block for one KV head, keys or values: it
-// reads them once, rotates them (fp32), reduces the largest magnitude to the
-// block's power-of-two scale, and writes the codes at that scale. The block is
-// the unit because its scale is: nothing is shared between CTAs, no atomics, one
-// launch. A block that already held tokens keeps its scale unless the new
-// tokens need a larger one; then its earlier codes are rounded to the new one
-// by the same CTA.
+// The unit is one block's new tokens of one KV head, keys or values, because that
+// is what has a scale: a CTA reads them once, rotates them (fp32), reduces the
+// largest magnitude to the block's power-of-two scale, and writes the codes at
+// that scale. Nothing is shared between CTAs, no atomics, one launch. A block that
+// already held tokens keeps its scale unless the new tokens need a larger one;
+// then its earlier codes are rounded to the new one by the same CTA.
+//
+// A CTA takes several heads of its block, as long as there are two CTAs for every
+// SM. The heads turn by the same angles, so cos and sin of each (token, pair) are
+// computed once, in shared memory: they are what a rotation costs. Nothing else is
+// held: the codes come from a second look at the input, which is still in the L1
+// cache, or at worst in the L2. (With the block in registers instead, the few CTAs
+// that fit an SM left it waiting: 28 us for the chunk below, 49 with more heads.)
 //
 // Bound: memory (2 or 4 bytes read and 1 written a value).
 #include "kv8_device.cuh"
@@ -15,7 +21,12 @@ namespace tq {
 namespace kv8 {
 namespace {
 
-constexpr int kHeld = 4;   // items (16 coordinates of one token) that a thread keeps in registers
+// max(m, |a|, |b|); NaN if one of them is.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
+}
 
 // The smallest e in [-63, 63] with top / 2^e <= the largest code (448 = 1.75 x
 // 2^8, 127 = 1.984375 x 2^6), from top's exponent and significand.
@@ -35,23 +46,25 @@ __device__ __forceinline__ uint32_t recode(uint32_t w, float down) {
     return encode4<I8>(a.x * down, a.y * down, b.x * down, b.y * down);
 }
 
-template <typename T, int D, bool I8>
-__global__ void __launch_bounds__(256) append_kernel(AppendArgs A) {
-    __shared__ uint64_t s_turns[128];
-    __shared__ float s_top[8];
-    __shared__ int s_id;
+// kMost threads at most.
+template <typename T, int D, bool I8, int kMost>
+__global__ void __launch_bounds__(kMost, 1024 / kMost) append_kernel(const __grid_constant__ AppendArgs A, int heads) {
+    extern __shared__ float2 s_angles[];   // [token of the block][pair], if the launch gave it room
+    __shared__ uint64_t s_turns[D / 2];
+    __shared__ uint32_t s_top[2][kMost / 32];
     const bool is_v = blockIdx.x & 1;
-    const int j = blockIdx.x >> 1, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+    const int j = blockIdx.x >> 1, b = blockIdx.z, tid = threadIdx.x, threads = blockDim.x;
     const Pool& P = A.pool;
     const int64_t start = A.seq[b];
     int n = A.news ? A.news[b] : A.n_new;
+    const bool first_cta = tid == 0 && j == 0 && blockIdx.y == 0;
     if (start < 0 || n < 0 || n > A.n_new) {
-        if (tid == 0 && j == 0 && h == 0) atomicOr(A.err, TQ_DEVERR_SEQLEN);
+        if (first_cta) atomicOr(A.err, TQ_DEVERR_SEQLEN);
         return;
     }
     const int64_t cap = static_cast<int64_t>(P.max_blocks) << P.bt_shift;
     if (start + n > cap) {
-        if (tid == 0 && j == 0 && h == 0) atomicOr(A.err, TQ_DEVERR_CAPACITY);
+        if (first_cta) atomicOr(A.err, TQ_DEVERR_CAPACITY);
         n = static_cast<int>(start < cap ? cap - start : 0);
     }
     const int64_t lb = (start >> P.bt_shift) + j;          // logical block
@@ -66,122 +79,172 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs A) {
     const int count = static_cast<int>((start + n < t0 + P.BT ? start + n - t0 : P.BT)) - first;
     const int i0 = static_cast<int>(t0 + first - start);   // its index among the new tokens
     const Rows& R = is_v ? A.v : A.k;
-    const T* src = static_cast<const T*>(R.data) + b * R.sb + h * R.sh + i0 * R.st;
     const bool turn = !is_v && A.rope.rot > 0;
+    const int rot = turn ? A.rope.rot : 0, inter = A.rope.inter, pairs = rot / 2;
+    const int32_t* pos = A.rope.positions ? A.rope.positions + b * static_cast<int64_t>(A.n_new) + i0 : nullptr;
+    auto position = [&](int tok) { return pos ? pos[tok] : static_cast<int>(t0) + first + tok; };
+    const bool shared = turn && A.angle_smem > 0;
     if (turn) {
-        for (int i = tid; i < A.rope.rot / 2; i += blockDim.x) s_turns[i] = turns_of(A.rope.inv_freq[i]);
+        for (int i = tid; i < pairs; i += threads) s_turns[i] = turns_of(A.rope.inv_freq[i]);
         __syncthreads();
     }
-    const int32_t* pos = A.rope.positions ? A.rope.positions + b * static_cast<int64_t>(A.n_new) + i0 : nullptr;
-
-    // item = token * (D / 16) + chunk pair
-    constexpr int J = D / 16;
-    const int items = count * J;
-    const int rot = turn ? A.rope.rot : 0, inter = A.rope.inter;
-    auto fetch = [&](int it, float (&xa)[8], float (&xb)[8]) {
-        const int tok = it / J, jj = it % J;
-        int a, c;
-        chunk_pair(jj, rot, inter, a, c);
-        load8(src + tok * R.st + a, xa);
-        load8(src + tok * R.st + c, xb);
-        if (turn) rotate_pair(xa, xb, jj, A.rope, s_turns, pos ? pos[tok] : static_cast<int>(t0) + first + tok);
-    };
-    float top = 0.0f;
-    bool odd = false;
-    auto look = [&](const float (&x)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float m = fabsf(x[i]);
-            const bool fine = m <= FLT_MAX;
-            odd |= !fine;
-            top = fmaxf(top, fine ? m : 0.0f);
+    // angle of token tok and pair 8 jj + i: neighbouring lanes (jj, then tok) on neighbouring banks
+    constexpr int J = D / 16, kPerToken = D / 2 + 8;
+    // a thread has chunk pair jj of tokens tok0, tok0 + step, ..
+    const int jj = tid % J, tok0 = tid / J, step = threads / J;
+    int ca, cc;
+    chunk_pair(jj, rot, inter, ca, cc);
+    const bool turns_here = 16 * jj < rot;
+    const int h_begin = blockIdx.y * heads, h_end = min(P.H, h_begin + heads);
+    if (shared) {
+        // the inputs on their way to the L2 cache meanwhile
+        for (int h = h_begin; h < h_end; ++h)
+            for (int tok = tok0; tok < count; tok += step)
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(static_cast<const T*>(R.data) + b * R.sb + h * R.sh + (i0 + tok) * R.st + ca));
+        // a thread has one pair, of every few tokens
+        const int q = tid % pairs, rows = threads / pairs;
+        if (rows == 0) {   // more pairs than threads
+            for (int e = tid; e < count * pairs; e += threads)
+                s_angles[e / pairs * kPerToken + e % pairs % 8 * J + e % pairs / 8] = angle_at(A.rope, s_turns[e % pairs], position(e / pairs));
+        } else if (tid < rows * pairs) {
+            const uint64_t turns = s_turns[q];
+            for (int tok = tid / pairs; tok < count; tok += rows)
+                s_angles[tok * kPerToken + q % 8 * J + q / 8] = angle_at(A.rope, turns, position(tok));
         }
-    };
-    float xa[kHeld][8], xb[kHeld][8];
+        __syncthreads();
+    }
+    for (int h = h_begin; h < h_end; ++h) {
+        const T* src = static_cast<const T*>(R.data) + b * R.sb + h * R.sh + i0 * R.st;
+        const int64_t unit = id * P.H + h;
+        uint8_t* sx = (is_v ? P.vx : P.kx) + unit;
+        const int e_old = first > 0 ? min(max(static_cast<int>(*sx) - 127, -126), 126) : -63;
+        // f(token, its two chunks) for each of the thread's tokens
+        auto each = [&](auto&& f) {
+            const T* pa = src + tok0 * R.st + ca;
+            const int to_c = cc - ca;
+            const int64_t stride = step * R.st;
+            const float2* cs = s_angles + tok0 * kPerToken + jj;
+#pragma unroll 2
+            for (int tok = tok0; tok < count; tok += step) {
+                float xa[8], xb[8];
+                load8(pa, xa);
+                load8(pa + to_c, xb);
+                pa += stride;
+                if (turns_here) {
+                    if (shared) rotate_by(xa, xb, inter, [&](int i) { return cs[i * J]; });
+                    else rotate_pair(xa, xb, jj, A.rope, s_turns, position(tok));
+                }
+                cs += step * kPerToken;
+                f(tok, xa, xb);
+            }
+        };
+        float peak = 0.0f;   // a NaN stays one
+        each([&](int, const float (&xa)[8], const float (&xb)[8]) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-        const int it = tid + k * blockDim.x;
-        if (it < items) {
-            fetch(it, xa[k], xb[k]);
-            look(xa[k]);
-            look(xb[k]);
+            for (int i = 0; i < 8; i += 2) {
+                peak = max_abs(peak, xa[i], xa[i + 1]);
+                peak = max_abs(peak, xb[i], xb[i + 1]);
+            }
+        });
+        // (two sets, in turn: one barrier a head; as bits, infinities and NaNs come out on top)
+        auto over_block = [&](uint32_t x) {
+            x = __reduce_max_sync(0xffffffffu, x);
+            if ((tid & 31) == 0) s_top[h & 1][tid >> 5] = x;
+            __syncthreads();
+            return __reduce_max_sync(0xffffffffu, (tid & 31) < threads / 32 ? s_top[h & 1][tid & 31] : 0u);
+        };
+        uint32_t top = over_block(__float_as_uint(peak) & 0x7FFFFFFFu);
+        const bool odd = top > 0x7F7FFFFFu;
+        if (odd) {   // again, without them
+            if (tid == 0) atomicOr(A.err, TQ_DEVERR_NONFINITE);
+            top = 0;
+            each([&](int, const float (&xa)[8], const float (&xb)[8]) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t u = __float_as_uint(i < 8 ? xa[i & 7] : xb[i & 7]) & 0x7FFFFFFFu;
+                    if (u <= 0x7F7FFFFFu) top = max(top, u);
+                }
+            });
+            __syncthreads();
+            top = over_block(top);
+            __syncthreads();
         }
-    }
-    for (int it = tid + kHeld * blockDim.x; it < items; it += blockDim.x) {
-        float ya[8], yb[8];
-        fetch(it, ya, yb);
-        look(ya);
-        look(yb);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((tid & 31) == 0) s_top[tid >> 5] = top;
-    if (odd) atomicOr(A.err, TQ_DEVERR_NONFINITE);
-    const int64_t unit = id * P.H + h;
-    uint8_t* sx = (is_v ? P.vx : P.kx) + unit;
-    if (tid == 0) s_id = first > 0 ? min(max(static_cast<int>(*sx) - 127, -126), 126) : -63;
-    __syncthreads();
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) top = fmaxf(top, s_top[w]);
-    const int e_old = s_id;
-    const int e = max(e_old, scale_exponent<I8>(top));
-    const float inv = exp2i(-e);
-    uint8_t* dst = (is_v ? P.vc : P.kc) + unit * (static_cast<int64_t>(P.BT) * D);
-    auto store = [&](int it, const float (&ya)[8], const float (&yb)[8]) {
-        const int tok = it / J, jj = it % J;
-        int a, c;
-        chunk_pair(jj, rot, inter, a, c);
-        uint8_t* d = dst + (first + tok) * D;
-        *reinterpret_cast<uint2*>(d + a) = make_uint2(encode4<I8>(ya[0] * inv, ya[1] * inv, ya[2] * inv, ya[3] * inv),
-                                                     encode4<I8>(ya[4] * inv, ya[5] * inv, ya[6] * inv, ya[7] * inv));
-        *reinterpret_cast<uint2*>(d + c) = make_uint2(encode4<I8>(yb[0] * inv, yb[1] * inv, yb[2] * inv, yb[3] * inv),
-                                                     encode4<I8>(yb[4] * inv, yb[5] * inv, yb[6] * inv, yb[7] * inv));
-    };
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-        const int it = tid + k * blockDim.x;
-        if (it < items) store(it, xa[k], xb[k]);
-    }
-    for (int it = tid + kHeld * blockDim.x; it < items; it += blockDim.x) {
-        float ya[8], yb[8];
-        fetch(it, ya, yb);
-        store(it, ya, yb);
-    }
-    if (first > 0 && e > e_old) {   // the earlier tokens' codes at the larger scale
-        const float down = exp2i(max(e_old - e, -126));
-        for (int c = tid; c < first * (D / 16); c += blockDim.x) {
-            uint4* p = reinterpret_cast<uint4*>(dst) + c;
-            uint4 w = *p;
-            w.x = recode<I8>(w.x, down), w.y = recode<I8>(w.y, down), w.z = recode<I8>(w.z, down), w.w = recode<I8>(w.w, down);
-            *p = w;
+        const int e_new = scale_exponent<I8>(__uint_as_float(top)), e = max(e_old, e_new);
+        const bool any = odd || e_new == 63;   // some value may be out of range
+        const float inv = exp2i(-e);
+        uint8_t* dst = (is_v ? P.vc : P.kc) + unit * (static_cast<int64_t>(P.BT) * D);
+        each([&](int tok, const float (&xa)[8], const float (&xb)[8]) {
+            uint8_t* d = dst + (first + tok) * D;
+            auto code = [&](const float (&y)[8]) {
+                return any ? make_uint2(encode4<I8>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv), encode4<I8>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv))
+                           : make_uint2(encode4<I8, false>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                                        encode4<I8, false>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+            };
+            const uint2 wa = code(xa), wb = code(xb);
+            if (cc == ca + 8) {
+                *reinterpret_cast<uint4*>(d + ca) = make_uint4(wa.x, wa.y, wb.x, wb.y);
+            } else {
+                *reinterpret_cast<uint2*>(d + ca) = wa;
+                *reinterpret_cast<uint2*>(d + cc) = wb;
+            }
+        });
+        if (first > 0 && e > e_old) {   // the earlier tokens' codes at the larger scale
+            const float down = exp2i(max(e_old - e, -126));
+            for (int c = tid; c < first * (D / 16); c += threads) {
+                uint4* p = reinterpret_cast<uint4*>(dst) + c;
+                uint4 w = *p;
+                w.x = recode<I8>(w.x, down), w.y = recode<I8>(w.y, down), w.z = recode<I8>(w.z, down), w.w = recode<I8>(w.w, down);
+                *p = w;
+            }
         }
+        if (tid == 0) *sx = static_cast<uint8_t>(e + 127);
     }
-    if (tid == 0) *sx = static_cast<uint8_t>(e + 127);
 }
 
-template <typename T, int D>
-cudaError_t launch_append_t(const AppendArgs& a, int format, cudaStream_t s) {
-    const int blocks = (a.n_new - 1) / a.pool.BT + 2;   // a run of n_new slots touches at most these
-    const int items = std::min(a.n_new, a.pool.BT) * (D / 16);
-    const int threads = std::min(256, (items + 31) / 32 * 32);
-    const dim3 grid(2 * (a.n_new == 1 ? 1 : blocks), a.pool.H, a.batch);
-    if (format == TQ_KV8_INT8) append_kernel<T, D, true><<<grid, threads, 0, s>>>(a);
-    else append_kernel<T, D, false><<<grid, threads, 0, s>>>(a);
+template <typename T, int D, bool I8>
+cudaError_t launch_append_f(const AppendArgs& args, int sms, cudaStream_t s) {
+    AppendArgs a = args;
+    const int blocks = a.n_new == 1 ? 1 : (a.n_new - 1) / a.pool.BT + 2;   // a run of n_new slots touches at most these
+    const int tokens = std::min(a.n_new, a.pool.BT);
+    // heads of a CTA: the most that leave two CTAs for every SM
+    int heads = 1;
+    while (heads < a.pool.H && static_cast<int64_t>(2) * blocks * a.batch * ((a.pool.H + 2 * heads - 1) / (2 * heads)) >= 2 * sms) heads *= 2;
+    // the angles in shared memory, but for the largest blocks and rotations; the more they take, the fewer
+    // CTAs an SM holds, and the more threads each has
+    constexpr int kMostSmem = 192 * 1024;
+    const int angles = a.rope.rot > 0 ? tokens * (D / 2 + 8) * 8 : 0;
+    a.angle_smem = angles <= kMostSmem ? angles : 0;
+    const int most = angles > 100 * 1024 ? 1024 : angles > 50 * 1024 ? 512 : 256;
+    const int threads = std::max(32, std::min(most, (tokens * (D / 16) + 31) / 32 * 32));
+    const int k = most == 1024 ? 2 : most == 512 ? 1 : 0;
+    auto kernel = k == 2 ? append_kernel<T, D, I8, 1024> : k == 1 ? append_kernel<T, D, I8, 512> : append_kernel<T, D, I8, 256>;
+    if (a.angle_smem > 48 * 1024) {
+        static std::atomic<uint64_t> allowed[3] = {};
+        const cudaError_t e = allow_smem(kernel, kMostSmem, allowed[k]);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<dim3(2 * blocks, (a.pool.H + heads - 1) / heads, a.batch), threads, a.angle_smem, s>>>(a, heads);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cudaGetLastError();
 }
 
+template <typename T, int D>
+cudaError_t launch_append_t(const AppendArgs& a, int format, int sms, cudaStream_t s) {
+    return format == TQ_KV8_INT8 ? launch_append_f<T, D, true>(a, sms, s) : launch_append_f<T, D, false>(a, sms, s);
+}
+
 template <typename T>
-cudaError_t launch_append_d(const AppendArgs& a, int D, int format, cudaStream_t s) {
-    return D == 64 ? launch_append_t<T, 64>(a, format, s)
-                   : D == 128 ? launch_append_t<T, 128>(a, format, s) : launch_append_t<T, 256>(a, format, s);
+cudaError_t launch_append_d(const AppendArgs& a, int D, int format, int sms, cudaStream_t s) {
+    return D == 64 ? launch_append_t<T, 64>(a, format, sms, s)
+                   : D == 128 ? launch_append_t<T, 128>(a, format, sms, s) : launch_append_t<T, 256>(a, format, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_append(const AppendArgs& a, int D, int format, int dtype, cudaStream_t s) {
-    if (dtype == TQ_F32) return launch_append_d<float>(a, D, format, s);
-    if (dtype == TQ_F16) return launch_append_d<__half>(a, D, format, s);
-    return launch_append_d<__nv_bfloat16>(a, D, format, s);
+cudaError_t launch_append(const AppendArgs& a, int D, int format, int dtype, int sms, cudaStream_t s) {
+    if (dtype == TQ_F32) return launch_append_d<float>(a, D, format, sms, s);
+    if (dtype == TQ_F16) return launch_append_d<__half>(a, D, format, sms, s);
+    return launch_append_d<__nv_bfloat16>(a, D, format, sms, s);
 }
 
 }  // namespace kv8

@@ -134,8 +134,7 @@ __device__ __forceinline__ void chunk_pair(int j, int rot, int inter, int& a, in
     }
 }
 
-// Rotate chunk pair j by `angle(i)`, cos and sin of its pair i < 8. Products and
-// differences are rounded one by one, as elementwise operations round them.
+// Rotate chunk pair j by `angle(i)`, cos and sin of its pair i < 8.
 template <typename F>
 __device__ __forceinline__ void rotate_by(float (&xa)[8], float (&xb)[8], int inter, F&& angle) {
 #pragma unroll
@@ -151,8 +150,8 @@ __device__ __forceinline__ void rotate_by(float (&xa)[8], float (&xb)[8], int in
             w = &xb[i];
         }
         const float x = *u, y = *w;
-        *u = __fsub_rn(__fmul_rn(x, cs.x), __fmul_rn(y, cs.y));
-        *w = __fadd_rn(__fmul_rn(y, cs.x), __fmul_rn(x, cs.y));
+        *u = fmaf(x, cs.x, -(y * cs.y));
+        *w = fmaf(y, cs.x, x * cs.y);
     }
 }
 
@@ -202,20 +201,20 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
     }
 }
 
-// Code of x (scale divided out), rounded to nearest even and kept in range; a
-// NaN becomes 0.
-template <bool I8>
+// Codes of four values (scale divided out), rounded to nearest even. kAny: they may
+// be out of range (kept in range) or NaN (0); else they are in range.
+template <bool I8, bool kAny = true>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    if constexpr (kAny) a = a == a ? a : 0.0f, b = b == b ? b : 0.0f, c = c == c ? c : 0.0f, d = d == d ? d : 0.0f;
     if constexpr (I8) {
         auto one = [](float x) {
+            if constexpr (kAny) x = fminf(fmaxf(x, -127.0f), 127.0f);
             int r;
-            asm("cvt.rni.s32.f32 %0, %1;\n" : "=r"(r) : "f"(fminf(fmaxf(x, -127.0f), 127.0f)));
-            return static_cast<uint32_t>(r) & 0xFFu;
+            asm("cvt.rni.s32.f32 %0, %1;\n" : "=r"(r) : "f"(x));
+            return static_cast<uint32_t>(r);
         };
-        a = a == a ? a : 0.0f, b = b == b ? b : 0.0f, c = c == c ? c : 0.0f, d = d == d ? d : 0.0f;
-        return one(a) | (one(b) << 8) | (one(c) << 16) | (one(d) << 24);
+        return __byte_perm(__byte_perm(one(a), one(b), 0x0040), __byte_perm(one(c), one(d), 0x0040), 0x5410);
     } else {
-        a = a == a ? a : 0.0f, b = b == b ? b : 0.0f, c = c == c ? c : 0.0f, d = d == d ? d : 0.0f;
         uint32_t r;
         asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
             " mov.b32 %0, {lo, hi};\n}\n"
