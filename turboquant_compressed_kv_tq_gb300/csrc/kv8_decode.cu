@@ -204,7 +204,11 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         if (w < warp) upto += s_scan[w];
         total += s_scan[w];
     }
-    const long long share = max(static_cast<long long>(S::kWarps), (total + gridDim.x - 1) / gridDim.x);
+    // equal shares, but at least a tile for each warp, and no cut through sequences that are all short
+    const long long even = total < (1ll << 31) ? static_cast<long long>((static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x)
+                                               : (total + gridDim.x - 1) / gridDim.x;
+    const int longest = (A.max_seq + 15) >> 4;
+    const long long share = max(static_cast<long long>(longest <= 2 * S::kWarps ? max(longest, 1) : S::kWarps), even);
     const long long begin = blockIdx.x * share, end = min(begin + share, total);
     if (begin >= end) return;
     if (upto - sum <= begin && begin < upto) {
@@ -239,8 +243,10 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         ++pair;
         continue;
     }
-    const int h = static_cast<int>((from - pair_at) / unit_tiles);
-    const int i_begin = static_cast<int>((from - pair_at) % unit_tiles);
+    const long long in_pair = from - pair_at;
+    const int h = static_cast<int>(in_pair < (1ll << 31) ? static_cast<long long>(static_cast<unsigned>(in_pair) / static_cast<unsigned>(unit_tiles))
+                                                         : in_pair / unit_tiles);
+    const int i_begin = static_cast<int>(in_pair - static_cast<long long>(h) * unit_tiles);
     const int i_all = static_cast<int>(min(static_cast<long long>(unit_tiles - i_begin), end - from));   // tiles of this segment
     const int i_end = min(i_begin + i_all, tiles.n1 + tiles.n2);                                        // without the one that is none
     const int per = (max(i_end - i_begin, 0) + S::kWarps - 1) / S::kWarps;   // tiles of a warp, consecutive
@@ -249,6 +255,66 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
     if (tid == 0 && i_begin == 0 && gridDim.x > 1)   // the shares that the unit lies in
         *reinterpret_cast<int2*>(A.unit_shares + 2 * unit) =
             make_int2(blockIdx.x, static_cast<int>((pair_at + static_cast<long long>(h + 1) * unit_tiles - 1) / share));
+
+    // ---------------- the copies of the first tiles, on their way while the queries are prepared
+    const bool busy = w_begin < w_end && !dead;
+    const int64_t unit_bytes = static_cast<int64_t>(P.BT) * D;
+
+    // lane k holds the block and scales of the warp's tile base + k, and of the 32 after those
+    int base = w_begin;
+    int64_t id = -1, id_next = -1;
+    uint32_t meta = 0, meta_next = 0;   // scale bytes, and whether there is a block
+    auto look_up = [&](int from, int64_t& x, uint32_t& sc) {
+        x = -1;
+        sc = 0;
+        const int i = from + lane;
+        if (i < w_end) {
+            const int lb = (tiles.at(i) << 4) >> P.bt_shift;
+            const int64_t at = P.table ? P.table[b * static_cast<int64_t>(P.max_blocks) + lb] : b * static_cast<int64_t>(P.max_blocks) + lb;
+            if (at >= 0 && at < P.num_blocks) {
+                x = at * P.H + h;
+                sc = P.kx[x] | (P.vx[x] << 8) | 0x10000u;
+            } else {
+                atomicOr(A.err, TQ_DEVERR_BLOCK);
+            }
+        }
+    };
+    constexpr int kStep = S::kTileBytes * S::kU, kU = S::kU;
+    unsigned char* ring = smem + warp * S::kStages * kStep;
+    uint32_t ahead[S::kStages - 1][kU];   // meta of the tiles on their way
+    // start the copies of the kU tiles from i (none behind the warp's last tile); their metas
+    auto fetch = [&](int i, uint32_t (&mt)[kU]) {
+        const unsigned st = puts % S::kStages;
+        if (i < w_end) {
+            if (lane == 0) tc::mbar_expect_tx(&bars[st], i + kU <= w_end ? kStep : S::kTileBytes);
+            ++puts;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            mt[u] = 0;
+            if (i + u >= w_end) continue;
+            if (i + u - base == 32) {
+                base = i + u;
+                id = id_next;
+                meta = meta_next;
+                look_up(base + 32, id_next, meta_next);
+            }
+            const int64_t x = __shfl_sync(0xffffffffu, id, i + u - base);
+            mt[u] = __shfl_sync(0xffffffffu, meta, i + u - base);
+            if (lane == 0) {   // where there is no block: any block, which nobody sees
+                const int64_t off = (x < 0 ? 0 : x) * unit_bytes + static_cast<int64_t>((tiles.at(i + u) << 4) & (P.BT - 1)) * D;
+                unsigned char* dst = ring + st * kStep + u * S::kTileBytes;
+                tc::bulk_g2s(dst, P.kc + off, 16 * D, &bars[st]);
+                tc::bulk_g2s(dst + 16 * D, P.vc + off, 16 * D, &bars[st]);
+            }
+        }
+    };
+    if (busy) {
+        look_up(base, id, meta);
+        look_up(base + 32, id_next, meta_next);
+#pragma unroll
+        for (int k = 0; k < S::kStages - 1; ++k) fetch(w_begin + k * kU, ahead[k]);
+    }
 
     // ---------------- the queries: rotated, scaled by a power of two, fp16
     if (i_begin < i_end) {
@@ -297,7 +363,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         m[nt][0] = m[nt][1] = kNone;
         l_sum[nt][0] = l_sum[nt][1] = 0.0f;
     }
-    if (w_begin < w_end && !dead) {
+    if (busy) {
         uint32_t qf[NT][D / 16][2];
         float fac[NT][2], slope[NT][2];
 #pragma unroll
@@ -318,61 +384,6 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         }
         const bool plain = A.cap <= 0.0f && !A.slopes;
         const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
-        const int64_t unit_bytes = static_cast<int64_t>(P.BT) * D;
-
-        // lane k holds the block and scales of the warp's tile base + k, and of the 32 after those
-        int base = w_begin;
-        int64_t id = -1, id_next = -1;
-        uint32_t meta = 0, meta_next = 0;   // scale bytes, and whether there is a block
-        auto look_up = [&](int from, int64_t& x, uint32_t& sc) {
-            x = -1;
-            sc = 0;
-            const int i = from + lane;
-            if (i < w_end) {
-                const int lb = (tiles.at(i) << 4) >> P.bt_shift;
-                const int64_t at = P.table ? P.table[b * static_cast<int64_t>(P.max_blocks) + lb] : b * static_cast<int64_t>(P.max_blocks) + lb;
-                if (at >= 0 && at < P.num_blocks) {
-                    x = at * P.H + h;
-                    sc = P.kx[x] | (P.vx[x] << 8) | 0x10000u;
-                } else {
-                    atomicOr(A.err, TQ_DEVERR_BLOCK);
-                }
-            }
-        };
-        look_up(base, id, meta);
-        look_up(base + 32, id_next, meta_next);
-        constexpr int kStep = S::kTileBytes * S::kU, kU = S::kU;
-        unsigned char* ring = smem + warp * S::kStages * kStep;
-        uint32_t ahead[S::kStages - 1][kU];   // meta of the tiles on their way
-        // start the copies of the kU tiles from i (none behind the warp's last tile); their metas
-        auto fetch = [&](int i, uint32_t (&mt)[kU]) {
-            const unsigned st = puts % S::kStages;
-            if (i < w_end) {
-                if (lane == 0) tc::mbar_expect_tx(&bars[st], i + kU <= w_end ? kStep : S::kTileBytes);
-                ++puts;
-            }
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                mt[u] = 0;
-                if (i + u >= w_end) continue;
-                if (i + u - base == 32) {
-                    base = i + u;
-                    id = id_next;
-                    meta = meta_next;
-                    look_up(base + 32, id_next, meta_next);
-                }
-                const int64_t x = __shfl_sync(0xffffffffu, id, i + u - base);
-                mt[u] = __shfl_sync(0xffffffffu, meta, i + u - base);
-                if (lane == 0) {   // where there is no block: any block, which nobody sees
-                    const int64_t off = (x < 0 ? 0 : x) * unit_bytes + static_cast<int64_t>((tiles.at(i + u) << 4) & (P.BT - 1)) * D;
-                    unsigned char* dst = ring + st * kStep + u * S::kTileBytes;
-                    tc::bulk_g2s(dst, P.kc + off, 16 * D, &bars[st]);
-                    tc::bulk_g2s(dst + 16 * D, P.vc + off, 16 * D, &bars[st]);
-                }
-            }
-        };
-#pragma unroll
-        for (int k = 0; k < S::kStages - 1; ++k) fetch(w_begin + k * kU, ahead[k]);
         for (int i = w_begin; i < w_end; i += kU) {
             uint32_t mt[kU];
             int t0[kU];   // a tile behind the warp's last one: behind the sequence's end
@@ -546,7 +557,8 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         if (lane == 0) atomicOr(A.err, TQ_DEVERR_TIMEOUT);
         for (; gets < puts; ++gets) (void)arrived(&bars[gets % S::kStages], (gets / S::kStages) & 1);
     }
-    // ---------------- the CTA's state of each row: the warps' states at their largest reference
+    // ---------------- the CTA's state of each row: the states of the warps that had tiles, at their largest reference
+    const int had = per > 0 ? (i_end - i_begin + per - 1) / per : 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -562,13 +574,14 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         }
     __syncthreads();   // and the queries in shared memory are done with
     float* s_o = reinterpret_cast<float*>(smem);   // [warps][kRows][D]
+    if (warp < had)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 8 * nt + 2 * c + e;
             float top = s_m[0][r];
-            for (int w = 1; w < S::kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+            for (int w = 1; w < had; ++w) top = fmaxf(top, s_m[w][r]);
             const float f = ex2(m[nt][e] - top);
             float* o = s_o + (warp * kRows + r) * D;
 #pragma unroll
@@ -587,10 +600,10 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         const int rr = grp * kRows + r, l = rr / A.G;
         if (l >= nq) continue;
         float top = s_m[0][r];
-        for (int w = 1; w < S::kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+        for (int w = 1; w < had; ++w) top = fmaxf(top, s_m[w][r]);
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float sum = 0.0f;
-        for (int w = 0; w < S::kWarps; ++w) {
+        for (int w = 0; w < had; ++w) {
             const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kRows + r) * D + d);
             o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
             sum = fmaf(s_l[w][r], ex2(s_m[w][r] - top), sum);
