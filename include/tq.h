@@ -722,15 +722,17 @@ typedef struct {
  *   new_lens   device int32 [batch] in [0, n_new], or NULL: n_new each
  *   positions  device int32 [batch][n_new], rotation positions, or NULL: the
  *              position in the cache
- *   block_table, max_blocks: as tq_encode_append; no block may belong to two
- *              of the batch's sequences at the places that are appended to
+ *   block_table, max_blocks: as tq_encode_append; no block may stand twice in
+ *              the batch's tables at the places that are appended to
  * Scale of a block and head: the smallest 2^e at which the largest magnitude
  * of its tokens is at most the largest code (448 or 127). A block that holds
  * earlier tokens keeps its scale, or takes the larger one that the new tokens
  * need: then its earlier codes are rounded to it (for e4m3, exact but for the
  * smallest codes). Bytes behind the last token stay as they were.
- * A NaN is stored as 0 and an infinity as the largest code of its sign, and
- * either sets TQ_DEVERR_NONFINITE: nothing in the cache poisons other rows.
+ * A NaN (after the rotation) is stored as 0 and an infinity as the largest code
+ * of its sign, and either sets TQ_DEVERR_NONFINITE: nothing in the cache poisons
+ * other rows. Magnitudes below 2^-73 or so become 0, those above 2^71 (e4m3; 2^69
+ * for integers) the largest code.
  * Tokens past a sequence's capacity or in a block id outside the pool are
  * skipped and flagged (TQ_DEVERR_CAPACITY, TQ_DEVERR_BLOCK), a sequence with a
  * negative length or a new_lens outside [0, n_new] too (TQ_DEVERR_SEQLEN).
@@ -783,9 +785,12 @@ tq_status tq_kv8_workspace_bytes(const tq_kv8_cache *cache, int batch, int num_q
  *   scores     NULL: plain causal attention
  *   workspace  device, >= tq_kv8_workspace_bytes(...), 256-byte aligned (NULL
  *              where that is 0); only this call uses it while it runs.
- * Operands are fp16 (cached codes are exact in it; queries are scaled by a power
- * of two per row, then rounded, where they were rotated; softmax weights are
- * rounded), sums and softmax statistics fp32, the output is rounded once.
+ * Operands are fp16: cached codes are exact in it (of many rows at once, as far
+ * as the scales of 64 to 128 neighbouring tokens lie within 2^15 of each other:
+ * then those of the smaller scale lose low bits); queries are scaled by a power of
+ * two per row, and rounded where they were rotated (for few rows of fp16 held in
+ * two parts); softmax weights are rounded. Sums and softmax statistics are fp32,
+ * the output is rounded once. The same call gives the same bits every time.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED as tq_kv8_append, also for f32
  * queries; TQ_ERR_CAPACITY if the workspace is too small.
  */

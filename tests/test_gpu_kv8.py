@@ -308,6 +308,11 @@ CASES = [
     (128, 128, 1, 8, 300, [300, 1111], [299, 300], {"rope": 128, "scale": 0.3}),
     (128, 16, 2, 2, 513, [513, 2049], None, {"empty": True}),
     (256, 256, 1, 8, 40, [40, 600], None, {"cap": 10.0, "prefix": [40, 1]}),
+    # more than 16 rows behind long sequences: still split over the tokens
+    (128, 64, 2, 4, 16, [20000, 9001], None, {"rope": 128}),
+    (64, 32, 4, 8, 12, [4000, 100, 33], [12, 5, 0], {"docs": 700, "prefix": [3999, 2, 0]}),
+    (64, 16, 4, 8, 12, [3000, 12, 13, 2999, 16, 1500, 600, 29], None, {"cap": 25.0, "bias": True}),
+    (256, 64, 1, 8, 50, [6000], None, {"window": 3000, "rope": 256}),
 ]
 
 

@@ -54,6 +54,7 @@ struct AttendArgs {
     // and x D, and the first and last such CTA of each unit [batch][groups][H]
     float *part_ml, *part_o;
     int* unit_shares;
+    int pad;                   // what a unit costs besides its tiles, in tiles: counted behind them when shares are dealt out
     unsigned* err;
 };
 
@@ -62,7 +63,7 @@ struct AttendPlan {
     int chunk;         // 1: the tensor-memory kernel (many rows), 0: the split kernel (few rows)
     int group_rows;    // query rows of a group
     int groups;        // ceil(G q_len / group_rows)
-    int ctas;          // of the split kernel
+    int ctas, pad;     // of the split kernel
     size_t ml_bytes, unit_bytes, total;
 };
 

@@ -89,7 +89,18 @@ tq_status check_sizes(const tq_kv8_cache* c, int batch, int Hq, int L, int max_s
 AttendPlan attend_plan(int D, int batch, int H, int G, int L, int max_seq, int num_sms) {
     AttendPlan p{};
     const int rows = G * L;
-    if (rows > 32) {   // the tensor-memory kernel
+    // Which kernel, for more than 16 rows a KV head. The split kernel reads the cache once for each 16 rows, at about
+    // 4.8 TB/s (4 at head_dim 64), behind some 18 us of set-up and 4 us for each unit that an SM takes; the chunk kernel
+    // reads it once for 256 (128), but walks a sequence on one SM, at 1.5 / 2.1 / 1.9 us a tile of 128 / 128 / 64 tokens.
+    // Measured, split and chunk, us: 4 heads x 16 queries over 32768 tokens, 8 KV heads, head_dim 128: 68, 531; 64 queries
+    // over 4096: 45, 82; 512 over 4096: 245, 83; 8 sequences x 32 over 1024: 67, 26; head_dim 256, 200 queries x 8 heads
+    // over 8192, 2 KV heads: 170, 235; 333 x 4 over 500: 61, 31; head_dim 64, 4 sequences, 16 x 8 over 8192: 81, 104.
+    const double kv_bytes = 2.0 * D * max_seq, sets = static_cast<double>(batch) * H;
+    const double split_units = sets * ((rows + 15) / 16), chunk_rows = D == 256 ? 128 : 256;
+    const double split_us = 18 + 4 * split_units / num_sms + split_units * kv_bytes / (D == 64 ? 4.0e6 : 4.8e6);
+    const double waves = std::ceil(sets * std::ceil(rows / chunk_rows) / num_sms);
+    const double chunk_us = 12 + waves * std::ceil(max_seq / (D == 256 ? 64.0 : 128.0)) * (D == 64 ? 1.5 : D == 128 ? 2.1 : 1.85);
+    if (rows > 16 && chunk_us < split_us) {
         p.chunk = 1;
         p.group_rows = D == 256 ? 128 : 256;
         p.groups = (rows + p.group_rows - 1) / p.group_rows;
@@ -101,6 +112,9 @@ AttendPlan attend_plan(int D, int batch, int H, int G, int L, int max_seq, int n
     const int64_t units = static_cast<int64_t>(batch) * H * p.groups;
     const int64_t tiles = units * std::max(1, (max_seq + 15) / 16);
     p.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms, (tiles + 7) / 8)));
+    // taking up a unit costs an SM about 4 us, some 32 tiles' time: counted where SMs take several, so that prompts' first
+    // rows, whose units have a tile or two, do not pile up on a few (512 x 4 rows over 512 tokens: 484 us without)
+    p.pad = units > num_sms ? 32 : 0;
     if (p.ctas > 1) {
         const size_t n = static_cast<size_t>(2) * p.ctas * p.group_rows;
         p.ml_bytes = (n * 8 + 255) / 256 * 256;
@@ -209,6 +223,7 @@ tq_status tq_kv8_attention(const tq_kv8_cache* cache, int layer, const tq_rows* 
     a.unit_shares = reinterpret_cast<int*>(ws + p.ml_bytes);
     a.part_o = reinterpret_cast<float*>(ws + p.ml_bytes + p.unit_bytes);
     a.groups = p.groups;
+    a.pad = p.pad;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = p.chunk ? launch_prefill(a, p, cache->head_dim, cache->format, dtype, s)
                                   : launch_decode(a, p, cache->head_dim, cache->format, dtype, s);

@@ -146,8 +146,10 @@ struct Tiles {
     }
     __device__ __forceinline__ bool none() const { return l_last < l_first; }   // only rows behind the sequence's queries
     __device__ __forceinline__ int at(int i) const { return i < n1 ? i : first + (i - n1); }
-    // a unit that sees nothing is a tile of its own: its rows are written too
+    // a unit that sees nothing counts as one tile: its rows are written too
     __device__ __forceinline__ int count() const { return none() ? 0 : max(1, n1 + n2); }
+    // its place in the shares
+    __device__ __forceinline__ int room(const AttendArgs& A) const { return none() ? 0 : count() + A.pad; }
 };
 
 template <typename T, int D, int NT, bool I8>
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         const int b = p / A.groups;
         const Seq q(A, b);
         if (q.bad && blockIdx.x == 0) atomicOr(A.err, TQ_DEVERR_SEQLEN);
-        sum += static_cast<long long>(Tiles(A, q, b, p % A.groups, kRows).count()) * P.H;
+        sum += static_cast<long long>(Tiles(A, q, b, p % A.groups, kRows).room(A)) * P.H;
     }
     long long upto = sum;   // inclusive over the threads
 #pragma unroll
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
     // equal shares, but at least a tile for each warp, and no cut through sequences that are all short
     const long long even = total < (1ll << 31) ? static_cast<long long>((static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x)
                                                : (total + gridDim.x - 1) / gridDim.x;
-    const int longest = (A.max_seq + 15) >> 4;
+    const int longest = ((A.max_seq + 15) >> 4) + A.pad;
     const long long share = max(static_cast<long long>(longest <= 2 * S::kWarps ? max(longest, 1) : S::kWarps), even);
     const long long begin = blockIdx.x * share, end = min(begin + share, total);
     if (begin >= end) return;
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
         long long at = upto - sum;
         for (int p = tid * each;; ++p) {
             const int b = p / A.groups;
-            const long long n = static_cast<long long>(Tiles(A, Seq(A, b), b, p % A.groups, kRows).count()) * P.H;
+            const long long n = static_cast<long long>(Tiles(A, Seq(A, b), b, p % A.groups, kRows).room(A)) * P.H;
             if (begin < at + n) {
                 s_pair = p;
                 s_at = at;
@@ -238,23 +240,35 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
     const Seq seq(A, b);
     const Tiles tiles(A, seq, b, grp, kRows);
     const int N = seq.N, nq = seq.nq, rows = tiles.rows, lo_max = tiles.lo_max, p_min = N - nq + tiles.l_first;
-    const int unit_tiles = tiles.count();
-    if (unit_tiles == 0) {
+    const int unit_tiles = tiles.count(), unit_room = tiles.room(A);
+    if (unit_room == 0) {
         ++pair;
         continue;
     }
     const long long in_pair = from - pair_at;
-    const int h = static_cast<int>(in_pair < (1ll << 31) ? static_cast<long long>(static_cast<unsigned>(in_pair) / static_cast<unsigned>(unit_tiles))
-                                                         : in_pair / unit_tiles);
-    const int i_begin = static_cast<int>(in_pair - static_cast<long long>(h) * unit_tiles);
-    const int i_all = static_cast<int>(min(static_cast<long long>(unit_tiles - i_begin), end - from));   // tiles of this segment
+    const int h = static_cast<int>(in_pair < (1ll << 31) ? static_cast<long long>(static_cast<unsigned>(in_pair) / static_cast<unsigned>(unit_room))
+                                                         : in_pair / unit_room);
+    const int i_begin = static_cast<int>(in_pair - static_cast<long long>(h) * unit_room);
+    const int i_room = static_cast<int>(min(static_cast<long long>(unit_room - i_begin), end - from));
+    auto next_segment = [&]() {
+        from += i_room;
+        if (from == pair_at + static_cast<long long>(unit_room) * P.H) {
+            pair_at = from;
+            ++pair;
+        }
+    };
+    if (i_begin >= unit_tiles) {   // only what is counted behind a unit's tiles
+        next_segment();
+        continue;
+    }
+    const int i_all = min(i_room, unit_tiles - i_begin);                                               // tiles of this segment
     const int i_end = min(i_begin + i_all, tiles.n1 + tiles.n2);                                        // without the one that is none
     const int per = (max(i_end - i_begin, 0) + S::kWarps - 1) / S::kWarps;   // tiles of a warp, consecutive
     const int w_begin = min(i_begin + warp * per, i_end), w_end = min(w_begin + per, i_end);
     const int64_t unit = static_cast<int64_t>(pair) * P.H + h;
     if (tid == 0 && i_begin == 0 && gridDim.x > 1)   // the shares that the unit lies in
         *reinterpret_cast<int2*>(A.unit_shares + 2 * unit) =
-            make_int2(blockIdx.x, static_cast<int>((pair_at + static_cast<long long>(h + 1) * unit_tiles - 1) / share));
+            make_int2(blockIdx.x, static_cast<int>((pair_at + static_cast<long long>(h) * unit_room + unit_tiles - 1) / share));
 
     // ---------------- the copies of the first tiles, on their way while the queries are prepared
     const bool busy = w_begin < w_end && !dead;
@@ -619,11 +633,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
             if (d == 0) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(top, sum);
         }
     }
-    from += i_all;
-    if (from == pair_at + static_cast<long long>(unit_tiles) * P.H) {
-        pair_at = from;
-        ++pair;
-    }
+    next_segment();
     tc::fence_proxy_async_smem();
     __syncthreads();   // before the next segment's queries and copies
     }
