@@ -83,8 +83,10 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[W], const unsigned char
 template <int D, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;
-    // warps by the registers that a warp needs, one CTA to an SM
-    static constexpr int kWarps = D * NT >= 256 ? 8 : D * NT == 128 ? 12 : 16;
+    // warps by the registers that a warp needs, one CTA to an SM (16 rows at head_dim 128 with the query fragments in
+    // registers: 8 warps, 119 us for the long case; from shared memory, 12 warps: 111)
+    static constexpr bool kQShared = D == 128 && NT == 2;   // the query fragments stay in shared memory
+    static constexpr int kWarps = kQShared ? 12 : D * NT >= 256 ? 8 : D * NT == 128 ? 12 : 16;
     static constexpr int kU = D == 256 ? 1 : 2;        // tiles taken together: two chains of dependent instructions
     static constexpr int kKL = D / 64;                 // key loads per token
     static constexpr int kVW = D >= 128 ? 4 : 2;       // words of a value load
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
+            for (int ks = 0; ks < (S::kQShared ? 0 : D / 16); ++ks) {
                 const uint2 f = reinterpret_cast<const uint2*>(smem + S::kSmem)[(nt * (D / 16) + ks) * 32 + lane];
                 qf[nt][ks][0] = f.x;
                 qf[nt][ks][1] = f.y;
@@ -434,7 +436,11 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
                 }
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    uint2 fine[NT];
+                    uint2 fine[NT], now[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        now[nt] = S::kQShared ? reinterpret_cast<const uint2*>(smem + S::kSmem)[(nt * (D / 16) + 4 * k + w) * 32 + lane]
+                                              : make_uint2(qf[nt][4 * k + w][0], qf[nt][4 * k + w][1]);
                     if constexpr (kFine)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -446,7 +452,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
                         codes_f16<I8>(w1[u][w], a1, a3);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(sc[u][nt], a0, a1, a2, a3, qf[nt][4 * k + w][0], qf[nt][4 * k + w][1]);
+                            mma16816(sc[u][nt], a0, a1, a2, a3, now[nt].x, now[nt].y);
                             if constexpr (kFine) mma16816(sc[u][nt], a0, a1, a2, a3, fine[nt].x, fine[nt].y);
                         }
                     }
