@@ -25,6 +25,7 @@
 // Bound: softmax and conversion instructions next to the tensor cores' 4 D
 // flops per row and key.
 #include <climits>
+#include <type_traits>
 
 #include "kv8_device.cuh"
 #include "tc_ptx.cuh"
@@ -39,14 +40,16 @@ constexpr float kNone = -1e30f;
 constexpr float kGap = 8.0f;
 constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 15, kThreads = 32 * (kMmaWarp + 1);
 
-template <int D>
+// kFine: the queries in two fp16 parts (head_dim 64).
+template <int D, bool kFine>
 struct Shape {
     static constexpr int kHalves = D == 256 ? 1 : 2;
     static constexpr int kRows = 128 * kHalves;
     static constexpr int kT = D == 256 ? 64 : 128;         // tokens of a tile
     static constexpr int kOperand = kT * D * 2;            // bytes of a tile's keys or values as fp16
     static constexpr int kVOff = 0, kKOff = 2 * kOperand, kQOff = 4 * kOperand;
-    static constexpr int kRawOff = kQOff + kRows * D * 2, kRaw = kT * D;   // a tile's codes, keys then values
+    static constexpr int kQ = kRows * D * 2;               // bytes of the queries (of each part)
+    static constexpr int kRawOff = kQOff + kQ * (kFine ? 2 : 1), kRaw = kT * D;   // a tile's codes, keys then values
     static constexpr int kSmem = kRawOff + 2 * kRaw;
     // TMEM columns: O, S and P of half (or tile parity) x
     static constexpr int kO = 0, kS = kHalves * D, kSStep = kT;
@@ -122,9 +125,9 @@ struct TileInfo {
     unsigned gone;     // groups of 8 tokens that belong to no block
 };
 
-template <typename T, int D, bool I8, bool MOD>
+template <typename T, int D, bool I8, bool MOD, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ AttendArgs A) {
-    using S = Shape<D>;
+    using S = Shape<D, kFine>;
     constexpr int kT = S::kT, kH = S::kHalves;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint64_t s_turns[D / 2];
@@ -246,13 +249,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 for (int o = J / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126), 126);
                 const float f = sign * exp2i(-e);
-                uint4 va, vb;
-                va.x = pack_out<__half>(xa[0] * f, xa[1] * f), va.y = pack_out<__half>(xa[2] * f, xa[3] * f);
-                va.z = pack_out<__half>(xa[4] * f, xa[5] * f), va.w = pack_out<__half>(xa[6] * f, xa[7] * f);
-                vb.x = pack_out<__half>(xb[0] * f, xb[1] * f), vb.y = pack_out<__half>(xb[2] * f, xb[3] * f);
-                vb.z = pack_out<__half>(xb[4] * f, xb[5] * f), vb.w = pack_out<__half>(xb[6] * f, xb[7] * f);
-                *reinterpret_cast<uint4*>(smem + S::kQOff + core<D>(r, a0)) = va;
-                *reinterpret_cast<uint4*>(smem + S::kQOff + core<D>(r, b0)) = vb;
+                auto put = [&](const float (&x)[8], int d) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __half2 w = __floats2half2_rn(x[2 * i] * f, x[2 * i + 1] * f);
+                        const float2 back = __half22float2(w);
+                        hi[i] = *reinterpret_cast<const uint32_t*>(&w);
+                        lo[i] = pack_out<__half>(x[2 * i] * f - back.x, x[2 * i + 1] * f - back.y);
+                    }
+                    unsigned char* at = smem + S::kQOff + core<D>(r, d);
+                    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if constexpr (kFine) *reinterpret_cast<uint4*>(at + S::kQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                };
+                put(xa, a0);
+                put(xb, b0);
                 if (j == 0) s_fac[r] = fabsf(A.scale) * exp2i(e);
             }
             tc::fence_proxy_async_smem();
@@ -580,6 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const uint64_t q = dq + static_cast<uint64_t>(x * 128 * D * 2 >> 4), k = dk + static_cast<uint64_t>(st * S::kOperand >> 4);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) tc::mma_f16(tmem + S::kS + buf * S::kSStep, q + 16 * s, k + 16 * s, id_s, s > 0);
+                if constexpr (kFine)
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        tc::mma_f16(tmem + S::kS + buf * S::kSStep, q + static_cast<uint64_t>(S::kQ >> 4) + 16 * s, k + 16 * s, id_s, 1);
                 tc::mma_commit(&s_ready[buf]);
             };
             // O += P V of 64 tokens, from step `from` on
@@ -667,25 +682,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         for (int s = 0; s < 18; ++s) tc::mbar_inval(&s_bar[s]);
 }
 
-template <typename T, int D, bool I8, bool MOD>
-cudaError_t launch_m(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-    using S = Shape<D>;
+template <typename T, int D, bool I8, bool MOD, bool kFine>
+cudaError_t launch_f(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+    using S = Shape<D, kFine>;
     static_assert(S::kSmem <= 227 * 1024 - 2560, "shared memory");
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_smem(prefill_kernel<T, D, I8, MOD>, S::kSmem, allowed);
+    const cudaError_t e = allow_smem(prefill_kernel<T, D, I8, MOD, kFine>, S::kSmem, allowed);
     if (e != cudaSuccess) return e;
-    prefill_kernel<T, D, I8, MOD><<<dim3(p.groups, a.pool.H, a.batch), kThreads, S::kSmem, s>>>(a);
+    prefill_kernel<T, D, I8, MOD, kFine><<<dim3(p.groups, a.pool.H, a.batch), kThreads, S::kSmem, s>>>(a);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cudaGetLastError();
+}
+
+template <typename T, int D, bool I8, bool MOD>
+cudaError_t launch_m(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+    // fp16 queries that are rotated here lose as much by one rounding as the output by its own (error 4.2e-4, and 2.5e-4
+    // with a second part, where the output's rounding alone is 2.1e-4; bf16 outputs do not notice). At head_dim 64 a
+    // second part costs 10 %; at 128 it would leave room for tiles of 64 tokens only (1211 us for 725), at 256 for none.
+    if constexpr (!std::is_same<T, __nv_bfloat16>::value && D == 64)
+        if (a.rope.rot > 0) return launch_f<T, D, I8, MOD, true>(a, p, s);
+    return launch_f<T, D, I8, MOD, false>(a, p, s);
 }
 
 template <typename T, int D>
 cudaError_t launch_d(const AttendArgs& a, const AttendPlan& p, int format, cudaStream_t s) {
     const bool mod = a.cap > 0.0f || a.slopes;
-    cudaError_t e;
-    if (format == TQ_KV8_INT8) e = mod ? launch_m<T, D, true, true>(a, p, s) : launch_m<T, D, true, false>(a, p, s);
-    else e = mod ? launch_m<T, D, false, true>(a, p, s) : launch_m<T, D, false, false>(a, p, s);
-    return e;
+    if (format == TQ_KV8_INT8) return mod ? launch_m<T, D, true, true>(a, p, s) : launch_m<T, D, true, false>(a, p, s);
+    return mod ? launch_m<T, D, false, true>(a, p, s) : launch_m<T, D, false, false>(a, p, s);
 }
 
 template <typename T>
