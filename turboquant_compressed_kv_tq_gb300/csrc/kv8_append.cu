@@ -12,9 +12,11 @@
 // computed once, in shared memory: they are what a rotation costs. Nothing else is
 // held: the codes come from a second look at the input, which is still in the L1
 // cache, or at worst in the L2. (With the block in registers instead, the few CTAs
-// that fit an SM left it waiting: 28 us for the chunk below, 49 with more heads.)
+// that fit an SM left it waiting: 28 us for the first case below, 49 with more heads.)
 //
-// Bound: memory (2 or 4 bytes read and 1 written a value).
+// Bound: memory (2 or 4 bytes read and 1 written a value), but for rotated keys
+// instructions. Measured: 8192 tokens of 8 heads of 128, bf16, blocks of 64: 25 us (2.0
+// TB/s; 15 unrotated); 6 x 4096 tokens of 4 heads of 256, f32, blocks of 128: 80 us (3.1).
 #include "kv8_device.cuh"
 
 namespace tq {
