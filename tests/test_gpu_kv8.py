@@ -460,6 +460,50 @@ def test_attention_violations_are_flagged(L):
     assert ((out[0].double() - want).abs() <= ref.bound(want, wv, size, BF16, 256, float(v.abs().max()), 64)).all()
 
 
+@pytest.mark.parametrize("L,G", [(1, 1), (3, 4), (60, 1), (60, 4)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_attention_rotation_positions(L, G, inter):
+    """Queries rotated to positions of the caller's, far ones among them; part of the head, and a scale."""
+    D, BT, N = 128, 32, 200
+    c = filled_cache(8, 2, BT, D, E4M3, 100)
+    table = shuffled_table(1, 8, 8, 101)
+    pos = torch.randint(0, 1 << 29, (1, L), generator=gen(102), device=DEV, dtype=torch.int32)
+    rope = tq.Rope.of_base(96, 1e6, interleaved=inter, scale=0.75)
+    for dtype in (BF16, F16):
+        q = torch.randn(1, 2 * G, L, D, generator=gen(103), device=DEV).to(dtype)
+        out = attend(c, q, [N], table, rope=rope, positions=pos)
+        check_attention(c, q, out, out, [N], [L], table, rope=rope, positions=pos)
+
+
+@pytest.mark.parametrize("L", [1, 5, 70])
+def test_attention_of_a_layer_and_with_a_negative_scale(L):
+    D, BT, N = 64, 16, 150
+    c = tq.KV8Cache(3, 10, BT, 1, D)
+    one = filled_cache(10, 1, BT, D, E4M3, 110)
+    for t, o in zip((c.k_codes, c.v_codes, c.k_scales, c.v_scales), (one.k_codes, one.v_codes, one.k_scales, one.v_scales)):
+        t[1] = o[0]
+    table = torch.arange(10, dtype=torch.int32, device=DEV).view(1, 10)
+    q = torch.randn(1, 4, L, D, generator=gen(111), device=DEV).to(BF16)
+    for scale in (0.2, -0.2):
+        out = c.attention(1, q, i32([N]), table, 10, N, scale=scale)
+        check_attention(one, q, out, out, [N], [L], table, scale=scale)
+        assert torch.equal(out, attend(one, q, [N], table, scale=scale))
+    # without a table, the blocks in order
+    assert torch.equal(c.attention(1, q, i32([N]), None, 10, N), attend(one, q, [N], table))
+
+
+@pytest.mark.parametrize("L", [1, 9, 300])
+def test_attention_over_nothing(L):
+    c = filled_cache(4, 2, 16, 128, INT8, 120)
+    q = torch.randn(3, 4, L, 128, generator=gen(121), device=DEV).to(F16)
+    out = torch.ones_like(q)
+    c.attention(0, q, i32([0, 0, 0]), None, 1, 0, out=out)
+    assert (out == 0).all()
+    out = torch.ones_like(q)
+    c.attention(0, q, i32([0, 16, 0]), None, 1, 16, out=out, q_lens=i32([L, 0, 1]))
+    assert (out[0] == 0).all() and (out[1] == 1).all() and (out[2, :, :1] == 0).all() and (out[2, :, 1:] == 1).all()
+
+
 # ------------------------------------------------------------------ together, as a program uses them
 
 def serve(c, table, k, v, q, steps, rope, L0, **kw):
