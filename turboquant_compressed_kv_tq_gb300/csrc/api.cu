@@ -7,6 +7,7 @@
 #include <mutex>
 #include <new>
 
+#include "kv8.h"
 #include "tq_internal.h"
 
 namespace tq {

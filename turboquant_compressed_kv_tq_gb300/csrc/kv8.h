@@ -6,6 +6,10 @@
 #include "tq_internal.h"
 
 namespace tq {
+
+// The current device's error word and its number of SMs (either may be null): api.cu.
+tq_status device_state(unsigned** err, int* num_sms);
+
 namespace kv8 {
 
 // One layer of an 8-bit cache and the block table over it.

@@ -236,9 +236,6 @@ cudaError_t launch_prefill(const DecodeArgs& a, const uint4* qfrag, cudaStream_t
 
 extern std::atomic<uint64_t> g_launches;
 
-// The current device's error word and its number of SMs (either may be null).
-tq_status device_state(unsigned** err, int* num_sms);
-
 // Looks up, once per device with that device current, the device address of
 // the fixed scratch array of tq_decode_attention_noalloc; loading the array's
 // module is what reserves its memory on the device.
