@@ -46,7 +46,7 @@ struct AttendArgs {
     Pool pool;
     Rows q, out;
     Rope rope;
-    int batch, Hq, G, L;
+    int batch, G, L;
     const int32_t *seq, *qlens;
     int max_seq;
     float scale, cap;

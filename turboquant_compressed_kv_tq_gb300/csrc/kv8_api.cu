@@ -206,7 +206,6 @@ tq_status tq_kv8_attention(const tq_kv8_cache* cache, int layer, const tq_rows* 
     a.q = make_rows(q);
     a.out = make_rows(out);
     a.batch = batch;
-    a.Hq = num_q_heads;
     a.G = num_q_heads / cache->num_kv_heads;
     a.L = q_len;
     a.seq = seq_lens;

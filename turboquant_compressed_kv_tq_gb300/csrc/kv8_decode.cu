@@ -240,410 +240,410 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
     int pair = s_pair;
     long long pair_at = s_at;
     for (long long from = begin; from < end;) {
-    const int b = pair / A.groups, grp = pair % A.groups;
-    const Seq seq(A, b);
-    const Tiles tiles(A, seq, b, grp, kRows);
-    const int N = seq.N, nq = seq.nq, rows = tiles.rows, lo_max = tiles.lo_max, p_min = N - nq + tiles.l_first;
-    const int unit_tiles = tiles.count(), unit_room = tiles.room(A);
-    if (unit_room == 0) {
-        ++pair;
-        continue;
-    }
-    const long long in_pair = from - pair_at;
-    const int h = static_cast<int>(in_pair < (1ll << 31) ? static_cast<long long>(static_cast<unsigned>(in_pair) / static_cast<unsigned>(unit_room))
-                                                         : in_pair / unit_room);
-    const int i_begin = static_cast<int>(in_pair - static_cast<long long>(h) * unit_room);
-    const int i_room = static_cast<int>(min(static_cast<long long>(unit_room - i_begin), end - from));
-    auto next_segment = [&]() {
-        from += i_room;
-        if (from == pair_at + static_cast<long long>(unit_room) * P.H) {
-            pair_at = from;
+        const int b = pair / A.groups, grp = pair % A.groups;
+        const Seq seq(A, b);
+        const Tiles tiles(A, seq, b, grp, kRows);
+        const int N = seq.N, nq = seq.nq, rows = tiles.rows, lo_max = tiles.lo_max, p_min = N - nq + tiles.l_first;
+        const int unit_tiles = tiles.count(), unit_room = tiles.room(A);
+        if (unit_room == 0) {
             ++pair;
+            continue;
         }
-    };
-    if (i_begin >= unit_tiles) {   // only what is counted behind a unit's tiles
-        next_segment();
-        continue;
-    }
-    const int i_all = min(i_room, unit_tiles - i_begin);                                               // tiles of this segment
-    const int i_end = min(i_begin + i_all, tiles.n1 + tiles.n2);                                        // without the one that is none
-    const int per = (max(i_end - i_begin, 0) + S::kWarps - 1) / S::kWarps;   // tiles of a warp, consecutive
-    const int w_begin = min(i_begin + warp * per, i_end), w_end = min(w_begin + per, i_end);
-    const int64_t unit = static_cast<int64_t>(pair) * P.H + h;
-    if (tid == 0 && i_begin == 0 && gridDim.x > 1)   // the shares that the unit lies in
-        *reinterpret_cast<int2*>(A.unit_shares + 2 * unit) =
-            make_int2(blockIdx.x, static_cast<int>((pair_at + static_cast<long long>(h) * unit_room + unit_tiles - 1) / share));
+        const long long in_pair = from - pair_at;
+        const int h = static_cast<int>(in_pair < (1ll << 31) ? static_cast<long long>(static_cast<unsigned>(in_pair) / static_cast<unsigned>(unit_room))
+                                                             : in_pair / unit_room);
+        const int i_begin = static_cast<int>(in_pair - static_cast<long long>(h) * unit_room);
+        const int i_room = static_cast<int>(min(static_cast<long long>(unit_room - i_begin), end - from));
+        auto next_segment = [&]() {
+            from += i_room;
+            if (from == pair_at + static_cast<long long>(unit_room) * P.H) {
+                pair_at = from;
+                ++pair;
+            }
+        };
+        if (i_begin >= unit_tiles) {   // only what is counted behind a unit's tiles
+            next_segment();
+            continue;
+        }
+        const int i_all = min(i_room, unit_tiles - i_begin);                                               // tiles of this segment
+        const int i_end = min(i_begin + i_all, tiles.n1 + tiles.n2);                                        // without the one that is none
+        const int per = (max(i_end - i_begin, 0) + S::kWarps - 1) / S::kWarps;   // tiles of a warp, consecutive
+        const int w_begin = min(i_begin + warp * per, i_end), w_end = min(w_begin + per, i_end);
+        const int64_t unit = static_cast<int64_t>(pair) * P.H + h;
+        if (tid == 0 && i_begin == 0 && gridDim.x > 1)   // the shares that the unit lies in
+            *reinterpret_cast<int2*>(A.unit_shares + 2 * unit) =
+                make_int2(blockIdx.x, static_cast<int>((pair_at + static_cast<long long>(h) * unit_room + unit_tiles - 1) / share));
 
-    // ---------------- the copies of the first tiles, on their way while the queries are prepared
-    const bool busy = w_begin < w_end && !dead;
-    const int64_t unit_bytes = static_cast<int64_t>(P.BT) * D;
+        // ---------------- the copies of the first tiles, on their way while the queries are prepared
+        const bool busy = w_begin < w_end && !dead;
+        const int64_t unit_bytes = static_cast<int64_t>(P.BT) * D;
 
-    // lane k holds the block and scales of the warp's tile base + k, and of the 32 after those
-    int base = w_begin;
-    int64_t id = -1, id_next = -1;
-    uint32_t meta = 0, meta_next = 0;   // scale bytes, and whether there is a block
-    auto look_up = [&](int from, int64_t& x, uint32_t& sc) {
-        x = -1;
-        sc = 0;
-        const int i = from + lane;
-        if (i < w_end) {
-            const int lb = (tiles.at(i) << 4) >> P.bt_shift;
-            const int64_t at = P.table ? P.table[b * static_cast<int64_t>(P.max_blocks) + lb] : b * static_cast<int64_t>(P.max_blocks) + lb;
-            if (at >= 0 && at < P.num_blocks) {
-                x = at * P.H + h;
-                sc = P.kx[x] | (P.vx[x] << 8) | 0x10000u;
-            } else {
-                atomicOr(A.err, TQ_DEVERR_BLOCK);
+        // lane k holds the block and scales of the warp's tile base + k, and of the 32 after those
+        int base = w_begin;
+        int64_t id = -1, id_next = -1;
+        uint32_t meta = 0, meta_next = 0;   // scale bytes, and whether there is a block
+        auto look_up = [&](int from, int64_t& x, uint32_t& sc) {
+            x = -1;
+            sc = 0;
+            const int i = from + lane;
+            if (i < w_end) {
+                const int lb = (tiles.at(i) << 4) >> P.bt_shift;
+                const int64_t at = P.table ? P.table[b * static_cast<int64_t>(P.max_blocks) + lb] : b * static_cast<int64_t>(P.max_blocks) + lb;
+                if (at >= 0 && at < P.num_blocks) {
+                    x = at * P.H + h;
+                    sc = P.kx[x] | (P.vx[x] << 8) | 0x10000u;
+                } else {
+                    atomicOr(A.err, TQ_DEVERR_BLOCK);
+                }
             }
-        }
-    };
-    constexpr int kStep = S::kTileBytes * S::kU, kU = S::kU;
-    unsigned char* ring = smem + warp * S::kStages * kStep;
-    uint32_t ahead[S::kStages - 1][kU];   // meta of the tiles on their way
-    // start the copies of the kU tiles from i (none behind the warp's last tile); their metas
-    auto fetch = [&](int i, uint32_t (&mt)[kU]) {
-        const unsigned st = puts % S::kStages;
-        if (i < w_end) {
-            if (lane == 0) tc::mbar_expect_tx(&bars[st], i + kU <= w_end ? kStep : S::kTileBytes);
-            ++puts;
-        }
+        };
+        constexpr int kStep = S::kTileBytes * S::kU, kU = S::kU;
+        unsigned char* ring = smem + warp * S::kStages * kStep;
+        uint32_t ahead[S::kStages - 1][kU];   // meta of the tiles on their way
+        // start the copies of the kU tiles from i (none behind the warp's last tile); their metas
+        auto fetch = [&](int i, uint32_t (&mt)[kU]) {
+            const unsigned st = puts % S::kStages;
+            if (i < w_end) {
+                if (lane == 0) tc::mbar_expect_tx(&bars[st], i + kU <= w_end ? kStep : S::kTileBytes);
+                ++puts;
+            }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            mt[u] = 0;
-            if (i + u >= w_end) continue;
-            if (i + u - base == 32) {
-                base = i + u;
-                id = id_next;
-                meta = meta_next;
-                look_up(base + 32, id_next, meta_next);
+            for (int u = 0; u < kU; ++u) {
+                mt[u] = 0;
+                if (i + u >= w_end) continue;
+                if (i + u - base == 32) {
+                    base = i + u;
+                    id = id_next;
+                    meta = meta_next;
+                    look_up(base + 32, id_next, meta_next);
+                }
+                const int64_t x = __shfl_sync(0xffffffffu, id, i + u - base);
+                mt[u] = __shfl_sync(0xffffffffu, meta, i + u - base);
+                if (lane == 0) {   // where there is no block: any block, which nobody sees
+                    const int64_t off = (x < 0 ? 0 : x) * unit_bytes + static_cast<int64_t>((tiles.at(i + u) << 4) & (P.BT - 1)) * D;
+                    unsigned char* dst = ring + st * kStep + u * S::kTileBytes;
+                    tc::bulk_g2s(dst, P.kc + off, 16 * D, &bars[st]);
+                    tc::bulk_g2s(dst + 16 * D, P.vc + off, 16 * D, &bars[st]);
+                }
             }
-            const int64_t x = __shfl_sync(0xffffffffu, id, i + u - base);
-            mt[u] = __shfl_sync(0xffffffffu, meta, i + u - base);
-            if (lane == 0) {   // where there is no block: any block, which nobody sees
-                const int64_t off = (x < 0 ? 0 : x) * unit_bytes + static_cast<int64_t>((tiles.at(i + u) << 4) & (P.BT - 1)) * D;
-                unsigned char* dst = ring + st * kStep + u * S::kTileBytes;
-                tc::bulk_g2s(dst, P.kc + off, 16 * D, &bars[st]);
-                tc::bulk_g2s(dst + 16 * D, P.vc + off, 16 * D, &bars[st]);
-            }
-        }
-    };
-    if (busy) {
-        look_up(base, id, meta);
-        look_up(base + 32, id_next, meta_next);
+        };
+        if (busy) {
+            look_up(base, id, meta);
+            look_up(base + 32, id_next, meta_next);
 #pragma unroll
-        for (int k = 0; k < S::kStages - 1; ++k) fetch(w_begin + k * kU, ahead[k]);
-    }
+            for (int k = 0; k < S::kStages - 1; ++k) fetch(w_begin + k * kU, ahead[k]);
+        }
 
-    // ---------------- the queries: rotated, scaled by a power of two, fp16
-    if (i_begin < i_end) {
-        constexpr int J = D / 16;   // chunk pairs of a row: J consecutive lanes
-        for (int it = tid; it < kRows * J; it += kThreads) {
-            const int r = it / J, j = it % J;
-            const int rr = grp * kRows + r, l = rr / A.G;
-            float xa[8] = {}, xb[8] = {};
-            int a0, b0;
-            chunk_pair(j, A.rope.rot, A.rope.inter, a0, b0);
-            if (r < rows && l < nq) {
-                const T* q = static_cast<const T*>(A.q.data) + b * A.q.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.q.sh + l * A.q.st;
-                load8(q + a0, xa);
-                load8(q + b0, xb);
-                if (A.rope.rot > 0)
-                    rotate_pair(xa, xb, j, A.rope, s_turns, A.rope.positions ? A.rope.positions[static_cast<int64_t>(b) * A.L + l] : N - nq + l);
+        // ---------------- the queries: rotated, scaled by a power of two, fp16
+        if (i_begin < i_end) {
+            constexpr int J = D / 16;   // chunk pairs of a row: J consecutive lanes
+            for (int it = tid; it < kRows * J; it += kThreads) {
+                const int r = it / J, j = it % J;
+                const int rr = grp * kRows + r, l = rr / A.G;
+                float xa[8] = {}, xb[8] = {};
+                int a0, b0;
+                chunk_pair(j, A.rope.rot, A.rope.inter, a0, b0);
+                if (r < rows && l < nq) {
+                    const T* q = static_cast<const T*>(A.q.data) + b * A.q.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.q.sh + l * A.q.st;
+                    load8(q + a0, xa);
+                    load8(q + b0, xb);
+                    if (A.rope.rot > 0)
+                        rotate_pair(xa, xb, j, A.rope, s_turns, A.rope.positions ? A.rope.positions[static_cast<int64_t>(b) * A.L + l] : N - nq + l);
+                }
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(xa[i]), fabsf(xb[i])));
+#pragma unroll
+                for (int o = J / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // to [1, 2): fp16 then keeps 11 bits down to 2^-14 of the row's largest
+                const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126), 126);
+                const float f = exp2i(-e);
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    uint2 lo;
+                    *s_frag(0, r, a0 + i) = split(xa[i] * f, xa[i + 1] * f, xa[i + 2] * f, xa[i + 3] * f, lo);
+                    if constexpr (kFine) *s_frag(1, r, a0 + i) = lo;
+                    *s_frag(0, r, b0 + i) = split(xb[i] * f, xb[i + 1] * f, xb[i + 2] * f, xb[i + 3] * f, lo);
+                    if constexpr (kFine) *s_frag(1, r, b0 + i) = lo;
+                }
+                if (j == 0) s_fac[r] = A.scale * exp2i(e);
             }
-            float top = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(xa[i]), fabsf(xb[i])));
-#pragma unroll
-            for (int o = J / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // to [1, 2): fp16 then keeps 11 bits down to 2^-14 of the row's largest
-            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126), 126);
-            const float f = exp2i(-e);
-#pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                uint2 lo;
-                *s_frag(0, r, a0 + i) = split(xa[i] * f, xa[i + 1] * f, xa[i + 2] * f, xa[i + 3] * f, lo);
-                if constexpr (kFine) *s_frag(1, r, a0 + i) = lo;
-                *s_frag(0, r, b0 + i) = split(xb[i] * f, xb[i + 1] * f, xb[i + 2] * f, xb[i + 3] * f, lo);
-                if constexpr (kFine) *s_frag(1, r, b0 + i) = lo;
-            }
-            if (j == 0) s_fac[r] = A.scale * exp2i(e);
         }
-    }
-    if (tid < kRows) s_sight[tid] = sight_of(A, seq, b, min((grp * kRows + tid) / A.G, tiles.l_last));
-    __syncthreads();
+        if (tid < kRows) s_sight[tid] = sight_of(A, seq, b, min((grp * kRows + tid) / A.G, tiles.l_last));
+        __syncthreads();
 
-    float acc[NT][S::kMT][4];
-    float m[NT][2], l_sum[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int j = 0; j < S::kMT; ++j) acc[nt][j][0] = acc[nt][j][1] = acc[nt][j][2] = acc[nt][j][3] = 0.0f;
-        m[nt][0] = m[nt][1] = kNone;
-        l_sum[nt][0] = l_sum[nt][1] = 0.0f;
-    }
-    if (busy) {
-        uint32_t qf[NT][D / 16][2];
-        float fac[NT][2], slope[NT][2];
+        float acc[NT][S::kMT][4];
+        float m[NT][2], l_sum[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int ks = 0; ks < (S::kQShared ? 0 : D / 16); ++ks) {
-                const uint2 f = reinterpret_cast<const uint2*>(smem + S::kSmem)[(nt * (D / 16) + ks) * 32 + lane];
-                qf[nt][ks][0] = f.x;
-                qf[nt][ks][1] = f.y;
+            for (int j = 0; j < S::kMT; ++j) acc[nt][j][0] = acc[nt][j][1] = acc[nt][j][2] = acc[nt][j][3] = 0.0f;
+            m[nt][0] = m[nt][1] = kNone;
+            l_sum[nt][0] = l_sum[nt][1] = 0.0f;
+        }
+        if (busy) {
+            uint32_t qf[NT][D / 16][2];
+            float fac[NT][2], slope[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int ks = 0; ks < (S::kQShared ? 0 : D / 16); ++ks) {
+                    const uint2 f = reinterpret_cast<const uint2*>(smem + S::kSmem)[(nt * (D / 16) + ks) * 32 + lane];
+                    qf[nt][ks][0] = f.x;
+                    qf[nt][ks][1] = f.y;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * nt + 2 * c + e;
+                    fac[nt][e] = s_fac[r];
+                    const int rr = grp * kRows + r;
+                    slope[nt][e] = A.slopes && r < rows ? A.slopes[h * A.G + rr % A.G] * kLog2e : 0.0f;
+                }
             }
+            const bool plain = A.cap <= 0.0f && !A.slopes;
+            const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
+            for (int i = w_begin; i < w_end; i += kU) {
+                uint32_t mt[kU];
+                int t0[kU];   // a tile behind the warp's last one: behind the sequence's end
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    mt[u] = ahead[0][u];
+                    t0[u] = i + u < w_end ? tiles.at(i + u) << 4 : N;
+#pragma unroll
+                    for (int k = 0; k < S::kStages - 2; ++k) ahead[k][u] = ahead[k + 1][u];
+                }
+                __syncwarp();   // every lane has read the stage that is filled now
+                fetch(i + (S::kStages - 1) * kU, ahead[S::kStages - 2]);
+                const unsigned st = gets % S::kStages;
+                dead = !arrived(&bars[st], (gets / S::kStages) & 1);
+                if (__any_sync(0xffffffffu, dead)) {
+                    dead = true;
+                    break;
+                }
+                ++gets;
+                const unsigned char* src = ring + st * kStep;
+                // ---------------- scores
+                float sc[kU][NT][4];
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) sc[u][nt][0] = sc[u][nt][1] = sc[u][nt][2] = sc[u][nt][3] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < S::kKL; ++k) {
+                    uint32_t w0[kU][4], w1[kU][4];
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) {
+                        load_words(w0[u], src + u * S::kTileBytes + g * D + 16 * (S::kKL * c + k));
+                        load_words(w1[u], src + u * S::kTileBytes + (g + 8) * D + 16 * (S::kKL * c + k));
+                    }
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint2 fine[NT], now[NT];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            now[nt] = S::kQShared ? reinterpret_cast<const uint2*>(smem + S::kSmem)[(nt * (D / 16) + 4 * k + w) * 32 + lane]
+                                                  : make_uint2(qf[nt][4 * k + w][0], qf[nt][4 * k + w][1]);
+                        if constexpr (kFine)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                fine[nt] = reinterpret_cast<const uint2*>(smem + S::kSmem)[((NT + nt) * (D / 16) + 4 * k + w) * 32 + lane];
+#pragma unroll
+                        for (int u = 0; u < kU; ++u) {
+                            uint32_t a0, a1, a2, a3;
+                            codes_f16<I8>(w0[u][w], a0, a2);
+                            codes_f16<I8>(w1[u][w], a1, a3);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma16816(sc[u][nt], a0, a1, a2, a3, now[nt].x, now[nt].y);
+                                if constexpr (kFine) mma16816(sc[u][nt], a0, a1, a2, a3, fine[nt].x, fine[nt].y);
+                            }
+                        }
+                    }
+                }
+                // ---------------- u = log2(e) score + log2(value scale), masked
+                float lg[kU][NT][4];
+                bool pass = false;
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int kx = mt[u] & 0xFF, vx = (mt[u] >> 8) & 0xFF;
+                    const bool here = mt[u] >> 16;
+                    const float ks2 = exp2i(kx == 0 ? -126 : kx - 127), lv = static_cast<float>(vx - 127);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {   // e: token g + 8 (e >> 1), row 2c + (e & 1)
+                            const float s = sc[u][nt][e] * (fac[nt][e & 1] * ks2);
+                            if (plain) {
+                                lg[u][nt][e] = fmaf(s, kLog2e, lv);
+                            } else {
+                                float y = s * kLog2e;
+                                if (A.cap > 0.0f) y = fmaf(-2.0f * cap2, rcp(1.0f + ex2(s * cap_in)), cap2);   // cap tanh(s / cap)
+                                if (A.slopes) {
+                                    const int p = s_sight[8 * nt + 2 * c + (e & 1)].p;
+                                    y -= slope[nt][e & 1] * fabsf(static_cast<float>(p - (t0[u] + g + 8 * (e >> 1))));
+                                }
+                                lg[u][nt][e] = y + lv;
+                            }
+                        }
+                    if (!(here && t0[u] + 15 <= p_min && t0[u] >= lo_max)) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int t = t0[u] + g + 8 * (e >> 1);
+                                if (!(here && t < N && s_sight[8 * nt + 2 * c + (e & 1)].sees(t))) lg[u][nt][e] = -INFINITY;
+                            }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) pass |= lg[u][nt][e] > m[nt][e & 1] + kGap;
+                }
+                // ---------------- the reference moves only when a score passes it by the gap
+                if (__any_sync(0xffffffffu, pass)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = fmaxf(lg[0][nt][e], lg[0][nt][e + 2]);
+                            if constexpr (kU == 2) x = fmaxf(x, fmaxf(lg[1][nt][e], lg[1][nt][e + 2]));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                            x = fmaxf(x, m[nt][e]);
+                            const float alpha = ex2(m[nt][e] - x);
+                            m[nt][e] = x;
+                            l_sum[nt][e] *= alpha;
+#pragma unroll
+                            for (int j = 0; j < S::kMT; ++j) {
+                                acc[nt][j][e] *= alpha;
+                                acc[nt][j][e + 2] *= alpha;
+                            }
+                        }
+                }
+                // ---------------- p, its sum, and p as the second operand (rows on N)
+                uint32_t pb[kU][NT][2];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int vx = (mt[u] >> 8) & 0xFF;
+                    const float iv = exp2i(127 - vx < -126 ? -126 : min(127 - vx, 126));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            p[e] = ex2(lg[u][nt][e] - m[nt][e & 1]);
+                            l_sum[nt][e & 1] = fmaf(p[e], iv, l_sum[nt][e & 1]);
+                        }
+                        pb[u][nt][0] = transpose8x8(pack_out<__half>(p[0], p[1]));
+                        pb[u][nt][1] = transpose8x8(pack_out<__half>(p[2], p[3]));
+                    }
+                }
+                // ---------------- O^T += V^T P
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+#pragma unroll
+                    for (int k = 0; k < S::kVL; ++k) {
+                        const unsigned char* from_v = src + u * S::kTileBytes + 16 * D + 32 * S::kVW * k + 4 * S::kVW * g;
+                        uint32_t vw[4][S::kVW];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) load_words(vw[t], from_v + (2 * c + (t & 1) + 8 * (t >> 1)) * D);
+                        // codes behind the sequence's end, or of no block, may be anything: their weight is 0, so they have to be finite
+                        if (t0[u] + 16 > N || !(mt[u] >> 16)) {
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                if (t0[u] + 2 * c + (t & 1) + 8 * (t >> 1) >= N || !(mt[u] >> 16))
+#pragma unroll
+                                    for (int w = 0; w < S::kVW; ++w) vw[t][w] = 0;
+                        }
+#pragma unroll
+                        for (int w = 0; w < S::kVW; ++w) {
+                            uint32_t x[2][4];   // [token pair][coordinate]: fp16 pairs of two tokens
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                const uint32_t a = vw[2 * t][w], d = vw[2 * t + 1][w];
+                                codes_f16<I8>(__byte_perm(a, d, 0x5140), x[t][0], x[t][1]);
+                                codes_f16<I8>(__byte_perm(a, d, 0x7362), x[t][2], x[t][3]);
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma16816(acc[nt][(k * S::kVW + w) * 2], x[0][0], x[0][1], x[1][0], x[1][1], pb[u][nt][0], pb[u][nt][1]);
+                                mma16816(acc[nt][(k * S::kVW + w) * 2 + 1], x[0][2], x[0][3], x[1][2], x[1][3], pb[u][nt][0], pb[u][nt][1]);
+                            }
+                        }
+                    }
+            }
+        }
+
+        if (dead) {   // what is in flight ends (or is given up) before its shared memory is used for anything else
+            if (lane == 0) atomicOr(A.err, TQ_DEVERR_TIMEOUT);
+            for (; gets < puts; ++gets) (void)arrived(&bars[gets % S::kStages], (gets / S::kStages) & 1);
+        }
+        // ---------------- the CTA's state of each row: the states of the warps that had tiles, at their largest reference
+        const int had = per > 0 ? (i_end - i_begin + per - 1) / per : 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = l_sum[nt][e];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                if (g == 0) {
+                    s_m[warp][8 * nt + 2 * c + e] = m[nt][e];
+                    s_l[warp][8 * nt + 2 * c + e] = x;
+                }
+            }
+        __syncthreads();   // and the queries in shared memory are done with
+        float* s_o = reinterpret_cast<float*>(smem);   // [warps][kRows][D]
+        if (warp < had)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * nt + 2 * c + e;
-                fac[nt][e] = s_fac[r];
-                const int rr = grp * kRows + r;
-                slope[nt][e] = A.slopes && r < rows ? A.slopes[h * A.G + rr % A.G] * kLog2e : 0.0f;
-            }
-        }
-        const bool plain = A.cap <= 0.0f && !A.slopes;
-        const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
-        for (int i = w_begin; i < w_end; i += kU) {
-            uint32_t mt[kU];
-            int t0[kU];   // a tile behind the warp's last one: behind the sequence's end
+                float top = s_m[0][r];
+                for (int w = 1; w < had; ++w) top = fmaxf(top, s_m[w][r]);
+                const float f = ex2(m[nt][e] - top);
+                float* o = s_o + (warp * kRows + r) * D;
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                mt[u] = ahead[0][u];
-                t0[u] = i + u < w_end ? tiles.at(i + u) << 4 : N;
-#pragma unroll
-                for (int k = 0; k < S::kStages - 2; ++k) ahead[k][u] = ahead[k + 1][u];
-            }
-            __syncwarp();   // every lane has read the stage that is filled now
-            fetch(i + (S::kStages - 1) * kU, ahead[S::kStages - 2]);
-            const unsigned st = gets % S::kStages;
-            dead = !arrived(&bars[st], (gets / S::kStages) & 1);
-            if (__any_sync(0xffffffffu, dead)) {
-                dead = true;
-                break;
-            }
-            ++gets;
-            const unsigned char* src = ring + st * kStep;
-            // ---------------- scores
-            float sc[kU][NT][4];
-#pragma unroll
-            for (int u = 0; u < kU; ++u)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) sc[u][nt][0] = sc[u][nt][1] = sc[u][nt][2] = sc[u][nt][3] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < S::kKL; ++k) {
-                uint32_t w0[kU][4], w1[kU][4];
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    load_words(w0[u], src + u * S::kTileBytes + g * D + 16 * (S::kKL * c + k));
-                    load_words(w1[u], src + u * S::kTileBytes + (g + 8) * D + 16 * (S::kKL * c + k));
-                }
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint2 fine[NT], now[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        now[nt] = S::kQShared ? reinterpret_cast<const uint2*>(smem + S::kSmem)[(nt * (D / 16) + 4 * k + w) * 32 + lane]
-                                              : make_uint2(qf[nt][4 * k + w][0], qf[nt][4 * k + w][1]);
-                    if constexpr (kFine)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            fine[nt] = reinterpret_cast<const uint2*>(smem + S::kSmem)[((NT + nt) * (D / 16) + 4 * k + w) * 32 + lane];
-#pragma unroll
-                    for (int u = 0; u < kU; ++u) {
-                        uint32_t a0, a1, a2, a3;
-                        codes_f16<I8>(w0[u][w], a0, a2);
-                        codes_f16<I8>(w1[u][w], a1, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(sc[u][nt], a0, a1, a2, a3, now[nt].x, now[nt].y);
-                            if constexpr (kFine) mma16816(sc[u][nt], a0, a1, a2, a3, fine[nt].x, fine[nt].y);
-                        }
-                    }
-                }
-            }
-            // ---------------- u = log2(e) score + log2(value scale), masked
-            float lg[kU][NT][4];
-            bool pass = false;
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int kx = mt[u] & 0xFF, vx = (mt[u] >> 8) & 0xFF;
-                const bool here = mt[u] >> 16;
-                const float ks2 = exp2i(kx == 0 ? -126 : kx - 127), lv = static_cast<float>(vx - 127);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {   // e: token g + 8 (e >> 1), row 2c + (e & 1)
-                        const float s = sc[u][nt][e] * (fac[nt][e & 1] * ks2);
-                        if (plain) {
-                            lg[u][nt][e] = fmaf(s, kLog2e, lv);
-                        } else {
-                            float y = s * kLog2e;
-                            if (A.cap > 0.0f) y = fmaf(-2.0f * cap2, rcp(1.0f + ex2(s * cap_in)), cap2);   // cap tanh(s / cap)
-                            if (A.slopes) {
-                                const int p = s_sight[8 * nt + 2 * c + (e & 1)].p;
-                                y -= slope[nt][e & 1] * fabsf(static_cast<float>(p - (t0[u] + g + 8 * (e >> 1))));
-                            }
-                            lg[u][nt][e] = y + lv;
-                        }
-                    }
-                if (!(here && t0[u] + 15 <= p_min && t0[u] >= lo_max)) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int t = t0[u] + g + 8 * (e >> 1);
-                            if (!(here && t < N && s_sight[8 * nt + 2 * c + (e & 1)].sees(t))) lg[u][nt][e] = -INFINITY;
-                        }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) pass |= lg[u][nt][e] > m[nt][e & 1] + kGap;
-            }
-            // ---------------- the reference moves only when a score passes it by the gap
-            if (__any_sync(0xffffffffu, pass)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(lg[0][nt][e], lg[0][nt][e + 2]);
-                        if constexpr (kU == 2) x = fmaxf(x, fmaxf(lg[1][nt][e], lg[1][nt][e + 2]));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        x = fmaxf(x, m[nt][e]);
-                        const float alpha = ex2(m[nt][e] - x);
-                        m[nt][e] = x;
-                        l_sum[nt][e] *= alpha;
-#pragma unroll
-                        for (int j = 0; j < S::kMT; ++j) {
-                            acc[nt][j][e] *= alpha;
-                            acc[nt][j][e + 2] *= alpha;
-                        }
-                    }
-            }
-            // ---------------- p, its sum, and p as the second operand (rows on N)
-            uint32_t pb[kU][NT][2];
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int vx = (mt[u] >> 8) & 0xFF;
-                const float iv = exp2i(127 - vx < -126 ? -126 : min(127 - vx, 126));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[e] = ex2(lg[u][nt][e] - m[nt][e & 1]);
-                        l_sum[nt][e & 1] = fmaf(p[e], iv, l_sum[nt][e & 1]);
-                    }
-                    pb[u][nt][0] = transpose8x8(pack_out<__half>(p[0], p[1]));
-                    pb[u][nt][1] = transpose8x8(pack_out<__half>(p[2], p[3]));
-                }
-            }
-            // ---------------- O^T += V^T P
-#pragma unroll
-            for (int u = 0; u < kU; ++u)
-#pragma unroll
-                for (int k = 0; k < S::kVL; ++k) {
-                    const unsigned char* from_v = src + u * S::kTileBytes + 16 * D + 32 * S::kVW * k + 4 * S::kVW * g;
-                    uint32_t vw[4][S::kVW];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) load_words(vw[t], from_v + (2 * c + (t & 1) + 8 * (t >> 1)) * D);
-                    // codes behind the sequence's end, or of no block, may be anything: their weight is 0, so they have to be finite
-                    if (t0[u] + 16 > N || !(mt[u] >> 16)) {
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-                            if (t0[u] + 2 * c + (t & 1) + 8 * (t >> 1) >= N || !(mt[u] >> 16))
-#pragma unroll
-                                for (int w = 0; w < S::kVW; ++w) vw[t][w] = 0;
-                    }
+                for (int k = 0; k < S::kVL; ++k)
 #pragma unroll
                     for (int w = 0; w < S::kVW; ++w) {
-                        uint32_t x[2][4];   // [token pair][coordinate]: fp16 pairs of two tokens
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const uint32_t a = vw[2 * t][w], d = vw[2 * t + 1][w];
-                            codes_f16<I8>(__byte_perm(a, d, 0x5140), x[t][0], x[t][1]);
-                            codes_f16<I8>(__byte_perm(a, d, 0x7362), x[t][2], x[t][3]);
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(acc[nt][(k * S::kVW + w) * 2], x[0][0], x[0][1], x[1][0], x[1][1], pb[u][nt][0], pb[u][nt][1]);
-                            mma16816(acc[nt][(k * S::kVW + w) * 2 + 1], x[0][2], x[0][3], x[1][2], x[1][3], pb[u][nt][0], pb[u][nt][1]);
-                        }
+                        const int j = (k * S::kVW + w) * 2;
+                        const int d = 32 * S::kVW * k + 4 * S::kVW * g + 4 * w;
+                        *reinterpret_cast<float4*>(o + d) =
+                            make_float4(acc[nt][j][e] * f, acc[nt][j][e + 2] * f, acc[nt][j + 1][e] * f, acc[nt][j + 1][e + 2] * f);
                     }
-                }
-        }
-    }
-
-    if (dead) {   // what is in flight ends (or is given up) before its shared memory is used for anything else
-        if (lane == 0) atomicOr(A.err, TQ_DEVERR_TIMEOUT);
-        for (; gets < puts; ++gets) (void)arrived(&bars[gets % S::kStages], (gets / S::kStages) & 1);
-    }
-    // ---------------- the CTA's state of each row: the states of the warps that had tiles, at their largest reference
-    const int had = per > 0 ? (i_end - i_begin + per - 1) / per : 0;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float x = l_sum[nt][e];
-            x += __shfl_xor_sync(0xffffffffu, x, 4);
-            x += __shfl_xor_sync(0xffffffffu, x, 8);
-            x += __shfl_xor_sync(0xffffffffu, x, 16);
-            if (g == 0) {
-                s_m[warp][8 * nt + 2 * c + e] = m[nt][e];
-                s_l[warp][8 * nt + 2 * c + e] = x;
             }
-        }
-    __syncthreads();   // and the queries in shared memory are done with
-    float* s_o = reinterpret_cast<float*>(smem);   // [warps][kRows][D]
-    if (warp < had)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 8 * nt + 2 * c + e;
+        __syncthreads();
+        for (int it = tid; it < rows * (D / 4); it += kThreads) {
+            const int r = it / (D / 4), d = 4 * (it % (D / 4));
+            const int rr = grp * kRows + r, l = rr / A.G;
+            if (l >= nq) continue;
             float top = s_m[0][r];
             for (int w = 1; w < had; ++w) top = fmaxf(top, s_m[w][r]);
-            const float f = ex2(m[nt][e] - top);
-            float* o = s_o + (warp * kRows + r) * D;
-#pragma unroll
-            for (int k = 0; k < S::kVL; ++k)
-#pragma unroll
-                for (int w = 0; w < S::kVW; ++w) {
-                    const int j = (k * S::kVW + w) * 2;
-                    const int d = 32 * S::kVW * k + 4 * S::kVW * g + 4 * w;
-                    *reinterpret_cast<float4*>(o + d) =
-                        make_float4(acc[nt][j][e] * f, acc[nt][j][e + 2] * f, acc[nt][j + 1][e] * f, acc[nt][j + 1][e + 2] * f);
-                }
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float sum = 0.0f;
+            for (int w = 0; w < had; ++w) {
+                const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kRows + r) * D + d);
+                o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+                sum = fmaf(s_l[w][r], ex2(s_m[w][r] - top), sum);
+            }
+            if (i_all == unit_tiles) {
+                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.out.sh + l * A.out.st + d;
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_out<T>(o.x * inv, o.y * inv), pack_out<T>(o.z * inv, o.w * inv));
+            } else {
+                // the unit goes on behind this share (state 1 of the CTA), or began before it (state 0)
+                const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + (i_begin == 0 ? 1 : 0)) * kRows + r;
+                *reinterpret_cast<float4*>(A.part_o + at * D + d) = o;
+                if (d == 0) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(top, sum);
+            }
         }
-    __syncthreads();
-    for (int it = tid; it < rows * (D / 4); it += kThreads) {
-        const int r = it / (D / 4), d = 4 * (it % (D / 4));
-        const int rr = grp * kRows + r, l = rr / A.G;
-        if (l >= nq) continue;
-        float top = s_m[0][r];
-        for (int w = 1; w < had; ++w) top = fmaxf(top, s_m[w][r]);
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float sum = 0.0f;
-        for (int w = 0; w < had; ++w) {
-            const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kRows + r) * D + d);
-            o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-            sum = fmaf(s_l[w][r], ex2(s_m[w][r] - top), sum);
-        }
-        if (i_all == unit_tiles) {
-            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-            T* dst = static_cast<T*>(A.out.data) + b * A.out.sb + static_cast<int64_t>(h * A.G + rr % A.G) * A.out.sh + l * A.out.st + d;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_out<T>(o.x * inv, o.y * inv), pack_out<T>(o.z * inv, o.w * inv));
-        } else {
-            // the unit goes on behind this share (state 1 of the CTA), or began before it (state 0)
-            const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + (i_begin == 0 ? 1 : 0)) * kRows + r;
-            *reinterpret_cast<float4*>(A.part_o + at * D + d) = o;
-            if (d == 0) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(top, sum);
-        }
-    }
-    next_segment();
-    tc::fence_proxy_async_smem();
-    __syncthreads();   // before the next segment's queries and copies
+        next_segment();
+        tc::fence_proxy_async_smem();
+        __syncthreads();   // before the next segment's queries and copies
     }
     tc::grid_release_dependents();
 }
