@@ -1,0 +1,190 @@
+"""The 8-bit cache's attention where it can go wrong: the chunk kernel's own forms, scales far apart, caps of any size,
+windows of any size, against the definition in 64 bits with a bound for each row."""
+import math
+
+import pytest
+import torch
+
+import kv8_util as ref
+import test_gpu_kv8 as base
+import turboquant_compressed_kv_tq_gb300 as tq
+from test_gpu_kv8 import BF16, DEV, E4M3, F16, F32, INT8, gen, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    base.tq_errors()
+    yield
+    torch.cuda.synchronize()
+    assert base.tq_errors() == 0
+
+
+def kernel_of(c, B, Hq, L, max_seq):
+    """"chunk" or "few": the chunk kernel takes no workspace, and the sizes here are beyond the eight tiles that few rows do without."""
+    H = c.num_kv_heads
+    assert B * H * -(-(Hq // H * L) // 16) * -(-max_seq // 16) > 8
+    return "few" if c.workspace_bytes(B, Hq, L, max_seq) else "chunk"
+
+
+def check(c, q, out, lens, news, table, kernel, scale=0.0, cap=0.0, slopes=None, window=0, prefixes=None, docs=None, rope=None):
+    """Every row against the definition, within what the roundings of its own visible keys may do:
+
+    scores, d: the queries' fp16 (2^-11 of each product if they were rotated and go in one part, else 2^-22; 2^-25 of the
+    row's largest coordinate for the small ones), the rotation in fp32 (2^-21), fp32 sums ((D + 8) 2^-24), the cap (2^-19
+    of the capped score), the bias (3 roundings of slope x distance), score plus scale exponent less reference in fp32
+    (2^-22 of the largest). An error d of every score moves the output by at most (e^2d - 1) sum w |v|.
+    weights: fp16 (2^-11); below 2^-14 of the reference an absolute 2^-25 of it (the reference is at most the row's
+    largest weight x value scale), or all of a smaller one; fp32 sums in steps of 16 keys (2^-22 each).
+    output: half a step."""
+    fmt, BT, D, H = c.format, c.block_tokens, c.head_dim, c.num_kv_heads
+    Hq = q.shape[1]
+    G = Hq // H
+    two = rope is None or (q.dtype == F16 and (kernel == "few" or D == 64))
+    tile = 16 if kernel == "few" else 64 if D == 256 else 128
+    limit = 15 if fmt == E4M3 else 24   # how far a tile's codes are brought to one scale
+    sc = scale or 1 / math.sqrt(D)
+    worst = 0.0
+    for b, (N, nq) in enumerate(zip(lens, news)):
+        ids = table[b, :-(-N // BT)].long().clamp(0, c.num_blocks - 1)
+        p, see = base.see_of(N, nq, window, prefixes[b] if prefixes else 0, docs[b, :nq] if docs is not None else None)
+        seen = see.any(0)
+        k, v = (ref.values(codes[0, ids], fmt).transpose(0, 1).reshape(H, -1, D)[:, :N] for codes in (c.k_codes, c.v_codes))
+        ek, ev = (s[0, ids].double().sub(127).transpose(0, 1).repeat_interleave(BT, 1)[:, :N] for s in (c.k_scales, c.v_scales))   # [H, N]
+        k, v = (torch.where(seen[:, None], x * torch.exp2(e)[..., None], 0.0) for x, e in ((k, ek), (v, ev)))
+        x0 = q[b, :, :nq].double()
+        qq, rsize = x0, torch.zeros_like(x0)
+        if rope is not None:
+            inter = bool(rope.desc.interleaved)
+            qq = ref.rotated(x0, p, rope.inv_freq, inter, rope.desc.scale)
+            rot = 2 * rope.inv_freq.numel()
+            z = x0[..., :rot].abs() * abs(rope.desc.scale)
+            z = (z[..., 0::2] + z[..., 1::2]).repeat_interleave(2, -1) if inter else (z[..., :rot // 2] + z[..., rot // 2:]).repeat(1, 1, 2)
+            rsize[..., :rot] = z
+        k_, v_, ev_ = (t.repeat_interleave(G, 0) for t in (k, v, ev))
+        kt = k_.transpose(1, 2)
+        s = (qq @ kt) * sc
+        size = (qq.abs() @ kt.abs()) * abs(sc)
+        d = size * ((2.0 ** -22 if two else 2.0 ** -11) + (D + 8) * 2.0 ** -24) + 2.0 ** -25 * qq.abs().amax(-1, keepdim=True) * kt.abs().sum(1, keepdim=True) * abs(sc)
+        d = d + (rsize @ kt.abs()) * abs(sc) * 2.0 ** -21
+        if cap:
+            s = cap * torch.tanh(s / cap)
+            d = d + 2.0 ** -19 * size.clamp(max=cap)
+        if slopes is not None:
+            far = slopes.double()[:, None, None] * (p[:, None] - torch.arange(N, device=DEV)).abs()
+            s = s - far
+            d = d + 3 * 2.0 ** -24 * far
+        d = d + 2.0 ** -22 * (s.abs() + ev_.abs()[:, None])
+        d = d.masked_fill(~see, 0.0).amax(-1, keepdim=True)
+        empty = ~see.any(1)
+        w = torch.softmax(s.masked_fill(~see, -math.inf).masked_fill(empty[:, None], 0.0), -1).masked_fill(empty[:, None], 0.0)
+        want, wv = w @ v_, w @ v_.abs()
+        small = torch.zeros_like(want)
+        T = -(-N // tile) * tile
+        top = torch.full((Hq, T), -1000.0, device=DEV, dtype=torch.float64)
+        top[:, :N] = torch.where(seen, ev_, -1000.0)
+        top = top.view(Hq, -1, tile).amax(-1).repeat_interleave(tile, 1)[:, :N]
+        for r in (ev_, torch.minimum(top, ev_ + limit)):
+            r = torch.where(seen, r, 0.0)
+            weight = w * torch.exp2(r)[:, None]
+            small = torch.maximum(small, torch.minimum(weight, 2.0 ** -25 * weight.amax(-1, keepdim=True)) @ (v_.abs() * torch.exp2(-r)[..., None]))
+        tol = want.abs() * (torch.finfo(q.dtype).eps / 2) + wv * (2.0 ** -11 + torch.expm1(2 * d) * 1.01 + (N / 16 + 16) * 2.0 ** -22) + small
+        tol = tol + (2.0 ** -25 if q.dtype == F16 else 2.0 ** -134)
+        got = out[b, :, :nq].double()
+        assert torch.isfinite(got).all(), b
+        assert (got[:, empty] == 0).all(), b
+        worst = max(worst, float(((got - want).abs() / tol).max()))
+    assert worst <= 1, worst
+
+
+def call(c, q, lens, table, max_seq=None, **kw):
+    return base.attend(c, q, lens, table, max_seq=max_seq, **kw)
+
+
+def straight(c, B=1):
+    """Sequences over the pool's blocks in order."""
+    return torch.arange(c.num_blocks, dtype=torch.int32, device=DEV).view(B, -1)
+
+
+# ------------------------------------------------------------------ the chunk kernel's forms
+
+FORMS = {
+    "plain": {},
+    "rotated": {"rope": 1.0},
+    "half rotated": {"rope": 0.5, "inter": True},
+    "cap": {"cap": 20.0},
+    "bias": {"bias": True},
+    "cap, bias, rotated": {"cap": 5.0, "bias": True, "rope": 1.0},
+    "prefix": {"prefix": [70, 333]},
+    "window, prefix, blocks gone": {"window": 50, "prefix": [5, 40], "gone": True},
+    "documents, prefix, cap": {"docs": 57, "prefix": [1, 200], "cap": 30.0},
+    "documents, bias": {"docs": 100, "bias": True, "rope": 1.0},
+    "uneven scales": {"spread": 14},
+    "uneven scales, cap, window": {"spread": 14, "cap": 8.0, "window": 200},
+}
+
+
+@pytest.mark.parametrize("fmt,dtype", [(E4M3, BF16), (INT8, F16)])
+@pytest.mark.parametrize("D,BT", [(64, 16), (128, 32), (128, 256), (256, 16)])
+@pytest.mark.parametrize("form", FORMS)
+def test_chunk_forms(form, D, BT, fmt, dtype):
+    o = FORMS[form]
+    B, H, G, L, lens, news = 2, 2, 4, 300, [600, 411], [300, 277]
+    width = -(-600 // BT) + 1
+    blocks = B * width + 2
+    c = base.filled_cache(blocks, H, BT, D, fmt, 200, spread=o.get("spread", 3))
+    table = base.shuffled_table(B, width, blocks, 201)
+    g = gen(202)
+    q = torch.randn(B, H * G, L, D, generator=g, device=DEV).to(dtype)
+    kw, ck = {}, {}
+    if "rope" in o:
+        kw["rope"] = ck["rope"] = tq.Rope.of_base(int(D * o["rope"]), interleaved=o.get("inter", False))
+    if "cap" in o:
+        kw["softcap"] = ck["cap"] = o["cap"]
+    if "bias" in o:
+        kw["slopes"] = ck["slopes"] = torch.rand(H * G, generator=g, device=DEV) * 0.2
+    if "window" in o:
+        kw["window"] = ck["window"] = o["window"]
+    if "prefix" in o:
+        kw["prefix_lens"], ck["prefixes"] = i32(o["prefix"]), o["prefix"]
+    if "docs" in o:
+        p = i32(lens)[:, None] - i32(news)[:, None] + torch.arange(L, device=DEV, dtype=torch.int32)
+        kw["doc_starts"] = ck["docs"] = (p // o["docs"] * o["docs"]).to(torch.int32).contiguous()
+    if "gone" in o:   # blocks between the prefix and the first window: no block at all
+        for b in range(B):
+            for lb in range(-(-o["prefix"][b] // BT), (lens[b] - news[b] - o["window"] + 1) // BT):
+                table[b, lb] = -7
+    assert kernel_of(c, B, H * G, L, max(lens)) == "chunk"
+    out = call(c, q, lens, table, q_lens=news, **kw)
+    check(c, q, out, lens, news, table, "chunk", **ck)
+    assert (out[1, :, news[1]:] == 0).all()
+
+
+@pytest.mark.parametrize("L", [1, 4, 300])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rotated_fp16_queries(D, L):
+    """In two parts for few rows and at head_dim 64: one would be 2^-11 of each product off."""
+    H, G, N, BT = 2, 4, 500, 64
+    c = base.filled_cache(8, H, BT, D, E4M3, 210)
+    q = (torch.randn(1, H * G, L, D, generator=gen(211), device=DEV) * 4).to(F16)
+    rope = tq.Rope.of_base(D)
+    kernel = kernel_of(c, 1, H * G, L, N)
+    assert kernel == ("chunk" if L == 300 else "few")
+    out = call(c, q, [N], straight(c), rope=rope)
+    check(c, q, out, [N], [L], straight(c), kernel, rope=rope)
+
+
+def test_chunk_far_into_the_pool():
+    """Codes behind 2^32 bytes, for the chunk kernel."""
+    D, BT, H, G, L, N = 128, 256, 4, 4, 600, 2400
+    blocks = (1 << 32) // (BT * H * D) + 10
+    c = tq.KV8Cache(1, blocks, BT, H, D)
+    few = base.filled_cache(10, H, BT, D, E4M3, 220)
+    for t, o in zip((c.k_codes, c.v_codes, c.k_scales, c.v_scales), (few.k_codes, few.v_codes, few.k_scales, few.v_scales)):
+        t[:, blocks - 10:] = o
+    q = torch.randn(1, H * G, L, D, generator=gen(221), device=DEV).to(BF16)
+    order = torch.randperm(10, generator=gen(222), device=DEV).to(torch.int32).view(1, 10)
+    assert kernel_of(c, 1, H * G, L, N) == "chunk"
+    out = call(c, q, [N], order + (blocks - 10))
+    check(few, q, out, [N], [L], order, "chunk")
