@@ -188,3 +188,19 @@ def test_chunk_far_into_the_pool():
     assert kernel_of(c, 1, H * G, L, N) == "chunk"
     out = call(c, q, [N], order + (blocks - 10))
     check(few, q, out, [N], [L], order, "chunk")
+
+
+# ------------------------------------------------------------------ windows of any size
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 300, 2 ** 30 + 5, 2 ** 30])
+@pytest.mark.parametrize("N,L", [(10, 64), (600, 700), (1, 300), (300, 300)])
+def test_windows_wider_than_everything(N, L, window):
+    """As no window, also for sequences shorter than the queries' padded length."""
+    H, G, D, BT = 2, 4, 128, 16
+    c = base.filled_cache(40, H, BT, D, E4M3, 230)
+    table = straight(c)
+    q = torch.randn(1, H * G, L, D, generator=gen(231), device=DEV).to(BF16)
+    assert kernel_of(c, 1, H * G, L, max(N, 8)) == "chunk"
+    out = call(c, q, [N], table, max_seq=max(N, 8), window=window)
+    assert torch.equal(out, call(c, q, [N], table, max_seq=max(N, 8)))
+    check(c, q, out, [N], [L], table, "chunk")

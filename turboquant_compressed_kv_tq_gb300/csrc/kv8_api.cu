@@ -214,7 +214,7 @@ tq_status tq_kv8_attention(const tq_kv8_cache* cache, int layer, const tq_rows* 
     a.scale = sc.scale == 0.0f ? 1.0f / std::sqrt(static_cast<float>(cache->head_dim)) : sc.scale;
     a.cap = sc.softcap;
     a.slopes = sc.slopes;
-    a.window = sc.window;
+    a.window = std::min(sc.window, kMaxTokens);   // wider than any sequence: none, and positions less it stay in 32 bits
     a.prefix = sc.prefix_lens;
     a.docs = sc.doc_starts;
     char* ws = static_cast<char*>(workspace);
