@@ -785,12 +785,12 @@ tq_status tq_kv8_workspace_bytes(const tq_kv8_cache *cache, int batch, int num_q
  *   scores     NULL: plain causal attention
  *   workspace  device, >= tq_kv8_workspace_bytes(...), 256-byte aligned (NULL
  *              where that is 0); only this call uses it while it runs.
- * Operands are fp16: cached codes are exact in it (of many rows at once, as far
- * as the scales of 64 to 128 neighbouring tokens lie within 2^15 of each other:
- * then those of the smaller scale lose low bits); queries are scaled by a power of
- * two per row, and rounded where they were rotated (fp16 queries in two parts, for
- * few rows and at head_dim 64); softmax weights are rounded. Sums and softmax statistics are fp32,
- * the output is rounded once. The same call gives the same bits every time.
+ * Operands are fp16: cached codes are exact in it, whatever their scales; queries
+ * are scaled by a power of two per row, and rounded where they were rotated (fp16
+ * queries in two parts, for few rows and at head_dim 64); softmax weights, times
+ * their value scale, are rounded (below 2^-14 of the row's largest to 2^-25 of it).
+ * Sums and softmax statistics are fp32, the output is rounded once. The same call
+ * gives the same bits every time.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED as tq_kv8_append, also for f32
  * queries; TQ_ERR_CAPACITY if the workspace is too small.
  */

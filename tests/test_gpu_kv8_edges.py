@@ -204,3 +204,75 @@ def test_windows_wider_than_everything(N, L, window):
     out = call(c, q, [N], table, max_seq=max(N, 8), window=window)
     assert torch.equal(out, call(c, q, [N], table, max_seq=max(N, 8)))
     check(c, q, out, [N], [L], table, "chunk")
+
+
+# ------------------------------------------------------------------ scales far apart
+
+@pytest.mark.parametrize("fmt", [E4M3, INT8])
+@pytest.mark.parametrize("cap", [0.0, 12.0])
+@pytest.mark.parametrize("D,BT", [(64, 32), (128, 64), (128, 16), (256, 32)])
+def test_masked_neighbours_of_other_scales(D, BT, cap, fmt):
+    """Documents of one block: a row sees one block only, whose scale may be 2^46 below its neighbours' in the same tile."""
+    H, G, N = 2, 4, 384
+    c = base.filled_cache(N // BT, H, BT, D, fmt, 240)
+    g = gen(241)
+    up = torch.randint(-8, -4, (2, N // BT, H), generator=g, device=DEV)
+    ek, ev = (u + torch.where(torch.arange(N // BT, device=DEV)[:, None] % 3 == i, 0, -42) for i, u in enumerate(up))
+    c.k_scales[0], c.v_scales[0] = (ek + 127).to(torch.uint8), (ev + 127).to(torch.uint8)
+    table = straight(c)
+    q = torch.randn(1, H, G, N, D, generator=g, device=DEV)
+    q = q * torch.exp2(-6.0 - ek.float()).T.repeat_interleave(BT, 1)[None, :, None, :, None]   # scores of size 1 with their own block
+    q = q.reshape(1, H * G, N, D).to(BF16)
+    docs = (torch.arange(N, device=DEV, dtype=torch.int32) // BT * BT).view(1, N)
+    assert kernel_of(c, 1, H * G, N, N) == "chunk"
+    out = call(c, q, [N], table, doc_starts=docs, softcap=cap)
+    check(c, q, out, [N], [N], table, "chunk", cap=cap, docs=docs)
+    small = out[0].double().abs().amax((0, 2)).view(-1, BT).amax(1)   # of each block's rows
+    assert (small > torch.exp2(ev.double().amax(1) - 4)).all()        # nothing vanished
+
+
+@pytest.mark.parametrize("fmt", [E4M3, INT8])
+@pytest.mark.parametrize("L", [1, 5, 300])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_seen_blocks_of_other_scales(D, L, fmt):
+    """Rows that see blocks of all scales; one block's keys are liked by every row, so that its small values count."""
+    H, G, N, BT, hot = 2, 4, 500, 16, 9
+    c = base.filled_cache(32, H, BT, D, fmt, 250)
+    g = gen(251)
+    ev = torch.randint(-45, -35, (32, H), generator=g, device=DEV)
+    ev[5] = ev[10] = ev[20] = -6
+    ev[hot] = -50
+    ev[12], c.v_codes[0, 12] = -63, 0
+    c.v_scales[0] = (ev + 127).to(torch.uint8)
+    one = torch.where(torch.rand(D, generator=g, device=DEV) < 0.5, -1.0, 1.0)
+    c.k_codes[0, hot] = ((one * 64).to(torch.float8_e4m3fn).view(torch.uint8) if fmt == E4M3 else (one * 64).to(torch.int8).view(torch.uint8))
+    q = (torch.randn(1, H * G, L, D, generator=g, device=DEV) * 0.2 + one * 60 / math.sqrt(D)).to(BF16)
+    table = straight(c)
+    kernel = kernel_of(c, 1, H * G, L, 512)
+    assert L == 5 or kernel == ("chunk" if L == 300 else "few")
+    out = call(c, q, [N], table, max_seq=512)
+    check(c, q, out, [N], [L], table, kernel)
+
+
+@pytest.mark.parametrize("kind", ["keys", "values"])
+@pytest.mark.parametrize("fmt,apart", [(E4M3, 14), (E4M3, 15), (E4M3, 16), (INT8, 23), (INT8, 24), (INT8, 25)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_at_the_edge_of_one_tile(D, fmt, apart, kind):
+    """The furthest apart that a tile's codes go to one scale, and the next: codes of every size, down to the smallest."""
+    H, G, N, BT = 2, 4, 384, 32
+    c = base.filled_cache(N // BT, H, BT, D, fmt, 245)
+    g = gen(246)
+    every = torch.arange(256, device=DEV, dtype=torch.int32).to(torch.uint8)
+    every = every[(every & 0x7F) != 0x7F] if fmt == E4M3 else every[every != 128]
+    low = torch.arange(N // BT, device=DEV) % 2 == 1
+    codes, exps = (c.k_codes, c.k_scales) if kind == "keys" else (c.v_codes, c.v_scales)
+    codes[0] = every[torch.randint(0, len(every), codes[0].shape, generator=g, device=DEV)]
+    exps[0] = (127 - 8 - low * apart)[:, None].to(torch.uint8)
+    q = torch.randn(1, H * G, N, D, generator=g, device=DEV)
+    if kind == "keys":   # scores of size 1 with their own block
+        q = q * torch.exp2(low.float() * apart).repeat_interleave(BT)[:, None]
+    q = q.to(BF16)
+    docs = (torch.arange(N, device=DEV, dtype=torch.int32) // BT * BT).view(1, N)
+    assert kernel_of(c, 1, H * G, N, N) == "chunk"
+    out = call(c, q, [N], straight(c), doc_starts=docs)
+    check(c, q, out, [N], [N], straight(c), "chunk", docs=docs)

@@ -18,9 +18,12 @@
 // are computed ahead into a second buffer.
 //
 // Block scales are powers of two. Within a tile the codes are brought to the
-// tile's largest scale in fp16 (exact down to 2^-24 of it); that one scale is a
-// factor of the row's scores, and for values moves the softmax's reference:
-// u = log2(e) score + log2(scale), p = 2^(u - M), l += p / scale.
+// tile's largest scale in fp16; that one scale is a factor of the row's scores, and
+// for values moves the softmax's reference: u = log2(e) score + log2(scale),
+// p = 2^(u - M), l += p / scale. Where the tile's scales lie too far apart for that
+// to be exact (2^15 for e4m3, 2^24 for integers: blocks of zeros, other documents),
+// the codes stay as they are and the softmax warps take each group of 8 tokens at
+// its own scales: the keys' a factor of its scores, the values' a part of its u.
 //
 // Bound: next to the tensor cores' 4 D flops per row and key, shared memory (both
 // operands of S and one of P V come from it, and the converters pass through it)
@@ -125,7 +128,79 @@ struct Tiles {
 struct TileInfo {
     int kref, vref;    // its scales' exponents
     unsigned gone;     // groups of 8 tokens that belong to no block
+    bool wide;         // too far apart for one scale in fp16: see s_below
 };
+
+// A row's softmax over a wide tile, in 8 columns at a time: a group's scores have its own key scale, its u its own value
+// scale. (Rare, and a function of its own: the usual tile's code and registers stay as they are without it.)
+struct WideTile {
+    uint32_t t_s, t_p, t_o;    // S, P and O of this thread's rows
+    bool some;                 // O holds something
+    const uint16_t* below;
+    int kref, vref;            // the tile's largest exponents
+    float fac, cap, slope;     // of the scores, but for the key scale
+    Sight sight;
+    int t0;
+    unsigned gone;
+    float m, l;
+};
+
+template <int D, int kT, bool MOD>
+__device__ __noinline__ float2 wide_tile(const WideTile w) {
+    const float cap2 = w.cap * kLog2e, cap_in = w.cap > 0.0f ? 2.0f * kLog2e / w.cap : 0.0f;
+    float m = w.m, l = w.l, top = -INFINITY;
+#pragma unroll 1
+    for (int g = 0; g < kT / 8; ++g) {   // u, masked, back to where the scores were
+        const float kg = w.fac * exp2i(max(w.kref - (w.below[g] & 0xFF), -126)), lv = static_cast<float>(w.vref - (w.below[g] >> 8));
+        float x[8];
+        tc::tmem_ld8(w.t_s + 8 * g, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int t = w.t0 + 8 * g + e;
+            x[e] *= kg;
+            x[e] = MOD && w.cap > 0.0f ? fmaf(-2.0f * cap2, rcp(1.0f + ex2(x[e] * cap_in)), cap2) : x[e] * kLog2e;
+            if (MOD) x[e] = fmaf(-w.slope, fabsf(static_cast<float>(t - w.sight.p)), x[e]);
+            x[e] = w.sight.sees(t) && !((w.gone >> g) & 1u) ? x[e] + lv : -INFINITY;
+            top = fmaxf(top, x[e]);
+        }
+        tc::tmem_st8(w.t_s + 8 * g, x);
+    }
+    if (__any_sync(0xffffffffu, top > m + kGap)) {
+        const float x = fmaxf(top, m);
+        const float alpha = ex2(m - x);
+        m = x;
+        l *= alpha;
+        if (w.some) {
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {
+                float v[8];
+                tc::tmem_ld8(w.t_o + 8 * c, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= alpha;
+                tc::tmem_st8(w.t_o + 8 * c, v);
+            }
+        }
+    }
+#pragma unroll 1
+    for (int n = 0; n < kT / 32; ++n) {   // p, 32 columns at a time (over scores that were read, where P lies over S)
+        uint32_t pr[16];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float lv = static_cast<float>(w.vref - (w.below[4 * n + g] >> 8));
+            float x[8];
+            tc::tmem_ld8(w.t_s + 32 * n + 8 * g, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] -= m;
+                l += ex2(x[e] - lv);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) pr[4 * g + e / 2] = pack_out<__half>(ex2(x[e]), ex2(x[e + 1]));
+        }
+        tc::tmem_st16u(w.t_p + 16 * n, pr);
+    }
+    return make_float2(m, l);
+}
 
 template <typename T, int D, bool I8, bool MOD, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ AttendArgs A) {
@@ -136,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     __shared__ __align__(8) uint64_t s_bar[18];
     __shared__ float s_fac[S::kRows];
     __shared__ TileInfo s_info[4];
+    __shared__ uint16_t s_below[4][S::kGroups];   // of a wide tile's groups: how far their exponents are below kref and (high byte) vref
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     uint64_t *k_full = s_bar, *k_free = s_bar + 2, *v_full = s_bar + 4, *v_free = s_bar + 6;
@@ -288,129 +364,153 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             const float fac = s_fac[min(row, S::kRows - 1)];
             const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
             const float slope = MOD && A.slopes ? A.slopes[h * A.G + rr % A.G] * kLog2e : 0.0f;
-            for (int i = 0; i < n_tiles && ok; ++i) {
-                const int t0 = tiles.at(i) * kT;
-                const int sb = kH == 2 ? half : i & 1;                    // buffer of S and P
-                ok = arrived(&s_ready[sb], kH == 2 ? i & 1 : (i >> 1) & 1);
-                if (!ok) break;
-                tc::tc_fence_after();
-                const TileInfo info = s_info[i & 3];
-                const float kf = fac * exp2i(info.kref), lv = static_cast<float>(info.vref);
-                const float f = MOD ? 1.0f : fmaxf(kf * kLog2e, FLT_MIN);
-                const bool open = info.gone == 0 && ((t0 + kT - 1 <= p_min && t0 >= lo_max) || t0 + kT <= pre);
-                // 64 columns of the row's scores, k a multiple of 64: cap and bias applied, unseen ones -inf
-                auto finish = [&](uint32_t (&sr)[64], int k) {
-                    if constexpr (MOD) {
-                        if (A.cap > 0.0f) {   // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
-                            const float k2 = kf * cap_in;
+            for (int i = 0;;) {
+                for (; i < n_tiles; ++i) {
+                    const int t0 = tiles.at(i) * kT;
+                    const int sb = kH == 2 ? half : i & 1;                    // buffer of S and P
+                    ok = arrived(&s_ready[sb], kH == 2 ? i & 1 : (i >> 1) & 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const TileInfo info = s_info[i & 3];
+                    const float kf = fac * exp2i(info.kref), lv = static_cast<float>(info.vref);
+                    if (info.wide) break;
+                    const float f = MOD ? 1.0f : fmaxf(kf * kLog2e, FLT_MIN);
+                    const bool open = info.gone == 0 && ((t0 + kT - 1 <= p_min && t0 >= lo_max) || t0 + kT <= pre);
+                    // 64 columns of the row's scores, k a multiple of 64: cap and bias applied, unseen ones -inf
+                    auto finish = [&](uint32_t (&sr)[64], int k) {
+                        if constexpr (MOD) {
+                            if (A.cap > 0.0f) {   // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+                                const float k2 = kf * cap_in;
 #pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                sr[e] = __float_as_uint(fmaf(-2.0f * cap2, rcp(1.0f + ex2(__uint_as_float(sr[e]) * k2)), cap2));
-                        } else {
-                            const float k2 = kf * kLog2e;
+                                for (int e = 0; e < 64; ++e)
+                                    sr[e] = __float_as_uint(fmaf(-2.0f * cap2, rcp(1.0f + ex2(__uint_as_float(sr[e]) * k2)), cap2));
+                            } else {
+                                const float k2 = kf * kLog2e;
 #pragma unroll
-                            for (int e = 0; e < 64; ++e) sr[e] = __float_as_uint(__uint_as_float(sr[e]) * k2);
+                                for (int e = 0; e < 64; ++e) sr[e] = __float_as_uint(__uint_as_float(sr[e]) * k2);
+                            }
+                            if (A.slopes) {
+                                const float from = static_cast<float>(t0 + k - sight.p);
+#pragma unroll
+                                for (int e = 0; e < 64; ++e)
+                                    sr[e] = __float_as_uint(fmaf(-slope, fabsf(from + static_cast<float>(e)), __uint_as_float(sr[e])));
+                            }
                         }
-                        if (A.slopes) {
-                            const float from = static_cast<float>(t0 + k - sight.p);
+                        if (!open) {
+                            // the seen columns as bits, 32 at a time
+                            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                sr[e] = __float_as_uint(fmaf(-slope, fabsf(from + static_cast<float>(e)), __uint_as_float(sr[e])));
+                            for (int n = 0; n < 64; n += 32) {
+                                const int at = t0 + k + n;
+                                uint32_t see = (below(sight.p - at + 1) & ~below(sight.lo - at)) | below(sight.prefix - at);
+                                if (info.gone) {
+#pragma unroll
+                                    for (int g = 0; g < 4; ++g)
+                                        if ((info.gone >> ((k + n) / 8 + g)) & 1u) see &= ~(0xFFu << (8 * g));
+                                }
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) sr[n + e] = (see >> e) & 1u ? sr[n + e] : 0xFF800000u;
+                            }
+                        }
+                    };
+                    auto largest = [&](const uint32_t (&sr)[64]) {
+                        float x[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            x[q] = max3(sr[16 * q], sr[16 * q + 1], sr[16 * q + 2]);
+#pragma unroll
+                            for (int e = 3; e < 15; e += 2) x[q] = max3(__float_as_uint(x[q]), sr[16 * q + e], sr[16 * q + e + 1]);
+                        }
+                        x[0] = max3(__float_as_uint(x[0]), sr[15], sr[31]);
+                        x[1] = max3(__float_as_uint(x[1]), sr[47], sr[63]);
+                        return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                    };
+                    // a row at once would be 128 registers: the upper 64 scores are looked at
+                    // for the maximum, and read again once the lower are done
+                    const uint32_t t_s = t_row + S::kS + sb * S::kSStep;
+                    uint32_t sr[64];
+                    float top = -INFINITY;
+#pragma unroll 1   // (unrolled, the two halves' registers would live side by side)
+                    for (int k = kT - 64; k >= 0; k -= 64) {
+                        tc::tmem_ld(t_s + k, sr);
+                        finish(sr, k);
+                        if (k > 0 && (MOD || !open)) tc::tmem_st(t_s + k, sr);
+                        top = fmaxf(top, largest(sr));
+                    }
+                    top = fmaf(top, f, lv);
+                    const bool pass = top > m + kGap;
+                    if (kH == 1 && i > 0) {   // every phase in its turn: a wait by parity tells neighbouring phases apart, no others
+                        ok = arrived(&o_done[0], (i - 1) & 1);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                    }
+                    if (__any_sync(0xffffffffu, pass)) {
+                        const float x = fmaxf(top, m);
+                        const float alpha = ex2(m - x);
+                        m = x;
+                        l_sum *= alpha;
+                        if (i > 0) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                float v[16];
+                                tc::tmem_ld16(t_o + 16 * c, v);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) v[e] *= alpha;
+                                tc::tmem_st16(t_o + 16 * c, v);
+                            }
                         }
                     }
-                    if (!open) {
-                        // the seen columns as bits, 32 at a time
-                        auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+                    const uint64_t f2 = pack2(f, f), o2 = pack2(lv - m, lv - m);
+                    uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll 1
+                    for (int k = 0; k < kT / 64; ++k) {
+                        if (k == 1) tc::tmem_ld(t_s + 64, sr);
 #pragma unroll
                         for (int n = 0; n < 64; n += 32) {
-                            const int at = t0 + k + n;
-                            uint32_t see = (below(sight.p - at + 1) & ~below(sight.lo - at)) | below(sight.prefix - at);
-                            if (info.gone) {
+                            uint32_t pr[16];
 #pragma unroll
-                                for (int g = 0; g < 4; ++g)
-                                    if ((info.gone >> ((k + n) / 8 + g)) & 1u) see &= ~(0xFFu << (8 * g));
+                            for (int e = 0; e < 32; e += 4) {
+                                float a, c, d, g;
+                                unpack2(fma2(pack2(__uint_as_float(sr[n + e]), __uint_as_float(sr[n + e + 1])), f2, o2), a, c);
+                                unpack2(fma2(pack2(__uint_as_float(sr[n + e + 2]), __uint_as_float(sr[n + e + 3])), f2, o2), d, g);
+                                a = ex2(a), c = ex2(c), d = ex2(d), g = ex2(g);
+                                sum0 = add2(sum0, pack2(a, c));
+                                sum1 = add2(sum1, pack2(d, g));
+                                pr[e / 2] = pack_out<__half>(a, c);
+                                pr[e / 2 + 1] = pack_out<__half>(d, g);
                             }
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) sr[n + e] = (see >> e) & 1u ? sr[n + e] : 0xFF800000u;
+                            tc::tmem_st16u(t_row + S::kP + sb * S::kPStep + (64 * k + n) / 2, pr);
                         }
+                        tc::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(k == 0 ? &p_ready[sb] : &p_second[sb]);
                     }
-                };
-                auto largest = [&](const uint32_t (&sr)[64]) {
-                    float x[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        x[q] = max3(sr[16 * q], sr[16 * q + 1], sr[16 * q + 2]);
-#pragma unroll
-                        for (int e = 3; e < 15; e += 2) x[q] = max3(__float_as_uint(x[q]), sr[16 * q + e], sr[16 * q + e + 1]);
-                    }
-                    x[0] = max3(__float_as_uint(x[0]), sr[15], sr[31]);
-                    x[1] = max3(__float_as_uint(x[1]), sr[47], sr[63]);
-                    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-                };
-                // a row at once would be 128 registers: the upper 64 scores are looked at
-                // for the maximum, and read again once the lower are done
-                const uint32_t t_s = t_row + S::kS + sb * S::kSStep;
-                uint32_t sr[64];
-                float top = -INFINITY;
-#pragma unroll 1   // (unrolled, the two halves' registers would live side by side)
-                for (int k = kT - 64; k >= 0; k -= 64) {
-                    tc::tmem_ld(t_s + k, sr);
-                    finish(sr, k);
-                    if (k > 0 && (MOD || !open)) tc::tmem_st(t_s + k, sr);
-                    top = fmaxf(top, largest(sr));
+                    float a, c, d, g;
+                    unpack2(sum0, a, c);
+                    unpack2(sum1, d, g);
+                    l_sum = fmaf((a + c) + (d + g), exp2i(-info.vref), l_sum);
                 }
-                top = fmaf(top, f, lv);
-                const bool pass = top > m + kGap;
-                if (kH == 1 && i > 0) {   // every phase in its turn: a wait by parity tells neighbouring phases apart, no others
+                if (!ok || i == n_tiles) break;
+                // a wide one, whose scores are there
+                const int t0 = tiles.at(i) * kT, sb = kH == 2 ? half : i & 1;
+                const TileInfo info = s_info[i & 3];
+                if (kH == 1 && i > 0) {
                     ok = arrived(&o_done[0], (i - 1) & 1);
                     if (!ok) break;
                     tc::tc_fence_after();
                 }
-                if (__any_sync(0xffffffffu, pass)) {
-                    const float x = fmaxf(top, m);
-                    const float alpha = ex2(m - x);
-                    m = x;
-                    l_sum *= alpha;
-                    if (i > 0) {
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            float v[16];
-                            tc::tmem_ld16(t_o + 16 * c, v);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] *= alpha;
-                            tc::tmem_st16(t_o + 16 * c, v);
-                        }
-                    }
+                const float2 ml = wide_tile<D, kT, MOD>(WideTile{
+                    t_row + S::kS + sb * S::kSStep, t_row + S::kP + sb * S::kPStep, t_o, i > 0, s_below[i & 3], info.kref,
+                    info.vref, fac, A.cap, slope, sight, t0, info.gone, m, l_sum});
+                m = ml.x;
+                l_sum = ml.y;
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive(&p_ready[sb]);
+                    if (kT == 128) tc::mbar_arrive(&p_second[sb]);
                 }
-                const uint64_t f2 = pack2(f, f), o2 = pack2(lv - m, lv - m);
-                uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll 1
-                for (int k = 0; k < kT / 64; ++k) {
-                    if (k == 1) tc::tmem_ld(t_s + 64, sr);
-#pragma unroll
-                    for (int n = 0; n < 64; n += 32) {
-                        uint32_t pr[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float a, c, d, g;
-                            unpack2(fma2(pack2(__uint_as_float(sr[n + e]), __uint_as_float(sr[n + e + 1])), f2, o2), a, c);
-                            unpack2(fma2(pack2(__uint_as_float(sr[n + e + 2]), __uint_as_float(sr[n + e + 3])), f2, o2), d, g);
-                            a = ex2(a), c = ex2(c), d = ex2(d), g = ex2(g);
-                            sum0 = add2(sum0, pack2(a, c));
-                            sum1 = add2(sum1, pack2(d, g));
-                            pr[e / 2] = pack_out<__half>(a, c);
-                            pr[e / 2 + 1] = pack_out<__half>(d, g);
-                        }
-                        tc::tmem_st16u(t_row + S::kP + sb * S::kPStep + (64 * k + n) / 2, pr);
-                    }
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(k == 0 ? &p_ready[sb] : &p_second[sb]);
-                }
-                float a, c, d, g;
-                unpack2(sum0, a, c);
-                unpack2(sum1, d, g);
-                l_sum = fmaf((a + c) + (d + g), exp2i(-info.vref), l_sum);
+                ++i;
             }
             if (ok) ok = arrived(&o_done[kH == 2 ? half : 0], kH == 2 ? 0 : (n_tiles - 1) & 1);
             if (!ok) {
@@ -467,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         // a batch of kPer tiles: lane kGroups j + g holds the block and scale bytes of tile j's group g. Looked up in
         // two steps, each a batch before what needs it: the block table's entry, then the scales
         constexpr int kPer = 32 / S::kGroups;
+        constexpr int kExact = I8 ? 24 : 15;     // 2^-kExact of the smallest code (1; 2^-9) is fp16's smallest
         const int my_tile = lane / S::kGroups, my_group = lane % S::kGroups;
         struct Found {
             int id, kx, vx;
@@ -512,9 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             }
             copies_close();
         };
-        // the codes times 2^(their group's exponent - ref), as fp16 (`left`: tokens that the sequence still has from
-        // the tile's first on; `id`: the groups' blocks)
-        auto convert_as = [&](auto plain, int ex, int ref, int id, int from, int left, unsigned char* dst) {
+        // the codes times 2^-below (their group's exponent under the tile's), as fp16 (`left`: tokens that the sequence
+        // still has from the tile's first on; `id`: the groups' blocks)
+        auto convert_as = [&](auto plain, int below, int id, int from, int left, unsigned char* dst) {
             constexpr bool kPlain = decltype(plain)::value;   // every token there, at the tile's scale
 #pragma unroll
             for (int q = 0; q < TG; ++q) {
@@ -524,8 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 __half2 mul2{};
                 if constexpr (!kPlain) {
                     here = __shfl_sync(0xffffffffu, id, from + g) >= 0 && 8 * g + tok < left;
-                    const int down = max(__shfl_sync(0xffffffffu, ex, from + g) - ref, -25);
-                    const __half mul = __float2half_rn(down < -24 ? 0.0f : exp2i(down));
+                    const __half mul = __float2half_rn(exp2i(-__shfl_sync(0xffffffffu, below, from + g)));
                     mul2 = __half2(mul, mul);
                 }
 #pragma unroll
@@ -550,10 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             }
         };
         // (a tile all there at one scale, the usual one, needs no multiplication: the prompt above: 678 us, from 728)
-        auto convert = [&](int ex, int ref, int id, int from, int left, unsigned char* dst) {
-            const bool plain = left >= kT && __all_sync(0xffffffffu, lane - from < 0 || lane - from >= S::kGroups || (id >= 0 && ex == ref));
-            if (plain) convert_as(std::true_type{}, ex, ref, id, from, left, dst);
-            else convert_as(std::false_type{}, ex, ref, id, from, left, dst);
+        auto convert = [&](int below, int id, int from, int left, unsigned char* dst) {
+            const bool plain = left >= kT && __all_sync(0xffffffffu, lane - from < 0 || lane - from >= S::kGroups || (id >= 0 && below == 0));
+            if (plain) convert_as(std::true_type{}, below, id, from, left, dst);
+            else convert_as(std::false_type{}, below, id, from, left, dst);
         };
         bool ok = true;
         if (n_tiles > 0) {
@@ -564,16 +664,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             for (int i = 0; i < n_tiles; ++i) {
                 const int st = i & 1, t0 = tiles.at(i) * kT, from = i % kPer * S::kGroups;
                 const bool mine = lane >= from && lane < from + S::kGroups;
-                const int kx = now.id < 0 ? -64 : now.kx - 127, vx = now.id < 0 ? -64 : now.vx - 127;
-                const int kref = __reduce_max_sync(0xffffffffu, mine ? kx : -64), vref = __reduce_max_sync(0xffffffffu, mine ? vx : -64);
+                const bool there = mine && now.id >= 0;
+                const int kx = now.kx - 127, vx = now.vx - 127;
+                const int kref = __reduce_max_sync(0xffffffffu, there ? kx : -64), vref = __reduce_max_sync(0xffffffffu, there ? vx : -64);
+                const int k_below = there ? kref - kx : 0, v_below = there ? vref - vx : 0;
+                const bool k_wide = __any_sync(0xffffffffu, k_below > kExact), v_wide = __any_sync(0xffffffffu, v_below > kExact);
                 // groups of no block among those that have tokens
                 const unsigned gone = __ballot_sync(0xffffffffu, mine && now.id < 0 && t0 + 8 * my_group < N) >> from;
                 copies_wait<0>();
                 if (i >= 2) ok = arrived(&free[st], ((i >> 1) - 1) & 1);
                 else if (i == 1) ok = arrived(q_ready, 0);   // whose angles are in the second stages
                 if (!ok) break;
-                if (warp == kKWarp && lane == 0) s_info[i & 3] = TileInfo{kref, vref, gone};
-                convert(is_v ? vx : kx, is_v ? vref : kref, now.id, from, N - t0, operand + st * S::kOperand);
+                if (warp == kKWarp) {
+                    if ((k_wide || v_wide) && mine) s_below[i & 3][my_group] = static_cast<uint16_t>((k_wide ? k_below : 0) | (v_wide ? v_below : 0) << 8);
+                    if (lane == 0) s_info[i & 3] = TileInfo{kref, vref, gone, k_wide || v_wide};
+                }
+                convert((is_v ? v_wide : k_wide) ? 0 : is_v ? v_below : k_below, now.id, from, N - t0, operand + st * S::kOperand);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&full[st]);

@@ -1,5 +1,5 @@
-// Wide tensor-memory loads and stores (32x32b: a warp's 32 lanes, one row of
-// columns a thread), each with its wait in the same statement, so that no use
+// Tensor-memory loads and stores (32x32b: a warp's 32 lanes, one row of columns
+// a thread), each with its wait in the same statement, so that no use
 // of the registers can be scheduled before it.
 #pragma once
 
@@ -47,6 +47,19 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[64])
           "r"(r[49]), "r"(r[50]), "r"(r[51]), "r"(r[52]), "r"(r[53]), "r"(r[54]), "r"(r[55]), "r"(r[56]),
           "r"(r[57]), "r"(r[58]), "r"(r[59]), "r"(r[60]), "r"(r[61]), "r"(r[62]), "r"(r[63])
         : "memory");
+}
+
+// 8 consecutive columns, as fp32, loaded and stored.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n tcgen05.wait::ld.sync.aligned;\n"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n tcgen05.wait::st.sync.aligned;\n" ::"r"(taddr),
+                 "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
 }
 
 }  // namespace tc
