@@ -276,3 +276,26 @@ def test_scales_at_the_edge_of_one_tile(D, fmt, apart, kind):
     assert kernel_of(c, 1, H * G, N, N) == "chunk"
     out = call(c, q, [N], straight(c), doc_starts=docs)
     check(c, q, out, [N], [N], straight(c), "chunk", docs=docs)
+
+
+@pytest.mark.parametrize("L", [1, 300])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("order", [(0, 1), (1, 0)])
+def test_zeros_next_to_the_largest_values(order, D, L):
+    """A block of zeros has the smallest scale, 2^-63; next to values of 2^70 its keys still take their share of the weights."""
+    H, G, BT = 2, 4, 256
+    N = 40 * BT if L == 1 else 2 * BT
+    c = base.filled_cache(N // BT, H, BT, D, E4M3, 260)
+    half = N // BT // 2
+    zero, large = (slice(0, half), slice(half, None))[order[0]], (slice(0, half), slice(half, None))[order[1]]
+    c.v_codes[0, zero], c.v_scales[0, zero] = 0, 127 - 63
+    c.v_scales[0, large] = 127 + 62
+    one = torch.where(torch.rand(D, generator=gen(261), device=DEV) < 0.5, -1.0, 1.0)
+    c.k_codes[0] = (one * 64).to(torch.float8_e4m3fn).view(torch.uint8)
+    c.k_codes[0, large] = (one * 96).to(torch.float8_e4m3fn).view(torch.uint8)
+    c.k_scales.fill_(127 - 6)
+    q = (one * (4 / math.sqrt(D)) * torch.ones(1, H * G, L, 1, device=DEV)).to(BF16)   # scores of 4 and 6
+    table = straight(c)
+    assert kernel_of(c, 1, H * G, L, N) == ("chunk" if L == 300 else "few")
+    out = call(c, q, [N], table)
+    check(c, q, out, [N], [L], table, kernel_of(c, 1, H * G, L, N))

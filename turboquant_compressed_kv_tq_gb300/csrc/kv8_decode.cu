@@ -18,7 +18,10 @@
 //   O^T += V^T P     A = the tile's value codes, B = p (two 8x8 transposes)
 // Codes become fp16 exactly; block scales are powers of two and stay out of the
 // operands: the keys' is a factor of the scores, the values' moves the softmax's
-// reference (p <= 2^8 whatever the scales are) and is divided out of the sum.
+// reference (p <= 2^8 whatever the scales are) and is divided out of the sum. So l
+// runs from 2^-63 to 2^63 a key: it is rescaled by the square root of alpha, twice,
+// and takes tiles of very small values (zeros) from u itself, whose p may be below
+// fp32's smallest.
 //
 // Layout. The coordinates (and for values the token pairs) that an MMA operand
 // wants in one lane are whatever order both operands share, so each lane takes
@@ -43,6 +46,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -1e30f;    // reference of a row that has seen nothing
 constexpr float kGap = 8.0f;       // how far scores may pass the reference (log2 units)
+constexpr int kDeep = -24;         // value exponents below it: p may be too small for fp32 where its share of l is not
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -511,9 +515,9 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                             x = fmaxf(x, m[nt][e]);
-                            const float alpha = ex2(m[nt][e] - x);
+                            const float half = ex2(0.5f * (m[nt][e] - x)), alpha = half * half;
                             m[nt][e] = x;
-                            l_sum[nt][e] *= alpha;
+                            l_sum[nt][e] = l_sum[nt][e] * half * half;
 #pragma unroll
                             for (int j = 0; j < S::kMT; ++j) {
                                 acc[nt][j][e] *= alpha;
@@ -526,7 +530,8 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
                     const int vx = (mt[u] >> 8) & 0xFF;
-                    const float iv = exp2i(127 - vx < -126 ? -126 : min(127 - vx, 126));
+                    const bool deep = (mt[u] >> 16) && vx < 127 + kDeep;
+                    const float iv = deep ? 0.0f : exp2i(127 - vx < -126 ? -126 : min(127 - vx, 126));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float p[4];
@@ -535,6 +540,9 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
                             p[e] = ex2(lg[u][nt][e] - m[nt][e & 1]);
                             l_sum[nt][e & 1] = fmaf(p[e], iv, l_sum[nt][e & 1]);
                         }
+                        if (deep)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) l_sum[nt][e & 1] += ex2(lg[u][nt][e] - static_cast<float>(vx - 127) - m[nt][e & 1]);
                         pb[u][nt][0] = transpose8x8(pack_out<__half>(p[0], p[1]));
                         pb[u][nt][1] = transpose8x8(pack_out<__half>(p[2], p[3]));
                     }
@@ -628,7 +636,8 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
             for (int w = 0; w < had; ++w) {
                 const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kRows + r) * D + d);
                 o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-                sum = fmaf(s_l[w][r], ex2(s_m[w][r] - top), sum);
+                const float half = ex2(0.5f * (s_m[w][r] - top));
+                sum = fmaf(s_l[w][r] * half, half, sum);
             }
             if (i_all == unit_tiles) {
                 const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
@@ -676,8 +685,8 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
     for (int i = sh.x; i <= sh.y; ++i) {
         const int64_t a = state(i);
         const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + 2 * a);
-        const float f = ex2(ml.x - top);
-        sum = fmaf(ml.y, f, sum);
+        const float half = ex2(0.5f * (ml.x - top)), f = half * half;
+        sum = fmaf(ml.y * half, half, sum);
         if (lane < kLanes)
 #pragma unroll
             for (int k = 0; k < kV; ++k) {

@@ -23,7 +23,8 @@
 // p = 2^(u - M), l += p / scale. Where the tile's scales lie too far apart for that
 // to be exact (2^15 for e4m3, 2^24 for integers: blocks of zeros, other documents),
 // the codes stay as they are and the softmax warps take each group of 8 tokens at
-// its own scales: the keys' a factor of its scores, the values' a part of its u.
+// its own scales: the keys' a factor of its scores, the values' a part of its u, and
+// l from u without it (2^63 a key of zeros, next to values whose M is 2^63).
 //
 // Bound: next to the tensor cores' 4 D flops per row and key, shared memory (both
 // operands of S and one of P V come from it, and the converters pass through it)
@@ -128,7 +129,7 @@ struct Tiles {
 struct TileInfo {
     int kref, vref;    // its scales' exponents
     unsigned gone;     // groups of 8 tokens that belong to no block
-    bool wide;         // too far apart for one scale in fp16: see s_below
+    bool wide;         // too far apart for one scale in fp16, or too small: see s_below
 };
 
 // A row's softmax over a wide tile, in 8 columns at a time: a group's scores have its own key scale, its u its own value
@@ -167,9 +168,9 @@ __device__ __noinline__ float2 wide_tile(const WideTile w) {
     }
     if (__any_sync(0xffffffffu, top > m + kGap)) {
         const float x = fmaxf(top, m);
-        const float alpha = ex2(m - x);
+        const float half = ex2(0.5f * (m - x)), alpha = half * half;   // (l may be 2^63 a key, of zeros, or 2^-63)
         m = x;
-        l *= alpha;
+        l = l * half * half;
         if (w.some) {
 #pragma unroll 1
             for (int c = 0; c < D / 8; ++c) {
@@ -446,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     }
                     if (__any_sync(0xffffffffu, pass)) {
                         const float x = fmaxf(top, m);
-                        const float alpha = ex2(m - x);
+                        const float half = ex2(0.5f * (m - x)), alpha = half * half;
                         m = x;
-                        l_sum *= alpha;
+                        l_sum = l_sum * half * half;
                         if (i > 0) {
 #pragma unroll 1
                             for (int c = 0; c < D / 16; ++c) {
@@ -567,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         // a batch of kPer tiles: lane kGroups j + g holds the block and scale bytes of tile j's group g. Looked up in
         // two steps, each a batch before what needs it: the block table's entry, then the scales
         constexpr int kPer = 32 / S::kGroups;
+        constexpr int kDeep = -24;               // value exponents below it: p may be too small for fp32 where its share of l is not
         constexpr int kExact = I8 ? 24 : 15;     // 2^-kExact of the smallest code (1; 2^-9) is fp16's smallest
         const int my_tile = lane / S::kGroups, my_group = lane % S::kGroups;
         struct Found {
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int kx = now.kx - 127, vx = now.vx - 127;
                 const int kref = __reduce_max_sync(0xffffffffu, there ? kx : -64), vref = __reduce_max_sync(0xffffffffu, there ? vx : -64);
                 const int k_below = there ? kref - kx : 0, v_below = there ? vref - vx : 0;
-                const bool k_wide = __any_sync(0xffffffffu, k_below > kExact), v_wide = __any_sync(0xffffffffu, v_below > kExact);
+                const bool k_wide = __any_sync(0xffffffffu, k_below > kExact), v_wide = __any_sync(0xffffffffu, v_below > kExact || (there && vx < kDeep));
                 // groups of no block among those that have tokens
                 const unsigned gone = __ballot_sync(0xffffffffu, mine && now.id < 0 && t0 + 8 * my_group < N) >> from;
                 copies_wait<0>();
