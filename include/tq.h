@@ -748,7 +748,8 @@ tq_status tq_kv8_append(const tq_kv8_cache *cache, int layer, const tq_rows *k, 
 /* How tq_kv8_attention scores and masks. All zero: plain causal attention. */
 typedef struct {
     float scale;                /* 0 means 1/sqrt(head_dim)                                   */
-    float softcap;              /* > 0: score = softcap * tanh(score / softcap)               */
+    float softcap;              /* > 0: score = softcap * tanh(score / softcap), to 2^-16 up  *
+                                 * to a cap of 64, to 2^-19 of itself above                    */
     const float *slopes;        /* device [num_q_heads] or NULL: score -= slope * |p - t|     */
     int window;                 /* > 0: a query at p sees keys t > p - window                 */
     const int32_t *prefix_lens; /* device [batch] or NULL: every query sees keys t < prefix   */

@@ -299,3 +299,19 @@ def test_zeros_next_to_the_largest_values(order, D, L):
     assert kernel_of(c, 1, H * G, L, N) == ("chunk" if L == 300 else "few")
     out = call(c, q, [N], table)
     check(c, q, out, [N], [L], table, kernel_of(c, 1, H * G, L, N))
+
+
+# ------------------------------------------------------------------ caps of any size
+
+@pytest.mark.parametrize("cap", [1e-42, 1e-3, 0.3, 3.0, 50.0, 256.0, 1e4, 1e6, 1e8, 1e20, 3e38])
+@pytest.mark.parametrize("D,L", [(64, 1), (128, 7), (256, 2), (64, 300), (128, 300), (256, 300)])
+def test_caps(D, L, cap):
+    """cap tanh(score / cap) to a relative error, whatever the cap."""
+    H, G, N, BT = 2, 4, 500, 64
+    c = base.filled_cache(8, H, BT, D, E4M3, 270)
+    q = (torch.randn(1, H * G, L, D, generator=gen(271), device=DEV) * 3).to(F16)
+    table = straight(c)
+    kernel = kernel_of(c, 1, H * G, L, 512)
+    assert kernel == ("chunk" if L == 300 else "few")
+    out = call(c, q, [N], table, max_seq=512, softcap=cap)
+    check(c, q, out, [N], [L], table, kernel, cap=float(torch.tensor(cap, dtype=torch.float32)))

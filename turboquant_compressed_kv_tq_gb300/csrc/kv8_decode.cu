@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
                 }
             }
             const bool plain = A.cap <= 0.0f && !A.slopes;
-            const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
+            const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 1.0f / A.cap : 0.0f;
             for (int i = w_begin; i < w_end; i += kU) {
                 uint32_t mt[kU];
                 int t0[kU];   // a tile behind the warp's last one: behind the sequence's end
@@ -473,23 +473,43 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
                     const int kx = mt[u] & 0xFF, vx = (mt[u] >> 8) & 0xFF;
                     const bool here = mt[u] >> 16;
                     const float ks2 = exp2i(kx == 0 ? -126 : kx - 127), lv = static_cast<float>(vx - 127);
+                    // e: token g + 8 (e >> 1), row 2c + (e & 1)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {   // e: token g + 8 (e >> 1), row 2c + (e & 1)
-                            const float s = sc[u][nt][e] * (fac[nt][e & 1] * ks2);
-                            if (plain) {
-                                lg[u][nt][e] = fmaf(s, kLog2e, lv);
-                            } else {
-                                float y = s * kLog2e;
-                                if (A.cap > 0.0f) y = fmaf(-2.0f * cap2, rcp(1.0f + ex2(s * cap_in)), cap2);   // cap tanh(s / cap)
+                        for (int e = 0; e < 4; ++e) sc[u][nt][e] *= fac[nt][e & 1] * ks2;
+                    if (plain) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) lg[u][nt][e] = fmaf(sc[u][nt][e], kLog2e, lv);
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) lg[u][nt][e] = sc[u][nt][e] * kLog2e;
+                        if (A.cap > kUsualCap) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) lg[u][nt][e] = capped_wide(sc[u][nt][e] * cap_in, cap2);
+                        } else if (A.cap > 0.0f) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) lg[u][nt][e] = capped(sc[u][nt][e] * cap_in, cap2);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
                                 if (A.slopes) {
                                     const int p = s_sight[8 * nt + 2 * c + (e & 1)].p;
-                                    y -= slope[nt][e & 1] * fabsf(static_cast<float>(p - (t0[u] + g + 8 * (e >> 1))));
+                                    lg[u][nt][e] -= slope[nt][e & 1] * fabsf(static_cast<float>(p - (t0[u] + g + 8 * (e >> 1))));
                                 }
-                                lg[u][nt][e] = y + lv;
+                                lg[u][nt][e] += lv;
                             }
-                        }
+                    }
                     if (!(here && t0[u] + 15 <= p_min && t0[u] >= lo_max)) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)

@@ -148,7 +148,7 @@ struct WideTile {
 
 template <int D, int kT, bool MOD>
 __device__ __noinline__ float2 wide_tile(const WideTile w) {
-    const float cap2 = w.cap * kLog2e, cap_in = w.cap > 0.0f ? 2.0f * kLog2e / w.cap : 0.0f;
+    const float cap2 = w.cap * kLog2e, cap_in = w.cap > 0.0f ? 1.0f / w.cap : 0.0f;
     float m = w.m, l = w.l, top = -INFINITY;
 #pragma unroll 1
     for (int g = 0; g < kT / 8; ++g) {   // u, masked, back to where the scores were
@@ -159,7 +159,7 @@ __device__ __noinline__ float2 wide_tile(const WideTile w) {
         for (int e = 0; e < 8; ++e) {
             const int t = w.t0 + 8 * g + e;
             x[e] *= kg;
-            x[e] = MOD && w.cap > 0.0f ? fmaf(-2.0f * cap2, rcp(1.0f + ex2(x[e] * cap_in)), cap2) : x[e] * kLog2e;
+            x[e] = MOD && w.cap > 0.0f ? capped_wide(x[e] * cap_in, cap2) : x[e] * kLog2e;
             if (MOD) x[e] = fmaf(-w.slope, fabsf(static_cast<float>(t - w.sight.p)), x[e]);
             x[e] = w.sight.sees(t) && !((w.gone >> g) & 1u) ? x[e] + lv : -INFINITY;
             top = fmaxf(top, x[e]);
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             const Sight sight = sight_of(l_row);
             const int p_min = __reduce_min_sync(0xffffffffu, sight.p), lo_max = __reduce_max_sync(0xffffffffu, sight.lo);
             const float fac = s_fac[min(row, S::kRows - 1)];
-            const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 2.0f * kLog2e / A.cap : 0.0f;
+            const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 1.0f / A.cap : 0.0f;
             const float slope = MOD && A.slopes ? A.slopes[h * A.G + rr % A.G] * kLog2e : 0.0f;
             for (int i = 0;;) {
                 for (; i < n_tiles; ++i) {
@@ -380,11 +380,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     // 64 columns of the row's scores, k a multiple of 64: cap and bias applied, unseen ones -inf
                     auto finish = [&](uint32_t (&sr)[64], int k) {
                         if constexpr (MOD) {
-                            if (A.cap > 0.0f) {   // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+                            if (A.cap > 0.0f) {
                                 const float k2 = kf * cap_in;
+                                if (A.cap <= kUsualCap) {
 #pragma unroll
-                                for (int e = 0; e < 64; ++e)
-                                    sr[e] = __float_as_uint(fmaf(-2.0f * cap2, rcp(1.0f + ex2(__uint_as_float(sr[e]) * k2)), cap2));
+                                    for (int e = 0; e < 64; ++e) sr[e] = __float_as_uint(capped(__uint_as_float(sr[e]) * k2, cap2));
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 64; ++e) sr[e] = __float_as_uint(capped_wide(__uint_as_float(sr[e]) * k2, cap2));
+                                }
                             } else {
                                 const float k2 = kf * kLog2e;
 #pragma unroll
