@@ -315,3 +315,39 @@ def test_caps(D, L, cap):
     assert kernel == ("chunk" if L == 300 else "few")
     out = call(c, q, [N], table, max_seq=512, softcap=cap)
     check(c, q, out, [N], [L], table, kernel, cap=float(torch.tensor(cap, dtype=torch.float32)))
+
+
+# ------------------------------------------------------------------ scores and queries at their ends
+
+@pytest.mark.parametrize("L", [1, 300])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_of_any_size(D, L):
+    """The first row of a sequence sees one key: its output is that key's value, however low the score."""
+    H, G, BT = 2, 4, 256
+    N = L if L > 1 else 1
+    c = base.filled_cache(2, H, BT, D, E4M3, 280)
+    c.k_codes[0] = torch.where(torch.arange(BT, device=DEV) % 3 == 1, 0x3B, 0x3D).to(torch.uint8)[:, None]   # 1.375 or 1.625
+    c.k_scales.fill_(127)
+    q = 1 + torch.rand(1, H * G, L, D, generator=gen(281), device=DEV).to(BF16)
+    table = straight(c)
+    v = (ref.values(c.v_codes[0, 0, :, 0], E4M3) * torch.exp2(c.v_scales[0, 0].double() - 127)[:, None]).repeat_interleave(G, 0)
+    for scale in (1e5, -1e5, 1e7, -1e7, 1e20, -1e20, 1e34, -1e34):
+        out = call(c, q, [N], table, max_seq=512, scale=scale)
+        assert out.isfinite().all()
+        assert ((out[0, :, 0].double() - v).abs() <= v.abs() * 2.0 ** -8 + 2.0 ** -20).all(), scale   # 2^-9 by weight and sum, half a step
+
+
+@pytest.mark.parametrize("L", [1, 300])
+def test_biases_of_any_size(L):
+    """Rows that see the sequence's first two keys only, so far away that the bias is beyond 2^24."""
+    D, H, G, BT, N = 128, 2, 4, 256, 512
+    c = base.filled_cache(2, H, BT, D, E4M3, 283)
+    c.k_codes[0] = 0x38
+    q = torch.ones(1, H * G, L, D, device=DEV).to(BF16)
+    v = (ref.values(c.v_codes[0, 0, :, :2], E4M3) * torch.exp2(c.v_scales[0, 0].double() - 127)[:, None, None]).repeat_interleave(G, 0)
+    for slope, want in ((0.0, v.mean(1)), (3e7, v[:, 1]), (1e12, v[:, 1])):   # the nearer key
+        slopes = torch.full((H * G,), slope, device=DEV)
+        docs = torch.full((1, L), N, dtype=torch.int32, device=DEV)
+        out = call(c, q, [N], straight(c), slopes=slopes, doc_starts=docs, prefix_lens=i32([2]))
+        w = want[:, None].expand(-1, L, -1)
+        assert ((out[0].double() - w).abs() <= w.abs() * 2.0 ** -8 + v.abs().amax() * 2.0 ** -11).all(), slope

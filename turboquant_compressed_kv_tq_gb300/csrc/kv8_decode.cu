@@ -44,7 +44,7 @@ namespace kv8 {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNone = -1e30f;    // reference of a row that has seen nothing
+constexpr float kNone = -FLT_MAX;  // reference of a row that has seen nothing: below every score
 constexpr float kGap = 8.0f;       // how far scores may pass the reference (log2 units)
 constexpr int kDeep = -24;         // tiles of value exponents below it: p may be too small for fp32 where its share of l is not,
 constexpr float kLift = 64.0f;     // so l takes p 2^kLift (without a branch: one cost 215 us for 212 in the batch measured above)

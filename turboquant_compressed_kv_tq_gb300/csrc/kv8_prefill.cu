@@ -42,7 +42,7 @@ namespace kv8 {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNone = -1e30f;
+constexpr float kNone = -FLT_MAX;   // below every score
 constexpr float kGap = 8.0f;
 constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 15, kThreads = 32 * (kMmaWarp + 1);
 
@@ -126,18 +126,18 @@ struct Tiles {
 };
 
 // What the converters say about a tile.
+constexpr int kWide = 1 << 12;
 struct TileInfo {
-    int kref, vref;    // its scales' exponents
+    int kref, vref;    // its scales' exponents; kref + kWide where they are too far apart for one scale in fp16, or too small: see s_below
     unsigned gone;     // groups of 8 tokens that belong to no block
-    bool wide;         // too far apart for one scale in fp16, or too small: see s_below
 };
 
-// A row's softmax over a wide tile, in 8 columns at a time: a group's scores have its own key scale, its u its own value
+// A row's softmax over a wide tile (or one of large scores), in 8 columns at a time: a group's scores have its own key scale, its u its own value
 // scale. (Rare, and a function of its own: the usual tile's code and registers stay as they are without it.)
 struct WideTile {
     uint32_t t_s, t_p, t_o;    // S, P and O of this thread's rows
     bool some;                 // O holds something
-    const uint16_t* below;
+    const uint16_t* below;     // s_below, or null: all of them at the tile's scales
     int kref, vref;            // the tile's largest exponents
     float fac, cap, slope;     // of the scores, but for the key scale
     Sight sight;
@@ -152,7 +152,8 @@ __device__ __noinline__ float2 wide_tile(const WideTile w) {
     float m = w.m, l = w.l, top = -INFINITY;
 #pragma unroll 1
     for (int g = 0; g < kT / 8; ++g) {   // u, masked, back to where the scores were
-        const float kg = w.fac * exp2i(max(w.kref - (w.below[g] & 0xFF), -126)), lv = static_cast<float>(w.vref - (w.below[g] >> 8));
+        const int below = w.below ? w.below[g] : 0;
+        const float kg = w.fac * exp2i(max(w.kref - (below & 0xFF), -126)), lv = static_cast<float>(w.vref - (below >> 8));
         float x[8];
         tc::tmem_ld8(w.t_s + 8 * g, x);
 #pragma unroll
@@ -187,7 +188,7 @@ __device__ __noinline__ float2 wide_tile(const WideTile w) {
         uint32_t pr[16];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const float lv = static_cast<float>(w.vref - (w.below[4 * n + g] >> 8));
+            const float lv = static_cast<float>(w.vref - (w.below ? w.below[4 * n + g] >> 8 : 0));
             float x[8];
             tc::tmem_ld8(w.t_s + 32 * n + 8 * g, x);
 #pragma unroll
@@ -365,6 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             const float fac = s_fac[min(row, S::kRows - 1)];
             const float cap2 = A.cap * kLog2e, cap_in = A.cap > 0.0f ? 1.0f / A.cap : 0.0f;
             const float slope = MOD && A.slopes ? A.slopes[h * A.G + rr % A.G] * kLog2e : 0.0f;
+            // u less its reference, in one rounding, leaves the row's largest within what the reference was rounded by: up to 1
+            // for scores below 2^24 (kref at most k_most by what queries in [1, 2) and the largest codes allow, and the bias).
+            // Larger ones go the way of wide tiles, where u is rounded first and the largest gets exactly 2^0
+            constexpr int kCodes = (I8 ? 8 : 10) + (D == 64 ? 6 : D == 128 ? 7 : 8);   // log2 (rounded down) of the largest code times log2(e), 2, D
+            const int k_most = __reduce_min_sync(0xffffffffu, fabsf(slope) * static_cast<float>(N) > 0x1p23f
+                                                                  ? -256 : 23 - kCodes - (static_cast<int>(__float_as_uint(fac) >> 23) - 126));
             for (int i = 0;;) {
                 for (; i < n_tiles; ++i) {
                     const int t0 = tiles.at(i) * kT;
@@ -373,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     if (!ok) break;
                     tc::tc_fence_after();
                     const TileInfo info = s_info[i & 3];
+                    if (info.kref > k_most) break;
                     const float kf = fac * exp2i(info.kref), lv = static_cast<float>(info.vref);
-                    if (info.wide) break;
                     const float f = MOD ? 1.0f : fmaxf(kf * kLog2e, FLT_MIN);
                     const bool open = info.gone == 0 && ((t0 + kT - 1 <= p_min && t0 >= lo_max) || t0 + kT <= pre);
                     // 64 columns of the row's scores, k a multiple of 64: cap and bias applied, unseen ones -inf
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     l_sum = fmaf((a + c) + (d + g), exp2i(-info.vref), l_sum);
                 }
                 if (!ok || i == n_tiles) break;
-                // a wide one, whose scores are there
+                // a wide one, or of large scores, which are there
                 const int t0 = tiles.at(i) * kT, sb = kH == 2 ? half : i & 1;
                 const TileInfo info = s_info[i & 3];
                 if (kH == 1 && i > 0) {
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     tc::tc_fence_after();
                 }
                 const float2 ml = wide_tile<D, kT, MOD>(WideTile{
-                    t_row + S::kS + sb * S::kSStep, t_row + S::kP + sb * S::kPStep, t_o, i > 0, s_below[i & 3], info.kref,
+                    t_row + S::kS + sb * S::kSStep, t_row + S::kP + sb * S::kPStep, t_o, i > 0, info.kref >= kWide / 2 ? s_below[i & 3] : nullptr, info.kref >= kWide / 2 ? info.kref - kWide : info.kref,
                     info.vref, fac, A.cap, slope, sight, t0, info.gone, m, l_sum});
                 m = ml.x;
                 l_sum = ml.y;
@@ -683,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 if (!ok) break;
                 if (warp == kKWarp) {
                     if ((k_wide || v_wide) && mine) s_below[i & 3][my_group] = static_cast<uint16_t>((k_wide ? k_below : 0) | (v_wide ? v_below : 0) << 8);
-                    if (lane == 0) s_info[i & 3] = TileInfo{kref, vref, gone, k_wide || v_wide};
+                    if (lane == 0) s_info[i & 3] = TileInfo{kref + (k_wide || v_wide ? kWide : 0), vref, gone};
                 }
                 convert((is_v ? v_wide : k_wide) ? 0 : is_v ? v_below : k_below, now.id, from, N - t0, operand + st * S::kOperand);
                 tc::fence_proxy_async_smem();
