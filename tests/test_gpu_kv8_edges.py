@@ -351,3 +351,25 @@ def test_biases_of_any_size(L):
         out = call(c, q, [N], straight(c), slopes=slopes, doc_starts=docs, prefix_lens=i32([2]))
         w = want[:, None].expand(-1, L, -1)
         assert ((out[0].double() - w).abs() <= w.abs() * 2.0 ** -8 + v.abs().amax() * 2.0 ** -11).all(), slope
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("L,row", [(2, 1), (300, 17), (300, 299)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_queries_that_are_no_numbers(D, L, row, bad):
+    """A NaN in a query makes its own row NaN, as the formula has it, and no other."""
+    H, G, N, BT = 2, 4, 500, 64
+    c = base.filled_cache(8, H, BT, D, E4M3, 290)
+    c.k_codes[..., 5] = 0x38          # infinite scores of one sign but for one key's
+    c.k_codes[0, 0, :, 0, 5] = 0xB8
+    q = torch.randn(1, H * G, L, D, generator=gen(291), device=DEV).to(BF16)
+    table = straight(c)
+    kernel = kernel_of(c, 1, H * G, L, 512)
+    assert kernel == ("chunk" if L == 300 else "few")
+    fine = call(c, q, [N], table, max_seq=512)
+    odd = q.clone()
+    odd[0, 2, row, 5] = bad
+    out = call(c, odd, [N], table, max_seq=512)
+    assert out[0, 2, row].isnan().all()
+    out[0, 2, row] = fine[0, 2, row]
+    check(c, q, out, [N], [L], table, kernel)

@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (mine) {
             // by way of the rows' own place among the queries (nothing reads it any more), so that a row's bytes
             // are stored together; 16-byte chunks trade places by their row, free of bank conflicts
-            const float inv = !failed && l_sum > 0.0f ? 1.0f / l_sum : 0.0f;
+            const bool some = !failed && l_sum != 0.0f;   // (a NaN among the scores makes the row NaN)
+            const float inv = some ? 1.0f / l_sum : 0.0f;
             constexpr int kChunks = D / 8;
             unsigned char* stage = smem + S::kQOff + (128 * half + 32 * (warp & 3)) * D * 2;
 #pragma unroll
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint4 w = make_uint4(0, 0, 0, 0);
-                    if (inv > 0.0f) {
+                    if (some) {
                         w.x = pack_out<T>(v[8 * e] * inv, v[8 * e + 1] * inv), w.y = pack_out<T>(v[8 * e + 2] * inv, v[8 * e + 3] * inv);
                         w.z = pack_out<T>(v[8 * e + 4] * inv, v[8 * e + 5] * inv), w.w = pack_out<T>(v[8 * e + 6] * inv, v[8 * e + 7] * inv);
                     }
