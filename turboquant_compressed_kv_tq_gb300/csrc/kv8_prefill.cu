@@ -81,6 +81,10 @@ __device__ __forceinline__ bool arrived(uint64_t* bar, unsigned parity) {
     return false;
 }
 
+// The same by a whole warp, with one answer for all its lanes: what follows, waited for or given up, is warp-wide
+// (tensor memory, shuffles), and must not find a part of the warp gone.
+__device__ __forceinline__ bool arrived_warp(uint64_t* bar, unsigned parity) { return __all_sync(0xffffffffu, arrived(bar, parity)); }
+
 // Byte offset of (row, d) in an operand of core matrices: 8 rows x 16 bytes.
 template <int D>
 __device__ __forceinline__ int core(int row, int d) {
@@ -376,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 for (; i < n_tiles; ++i) {
                     const int t0 = tiles.at(i) * kT;
                     const int sb = kH == 2 ? half : i & 1;                    // buffer of S and P
-                    ok = arrived(&s_ready[sb], kH == 2 ? i & 1 : (i >> 1) & 1);
+                    ok = arrived_warp(&s_ready[sb], kH == 2 ? i & 1 : (i >> 1) & 1);
                     if (!ok) break;
                     tc::tc_fence_after();
                     const TileInfo info = s_info[i & 3];
@@ -452,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     top = fmaf(top, f, lv);
                     const bool pass = top > m + kGap;
                     if (kH == 1 && i > 0) {   // every phase in its turn: a wait by parity tells neighbouring phases apart, no others
-                        ok = arrived(&o_done[0], (i - 1) & 1);
+                        ok = arrived_warp(&o_done[0], (i - 1) & 1);
                         if (!ok) break;
                         tc::tc_fence_after();
                     }
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int t0 = tiles.at(i) * kT, sb = kH == 2 ? half : i & 1;
                 const TileInfo info = s_info[i & 3];
                 if (kH == 1 && i > 0) {
-                    ok = arrived(&o_done[0], (i - 1) & 1);
+                    ok = arrived_warp(&o_done[0], (i - 1) & 1);
                     if (!ok) break;
                     tc::tc_fence_after();
                 }
@@ -524,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 }
                 ++i;
             }
-            if (ok) ok = arrived(&o_done[kH == 2 ? half : 0], kH == 2 ? 0 : (n_tiles - 1) & 1);
+            if (ok) ok = arrived_warp(&o_done[kH == 2 ? half : 0], kH == 2 ? 0 : (n_tiles - 1) & 1);
             if (!ok) {
                 s_fail = 1;
                 atomicOr(A.err, TQ_DEVERR_TIMEOUT);
@@ -686,9 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 // groups of no block among those that have tokens
                 const unsigned gone = __ballot_sync(0xffffffffu, mine && now.id < 0 && t0 + 8 * my_group < N) >> from;
                 copies_wait<0>();
-                if (i >= 2) ok = arrived(&free[st], ((i >> 1) - 1) & 1);
-                else if (i == 1) ok = arrived(q_ready, 0);   // whose angles are in the second stages
-                if (!ok) break;
+                // (a lane whose wait ran out waits no more, but goes on with its warp: the prompt above: 676 us; with a vote here 688)
+                if (i > 0 && ok) ok = i >= 2 ? arrived(&free[st], ((i >> 1) - 1) & 1) : arrived(q_ready, 0);   // whose angles are in the second stages
                 if (warp == kKWarp) {
                     if ((k_wide || v_wide) && mine) s_below[i & 3][my_group] = static_cast<uint16_t>((k_wide ? k_below : 0) | (v_wide ? v_below : 0) << 8);
                     if (lane == 0) s_info[i & 3] = TileInfo{kref + (k_wide || v_wide ? kWide : 0), vref, gone};
