@@ -373,3 +373,17 @@ def test_queries_that_are_no_numbers(D, L, row, bad):
     assert out[0, 2, row].isnan().all()
     out[0, 2, row] = fine[0, 2, row]
     check(c, q, out, [N], [L], table, kernel)
+
+
+# ------------------------------------------------------------------ appends of every block size
+
+@pytest.mark.parametrize("D,BT,n", [(64, 256, 150), (64, 256, 152), (64, 256, 153), (64, 256, 154), (128, 128, 84), (128, 128, 85), (128, 256, 86),
+                                    (256, 64, 44), (256, 64, 45), (256, 128, 46)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_appends_whose_angles_fill_48_kb(D, BT, n, dtype):
+    c = base.dirty_cache(2, 1, BT, D, E4M3, 300)
+    k, v = (torch.randn(1, 1, n, D, generator=gen(s), device=DEV).to(dtype) for s in (301, 302))
+    rope = tq.Rope.of_base(D)
+    before = base.tensors(c)
+    c.append(0, k, v, i32([0]), straight(c), 2, rope=rope)
+    base.check_append(c, before, k, v, [0], [n], straight(c), rope)

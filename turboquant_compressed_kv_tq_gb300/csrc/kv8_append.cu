@@ -220,7 +220,7 @@ cudaError_t launch_append_f(const AppendArgs& args, int sms, cudaStream_t s) {
     const int threads = std::max(32, std::min(most, (tokens * (D / 16) + 31) / 32 * 32));
     const int k = most == 1024 ? 2 : most == 512 ? 1 : 0;
     auto kernel = k == 2 ? append_kernel<T, D, I8, 1024> : k == 1 ? append_kernel<T, D, I8, 512> : append_kernel<T, D, I8, 256>;
-    if (a.angle_smem > 48 * 1024) {
+    if (a.angle_smem > 40 * 1024) {   // (a launch's first 48 KB hold the static arrays too, 1.3 KB at most)
         static std::atomic<uint64_t> allowed[3] = {};
         const cudaError_t e = allow_smem(kernel, kMostSmem, allowed[k]);
         if (e != cudaSuccess) return e;
