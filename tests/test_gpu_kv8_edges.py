@@ -387,3 +387,25 @@ def test_appends_whose_angles_fill_48_kb(D, BT, n, dtype):
     before = base.tensors(c)
     c.append(0, k, v, i32([0]), straight(c), 2, rope=rope)
     base.check_append(c, before, k, v, [0], [n], straight(c), rope)
+
+
+# ------------------------------------------------------------------ another stream than the current one
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_and_workspaces_belong_to_the_calls_stream(raw):
+    """The output (zeroed behind q_lens) and the workspace are made on the stream that the call names."""
+    c = base.filled_cache(64, 2, 64, 128, E4M3, 310)
+    table = straight(c)
+    q = torch.randn(1, 8, 3, 128, generator=gen(311), device=DEV).to(BF16)
+    n, nq = i32([4000]), i32([2])
+    want = c.attention(0, q, n, table, 64, 4096, q_lens=nq)
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)   # about 10 ms of the current stream
+        out = c.attention(0, q, n, table, 64, 4096, q_lens=nq, stream=side.cuda_stream if raw else side)
+        side.synchronize()
+        assert torch.equal(out, want)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        del out

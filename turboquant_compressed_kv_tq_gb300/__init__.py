@@ -538,6 +538,12 @@ _pack_rows = struct.Struct("@Pqqq").pack                 # tq_rows
 _pack_scores = struct.Struct("@ffPiPPPP").pack           # tq_kv8_scores
 
 
+def _on(stream):
+    """Allocations and fills on the stream that a call names (None: the current one)."""
+    cuda = _torch().cuda
+    return cuda.stream(cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _rows(t, name, dtype, device, batch, heads, tokens, dim) -> bytes:
     """tq_rows of a [batch, heads, tokens, head_dim] view, in whatever order its first three axes lie."""
     if t.shape != (batch, heads, tokens, dim):
@@ -628,8 +634,8 @@ def tq_kv8_attention(cache: "KV8Cache", layer, q, seq_lens, block_table=None, ma
                      doc_starts=None, rope=None, positions=None, stream=None):
     """Attention of q [batch, query heads, q_len, head_dim] over the cache; returns out (like q if None).
 
-    Without `out`, rows behind q_lens are zero. Without `workspace`, one is taken from torch's allocator on the
-    current stream, so give one where `stream` is another.
+    Without `out`, rows behind q_lens are zero. An output and a workspace that are not given are made on `stream`, and
+    belong to it in torch's allocator.
     """
     t, device = _kv8(), cache.index
     if t.device() != device:
@@ -646,7 +652,8 @@ def tq_kv8_attention(cache: "KV8Cache", layer, q, seq_lens, block_table=None, ma
         raise TypeError(f"unsupported dtype {dtype}")
     qr = _rows(q, "q", dtype, device, batch, heads, q_len, dim)
     if out is None:
-        out = _torch().empty_like(q) if q_lens is None else _torch().zeros_like(q)
+        with _on(stream):
+            out = _torch().empty_like(q) if q_lens is None else _torch().zeros_like(q)
     if rope is not None and rope.device != device:
         raise ValueError(f"rope must be on cuda:{device}")
     per, each, sc = (batch,), (batch, q_len), None
@@ -658,7 +665,9 @@ def tq_kv8_attention(cache: "KV8Cache", layer, q, seq_lens, block_table=None, ma
                           _array(positions, "positions", i32, device, each) or 0)
     if workspace is None:
         n = tq_kv8_workspace_bytes(cache, batch, heads, q_len, max_seq_len)
-        workspace = _torch().empty(n, dtype=_torch().uint8, device=cache.device) if n else None
+        if n:
+            with _on(stream):
+                workspace = _torch().empty(n, dtype=_torch().uint8, device=cache.device)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on cuda:{device}")
     status = t.attention(
