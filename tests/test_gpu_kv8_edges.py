@@ -409,3 +409,27 @@ def test_outputs_and_workspaces_belong_to_the_calls_stream(raw):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
         del out
+
+
+# ------------------------------------------------------------------ outputs between the queries
+
+@pytest.mark.parametrize("L", [1, 3, 300])
+def test_outputs_in_the_queries_tensor(L):
+    """Next to the queries, in a slot of its own of one tensor: every layout whose rows are apart."""
+    B, H, G, D, BT, N = 2, 2, 4, 64, 64, 400
+    c = base.filled_cache(16, H, BT, D, E4M3, 320)
+    table = straight(c, B)
+    both = torch.randn(B, L, 2, H * G, D, generator=gen(321), device=DEV).to(BF16)
+    q, out = both[:, :, 0].transpose(1, 2), both[:, :, 1].transpose(1, 2)
+    want = call(c, q.clone(), [N, N], table, max_seq=512)
+    before = both.clone()
+    assert call(c, q, [N, N], table, max_seq=512, out=out) is out
+    assert torch.equal(out, want) and torch.equal(both[:, :, 0], before[:, :, 0])
+    # one after the other, and heads of the two in turn
+    flat = torch.empty(2, B, H * G, L, D, device=DEV, dtype=BF16)
+    turn = torch.empty(B, H * G, 2, L, D, device=DEV, dtype=BF16)
+    for q1, out1 in ((flat[0], flat[1]), (flat[1], flat[0]), (turn[:, :, 0], turn[:, :, 1]), (turn[:, :, 1], turn[:, :, 0])):
+        q1.copy_(before[:, :, 0].transpose(1, 2))
+        assert torch.equal(call(c, q1, [N, N], table, max_seq=512, out=out1), want)
+    with pytest.raises(tq.TQError):
+        call(c, q[:, :4], [N, N], table, max_seq=512, out=q[:, 1:5])

@@ -3,6 +3,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
+#include <utility>
 
 #include "kv8.h"
 
@@ -47,6 +49,39 @@ tq_status check_rows(const tq_rows* r, int elem) {
     if (r->stride_batch * elem % 16 != 0 || r->stride_head * elem % 16 != 0 || r->stride_token * elem % 16 != 0)
         return TQ_ERR_INVALID_ARG;
     return TQ_OK;
+}
+
+// The axes of rows of heads, in elements, the largest stride first; an axis of one element has none.
+struct Axes {
+    int64_t stride[3], n[3];
+    Axes(const tq_rows* r, int64_t nb, int64_t nh, int64_t nt) : stride{r->stride_batch, r->stride_head, r->stride_token}, n{nb, nh, nt} {
+        for (int i = 0; i < 3; ++i) stride[i] = n[i] > 1 ? std::abs(stride[i]) : 0;
+        for (int i = 0; i < 2; ++i)
+            for (int k = 0; k < 2 - i; ++k)
+                if (stride[k] < stride[k + 1]) std::swap(stride[k], stride[k + 1]), std::swap(n[k], n[k + 1]);
+    }
+    // Whether two rows whose starts differ by a sum of steps along axes k.. lie within D elements of being `delta` apart. A
+    // yes has such rows to show; a no is sure where each stride is as long as what the smaller ones span.
+    bool meet(int64_t delta, int k, int D) const {
+        if (k == 3 || stride[k] == 0) return std::abs(delta) < D;
+        const int64_t d = delta / stride[k];
+        for (int64_t i = d - 1; i <= d + 1; ++i)
+            if (std::abs(i) < n[k] && meet(delta - i * stride[k], k + 1, D)) return true;
+        return false;
+    }
+};
+
+// Whether rows of out share memory with each other, or with q's rows where those lie as out's do.
+bool out_overlaps(const tq_rows* q, const tq_rows* out, int64_t nb, int64_t nh, int64_t nt, int D) {
+    const Axes o(out, nb, nh, nt);
+    for (int k = 0; k < 3; ++k)
+        if ((o.stride[k] > 0 && o.meet(o.stride[k], k + 1, D)) || (o.stride[k] == 0 && o.n[k] > 1)) return true;
+    if (q->data == out->data) return true;
+    if ((nb > 1 && q->stride_batch != out->stride_batch) || (nh > 1 && q->stride_head != out->stride_head) ||
+        (nt > 1 && q->stride_token != out->stride_token))
+        return false;
+    const int64_t apart = (reinterpret_cast<intptr_t>(out->data) - reinterpret_cast<intptr_t>(q->data)) / 2;
+    return o.meet(apart, 0, D);
 }
 
 tq_status make_rope(const tq_rope* r, int D, const int32_t* positions, Rope* out) {
@@ -194,7 +229,7 @@ tq_status tq_kv8_attention(const tq_kv8_cache* cache, int layer, const tq_rows* 
     if ((st = make_rope(sc.rope, cache->head_dim, sc.positions, &a.rope)) != TQ_OK) return st;
     if (batch == 0 || q_len == 0) return TQ_OK;
     if ((st = check_rows(q, 2)) != TQ_OK || (st = check_rows(out, 2)) != TQ_OK) return st;
-    if (!seq_lens || q->data == out->data) return TQ_ERR_INVALID_ARG;
+    if (!seq_lens || out_overlaps(q, out, batch, num_q_heads, q_len, cache->head_dim)) return TQ_ERR_INVALID_ARG;
     int sms = 0;
     if (device_state(&a.err, &sms) != TQ_OK) return TQ_ERR_CUDA;
     const AttendPlan p = attend_plan(cache->head_dim, batch, cache->num_kv_heads, num_q_heads / cache->num_kv_heads, q_len, max_seq_len, sms);
