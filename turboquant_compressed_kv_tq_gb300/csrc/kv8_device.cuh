@@ -81,7 +81,7 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
     const int ex = static_cast<int>((u >> 52) & 0x7FF);
     if (ex == 0) return 0;   // zero, and subnormals
     const uint64_t m = (u & 0xFFFFFFFFFFFFFull) | (1ull << 52);
-    const uint64_t kC = 0xA2F9836E4E441529ull;   // 2^66 / (2 pi)
+    const uint64_t kC = 0xA2F9836E4E44152Aull;   // 2^66 / (2 pi)
     const uint64_t hi = __umul64hi(m, kC), lo = m * kC;
     const int sh = 54 - (ex - 1023);   // value = (hi:lo) >> sh
     uint64_t t;
