@@ -338,6 +338,35 @@ def test_scores_of_any_size(D, L):
 
 
 @pytest.mark.parametrize("L", [1, 300])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_small_values_under_large_scores(D, L):
+    """Every second block's values are of the smallest scales; all keys have one score. And the newest block alone, under
+    scores of any size.
+
+    The exponent of a weight is one fp32 number, score x log2(e) + the value scale's exponent. At the larger of the first
+    scores, 1e4 (2^13.8 in log2 units), it is rounded by up to 2^-11, next to half a step of bf16 (2^-9) and the weights'
+    2^-11; from 2^24 on by more than 1, so that the scales of different blocks are not told apart: no case for that."""
+    H, G, BT, N = 2, 4, 16, 512
+    c = base.filled_cache(32, H, BT, D, E4M3, 284)
+    c.k_codes[0], c.k_scales[0] = 0x38, 127
+    c.v_scales[0, ::2] = 127 - 50
+    q = torch.ones(1, H * G, L, D, device=DEV).to(BF16)
+    table = straight(c)
+    docs = torch.arange(N - L, N, dtype=torch.int32, device=DEV).view(1, L)
+    for scale in (0.01, 1e4 / D, 1e6, 1e20):
+        if scale < 1e3:
+            out = call(c, q, [N], table, scale=scale)
+            if scale == 0.01:
+                check(c, q, out, [N], [L], table, kernel_of(c, 1, H * G, L, N), scale=scale)
+                want = out.double()
+            assert ((out.double() - want).abs() <= want.abs() * 2.0 ** -7 + 2.0 ** -12).all(), scale
+        # the newest block alone, of small values
+        out = call(c, q, [N - BT], table, max_seq=N, scale=scale, doc_starts=docs - BT)
+        v = (ref.values(c.v_codes[0, 30].transpose(0, 1), E4M3) * 2.0 ** -50)[-min(L, BT):].repeat_interleave(G, 1)   # [n, heads, D]
+        assert ((out[0, :, L - len(v):].double() - v.transpose(0, 1)).abs() <= v.transpose(0, 1).abs() * 2.0 ** -8 + 2.0 ** -134).all(), scale
+
+
+@pytest.mark.parametrize("L", [1, 300])
 def test_biases_of_any_size(L):
     """Rows that see the sequence's first two keys only, so far away that the bias is beyond 2^24."""
     D, H, G, BT, N = 128, 2, 4, 256, 512

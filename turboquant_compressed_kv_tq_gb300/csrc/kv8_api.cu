@@ -247,7 +247,7 @@ tq_status tq_kv8_attention(const tq_kv8_cache* cache, int layer, const tq_rows* 
     a.qlens = q_lens;
     a.max_seq = max_seq_len;
     a.scale = sc.scale == 0.0f ? 1.0f / std::sqrt(static_cast<float>(cache->head_dim)) : sc.scale;
-    a.cap = sc.softcap > 0.0f ? std::min(std::max(sc.softcap, 1e-30f), 0x1p120f) : 0.0f;   // beyond: all scores alike, or none capped
+    a.cap = sc.softcap > 0.0f ? std::min(std::max(sc.softcap, 1e-20f), 0x1p120f) : 0.0f;   // beyond: all scores alike, or none capped
     a.slopes = sc.slopes;
     a.window = std::min(sc.window, kMaxTokens);   // wider than any sequence: none, and positions less it stay in 32 bits
     a.prefix = sc.prefix_lens;

@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::kWarps, 1) decode_kernel(co
                         float p[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            p[e] = ex2(lg[u][nt][e] - (m[nt][e & 1] - lift));
+                            p[e] = ex2((lg[u][nt][e] - m[nt][e & 1]) + lift);
                             l_sum[nt][e & 1] = fmaf(p[e], iv, l_sum[nt][e & 1]);
                         }
                         pb[u][nt][0] = transpose8x8(pack_out<__half>(p[0] * drop, p[1] * drop));
