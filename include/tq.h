@@ -668,7 +668,14 @@ tq_status tq_decode_attention_noalloc(const tq_codec *key_codec, const tq_codec 
  * apart: e4m3 values, or two's-complement integers. Each (block, KV head) has
  * one scale for its keys and one for its values, a power of two held as the
  * byte x = e + 127 (scale 2^e; the E8M0 reading). A cached value is code * 2^e.
- * The append writes e in [-63, 63], and attention takes no other.
+ * The append writes e in [-63, 63] and no NaN code (0x7F, 0xFF of e4m3); attention
+ * takes no other scale, and no NaN code among a sequence's tokens (behind them
+ * any byte may stand).
+ *
+ * tq_batch_extend, tq_batch_merge, tq_batch_extract and tq_cache_copy_blocks move
+ * the compressed cache's blocks only. Where they give a sequence other blocks and
+ * an 8-bit cache shares the block table, the caller copies the codes and scales of
+ * those blocks too ([block] is the outer axis of a layer's tensors).
  */
 typedef enum { TQ_KV8_E4M3 = 0, TQ_KV8_INT8 = 1 } tq_kv8_format;
 
@@ -721,7 +728,7 @@ typedef struct {
  *   seq_lens   device int32 [batch], tokens already cached (not modified)
  *   new_lens   device int32 [batch] in [0, n_new], or NULL: n_new each
  *   positions  device int32 [batch][n_new], rotation positions, or NULL: the
- *              position in the cache
+ *              position in the cache (without a rope they are not looked at)
  *   block_table, max_blocks: as tq_encode_append; no block may stand twice in
  *              the batch's tables at the places that are appended to
  * Scale of a block and head: the smallest 2^e at which the largest magnitude
@@ -756,7 +763,7 @@ typedef struct {
     const int32_t *doc_starts;  /* device [batch][q_len] or NULL: query l sees t >= doc_start */
     const tq_rope *rope;        /* rotate the queries on the way in, or NULL                  */
     const int32_t *positions;   /* device [batch][q_len], the queries' rotation positions, or *
-                                 * NULL: their positions in the cache                          */
+                                 * NULL: their positions in the cache (no rope: not looked at) */
 } tq_kv8_scores;
 
 /* Workspace (device bytes) tq_kv8_attention needs for these sizes on the current device. */
@@ -781,8 +788,10 @@ tq_status tq_kv8_workspace_bytes(const tq_kv8_cache *cache, int batch, int num_q
  *              TQ_DEVERR_SEQLEN
  *   q_lens     device int32 [batch] in [0, q_len], or NULL: q_len each (others:
  *              TQ_DEVERR_SEQLEN, and the nearest of them)
- *   block_table, max_blocks: as tq_encode_append. Blocks that no query of the
- *              sequence sees are not looked at (their entries may be anything);
+ *   block_table, max_blocks: as tq_encode_append. Blocks between the prefix and
+ *              the queries' first key, the smallest max(p - window + 1, doc_start)
+ *              of the sequence, are not looked at, nor are those behind its end
+ *              (their entries may be anything);
  *              an id outside the pool counts as a block that nobody sees and
  *              sets TQ_DEVERR_BLOCK.
  *   scores     NULL: plain causal attention

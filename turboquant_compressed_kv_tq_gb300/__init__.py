@@ -694,7 +694,8 @@ class KV8Cache:
 
     @classmethod
     def wrap(cls, k_codes, v_codes, k_scales, v_scales, format: int = TQ_KV8_E4M3) -> "KV8Cache":
-        """A cache over tensors of the caller's (uint8; without the layer axis: one layer). Scale bytes in [64, 190]."""
+        """A cache over tensors of the caller's (uint8; without the layer axis: one layer). Scale bytes in [64, 190], and
+        no NaN codes among the tokens that attention is to see."""
         self = cls.__new__(cls)
         if k_codes.dim() == 4:
             k_codes, v_codes, k_scales, v_scales = (t.unsqueeze(0) for t in (k_codes, v_codes, k_scales, v_scales))

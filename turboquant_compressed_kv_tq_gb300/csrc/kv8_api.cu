@@ -124,7 +124,8 @@ tq_status check_sizes(const tq_kv8_cache* c, int batch, int Hq, int L, int max_s
 AttendPlan attend_plan(int D, int batch, int H, int G, int L, int max_seq, int num_sms) {
     AttendPlan p{};
     const int rows = G * L;
-    // Which kernel, for more than 16 rows a KV head. The split kernel reads the cache once for each 16 rows, at about
+    // Which kernel, for more than 16 rows a KV head (by lengths alone: what a window or documents hide is not counted, and
+    // costs both less). The split kernel reads the cache once for each 16 rows, at about
     // 4.8 TB/s (4 at head_dim 64), behind some 18 us of set-up and 4 us for each unit that an SM takes; the chunk kernel
     // reads it once for 256 (128), but walks a sequence on one SM, at 1.5 / 2.1 / 1.9 us a tile of 128 / 128 / 64 tokens.
     // Measured, split and chunk, us: 4 heads x 16 queries over 32768 tokens, 8 KV heads, head_dim 128: 68, 531; 64 queries
