@@ -31,8 +31,8 @@
 // warp's own queue of stages in shared memory.
 //
 // Bound: memory, 2 D bytes a token. Measured: 32 sequences of 4096 to 32,768 tokens,
-// 8 KV heads of 128, 4 rows each: 211 us, 5.9 TB/s (87 % of a plain copy); 16 rows
-// over 262,144 tokens: 111 us, 4.8 TB/s (instructions that wait on one another).
+// 8 KV heads of 128, 4 rows each: 213 us, 5.8 TB/s (86 % of a plain copy); 16 rows
+// over 262,144 tokens: 109 us, 4.9 TB/s (instructions that wait on one another).
 #include <climits>
 #include <type_traits>
 
