@@ -782,7 +782,7 @@ tq_status tq_kv8_workspace_bytes(const tq_kv8_cache *cache, int batch, int num_q
  *              or f16; query head hq reads KV head hq / (num_q_heads/num_kv_heads).
  *              Rows l >= q_lens[b] of out stay as they were. Rows of out may not share memory
  *              with each other or with q (TQ_ERR_INVALID_ARG where out's own strides, or q's
- *              equal ones, show that they do).
+ *              equal ones, show that they do; with q_lens, only a row's heads are looked at).
  *   seq_lens   device int32 [batch] in [0, min(max_seq_len, capacity)]: all
  *              tokens, the queries' own among them; others count as 0 and set
  *              TQ_DEVERR_SEQLEN

@@ -462,3 +462,19 @@ def test_outputs_in_the_queries_tensor(L):
         assert torch.equal(call(c, q1, [N, N], table, max_seq=512, out=out1), want)
     with pytest.raises(tq.TQError):
         call(c, q[:, :4], [N, N], table, max_seq=512, out=q[:, 1:5])
+
+
+@pytest.mark.parametrize("L", [3, 300])
+def test_rows_behind_the_queries_may_lie_over_others(L):
+    """Sequences packed one after another, each shorter than q_len: rows behind q_lens lie over the next sequence's."""
+    H, G, D, BT, N = 2, 4, 64, 64, 400
+    c = base.filled_cache(24, H, BT, D, E4M3, 330)
+    table = straight(c, 3)
+    n = L // 2 + 1
+    packed = torch.randn(2 * n + L, H * G, D, generator=gen(331), device=DEV).to(BF16)
+    result = torch.zeros_like(packed)
+    q, out = (t.as_strided((3, H * G, L, D), (n * H * G * D, D, H * G * D, 1)) for t in (packed, result))
+    want = torch.cat([call(c, q[b:b + 1, :, :n].contiguous(), [N], table[b:b + 1], max_seq=512)[0].transpose(0, 1) for b in range(3)])
+    call(c, q, [N] * 3, table, max_seq=512, q_lens=[n] * 3, out=out)
+    assert ((result[:3 * n].double() - want.double()).abs() <= want.double().abs() * 2.0 ** -7 + 2.0 ** -9).all()   # (another choice of kernel: two roundings, and the weights')
+    assert (result[3 * n:] == 0).all()

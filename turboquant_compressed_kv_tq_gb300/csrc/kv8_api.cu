@@ -230,7 +230,8 @@ tq_status tq_kv8_attention(const tq_kv8_cache* cache, int layer, const tq_rows* 
     if ((st = make_rope(sc.rope, cache->head_dim, sc.positions, &a.rope)) != TQ_OK) return st;
     if (batch == 0 || q_len == 0) return TQ_OK;
     if ((st = check_rows(q, 2)) != TQ_OK || (st = check_rows(out, 2)) != TQ_OK) return st;
-    if (!seq_lens || out_overlaps(q, out, batch, num_q_heads, q_len, cache->head_dim)) return TQ_ERR_INVALID_ARG;
+    // (with q_lens, rows behind a sequence's queries are neither read nor written: only a row's own heads are known to be)
+    if (!seq_lens || out_overlaps(q, out, q_lens ? 1 : batch, num_q_heads, q_lens ? 1 : q_len, cache->head_dim)) return TQ_ERR_INVALID_ARG;
     int sms = 0;
     if (device_state(&a.err, &sms) != TQ_OK) return TQ_ERR_CUDA;
     const AttendPlan p = attend_plan(cache->head_dim, batch, cache->num_kv_heads, num_q_heads / cache->num_kv_heads, q_len, max_seq_len, sms);
