@@ -478,3 +478,22 @@ def test_rows_behind_the_queries_may_lie_over_others(L):
     call(c, q, [N] * 3, table, max_seq=512, q_lens=[n] * 3, out=out)
     assert ((result[:3 * n].double() - want.double()).abs() <= want.double().abs() * 2.0 ** -7 + 2.0 ** -9).all()   # (another choice of kernel: two roundings, and the weights')
     assert (result[3 * n:] == 0).all()
+
+
+class RawStream:
+    def __init__(self, stream):
+        self.cuda_stream = stream.cuda_stream
+
+
+@pytest.mark.parametrize("kind", ["torch", "object", "number", "default"])
+def test_streams_of_every_kind(kind):
+    c = base.filled_cache(64, 2, 64, 128, E4M3, 340)
+    q = torch.randn(1, 8, 3, 128, generator=gen(341), device=DEV).to(BF16)
+    n = i32([4000])
+    want = c.attention(0, q, n, straight(c), 64, 4096)
+    torch.cuda.synchronize()
+    s = torch.cuda.default_stream() if kind == "default" else torch.cuda.Stream()
+    given = {"torch": s, "object": RawStream(s), "number": s.cuda_stream, "default": 0}[kind]
+    out = c.attention(0, q, n, straight(c), 64, 4096, stream=given)
+    s.synchronize()
+    assert torch.equal(out, want)

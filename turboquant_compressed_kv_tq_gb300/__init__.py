@@ -541,7 +541,9 @@ _pack_scores = struct.Struct("@ffPiPPPP").pack           # tq_kv8_scores
 def _on(stream):
     """Allocations and fills on the stream that a call names (None: the current one)."""
     cuda = _torch().cuda
-    return cuda.stream(cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    if stream is not None and not isinstance(stream, cuda.Stream):
+        stream = cuda.ExternalStream(stream if isinstance(stream, int) else stream.cuda_stream)
+    return cuda.stream(stream)
 
 
 def _rows(t, name, dtype, device, batch, heads, tokens, dim) -> bytes:
