@@ -497,3 +497,41 @@ def test_streams_of_every_kind(kind):
     out = c.attention(0, q, n, straight(c), 64, 4096, stream=given)
     s.synchronize()
     assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------ the chunk kernel in graphs and on several streams
+
+def test_chunks_captured_replayed_and_at_once():
+    """Chunks with and without wide tiles: the same bits from two streams at once, and from a graph with other inputs."""
+    H, G, L, N, BT, D = 2, 4, 300, 600, 32, 128
+    caches = [base.filled_cache(19, H, BT, D, E4M3, 350 + i) for i in range(2)]
+    caches[1].k_scales[0, ::2] -= 30
+    caches[1].v_scales[0, 1::2] -= 30
+    table = straight(caches[0])
+    lens = i32([N])
+    qs = [torch.randn(1, H * G, L, D, generator=gen(352 + i), device=DEV).to(BF16) for i in range(2)]
+    assert kernel_of(caches[0], 1, H * G, L, 600) == "chunk"
+    want = [c.attention(0, q, lens, table, 19, 600) for c, q in zip(caches, qs)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in qs], [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(caches[i].attention(0, qs[i], lens, table, 19, 600))
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w, o) for o in outs)
+    outs = [torch.empty_like(q) for q in qs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for c, q, o in zip(caches, qs, outs):
+            c.attention(0, q, lens, table, 19, 600, out=o)
+    for n in (600, 431):
+        lens.fill_(n)
+        for q in qs:
+            q.copy_(torch.randn(q.shape, generator=gen(360 + n), device=DEV).to(BF16))
+        graph.replay()
+        torch.cuda.synchronize()
+        for c, q, o in zip(caches, qs, outs):
+            assert torch.equal(o, c.attention(0, q, lens, table, 19, 600))
+            check(c, q, o, [n], [L], table, "chunk")
