@@ -800,7 +800,8 @@ tq_status tq_kv8_workspace_bytes(const tq_kv8_cache *cache, int batch, int num_q
  * Operands are fp16: cached codes are exact in it, whatever their scales; queries
  * are scaled by a power of two per row, and rounded where they were rotated (fp16
  * queries in two parts, for few rows and at head_dim 64); softmax weights, times
- * their value scale, are rounded (below 2^-14 of the row's largest to 2^-25 of it).
+ * their value scale, are rounded (below 2^-14 of the row's largest to 2^-25 of it; of
+ * many rows at once 2^-8 and 2^-19, where 128 neighbouring tokens' scales differ).
  * Sums and softmax statistics are fp32, the output is rounded once. The exponent of a
  * weight is one fp32 number, the score times log2(e) plus the value scale's exponent:
  * scores are rounded by 2^-24 of themselves, and from 2^24 on a row that sees blocks of

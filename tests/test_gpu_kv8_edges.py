@@ -35,15 +35,16 @@ def check(c, q, out, lens, news, table, kernel, scale=0.0, cap=0.0, slopes=None,
     row's largest coordinate for the small ones), the rotation in fp32 (2^-21), fp32 sums ((D + 8) 2^-24), the cap (2^-19
     of the capped score), the bias (3 roundings of slope x distance), score plus scale exponent less reference in fp32
     (2^-22 of the largest). An error d of every score moves the output by at most (e^2d - 1) sum w |v|.
-    weights: fp16 (2^-11); below 2^-14 of the reference an absolute 2^-25 of it (the reference is at most the row's
-    largest weight x value scale), or all of a smaller one; fp32 sums in steps of 16 keys (2^-22 each).
+    weights: fp16 (2^-11) of weight x value scale, for which the chunk kernel takes the tile's largest up to 2^6 apart;
+    below 2^-14 of the reference an absolute 2^-25 of it (the reference is at most the row's largest such product), or all
+    of a smaller one; fp32 sums in steps of 16 keys (2^-22 each).
     output: half a step."""
     fmt, BT, D, H = c.format, c.block_tokens, c.head_dim, c.num_kv_heads
     Hq = q.shape[1]
     G = Hq // H
     two = rope is None or (q.dtype == F16 and (kernel == "few" or D == 64))
     tile = 16 if kernel == "few" else 64 if D == 256 else 128
-    limit = 15 if fmt == E4M3 else 24   # how far a tile's codes are brought to one scale
+    limit = 0 if kernel == "few" else 6
     sc = scale or 1 / math.sqrt(D)
     worst = 0.0
     for b, (N, nq) in enumerate(zip(lens, news)):
@@ -80,15 +81,13 @@ def check(c, q, out, lens, news, table, kernel, scale=0.0, cap=0.0, slopes=None,
         empty = ~see.any(1)
         w = torch.softmax(s.masked_fill(~see, -math.inf).masked_fill(empty[:, None], 0.0), -1).masked_fill(empty[:, None], 0.0)
         want, wv = w @ v_, w @ v_.abs()
-        small = torch.zeros_like(want)
         T = -(-N // tile) * tile
         top = torch.full((Hq, T), -1000.0, device=DEV, dtype=torch.float64)
         top[:, :N] = torch.where(seen, ev_, -1000.0)
         top = top.view(Hq, -1, tile).amax(-1).repeat_interleave(tile, 1)[:, :N]
-        for r in (ev_, torch.minimum(top, ev_ + limit)):
-            r = torch.where(seen, r, 0.0)
-            weight = w * torch.exp2(r)[:, None]
-            small = torch.maximum(small, torch.minimum(weight, 2.0 ** -25 * weight.amax(-1, keepdim=True)) @ (v_.abs() * torch.exp2(-r)[..., None]))
+        ev0 = torch.where(seen, ev_, 0.0)
+        most = (w * torch.exp2(torch.where(seen, torch.minimum(top, ev_ + limit), 0.0))[:, None]).amax(-1, keepdim=True)
+        small = torch.minimum(w * torch.exp2(ev0)[:, None], 2.0 ** -25 * most) @ (v_.abs() * torch.exp2(-ev0)[..., None])
         tol = want.abs() * (torch.finfo(q.dtype).eps / 2) + wv * (2.0 ** -11 + torch.expm1(2 * d) * 1.01 + (N / 16 + 16) * 2.0 ** -22) + small
         tol = tol + (2.0 ** -25 if q.dtype == F16 else 2.0 ** -134)
         got = out[b, :, :nq].double()
@@ -229,6 +228,26 @@ def test_masked_neighbours_of_other_scales(D, BT, cap, fmt):
     check(c, q, out, [N], [N], table, "chunk", cap=cap, docs=docs)
     small = out[0].double().abs().amax((0, 2)).view(-1, BT).amax(1)   # of each block's rows
     assert (small > torch.exp2(ev.double().amax(1) - 4)).all()        # nothing vanished
+
+
+@pytest.mark.parametrize("fmt", [E4M3, INT8])
+@pytest.mark.parametrize("apart", [3, 6, 7, 14, 23])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_masked_values_next_to_seen_ones(D, apart, fmt):
+    """Most rows see the first block and their own; the first one's neighbours, of larger values, are masked. Their scale may not
+    cost the rows' own values, 2^-9 below the first block's, their digits."""
+    H, G, N, L, BT = 2, 4, 600, 300, 16
+    c = base.filled_cache(38, H, BT, D, fmt, 248)
+    c.v_scales[0] = 127 - 15
+    c.v_scales[0, 0] = 127 - 6
+    c.v_scales[0, 1:8] = 127 - 6 + apart
+    c.v_codes[0, 0, ..., ::2] = 0   # half the coordinates are the rows' own alone
+    q = (torch.randn(1, H * G, L, D, generator=gen(249), device=DEV) * 0.1).to(BF16)
+    assert kernel_of(c, 1, H * G, L, N) == "chunk"
+    p = torch.arange(N - L, N, dtype=torch.int32, device=DEV)
+    docs = torch.where(p % 20 == 0, 0, p - 15).to(torch.int32).view(1, L)   # a few rows see everything: nothing is skipped
+    out = call(c, q, [N], straight(c), doc_starts=docs, prefix_lens=i32([16]))
+    check(c, q, out, [N], [L], straight(c), "chunk", docs=docs, prefixes=[16])
 
 
 @pytest.mark.parametrize("fmt", [E4M3, INT8])

@@ -21,8 +21,8 @@
 // tile's largest scale in fp16; that one scale is a factor of the row's scores, and
 // for values moves the softmax's reference: u = log2(e) score + log2(scale),
 // p = 2^(u - M), l += p / scale. Where the tile's scales lie too far apart for that
-// to be exact (2^15 for e4m3, 2^24 for integers: blocks of zeros, other documents),
-// the codes stay as they are and the softmax warps take each group of 8 tokens at
+// (keys: 2^15 for e4m3, 2^24 for integers, to be exact; values: 2^6; blocks of zeros,
+// other documents), the codes stay as they are and the softmax warps take each group of 8 tokens at
 // its own scales: the keys' a factor of its scores, the values' a part of its u, and
 // l from u without it (2^63 a key of zeros, next to values whose M is 2^63).
 //
@@ -586,7 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         // two steps, each a batch before what needs it: the block table's entry, then the scales
         constexpr int kPer = 32 / S::kGroups;
         constexpr int kDeep = -24;               // value exponents below it: p may be too small for fp32 where its share of l is not
-        constexpr int kExact = I8 ? 24 : 15;     // 2^-kExact of the smallest code (1; 2^-9) is fp16's smallest
+        constexpr int kExact = I8 ? 24 : 15;     // keys: 2^-kExact of the smallest code (1; 2^-9) is fp16's smallest
+        // values: a token's weight goes by the tile's largest scale, which may be that of a block its row does not see, and
+        // takes as much from the fp16 range that other tiles' weights have below it: 2^6 of 2^14
+        constexpr int kClose = 6;
         const int my_tile = lane / S::kGroups, my_group = lane % S::kGroups;
         struct Found {
             int id, kx, vx;
@@ -688,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int kx = now.kx - 127, vx = now.vx - 127;
                 const int kref = __reduce_max_sync(0xffffffffu, there ? kx : -64), vref = __reduce_max_sync(0xffffffffu, there ? vx : -64);
                 const int k_below = there ? kref - kx : 0, v_below = there ? vref - vx : 0;
-                const bool k_wide = __any_sync(0xffffffffu, k_below > kExact), v_wide = __any_sync(0xffffffffu, v_below > kExact || (there && vx < kDeep));
+                const bool k_wide = __any_sync(0xffffffffu, k_below > kExact), v_wide = __any_sync(0xffffffffu, v_below > kClose || (there && vx < kDeep));
                 // groups of no block among those that have tokens
                 const unsigned gone = __ballot_sync(0xffffffffu, mine && now.id < 0 && t0 + 8 * my_group < N) >> from;
                 copies_wait<0>();
