@@ -85,7 +85,7 @@ typedef enum {
 #define TQ_DEVERR_BLOCK 2u      /* block id outside [0, num_blocks)              */
 #define TQ_DEVERR_SEQLEN 4u     /* decode seq_len outside [q_len, capacity]      */
 #define TQ_DEVERR_TIMEOUT 8u    /* a bounded wait for a bulk copy ran out         */
-#define TQ_DEVERR_NONFINITE 16u /* tq_kv8_append met a NaN or an infinity          */
+#define TQ_DEVERR_NONFINITE 16u /* tq_kv8_append met a NaN or an infinity; tq_verify_drafts too, or a row without a token */
 
 /* ------------------------------------------------------------------ */
 /* Codecs                                                               */
@@ -814,6 +814,142 @@ tq_status tq_kv8_attention(const tq_kv8_cache *cache, int layer, const tq_rows *
                            int num_q_heads, int q_len, const int32_t *seq_lens, const int32_t *q_lens,
                            const int32_t *block_table, int max_blocks, int max_seq_len, const tq_kv8_scores *scores,
                            const tq_rows *out, void *workspace, size_t workspace_bytes, tq_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Around the caches' calls: blocks, positions, drafted tokens          */
+/* ------------------------------------------------------------------ */
+
+/*
+ * Block tables from request lengths (the pages have no counterpart: there a batch is
+ * one padded array). A table is rows of block ids, -1 = no block, as the appends and
+ * attention calls take them; the blocks that no row holds are free_blocks[n_used],
+ * .., free_blocks[n_free - 1], the free list that tq_batch_extend, tq_batch_merge and
+ * tq_batch_extract also take blocks from. Everything stands on the device, so that a
+ * step needs no word from the host: calls on one table go in one stream, or are
+ * ordered by events.
+ */
+typedef struct {
+    int32_t *table;        /* device [rows][max_blocks]                              */
+    int32_t *free_blocks;  /* device [n_free]                                        */
+    int32_t *n_used;       /* device int32, in [0, n_free]                           */
+    int n_free, max_blocks;
+    int block_tokens;      /* power of two, at least 16                              */
+    int num_blocks;        /* of the caches that the table addresses                 */
+} tq_blocks;
+
+/* Where the tokens of a call lie, packed one sequence behind the other. Each may be NULL, starts where no map is asked for. */
+typedef struct {
+    int32_t *granted;      /* device [batch]: tokens that have a place               */
+    int32_t *starts;       /* device [batch + 1]: a sequence's first packed token; the last: all of them */
+    int32_t *seq_ids;      /* device [max_tokens]: the token's row, -1 behind the last token */
+    int32_t *positions;    /* device [max_tokens]: its position in the sequence, 0 behind */
+    int64_t *slots;        /* device [max_tokens]: block id * block_tokens + place in the block, -1 behind */
+    int max_tokens;
+} tq_places;
+
+/*
+ * A place for each of new_lens[b] tokens (NULL: n_new each) behind the seq_lens[b] that row
+ * b < batch holds: every block of the places that the row has none for (a negative
+ * entry) comes off the free list, row by row, in the order of their places. Entries
+ * that are there stay: the same call again takes nothing. seq_lens is not modified
+ * (an append takes the lengths before it).
+ *   places  NULL, or where the maps go. granted[b] is below new_lens[b] where the row is
+ *           full or the free list is empty: the tokens before the first place without
+ *           a block (TQ_DEVERR_CAPACITY). Tokens behind the first max_tokens packed ones
+ *           stand in no map (TQ_DEVERR_CAPACITY, if there is a map).
+ * Only the entries of the new tokens' places are read or written. An id outside the pool, in
+ * the table or from the free list, stays in its entry, sets TQ_DEVERR_BLOCK, and its
+ * tokens' slots are -1. A length outside [0, max_blocks * block_tokens] counts as no
+ * new tokens, new_lens outside [0, n_new] as the nearest (TQ_DEVERR_SEQLEN); an n_used outside [0,
+ * n_free] as an empty list (TQ_DEVERR_CAPACITY).
+ * Errors: TQ_ERR_INVALID_ARG (pointers, sizes; max_blocks * block_tokens or batch times the
+ * most that a row can be given above 2^31 - 1), TQ_ERR_UNSUPPORTED (block_tokens).
+ */
+tq_status tq_blocks_reserve(const tq_blocks *blocks, int batch, const int32_t *seq_lens, const int32_t *new_lens, int n_new,
+                            const tq_places *places, tq_stream_t stream);
+
+/*
+ * Row b < batch keeps the blocks of its first keep_lens[b] tokens: the entries behind
+ * them, up to the row's first negative one, become -1, and their blocks go back to the
+ * free list, before the ones that are left there, row by row in the order of their
+ * places. A negative length leaves its row as it is (TQ_DEVERR_SEQLEN). Ids outside the
+ * pool are dropped (TQ_DEVERR_BLOCK), and the first ones where more come back than
+ * were taken (TQ_DEVERR_CAPACITY). Errors as tq_blocks_reserve.
+ */
+tq_status tq_blocks_release(const tq_blocks *blocks, int batch, const int32_t *keep_lens, tq_stream_t stream);
+
+/*
+ * Position rotation of queries and keys on the way to a cache that does not rotate
+ * (tq_encode_append, tq_decode_attention, tq_decode_step, tq_prefill_attention), by the
+ * rope that the 8-bit cache's calls take; the rows are read and written in the layouts that the
+ * caller has and wants (out of a fused projection, into contiguous heads).
+ *   q, q_out   [batch][q_heads][n][head_dim], one dtype; k, k_out likewise (k NULL: only q)
+ *   position of token i of sequence b: positions[b][i] (device int32 [batch][n]), or starts[b] + i
+ *              (device int32 [batch]), or i, where those are NULL
+ *   new_lens   device int32 [batch] in [0, n], or NULL: rows i >= new_lens[b] are
+ *              neither read nor written (others count as the nearest, TQ_DEVERR_SEQLEN)
+ *   transposed 1: by the opposite angle (times the same scale): the gradient with respect to
+ *              the rows that went in; at scale 1 also the way back
+ * Coordinates behind rot_dim pass as they are. An output is its input (in place), or shares no memory with the
+ * inputs or the other output, and its rows share none with each other: TQ_ERR_INVALID_ARG where they do, and
+ * also where two that lie in different layouts are not apart as a whole.
+ * head_dim a multiple of 16, at most 1024. Arithmetic is fp32, the angle exact (see tq_rope); one rounding.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, rot_dim).
+ */
+tq_status tq_rope_apply(const tq_rope *rope, int transposed, tq_dtype dtype, int head_dim, int batch, int n,
+                        const tq_rows *q, int q_heads, const tq_rows *q_out, const tq_rows *k, int k_heads,
+                        const tq_rows *k_out, const int32_t *starts, const int32_t *new_lens, const int32_t *positions,
+                        tq_stream_t stream);
+
+/*
+ * Verification of drafted tokens. A step that ran num_drafts guessed tokens of each
+ * sequence through the model, behind the token that it had ("lightning-mlx/plan.md": a speculative
+ * step verifies several tokens at one read of the cache), has num_drafts + 1 rows of
+ * logits: row i is for the place of draft i, the last for the token behind them.
+ *   p_i = softmax(logits_i / temperature), or the row itself with target_probs
+ *   draft i is kept if all before it are and u_i q_i(d_i) < p_i(d_i);
+ *   with n kept, the next token is the largest of max(p_n - q_n, 0) / noise (of p_n / noise where
+ *   that is 0 everywhere, and behind the last draft), the lowest of equals. With independent
+ *   uniform u in [0, 1) and exponential noise (mean 1), and drafts drawn from q, the tokens are distributed as
+ *   tokens drawn from p one by one.
+ * A temperature of 0 (or below, or NaN) is greedy: p is 1 at the row's largest value, the lowest of equals. Others count
+ * as the nearest in [2^-120, 2^100].
+ *   target      device, row i of sequence b at target + b * target_stride_batch + i * target_stride_row
+ *               (elements), vocab contiguous values of target_dtype
+ *   draft_tokens device int32 [batch][num_drafts]; an id outside [0, vocab) is never kept
+ *   draft       device, the probabilities q that the drafts were drawn from, as target, or NULL: the drafts were
+ *               not drawn (q is 1 at the draft, 0 elsewhere)
+ *   draft_lens  device int32 [batch] in [0, num_drafts], or NULL: num_drafts each (others: the nearest, TQ_DEVERR_SEQLEN)
+ *   temperatures device float [batch], or NULL: 1 each (with target_probs a positive one says nothing)
+ *   uniforms    device float [batch][num_drafts]
+ *   noise       device float, [vocab] at noise + b * noise_stride; values below 2^-100 and NaN count as that.
+ *               NULL: all sequences are greedy, and neither temperatures nor uniforms (which may then be NULL) are looked at
+ *   seq_lens    device int32 [batch] or NULL: tokens cached before the step, for keep_lens
+ *   accepted    device int32 [batch]: n
+ *   tokens      device int32 [batch][num_drafts + 1]: the kept drafts, the next token, then -1
+ *   logprobs    device float [batch][num_drafts + 1] or NULL: ln of each one's softmax(logits / temperature) (greedy: at
+ *               temperature 1; with target_probs: ln p), 0 behind
+ *   keep_lens   device int32 [batch] or NULL: seq_lens[b] + n + 1, the tokens whose keys and values stand
+ * num_drafts = 0 draws one token for each sequence. -inf is a token that cannot be; +inf, the largest number; NaN counts as -inf.
+ * A row that is looked at and holds +inf or a NaN sets TQ_DEVERR_NONFINITE, and so does one in which nothing
+ * can be: its token is -1 (logprob 0). Sums are fp32 over weights to 2^-21, what one token hangs on 64 bits; probabilities below 2^-126
+ * count as 0. The same call gives the same bits every time. No workspace.
+ * Errors: TQ_ERR_INVALID_ARG (pointers, sizes, dtypes), TQ_ERR_UNSUPPORTED (num_drafts above 64).
+ */
+typedef struct {
+    const void *target;
+    int64_t target_stride_batch, target_stride_row;
+    const void *draft;
+    int64_t draft_stride_batch, draft_stride_row;
+    const int32_t *draft_tokens, *draft_lens;
+    const float *temperatures, *uniforms, *noise;
+    int64_t noise_stride;
+    const int32_t *seq_lens;
+    int target_dtype, draft_dtype, target_probs;
+} tq_drafts;
+
+tq_status tq_verify_drafts(const tq_drafts *drafts, int batch, int num_drafts, int vocab, int32_t *accepted, int32_t *tokens,
+                           float *logprobs, int32_t *keep_lens, tq_stream_t stream);
 
 /* ------------------------------------------------------------------ */
 /* Diagnostics                                                          */

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import numpy as np
 
@@ -17,7 +17,7 @@ from . import _lib
 from ._lib import (TQ_BF16, TQ_DEVERR_BLOCK, TQ_DEVERR_CAPACITY, TQ_DEVERR_NONFINITE, TQ_DEVERR_SEQLEN, TQ_ENCODE_AUTO,
                    TQ_ENCODE_EXACT, TQ_F16, TQ_F32, TQ_KV8_E4M3, TQ_KV8_INT8, TQ_MODE_GROUP, TQ_MODE_MSE, TQ_MODE_PROD,
                    TQ_OK, TQError, check, lib, library_path, status_string, tq_batch, tq_cache_desc, tq_codec_info_t,
-                   tq_kv8_cache, tq_kv8_scores, tq_rope, tq_rows, tq_split_state)
+                   tq_blocks, tq_kv8_cache, tq_kv8_scores, tq_places, tq_rope, tq_rows, tq_split_state)
 
 __all__ = [
     "tq_codec_create", "tq_codec_create_group", "tq_codec_destroy", "tq_codec_info",
@@ -30,6 +30,7 @@ __all__ = [
     "tq_encode_append_split", "tq_decode_workspace_bytes_split", "tq_decode_attention_split", "SplitCache",
     "tq_batch_filter", "tq_batch_extend", "tq_batch_merge", "tq_batch_extract", "Batch",
     "tq_kv8_append", "tq_kv8_attention", "tq_kv8_workspace_bytes", "KV8Cache", "Rope",
+    "tq_rope_apply", "tq_blocks_reserve", "tq_blocks_release", "tq_verify_drafts", "BlockTable", "Places", "Verified",
     "tq_device_error", "tq_selftest_wait_timeout",
     "tq_launch_count", "tq_abi_version", "Codec", "CompressedKVCache", "TQError",
     "TQ_MODE_MSE", "TQ_MODE_PROD", "TQ_MODE_GROUP", "TQ_F32", "TQ_BF16", "TQ_F16",
@@ -507,7 +508,7 @@ class CompressedKVCache:
 # ----------------------------------------------------------------- 8-bit cache
 
 class _KV8:
-    """What the two calls below need of torch and the library, looked up once (they are short: every lookup counts)."""
+    """What the calls below need of torch and the library, looked up once (they are short: every lookup counts)."""
 
     def __init__(self):
         torch = _torch()
@@ -516,6 +517,8 @@ class _KV8:
         self.device = torch._C._cuda_getDevice                # of torch.cuda.current_device
         self.stream = torch._C._cuda_getCurrentRawStream      # of torch.cuda.current_stream(device).cuda_stream
         self.append, self.attention = lib().tq_kv8_append, lib().tq_kv8_attention
+        self.rope, self.verify = lib().tq_rope_apply, lib().tq_verify_drafts
+        self.reserve, self.release = lib().tq_blocks_reserve, lib().tq_blocks_release
 
 
 _kv8_found = None
@@ -591,8 +594,45 @@ class Rope:
     def of_base(cls, rot_dim: int, base: float = 10000.0, device="cuda", interleaved: bool = False, scale: float = 1.0):
         """inv_freq[i] = base ** (-2 i / rot_dim)."""
         torch = _torch()
+        return cls(cls._frequencies(rot_dim, base, device), interleaved, scale)
+
+    # Forms for contexts longer than the trained one, as frequencies of their own.
+
+    @classmethod
+    def linear(cls, rot_dim: int, factor: float, base: float = 10000.0, device="cuda", interleaved: bool = False,
+               scale: float = 1.0):
+        """Positions divided by `factor`."""
+        return cls(cls._frequencies(rot_dim, base, device) / factor, interleaved, scale)
+
+    @classmethod
+    def ntk(cls, rot_dim: int, factor: float, base: float = 10000.0, device="cuda", interleaved: bool = False,
+            scale: float = 1.0):
+        """The base times factor ** (rot_dim / (rot_dim - 2)): the slowest pair turns `factor` times slower, the fastest as before."""
+        if rot_dim <= 2:
+            raise ValueError("rot_dim must be above 2")
+        return cls(cls._frequencies(rot_dim, base * factor ** (rot_dim / (rot_dim - 2)), device), interleaved, scale)
+
+    @classmethod
+    def by_parts(cls, rot_dim: int, factor: float, original: int, low: float = 1.0, high: float = 32.0,
+                 base: float = 10000.0, device="cuda", interleaved: bool = False, scale: float = 1.0):
+        """Pairs that turn fewer than `low` times over the `original` trained positions turn `factor` times slower, those
+        above `high` turns as before, those between by a ramp in their turns. `scale`: with these defaults usually
+        1 + 0.1 ln(factor)."""
+        if not low < high:
+            raise ValueError("low must be below high")
+        f = cls._frequencies(rot_dim, base, device)
+        ramp = ((original / (2 * np.pi) * f - low) / (high - low)).clamp(0, 1)
+        return cls(f * ((1 - ramp) / factor + ramp), interleaved, scale)
+
+    @staticmethod
+    def _frequencies(rot_dim, base, device):
+        torch = _torch()
         i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
-        return cls(base ** (-i / rot_dim), interleaved, scale)
+        return base ** (-i / rot_dim)
+
+    def apply(self, q, k=None, out=None, k_out=None, starts=None, positions=None, new_lens=None, transposed=False,
+              stream=None):
+        return tq_rope_apply(self, q, k, out, k_out, starts, positions, new_lens, transposed, stream)
 
 
 def tq_kv8_append(cache: "KV8Cache", layer, k, v, seq_lens, block_table=None, max_blocks=0, new_lens=None, rope=None,
@@ -737,3 +777,226 @@ class KV8Cache:
                   rope=None, positions=None, stream=None):
         return tq_kv8_attention(self, layer, q, seq_lens, block_table, max_blocks, max_seq_len, out, workspace, q_lens,
                                 scale, softcap, slopes, window, prefix_lens, doc_starts, rope, positions, stream)
+
+
+# ----------------------------------------------------------------- around the caches' calls
+
+_pack_drafts = struct.Struct("@PqqPqqPPPPPqPiii4x").pack   # tq_drafts
+
+
+def tq_rope_apply(rope: Rope, q, k=None, out=None, k_out=None, starts=None, positions=None, new_lens=None,
+                  transposed=False, stream=None):
+    """q, k [batch, heads, n, head_dim] (views in any order of the first three axes) turned by `rope`: (out, k_out).
+
+    Token i of sequence b is at positions[b, i], or starts[b] + i, or i. An output may be its input; one that is not given
+    is made on `stream`, contiguous, rows behind new_lens zero. `transposed`: by the opposite angle (the gradient).
+    """
+    t, device = _kv8(), rope.device
+    if t.device() != device:
+        with _torch().cuda.device(device):
+            return tq_rope_apply(rope, q, k, out, k_out, starts, positions, new_lens, transposed, stream)
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, heads, tokens, head_dim]")
+    batch, heads, n, dim = q.shape
+    dtype, i32 = q.dtype, t.i32
+    code = t.codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    qr = _rows(q, "q", dtype, device, batch, heads, n, dim)
+    kr = ko = None
+    k_heads = 0
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("k must be [batch, heads, tokens, head_dim]")
+        k_heads = k.shape[1]
+        kr = _rows(k, "k", dtype, device, batch, k_heads, n, dim)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if out is None or (k is not None and k_out is None):
+        make = _torch().empty if new_lens is None else _torch().zeros
+        with _on(stream):
+            if out is None:
+                out = make(q.shape, dtype=dtype, device=q.device)
+            if k is not None and k_out is None:
+                k_out = make(k.shape, dtype=dtype, device=q.device)
+    if k is not None:
+        ko = _rows(k_out, "k_out", dtype, device, batch, k_heads, n, dim)
+    per = (batch,)
+    status = t.rope(
+        rope.address, int(transposed), code, dim, batch, n, qr, heads, _rows(out, "out", dtype, device, batch, heads, n, dim),
+        kr, k_heads, ko, _array(starts, "starts", i32, device, per), _array(new_lens, "new_lens", i32, device, per),
+        _array(positions, "positions", i32, device, (batch, n)), _raw_stream(t, stream, device))
+    if status:
+        check(status, "tq_rope_apply")
+    return out, k_out
+
+
+class Places:
+    """Where the tokens of a reservation lie: per sequence granted [batch] and starts [batch + 1], per packed token
+    seq_ids, positions and slots [max_tokens] (max_tokens = 0: no maps)."""
+
+    def __init__(self, batch: int, max_tokens: int = 0, device="cuda"):
+        torch = _torch()
+        self.granted = torch.zeros(batch, dtype=torch.int32, device=device)
+        self.starts = torch.zeros(batch + 1, dtype=torch.int32, device=device)
+        self.seq_ids = torch.full((max_tokens,), -1, dtype=torch.int32, device=device)
+        self.positions = torch.zeros(max_tokens, dtype=torch.int32, device=device)
+        self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=device)
+        self.batch, self.max_tokens, self.index = batch, max_tokens, self.granted.get_device()
+        maps = (self.seq_ids.data_ptr(), self.positions.data_ptr(), self.slots.data_ptr()) if max_tokens else (None,) * 3
+        self.desc = tq_places(self.granted.data_ptr(), self.starts.data_ptr(), *maps, max_tokens)
+        self.address = ctypes.addressof(self.desc)
+
+
+class BlockTable:
+    """Rows of block ids (-1 = no block) and the free list of the blocks that no row holds, on the device.
+
+    `table` [rows, max_blocks] goes into the caches' calls; `free_blocks` and `n_used` into tq_batch_extend, tq_batch_merge
+    and tq_batch_extract, which take from the same list.
+    """
+
+    def __init__(self, rows: int, max_blocks: int, num_blocks: int, block_tokens: int, device="cuda"):
+        torch = _torch()
+        self._set(torch.full((rows, max_blocks), -1, dtype=torch.int32, device=device),
+                  torch.arange(num_blocks, dtype=torch.int32, device=device), torch.zeros(1, dtype=torch.int32, device=device),
+                  block_tokens, num_blocks)
+
+    @classmethod
+    def wrap(cls, table, free_blocks, n_used, block_tokens: int, num_blocks: int) -> "BlockTable":
+        """A table and a free list of the caller's (int32): free_blocks[n_used[0]:] are free."""
+        self = cls.__new__(cls)
+        self._set(table, free_blocks, n_used, block_tokens, num_blocks)
+        return self
+
+    def _set(self, table, free_blocks, n_used, block_tokens, num_blocks):
+        i32 = _torch().int32
+        if table.dim() != 2 or free_blocks.dim() != 1 or n_used.shape != (1,):
+            raise ValueError("table must be [rows, max_blocks], free_blocks one-dimensional, n_used of one element")
+        for t in (table, free_blocks, n_used):
+            if t.dtype != i32 or not t.is_contiguous() or t.device != table.device or not t.is_cuda:
+                raise ValueError("table, free_blocks and n_used must be contiguous int32 tensors on one CUDA device")
+        self.table, self.free_blocks, self.n_used = table, free_blocks, n_used
+        self.rows, self.max_blocks = table.shape
+        self.block_tokens, self.num_blocks = block_tokens, num_blocks
+        self.device, self.index = table.device, table.get_device()
+        self.desc = tq_blocks(table.data_ptr(), free_blocks.data_ptr(), n_used.data_ptr(), free_blocks.numel(),
+                              self.max_blocks, block_tokens, num_blocks)
+        self.address = ctypes.addressof(self.desc)
+
+    def batch(self, cache: "CompressedKVCache", lens, batch: int) -> Batch:
+        """The first `batch` rows, with lengths `lens` [rows], as the batch calls take them."""
+        return Batch(cache, self.rows, self.max_blocks, table=self.table, lens=lens, batch=batch)
+
+    def reserve(self, seq_lens, new_lens=None, n_new: int = 1, places: Optional[Places] = None, stream=None):
+        tq_blocks_reserve(self, seq_lens, new_lens, n_new, places, stream)
+
+    def release(self, keep_lens, stream=None):
+        tq_blocks_release(self, keep_lens, stream)
+
+
+def _rows_in_use(blocks: BlockTable, lens, name):
+    if lens.dim() != 1 or lens.shape[0] > blocks.rows:
+        raise ValueError(f"{name} must be one-dimensional, of at most {blocks.rows} rows")
+    return lens.shape[0]
+
+
+def tq_blocks_reserve(blocks: BlockTable, seq_lens, new_lens=None, n_new: int = 1, places: Optional[Places] = None,
+                      stream=None) -> None:
+    """Blocks for new_lens[b] <= n_new tokens (None: n_new each) behind seq_lens[b], and where the tokens lie (see include/tq.h)."""
+    t, device = _kv8(), blocks.index
+    if t.device() != device:
+        with _torch().cuda.device(device):
+            return tq_blocks_reserve(blocks, seq_lens, new_lens, n_new, places, stream)
+    batch = _rows_in_use(blocks, seq_lens, "seq_lens")
+    if places is not None and (places.batch != batch or places.index != device):
+        raise ValueError(f"places must be of {batch} sequences on cuda:{device}")
+    per = (batch,)
+    status = t.reserve(blocks.address, batch, _array(seq_lens, "seq_lens", t.i32, device, per),
+                       _array(new_lens, "new_lens", t.i32, device, per), n_new,
+                       places.address if places is not None else None, _raw_stream(t, stream, device))
+    if status:
+        check(status, "tq_blocks_reserve")
+
+
+def tq_blocks_release(blocks: BlockTable, keep_lens, stream=None) -> None:
+    """Blocks behind the first keep_lens[b] tokens of each row back to the free list."""
+    t, device = _kv8(), blocks.index
+    if t.device() != device:
+        with _torch().cuda.device(device):
+            return tq_blocks_release(blocks, keep_lens, stream)
+    batch = _rows_in_use(blocks, keep_lens, "keep_lens")
+    status = t.release(blocks.address, batch, _array(keep_lens, "keep_lens", t.i32, device, (batch,)), _raw_stream(t, stream, device))
+    if status:
+        check(status, "tq_blocks_release")
+
+
+class Verified(NamedTuple):
+    """accepted [batch], tokens and logprobs [batch, drafts + 1], keep_lens [batch] (None without seq_lens)."""
+    accepted: object
+    tokens: object
+    keep_lens: object
+    logprobs: object
+
+
+def _row_strides(x, name, device, shape):
+    if x.shape != shape or x.get_device() != device or (shape[-1] > 1 and x.stride(-1) != 1):
+        raise ValueError(f"{name} must be {shape} on cuda:{device} with contiguous rows, not {tuple(x.shape)} on {x.device}")
+    return x.stride()[:-1]
+
+
+def tq_verify_drafts(target, draft_tokens=None, draft_probs=None, uniforms=None, noise=None, temperatures=None,
+                     draft_lens=None, seq_lens=None, target_probs=False, out: Optional[Verified] = None, stream=None) -> Verified:
+    """Which of draft_tokens [batch, drafts] stand against target [batch, drafts + 1, vocab] (logits, or probabilities with
+    target_probs), and the token behind them (see include/tq.h). Without draft_tokens: one token of each row target[:, 0].
+
+    draft_probs [batch, drafts, vocab]: what the drafts were drawn from (None: they were not); uniforms [batch, drafts] in
+    [0, 1), noise [batch, vocab] exponential; without noise the tokens are the likeliest. What is returned is made on `stream`.
+    """
+    t = _kv8()
+    if target.dim() != 3 or not target.is_cuda:
+        raise ValueError("target must be [batch, drafts + 1, vocab] on a CUDA device")
+    device = target.get_device()
+    if t.device() != device:
+        with _torch().cuda.device(device):
+            return tq_verify_drafts(target, draft_tokens, draft_probs, uniforms, noise, temperatures, draft_lens, seq_lens,
+                                    target_probs, out, stream)
+    batch, rows, vocab = target.shape
+    drafts = rows - 1
+    if drafts < 0 or (drafts > 0 and draft_tokens is None):
+        raise ValueError("target must have a row behind the last draft, and drafts their tokens")
+    i32, f32 = t.i32, t.f32
+    code = t.codes.get(target.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {target.dtype}")
+    tb, tr = _row_strides(target, "target", device, (batch, rows, vocab))
+    db = dr = nb = draft = dcode = 0
+    if draft_probs is not None and drafts:
+        db, dr = _row_strides(draft_probs, "draft_probs", device, (batch, drafts, vocab))
+        dcode = t.codes.get(draft_probs.dtype)
+        if dcode is None:
+            raise TypeError(f"unsupported dtype {draft_probs.dtype}")
+        draft = draft_probs.data_ptr()
+    if noise is not None:
+        nb, = _row_strides(noise, "noise", device, (batch, vocab))
+        if noise.dtype != f32:
+            raise TypeError(f"noise must be float32, not {noise.dtype}")
+    per, each, full = (batch,), (batch, drafts), (batch, rows)
+    if out is None:
+        torch = _torch()
+        with _on(stream):
+            out = Verified(torch.empty(batch, dtype=i32, device=target.device), torch.empty(full, dtype=i32, device=target.device),
+                           torch.empty(batch, dtype=i32, device=target.device) if seq_lens is not None else None,
+                           torch.empty(full, dtype=f32, device=target.device))
+    elif (seq_lens is None) != (out.keep_lens is None):
+        raise ValueError("keep_lens go with seq_lens")
+    packed = _pack_drafts(
+        target.data_ptr(), tb, tr, draft, db, dr, (_array(draft_tokens, "draft_tokens", i32, device, each) or 0) if drafts else 0,
+        _array(draft_lens, "draft_lens", i32, device, per) or 0, _array(temperatures, "temperatures", f32, device, per) or 0,
+        (_array(uniforms, "uniforms", f32, device, each) or 0) if drafts else 0, noise.data_ptr() if noise is not None else 0, nb,
+        _array(seq_lens, "seq_lens", i32, device, per) or 0, code, dcode, int(target_probs))
+    status = t.verify(packed, batch, drafts, vocab, _array(out.accepted, "accepted", i32, device, per),
+                      _array(out.tokens, "tokens", i32, device, full), _array(out.logprobs, "logprobs", f32, device, full),
+                      _array(out.keep_lens, "keep_lens", i32, device, per), _raw_stream(t, stream, device))
+    if status:
+        check(status, "tq_verify_drafts")
+    return out

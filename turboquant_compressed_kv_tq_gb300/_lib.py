@@ -112,6 +112,26 @@ class tq_kv8_scores(ctypes.Structure):
                 ("rope", ctypes.POINTER(tq_rope)), ("positions", ctypes.c_void_p)]
 
 
+class tq_blocks(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("free_blocks", ctypes.c_void_p), ("n_used", ctypes.c_void_p),
+                ("n_free", ctypes.c_int), ("max_blocks", ctypes.c_int), ("block_tokens", ctypes.c_int),
+                ("num_blocks", ctypes.c_int)]
+
+
+class tq_places(ctypes.Structure):
+    _fields_ = [("granted", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("seq_ids", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("max_tokens", ctypes.c_int)]
+
+
+class tq_drafts(ctypes.Structure):
+    _fields_ = [("target", ctypes.c_void_p), ("target_stride_batch", ctypes.c_int64), ("target_stride_row", ctypes.c_int64),
+                ("draft", ctypes.c_void_p), ("draft_stride_batch", ctypes.c_int64), ("draft_stride_row", ctypes.c_int64),
+                ("draft_tokens", ctypes.c_void_p), ("draft_lens", ctypes.c_void_p), ("temperatures", ctypes.c_void_p),
+                ("uniforms", ctypes.c_void_p), ("noise", ctypes.c_void_p), ("noise_stride", ctypes.c_int64),
+                ("seq_lens", ctypes.c_void_p), ("target_dtype", ctypes.c_int), ("draft_dtype", ctypes.c_int),
+                ("target_probs", ctypes.c_int)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
@@ -168,6 +188,11 @@ SIGNATURES = {
     "tq_kv8_append": (_ST, [_P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P]),
     "tq_kv8_workspace_bytes": (_ST, [_P, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "tq_kv8_attention": (_ST, [_P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]),
+    # (and so do those of these four)
+    "tq_blocks_reserve": (_ST, [_P, _I, _P, _P, _I, _P, _P]),
+    "tq_blocks_release": (_ST, [_P, _I, _P, _P]),
+    "tq_rope_apply": (_ST, [_P, _I, _I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _P, _P, _P, _P]),
+    "tq_verify_drafts": (_ST, [_P, _I, _I, _I, _P, _P, _P, _P, _P]),
     "tq_device_error": (_ST, [ctypes.POINTER(ctypes.c_uint32)]),
     "tq_selftest_wait_timeout": (_ST, [ctypes.c_double, _P]),
 }

@@ -4,17 +4,15 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
-#include <utility>
 
 #include "kv8.h"
+#include "rows.h"
 
 namespace tq {
 namespace kv8 {
 namespace {
 
 constexpr int kMaxTokens = 1 << 30;   // positions, with room for sums in 32 bits
-
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 tq_status check_cache(const tq_kv8_cache* c) {
     if (!c) return TQ_ERR_INVALID_ARG;
@@ -44,42 +42,11 @@ tq_status check_table(const tq_kv8_cache* c, int batch, const int32_t* table, in
     return TQ_OK;
 }
 
-tq_status check_rows(const tq_rows* r, int elem) {
-    if (!r || !r->data || !aligned(r->data, 16)) return TQ_ERR_INVALID_ARG;
-    if (r->stride_batch * elem % 16 != 0 || r->stride_head * elem % 16 != 0 || r->stride_token * elem % 16 != 0)
-        return TQ_ERR_INVALID_ARG;
-    return TQ_OK;
-}
-
-// The axes of rows of heads, in elements, the largest stride first; an axis of one element has none.
-struct Axes {
-    int64_t stride[3], n[3];
-    Axes(const tq_rows* r, int64_t nb, int64_t nh, int64_t nt) : stride{r->stride_batch, r->stride_head, r->stride_token}, n{nb, nh, nt} {
-        for (int i = 0; i < 3; ++i) stride[i] = n[i] > 1 ? std::abs(stride[i]) : 0;
-        for (int i = 0; i < 2; ++i)
-            for (int k = 0; k < 2 - i; ++k)
-                if (stride[k] < stride[k + 1]) std::swap(stride[k], stride[k + 1]), std::swap(n[k], n[k + 1]);
-    }
-    // Whether two rows whose starts differ by a sum of steps along axes k.. lie within D elements of being `delta` apart. A
-    // yes has such rows to show; a no is sure where each stride is as long as what the smaller ones span.
-    bool meet(int64_t delta, int k, int D) const {
-        if (k == 3 || stride[k] == 0) return std::abs(delta) < D;
-        const int64_t d = delta / stride[k];
-        for (int64_t i = d - 1; i <= d + 1; ++i)
-            if (std::abs(i) < n[k] && meet(delta - i * stride[k], k + 1, D)) return true;
-        return false;
-    }
-};
-
 // Whether rows of out share memory with each other, or with q's rows where those lie as out's do.
 bool out_overlaps(const tq_rows* q, const tq_rows* out, int64_t nb, int64_t nh, int64_t nt, int D) {
     const Axes o(out, nb, nh, nt);
-    for (int k = 0; k < 3; ++k)
-        if ((o.stride[k] > 0 && o.meet(o.stride[k], k + 1, D)) || (o.stride[k] == 0 && o.n[k] > 1)) return true;
-    if (q->data == out->data) return true;
-    if ((nb > 1 && q->stride_batch != out->stride_batch) || (nh > 1 && q->stride_head != out->stride_head) ||
-        (nt > 1 && q->stride_token != out->stride_token))
-        return false;
+    if (o.meets_itself(D) || q->data == out->data) return true;
+    if (!same_layout(q, out, nb, nh, nt)) return false;
     const int64_t apart = (reinterpret_cast<intptr_t>(out->data) - reinterpret_cast<intptr_t>(q->data)) / 2;
     return o.meet(apart, 0, D);
 }
