@@ -934,7 +934,7 @@ tq_status tq_rope_apply(const tq_rope *rope, int transposed, tq_dtype dtype, int
  * A row that is looked at and holds +inf or a NaN sets TQ_DEVERR_NONFINITE, and so does one in which nothing
  * can be: its token is -1 (logprob 0). Sums are fp32 over weights to 2^-21, what one token hangs on 64 bits; probabilities below 2^-126
  * count as 0. The same call gives the same bits every time. No workspace.
- * Errors: TQ_ERR_INVALID_ARG (pointers, sizes, dtypes), TQ_ERR_UNSUPPORTED (num_drafts above 64).
+ * Errors: TQ_ERR_INVALID_ARG (pointers, sizes, dtypes; batch above 2^24), TQ_ERR_UNSUPPORTED (num_drafts above 64).
  */
 typedef struct {
     const void *target;
