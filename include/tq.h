@@ -922,7 +922,7 @@ tq_status tq_rope_apply(const tq_rope *rope, int transposed, tq_dtype dtype, int
  *   draft_lens  device int32 [batch] in [0, num_drafts], or NULL: num_drafts each (others: the nearest, TQ_DEVERR_SEQLEN)
  *   temperatures device float [batch], or NULL: 1 each (with target_probs a positive one says nothing)
  *   uniforms    device float [batch][num_drafts]
- *   noise       device float, [vocab] at noise + b * noise_stride; values below 2^-100 and NaN count as that.
+ *   noise       device float, [vocab] at noise + b * noise_stride; values count as the nearest in [2^-100, 2^24], NaN as 2^-100.
  *               NULL: all sequences are greedy, and neither temperatures nor uniforms (which may then be NULL) are looked at
  *   seq_lens    device int32 [batch] or NULL: tokens cached before the step, for keep_lens
  *   accepted    device int32 [batch]: n
@@ -932,9 +932,9 @@ tq_status tq_rope_apply(const tq_rope *rope, int transposed, tq_dtype dtype, int
  *   keep_lens   device int32 [batch] or NULL: seq_lens[b] + n + 1, the tokens whose keys and values stand
  * num_drafts = 0 draws one token for each sequence. -inf is a token that cannot be; +inf, the largest number; NaN counts as -inf.
  * A row that is looked at and holds +inf or a NaN sets TQ_DEVERR_NONFINITE, and so does one in which nothing
- * can be: its token is -1 (logprob 0). Sums are fp32 over weights to 2^-21, what one token hangs on 64 bits; probabilities below 2^-126
- * count as 0. The same call gives the same bits every time. No workspace.
- * Errors: TQ_ERR_INVALID_ARG (pointers, sizes, dtypes; batch above 2^24), TQ_ERR_UNSUPPORTED (num_drafts above 64).
+ * can be: its token is -1 (logprob 0). Sums are fp32, over weights to 2^-20; the weights that one token hangs on are good to
+ * 2^-21; probabilities below 2^-100 (of the row's largest) count as 0. The same call gives the same bits every time. No workspace.
+ * Errors: TQ_ERR_INVALID_ARG (pointers, sizes, dtypes; batch above 2^24, vocab above 2^28), TQ_ERR_UNSUPPORTED (num_drafts above 64).
  */
 typedef struct {
     const void *target;

@@ -122,7 +122,7 @@ tq_status tq_rope_apply(const tq_rope* rope, int transposed, tq_dtype dtype, int
 
 tq_status tq_verify_drafts(const tq_drafts* drafts, int batch, int num_drafts, int vocab, int32_t* accepted, int32_t* tokens,
                            float* logprobs, int32_t* keep_lens, tq_stream_t stream) {
-    if (!drafts || batch < 0 || batch > (1 << 24) || num_drafts < 0 || vocab <= 0) return TQ_ERR_INVALID_ARG;
+    if (!drafts || batch < 0 || batch > (1 << 24) || num_drafts < 0 || vocab <= 0 || vocab > (1 << 28)) return TQ_ERR_INVALID_ARG;
     if (num_drafts > 64) return TQ_ERR_UNSUPPORTED;
     auto known = [](int t) { return t == TQ_F32 || t == TQ_BF16 || t == TQ_F16; };
     if (!known(drafts->target_dtype) || (drafts->draft && !known(drafts->draft_dtype))) return TQ_ERR_INVALID_ARG;
