@@ -922,7 +922,7 @@ tq_status tq_rope_apply(const tq_rope *rope, int transposed, tq_dtype dtype, int
  *   draft_lens  device int32 [batch] in [0, num_drafts], or NULL: num_drafts each (others: the nearest, TQ_DEVERR_SEQLEN)
  *   temperatures device float [batch], or NULL: 1 each (with target_probs a positive one says nothing)
  *   uniforms    device float [batch][num_drafts]
- *   noise       device float, [vocab] at noise + b * noise_stride; values count as the nearest in [2^-100, 2^24], NaN as 2^-100.
+ *   noise       device float, [vocab] at noise + b * noise_stride; values below 2^-100, and NaN, count as 2^-100, those above 2^126 as infinite.
  *               NULL: all sequences are greedy, and neither temperatures nor uniforms (which may then be NULL) are looked at
  *   seq_lens    device int32 [batch] or NULL: tokens cached before the step, for keep_lens
  *   accepted    device int32 [batch]: n

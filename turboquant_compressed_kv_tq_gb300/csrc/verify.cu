@@ -5,21 +5,20 @@
 // So every logit is read once, and one row of the drafts' probabilities, of the noise and, out of the L2 cache, of the logits
 // again: memory bounds it where there is much to read, the chain of steps where there is little.
 //
-// A cluster of CTAs has a sequence: each CTA a part of the vocabulary, of all its rows in a run without a barrier between them. The
-// parts' (largest, where, sum) go into every CTA of the cluster, which all find the same number of kept drafts, and take the
-// next token's row, again in parts. One launch, no workspace, nothing that two calls share; no order of arrival changes a result.
-#include <cooperative_groups.h>
+// A cluster of CTAs has a sequence: each CTA a part of the vocabulary, of all its rows in a run. Each warp has a ring of bulk copies of its own
+// (2 KB a piece) and goes through its pieces without waiting for other warps; what it saw of a row goes into every CTA of the cluster as soon
+// as the row is through. All find the same number of kept drafts then, and take the next token's row, again in parts.
+// One launch, no workspace, nothing that two calls share; no order of arrival changes a result.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "kv8_device.cuh"
 #include "serve.h"
 #include "tc_ptx.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace tq {
 namespace serve {
@@ -27,63 +26,40 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;
-constexpr int kUnits = 128, kStages = 3;   // a warp's pieces of a row: units of 16 bytes, and how many are on their way
+constexpr int kUnits = 128, kStages = 2;   // a warp's pieces of a row: units of 16 bytes, and how many are on their way
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLn2 = 0.69314718f;
+constexpr float kUsual = 8192.0f;   // exponents below which one product makes a weight
 
 __device__ __forceinline__ float number(float x) { return x; }
 __device__ __forceinline__ float number(__half x) { return __half2float(x); }
 __device__ __forceinline__ float number(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// The values of 16 bytes.
-__device__ __forceinline__ void numbers(const uint4& u, float* x, float) {
-    x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+// The values of 16 bytes, in pairs.
+__device__ __forceinline__ void numbers(const uint4& u, float2* x, float) {
+    x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
 }
-__device__ __forceinline__ void numbers(const uint4& u, float* x, __nv_bfloat16) {
+__device__ __forceinline__ void numbers(const uint4& u, float2* x, __nv_bfloat16) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ void numbers(const uint4& u, float* x, __half) {
+__device__ __forceinline__ void numbers(const uint4& u, float2* x, __half) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 4; ++i) x[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
 }
 // 8 values at a 16-byte boundary.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+__device__ __forceinline__ void load8(const T* p, float2 (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) numbers(__ldg(reinterpret_cast<const uint4*>(p) + i), x + i * 16 / sizeof(T), T());
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) numbers(__ldg(reinterpret_cast<const uint4*>(p) + i), x + i * 8 / sizeof(T), T());
 }
 
 using kv8::ex2;
 using kv8::rcp;
 
-// Pairs of fp32 numbers in one register pair.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void split(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // A logit as it counts: +inf the largest number, NaN -inf.
 __device__ __forceinline__ float logit(float x) { return x == x ? fminf(x, FLT_MAX) : -INFINITY; }
@@ -91,11 +67,12 @@ __device__ __forceinline__ float logit(float x) { return x == x ? fminf(x, FLT_M
 // log2(e) / T as c + lo, both positive, so that what is masked (-inf) stays -inf in either product: log2(e) = 1.442695 (rounded down)
 // + 1.9259630e-8, the quotient rounded down, and what the division leaves. To 2^-44.
 struct Scale {
-    float c, lo;
+    float c, lo, near;   // near: c + lo in one number, off by 2^-25 of itself
     __device__ __forceinline__ explicit Scale(float T) {
         constexpr float hi = 0x1.715476p+0f, rest = 1.9259630e-8f;
         c = __fdiv_rd(hi, T);
         lo = __fdividef(fmaf(-c, T, hi) + rest, T);
+        near = c + lo;
     }
     __device__ __forceinline__ float weight(float d) const { return ex2(fmaf(d, c, d * lo)); }   // d <= 0
     // The same with the exponent's rounding put back: to 2^-22. NaN of a masked value.
@@ -108,6 +85,40 @@ struct Scale {
         return fmaf(t, kLn2, fmaf(d, lo, fmaf(d, c, -t)) * kLn2 + t * -1.9046543e-9f);   // (ln 2 less kLn2)
     }
 };
+
+// ------------------------------------------------------------------ the cluster
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+// A shared-memory address of this CTA in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(tc::smem_addr(p)), "r"(rank));
+    return r;
+}
+// 16 or 8 bytes into another CTA's shared memory, counted on a barrier there.
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];\n" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, uint32_t a, uint32_t b) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];\n" ::"r"(to), "r"(a), "r"(b), "r"(bar) : "memory");
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar) {   // for the barrier's first phase, and what other CTAs sent with it
+    const uint32_t a = tc::smem_addr(bar);
+    for (unsigned it = 0; it < tc::kSpinLimit; ++it) {
+        uint32_t done;
+        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n selp.u32 %0, 1, 0, p;\n}\n"
+                     : "=r"(done)
+                     : "r"(a)
+                     : "memory");
+        if (done) return true;
+    }
+    return false;
+}
 
 // Values [i0, i1) of a row on their way into the L2 cache (one thread; whole units).
 template <typename T>
@@ -133,219 +144,281 @@ __device__ __forceinline__ Units units(const T* row, int V, int each, int rank) 
 }
 
 // What is known of a row, or a part of it: the largest value, the sum of weights relative to it, and where it is.
-struct Seen {
+struct __align__(16) Seen {
     float top, sum;   // (nothing but masked values: sum 0)
-    int at;
-    template <int N, typename F>
-    __device__ __forceinline__ void take(const float (&x)[N], const Scale& S, bool where, F&& index) {
-        float t = x[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) t = fmaxf(t, x[i]);
+    int at, piece;    // of a lane while it goes through a row: the piece (its first unit) in which the largest stood first, or -1
+
+    __device__ __forceinline__ void rise(float t, const Scale& S, int from_piece) {
         if (t > top) {
             sum *= S.weight(top - t);
             top = t;
             at = INT_MAX;
-        }
-        if (where && t == top) {
-#pragma unroll
-            for (int i = N - 1; i >= 0; --i)
-                if (x[i] == t) at = min(at, index(i));
-        }
-        if constexpr (N == 1) {
-            sum += S.weight(x[0] - top);
-        } else {
-            const uint64_t off = pair(-top, -top), c = pair(S.c, S.c), lo = pair(S.lo, S.lo);
-            uint64_t s = 0;
-#pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                const uint64_t d = add2(pair(x[i], x[i + 1]), off);
-                float a, b;
-                split(fma2(d, c, mul2(d, lo)), a, b);
-                s = add2(s, pair(ex2(a), ex2(b)));
-            }
-            float a, b;
-            split(s, a, b);
-            sum += a + b;
+            piece = from_piece;
         }
     }
-    // With what the lanes o apart know, for all of them.
-    __device__ __forceinline__ void join(const Scale& S, int lanes) {
-        float t = top;
-        for (int o = lanes / 2; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, o));
-        sum *= S.weight(top - t);
-        if (top < t) at = INT_MAX;
-        top = t;
-        for (int o = lanes / 2; o > 0; o >>= 1) {
-            sum += __shfl_xor_sync(kAll, sum, o);
-            at = min(at, __shfl_xor_sync(kAll, at, o));
+    __device__ __forceinline__ void take(float x, const Scale& S, int i) {
+        rise(x, S, -1);
+        if (x == top) at = min(at, i);
+        sum += S.weight(x - top);
+    }
+    // A lane's units of a piece, every 32nd from `from`. Usually the weights are
+    // 2^(x c - m), m = top c rounded, so that each takes one product, and their sum is brought from m to the exact top c (a factor
+    // 1 - delta ln 2, |delta| < 2^-11) once; c's own error, 2^-25 of itself, is common to sum and weights but for what it does to
+    // (x - top) / T. Where m is large (temperatures near 0, rows of the lowest numbers) differences come first.
+    template <typename T>
+    __device__ __forceinline__ void take(const uint4* from, const Scale& S, int from_piece) {
+        constexpr int kIn = 16 / sizeof(T), kPer = kUnits / 32, N = kPer * kIn / 2;
+        float2 x[N];
+#pragma unroll
+        for (int v = 0; v < kPer; ++v) numbers(from[v * 32], x + v * kIn / 2, T());
+        float t = fmaxf(x[0].x, x[0].y);
+#pragma unroll
+        for (int i = 1; i < N; ++i) t = fmaxf(fmaxf(t, x[i].x), x[i].y);
+        rise(t, S, from_piece);
+        const float m = top * S.near;
+        if (fabsf(m) < kUsual) {
+            const float2 c = both(S.near), off = both(-m);
+            float2 s = both(0.0f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float2 e = __ffma2_rn(x[i], c, off);
+                s = __fadd2_rn(s, make_float2(ex2(e.x), ex2(e.y)));
+            }
+            sum = fmaf(s.x + s.y, fmaf(fmaf(top, S.near, -m), -kLn2, 1.0f), sum);
+        } else {   // seldom: one value after the other
+#pragma unroll 1
+            for (int e = 0; e < kPer * kIn; ++e) sum += S.weight(number(reinterpret_cast<const T*>(from + e / kIn * 32)[e % kIn]) - top);
         }
+    }
+    // Where the largest value is, by another look at the piece (`row`: its first whole unit, of `end` units; value 0 of it is value
+    // `head`): only lanes that have the warp's largest look.
+    template <typename T>
+    __device__ __forceinline__ void find(const T* row, int end, int head) {
+        constexpr int kIn = 16 / sizeof(T);
+        float t = top;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, o));
+        if (top == t && piece >= 0) {
+#pragma unroll 1
+            for (int v = kUnits / 32 - 1; v >= 0; --v) {
+                const int u = piece + v * 32 + threadIdx.x % 32;
+                if (u >= end) continue;
+                float2 x[kIn / 2];
+                numbers(__ldg(reinterpret_cast<const uint4*>(row) + u), x, T());
+#pragma unroll
+                for (int i = kIn / 2 - 1; i >= 0; --i) {
+                    if (x[i].y == t) at = min(at, head + u * kIn + 2 * i + 1);
+                    if (x[i].x == t) at = min(at, head + u * kIn + 2 * i);
+                }
+            }
+        }
+    }
+    // With what the warp's other lanes know, for all of them.
+    __device__ __forceinline__ void join(const Scale& S) {
+        float t = top;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, o));
+        sum *= S.weight(top - t);
+        at = static_cast<int>(__reduce_min_sync(kAll, static_cast<unsigned>(top < t ? INT_MAX : at)));
+        top = t;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     }
 };
-__device__ __forceinline__ Seen nothing() { return Seen{-FLT_MAX, 0.0f, INT_MAX}; }
+__device__ __forceinline__ Seen nothing() { return Seen{-FLT_MAX, 0.0f, INT_MAX, -1}; }
 
-struct Best {
+struct __align__(8) Best {
     float v;   // a positive score
     int i;
     __device__ __forceinline__ void meet(float w, int j) {   // the larger, the lower index of equals
         if (w > v || (w == v && j < i)) v = w, i = j;
     }
+    __device__ __forceinline__ void join() {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) meet(__shfl_xor_sync(kAll, v, o), __shfl_xor_sync(kAll, i, o));
+    }
 };
-__device__ __forceinline__ Best nobody() { return Best{0.0f, INT_MAX}; }
+
+constexpr int kParts = kWarps * kMostCtas;   // the cluster's warps
 
 struct Shared {
     uint64_t bars[kWarps][kStages];
-    Best best_warp[kWarps];
-    Best best[2][kMostCtas];   // written by each CTA of the cluster
-    int kept, odd;             // odd: a value of this CTA's part of some row is +inf or NaN
+    uint64_t arrived[3];       // what the cluster's warps saw of the rows, and their best tokens of either round
+    Best best[2][kParts];      // written by every warp of the cluster
+    int odd[kWarps];           // a value of the warp's part of some row is +inf or NaN
+    int kept;
 };
 
-// Shared memory behind `Shared`: of each row what the warps saw, what the CTAs saw (written by each of the cluster), and all of it;
-// then the warps' pieces.
-__host__ __device__ constexpr int seen_bytes(int rows) { return (rows * (kWarps + kMostCtas + 1) * static_cast<int>(sizeof(Seen)) + 127) / 128 * 128; }
+// Shared memory behind `Shared`: of each row what the cluster's warps saw (written by them) and all of it; then the warps' pieces.
+__host__ __device__ constexpr int seen_bytes(int rows) { return rows * (kParts + 1) * static_cast<int>(sizeof(Seen)); }
 constexpr int kRing = kWarps * kStages * kUnits * 16;
 
 template <typename T, typename Q>
-__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_constant__ VerifyArgs A) {
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_constant__ VerifyArgs A, int log_ctas) {
     constexpr int kIn = 16 / sizeof(T), kPer = kUnits / 32;   // values of a unit, units of a lane in a piece
     __shared__ Shared S;
     extern __shared__ __align__(128) unsigned char s_dynamic[];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
-    const int b = blockIdx.x / ctas, tid = threadIdx.x, lane = tid % 32, warp = tid / 32, V = A.V, K = A.K;
+    const int ctas = 1 << log_ctas, rank = cluster_rank();
+    const int b = blockIdx.x >> log_ctas, tid = threadIdx.x, lane = tid % 32, warp = tid / 32, V = A.V, K = A.K;
     const tq_drafts& D = A.d;
-    Seen* const seen_warp = reinterpret_cast<Seen*>(s_dynamic);    // [row][warp]
-    Seen* const seen_part = seen_warp + (K + 1) * kWarps;           // [row][CTA]
-    Seen* const seen = seen_part + (K + 1) * kMostCtas;             // [row]
+    int k = D.draft_lens ? D.draft_lens[b] : K;
+    const float asked_T = !D.noise ? 0.0f : D.temperatures ? D.temperatures[b] : 1.0f;
+    Seen* const seen = reinterpret_cast<Seen*>(s_dynamic);     // [row]
+    Seen* const seen_part = seen + K + 1;                       // [row][CTA][warp]
     uint4* const ring = reinterpret_cast<uint4*>(s_dynamic + seen_bytes(K + 1)) + warp * kStages * kUnits;
-    cluster.barrier_arrive();   // (waited for before the first write into another CTA)
     const bool probs = D.target_probs != 0;
     const T* target = static_cast<const T*>(D.target) + b * D.target_stride_batch;
     const Q* draft = static_cast<const Q*>(D.draft) + (D.draft ? b * D.draft_stride_batch : 0);
-    const int each = (static_cast<int>(V / kIn) + ctas - 1) / ctas;
-    if (tid == 0) S.kept = K, S.odd = 0;
+    const int each = (V / kIn + ctas - 1) >> log_ctas;
+    if (tid < 3) tc::mbar_init(&S.arrived[tid], 1);
     if (lane < kStages) tc::mbar_init(&S.bars[warp][lane], 1);
+    if (lane == 0) S.odd[warp] = 0;
+    if (tid == 0) S.kept = K;
     tc::mbar_fence_init();
     __syncwarp();
-    // ---- a warp's pieces of the rows, one row behind the other (lane 0 asks for them)
-    int issued = 0, done = 0, last_row = probs ? -1 : 0, ask_row = 0;   // the first row is needed whatever k is
-    Units ask = units(target, V, each, rank);
-    int ask_u = ask.u0 + warp * kUnits;
-    auto fill = [&]() {
-        while (issued - done < kStages && last_row >= 0) {
-            if (ask_u < ask.u1) {
-                const T* from = target + ask_row * D.target_stride_row + ask.head + static_cast<int64_t>(ask_u) * kIn;
-                const unsigned bytes = min(kUnits, ask.u1 - ask_u) * 16;
-                uint64_t* bar = &S.bars[warp][issued % kStages];
-                tc::mbar_expect_tx(bar, bytes);
-                tc::bulk_g2s(ring + issued % kStages * kUnits, from, bytes, bar);
-                ++issued;
-                ask_u += kWarps * kUnits;
-            } else if (ask_row < last_row) {
-                ++ask_row;
-                ask = units(target + ask_row * D.target_stride_row, V, each, rank);
-                ask_u = ask.u0 + warp * kUnits;
-            } else {
-                break;
-            }
-        }
+    // (waited for before the first word to another CTA)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+    // ---- a warp's pieces of the rows, one row behind the other (lane 0 asks for them, each as another has been taken)
+    int last_row = 0, ask_row = 0, ask_u = 0, ask_end = 0, ask_st = 0, asked = 0;   // the first row is needed whatever k is
+    const T* ask_from = target;   // of unit 0
+    auto start_row = [&]() {
+        const T* r = target + ask_row * D.target_stride_row;
+        const Units part = units(r, V, each, rank);
+        ask_from = r + part.head;
+        ask_u = part.u0 + warp * kUnits;
+        ask_end = part.u1;
     };
-    if (lane == 0) fill();
-    int k = D.draft_lens ? D.draft_lens[b] : K;
-    const float T_ = !D.noise ? 0.0f : D.temperatures ? D.temperatures[b] : 1.0f;
+    auto ask = [&]() {
+        while (ask_u >= ask_end) {
+            if (ask_row >= last_row) return;
+            ++ask_row;
+            start_row();
+        }
+        const unsigned bytes = min(kUnits, ask_end - ask_u) * 16;
+        uint64_t* bar = &S.bars[warp][ask_st];
+        tc::mbar_expect_tx(bar, bytes);
+        tc::bulk_g2s(ring + ask_st * kUnits, ask_from + static_cast<int64_t>(ask_u) * kIn, bytes, bar);
+        ask_u += kWarps * kUnits;
+        ask_st = ask_st + 1 < kStages ? ask_st + 1 : 0;
+        ++asked;
+    };
+    if (lane == 0 && !probs) {
+        start_row();
+#pragma unroll 1
+        for (int i = 0; i < kStages; ++i) ask();
+    }
     if (k < 0 || k > K) {
         if (rank == 0 && tid == 0) atomicOr(A.err, TQ_DEVERR_SEQLEN);
         k = min(max(k, 0), K);
     }
-    const bool greedy = !(T_ > 0.0f), stats = !probs || greedy;   // (probabilities are as they are)
-    const Scale scale(greedy ? 1.0f : fminf(fmaxf(T_, 0x1p-120f), 0x1p100f));
-    last_row = stats ? k : -1;
-    if (lane == 0) fill();
     // draft i is lane i / 8 of warp i % 8's
     const int mine = warp + kWarps * lane;
+    const bool greedy = !(asked_T > 0.0f), stats = !probs || greedy;   // (probabilities are as they are)
     int d = -1;
     float x_d = 0.0f, q_d = 1.0f, u_d = 0.0f;
     if (lane < 8 && mine < k) {
         d = D.draft_tokens[static_cast<int64_t>(b) * K + mine];
         if (!greedy) u_d = D.uniforms[static_cast<int64_t>(b) * K + mine];
     }
-    const int share = (V + ctas - 1) / ctas, i_begin = min(V, rank * share), i_end = min(V, i_begin + share);
-    if (tid == 32 && !greedy) ahead(D.noise + b * D.noise_stride, i_begin, i_end);
+    const Scale scale(greedy ? 1.0f : fminf(fmaxf(asked_T, 0x1p-120f), 0x1p100f));
+    const int share = (V + ctas - 1) >> log_ctas, i_begin = min(V, rank * share), i_end = min(V, i_begin + share);
+    if (stats) {
+        last_row = k;
+        if (lane == 0) {
+            if (probs) start_row();
+#pragma unroll 1
+            while (asked < kStages && (ask_u < ask_end || ask_row < last_row)) ask();
+        }
+        if (tid == 0) tc::mbar_expect_tx(&S.arrived[0], (k + 1) * ctas * kWarps * static_cast<int>(sizeof(Seen)));
+    }
+    if (tid == 32 && !greedy) {
+        ahead(D.noise + b * D.noise_stride, i_begin, i_end);
+        tc::mbar_expect_tx(&S.arrived[1], ctas * kWarps * static_cast<int>(sizeof(Best)));
+    }
+    auto late = [&](auto&& wait) {   // a wait that may run out: once more then, so that nothing is on its way when the kernel ends
+        if (!wait()) {
+            atomicOr(A.err, TQ_DEVERR_TIMEOUT);
+            wait();
+        }
+    };
+    bool begun = false;   // all CTAs of the cluster have
+    auto begin = [&]() {
+        __syncwarp();
+        if (!begun) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+        begun = true;
+    };
     // ---- each row's largest value, where it is, and its sum
     if (stats) {
+        int st = 0, phase = 0;
+#pragma unroll 1
         for (int i = 0; i <= k; ++i) {
             const T* row = target + i * D.target_stride_row;
             const Units part = units(row, V, each, rank);
             // what lies outside whole units: before them the first CTA's, behind them the last one's
             int edge = -1;
+            float x_edge = 0.0f;
             if (warp == 0) {
                 if (rank == 0 && lane < part.head) edge = lane;
                 if (rank == ctas - 1 && lane >= 16 && part.tail + lane - 16 < V) edge = part.tail + lane - 16;
+                if (edge >= 0) x_edge = number(row[edge]);
             }
             Seen s = nothing();
             auto where = [&](int u, int e) { return part.head + (u + e / kIn * 32 + lane) * kIn + e % kIn; };
+#pragma unroll 1
             for (int u = part.u0 + warp * kUnits; u < part.u1; u += kWarps * kUnits) {
-                const int st = done % kStages;
-                if (!tc::mbar_wait(&S.bars[warp][st], done / kStages & 1)) {
-                    if (lane == 0) atomicOr(A.err, TQ_DEVERR_TIMEOUT);
-                    tc::mbar_wait(&S.bars[warp][st], done / kStages & 1);
+                late([&]() { return tc::mbar_wait(&S.bars[warp][st], phase); });
+                uint4* from = ring + st * kUnits + lane;
+                if (u + kUnits > part.u1) {   // behind the last unit nothing can be
+                    const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+#pragma unroll 1
+                    for (int v = 0; v < kPer; ++v)
+                        if (u + v * 32 + lane >= part.u1) from[v * 32] = make_uint4(none, none, none, none);
+                    tc::fence_proxy_async_smem();
                 }
-                float x[kPer * kIn];
-#pragma unroll
-                for (int v = 0; v < kPer; ++v) {
-                    if (u + v * 32 + lane < part.u1) {
-                        numbers(ring[st * kUnits + v * 32 + lane], x + v * kIn, T());
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < kIn; ++e) x[v * kIn + e] = -INFINITY;
-                    }
-                }
+                s.template take<T>(from, scale, u);
                 __syncwarp();
-                ++done;
-                if (lane == 0) fill();
-                s.take(x, scale, greedy, [&](int e) { return where(u, e); });
+                if (lane == 0) ask();
+                if (++st == kStages) st = 0, phase ^= 1;
             }
-            if (edge >= 0) {
-                const float x[1] = {number(row[edge])};
-                s.take(x, scale, greedy, [&](int) { return edge; });
-            }
+            if (edge >= 0) s.take(x_edge, scale, edge);
             if (!(s.sum < INFINITY)) {   // a NaN, or +inf (inf - inf): once more, as they count
-                S.odd = 1;
+                S.odd[warp] = 1;
                 atomicOr(A.err, TQ_DEVERR_NONFINITE);
                 s = nothing();
-                auto one = [&](int at) {
-                    const float x[1] = {logit(number(row[at]))};
-                    s.take(x, scale, greedy, [&](int) { return at; });
-                };
+#pragma unroll 1
                 for (int u = part.u0 + warp * kUnits; u < part.u1; u += kWarps * kUnits)
+#pragma unroll 1
                     for (int e = 0; e < kPer * kIn; ++e)
-                        if (u + e / kIn * 32 + lane < part.u1) one(where(u, e));
-                if (edge >= 0) one(edge);
+                        if (u + e / kIn * 32 + lane < part.u1) s.take(logit(number(row[where(u, e)])), scale, where(u, e));
+                if (edge >= 0) s.take(logit(x_edge), scale, edge);
             }
-            s.join(scale, 32);
-            if (lane == 0) seen_warp[i * kWarps + warp] = s;
+            if (greedy) s.find(row + part.head, part.u1, part.head);
+            s.join(scale);
+            begin();
+            if (lane < ctas)
+                send(remote(&seen_part[(i * kMostCtas + rank) * kWarps + warp], lane), remote(&S.arrived[0], lane), __float_as_uint(s.top), __float_as_uint(s.sum),
+                     static_cast<uint32_t>(s.at), 0u);
         }
     }
     if (lane < 8 && mine < k && d >= 0 && d < V) {
         x_d = number(target[mine * D.target_stride_row + d]);
         if (D.draft && !greedy) q_d = number(draft[mine * D.draft_stride_row + d]);
     }
-    __syncthreads();
-    cluster.barrier_wait();
-    if (stats) {   // row i is warp i % 8's, here and below
-        for (int i = warp; i <= k; i += kWarps) {
-            Seen s = lane < kWarps ? seen_warp[i * kWarps + lane] : nothing();
-            s.join(scale, kWarps);
-            if (lane < ctas) cluster.map_shared_rank(seen_part, lane)[i * kMostCtas + rank] = s;
-        }
-        cluster.sync();
-    }
-    // ---- how many drafts stand
+    begin();
+    __syncthreads();   // (S.kept, S.odd)
+    // ---- how many drafts stand: row i is warp i % 8's
+    if (stats) late([&]() { return wait_cluster(&S.arrived[0]); });
+#pragma unroll 1
     for (int i = warp; i <= k; i += kWarps) {
         Seen s = nothing();
         if (stats) {
-            if (lane < ctas) s = seen_part[i * kMostCtas + lane];
-            s.join(scale, kMostCtas);
-            s.top = __shfl_sync(kAll, s.top, 0), s.sum = __shfl_sync(kAll, s.sum, 0), s.at = __shfl_sync(kAll, s.at, 0);
+            const Seen* p = seen_part + i * kParts;
+            if (lane < ctas * kWarps) s = p[lane];
+            Seen more = lane + 32 < ctas * kWarps ? p[lane + 32] : nothing();
+            if (more.top > s.top) { const Seen x = s; s = more; more = x; }
+            s.sum += more.sum * scale.weight(more.top - s.top);
+            if (more.top == s.top) s.at = min(s.at, more.at);
+            s.join(scale);
             if (lane == 0) seen[i] = s;
         }
         if (lane == i / kWarps && i < k) {
@@ -353,8 +426,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             if (greedy) {
                 stands = stands && d == s.at && (probs ? s.top > 0.0f : s.sum > 0.0f);
             } else if (stands) {   // u q < p, times the sum
-                const float p = probs ? x_d : scale.weight_near(logit(x_d) - s.top);
-                stands = static_cast<double>(u_d) * q_d * (probs ? 1.0f : s.sum) < p;
+                stands = u_d * q_d * (probs ? 1.0f : s.sum) < (probs ? x_d : scale.weight_near(logit(x_d) - s.top));
             }
             if (!stands) atomicMin(&S.kept, i);
         }
@@ -371,97 +443,103 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
         // drafts' probabilities
         const float* noise = D.noise + b * D.noise_stride;
         const float top = probs ? 0.0f : seen[n].top, sum = probs ? 1.0f : seen[n].sum;
-        const bool odd = S.odd != 0;
-        const uint64_t off = pair(-top, -top), c = pair(scale.c, scale.c), nc = pair(-scale.c, -scale.c), nlo = pair(-scale.lo, -scale.lo),
-                       nln2 = pair(-kLn2, -kLn2), nsum = pair(-sum, -sum);
+        bool odd = false;
+        for (int w = 0; w < kWarps; ++w) odd |= S.odd[w] != 0;
+        const float m = top * scale.near;
+        const bool usual = fabsf(m) < kUsual;   // as in Seen::take: the weights are then relative to m, and so is their sum
+        const float whole = usual && !probs ? fmaf(sum, fmaf(top, scale.near, -m) * kLn2, sum) : sum;
+        const int head = units(row, V, each, rank).head, chunks = (V - head) / 8;
+#pragma unroll 1
         for (int round = 0; round < 2 && next < 0; ++round) {
             const bool minus = round == 0 && n < k;
             if (round == 1 && n == k) break;
             const Q* q = minus && D.draft ? draft + n * D.draft_stride_row : nullptr;
             const int own = minus && !D.draft ? D.draft_tokens[static_cast<int64_t>(b) * K + n] : -1;
             if (tid == 0 && q) ahead(q, i_begin, i_end);
-            Best best = nobody();
+            if (tid == 0 && round == 1) tc::mbar_expect_tx(&S.arrived[2], ctas * kWarps * static_cast<int>(sizeof(Best)));
+            Best best{0.0f, INT_MAX};
             // 8 values, those that are none -inf (0 of probabilities)
-            auto race = [&](float (&x)[8], float (&y)[8], const float (&e)[8], auto&& index) {
-                if (odd && !probs) {
+            auto race = [&](float2 (&x)[4], float2 (&y)[4], const float2 (&e)[4], auto&& index) {
+                if (!probs) {
+                    if (odd) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = logit(x[i]);
+                        for (int i = 0; i < 4; ++i) x[i] = make_float2(logit(x[i].x), logit(x[i].y));
+                    }
+                    if (usual) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 t = __ffma2_rn(x[i], both(scale.near), both(-m));
+                            x[i] = make_float2(ex2(t.x), ex2(t.y));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = make_float2(scale.weight(x[i].x - top), scale.weight(x[i].y - top));
+                    }
                 }
                 if (own >= 0) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (index(i) == own) y[i] = 1.0f;
-                }
-                float s[8];
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    uint64_t w = pair(x[i], x[i + 1]);
-                    if (!probs) {   // the exponent's rounding goes back into the weight (NaN of a masked value, which wins nothing)
-                        const uint64_t z = add2(w, off), t = mul2(z, c), r = fma2(z, nlo, fma2(z, nc, t));
-                        float t0, t1;
-                        split(t, t0, t1);
-                        w = pair(ex2(t0), ex2(t1));
-                        w = fma2(mul2(w, nln2), r, w);
+                    for (int i = 0; i < 4; ++i) {
+                        if (index(2 * i) == own) y[i].x = 1.0f;
+                        if (index(2 * i + 1) == own) y[i].y = 1.0f;
                     }
-                    if (minus) w = fma2(pair(y[i], y[i + 1]), nsum, w);
-                    const float e0 = fminf(fmaxf(e[i], 0x1p-100f), 0x1p24f), e1 = fminf(fmaxf(e[i + 1], 0x1p-100f), 0x1p24f);
-                    split(mul2(w, pair(rcp(e0), rcp(e1))), s[i], s[i + 1]);
                 }
-                float m = s[0];
+                float2 s[4];
 #pragma unroll
-                for (int i = 1; i < 8; ++i) m = fmaxf(m, s[i]);
-                if (m > best.v) {
-                    best.v = m;
+                for (int i = 0; i < 4; ++i) {
+                    const float2 w = minus ? __ffma2_rn(y[i], both(-whole), x[i]) : x[i];
+                    s[i] = __fmul2_rn(w, make_float2(rcp(fmaxf(e[i].x, 0x1p-100f)), rcp(fmaxf(e[i].y, 0x1p-100f))));
+                }
+                const float here = fmaxf(fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[1].x, s[1].y)), fmaxf(fmaxf(s[2].x, s[2].y), fmaxf(s[3].x, s[3].y)));
+                if (here >= best.v && here > 0.0f) {
+                    int at = 0;
 #pragma unroll
-                    for (int i = 7; i >= 0; --i)
-                        if (s[i] == m) best.i = index(i);
+                    for (int i = 3; i >= 0; --i) {
+                        if (s[i].y == here) at = index(2 * i + 1);
+                        if (s[i].x == here) at = index(2 * i);
+                    }
+                    best.meet(here, at);
                 }
             };
-            const float none = probs ? 0.0f : -INFINITY;
-            auto scattered = [&](int first, int step, int end) {
-                for (int i0 = first; i0 < end; i0 += 8 * step) {
-                    float x[8], y[8], e[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int at = i0 + i * step;
-                        x[i] = none, y[i] = 0.0f, e[i] = 1.0f;
-                        if (at < end) {
-                            x[i] = number(row[at]), e[i] = noise[at];
-                            if (q) y[i] = number(q[at]);
-                        }
-                    }
-                    race(x, y, e, [&](int i) { return i0 + i * step; });
-                }
-            };
-            const int head = units(row, V, each, rank).head;
-            if (reinterpret_cast<uintptr_t>(noise + head) % 16 == 0 && (!q || reinterpret_cast<uintptr_t>(q + head) % 16 == 0)) {
-                const int chunks = (V - head) / 8, per = (chunks + ctas - 1) / ctas, end = min(chunks, (rank + 1) * per);
-#pragma unroll 2
+            const bool alike = reinterpret_cast<uintptr_t>(noise + head) % 16 == 0 && (!q || reinterpret_cast<uintptr_t>(q + head) % 16 == 0);
+            if (alike) {
+                const int per = (chunks + ctas - 1) >> log_ctas, end = min(chunks, (rank + 1) * per);
+#pragma unroll 1
                 for (int v = rank * per + tid; v < end; v += kThreads) {
                     const int i0 = head + v * 8;
-                    float x[8], y[8] = {}, e[8];
+                    float2 x[4], y[4] = {}, e[4];
                     load8(row + i0, x);
                     load8(noise + i0, e);
                     if (q) load8(q + i0, y);
                     race(x, y, e, [&](int i) { return i0 + i; });
                 }
-                if (rank == 0) scattered(tid, kThreads, head);
-                if (rank == ctas - 1) scattered(head + chunks * 8 + tid, kThreads, V);
-            } else {   // rows that do not lie alike: one value at a time
-                scattered(i_begin + tid, kThreads, i_end);
             }
+            // one value at a time: all of rows that do not lie alike, else what lies outside chunks (the first CTA's)
+            const int count = !alike ? i_end - i_begin : rank == 0 ? V - chunks * 8 : 0;
+            auto place = [&](int j) { return !alike ? i_begin + j : j < head ? j : j + chunks * 8; };
+#pragma unroll 1
+            for (int j0 = tid; j0 < count; j0 += 8 * kThreads) {
+                float2 x[4], y[4], e[4];
+                const float none = probs ? 0.0f : -INFINITY;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) best.meet(__shfl_xor_sync(kAll, best.v, o), __shfl_xor_sync(kAll, best.i, o));
-            if (lane == 0) S.best_warp[warp] = best;
-            __syncthreads();
-            if (tid < ctas) {
-                best = S.best_warp[0];
-                for (int w = 1; w < kWarps; ++w) best.meet(S.best_warp[w].v, S.best_warp[w].i);
-                cluster.map_shared_rank(&S, tid)->best[round][rank] = best;
+                for (int i = 0; i < 8; ++i) {
+                    float &xi = i % 2 ? x[i / 2].y : x[i / 2].x, &yi = i % 2 ? y[i / 2].y : y[i / 2].x, &ei = i % 2 ? e[i / 2].y : e[i / 2].x;
+                    xi = none, yi = 0.0f, ei = 1.0f;
+                    if (j0 + i * kThreads < count) {
+                        const int at = place(j0 + i * kThreads);
+                        xi = number(row[at]), ei = noise[at];
+                        if (q) yi = number(q[at]);
+                    }
+                }
+                race(x, y, e, [&](int i) { return place(j0 + i * kThreads); });
             }
-            cluster.sync();
-            best = nobody();
-            for (int r = 0; r < ctas; ++r) best.meet(S.best[round][r].v, S.best[round][r].i);
+            best.join();
+            if (lane < ctas)
+                send(remote(&S.best[round][rank * kWarps + warp], lane), remote(&S.arrived[1 + round], lane), __float_as_uint(best.v), static_cast<uint32_t>(best.i));
+            late([&]() { return wait_cluster(&S.arrived[1 + round]); });
+            best = Best{0.0f, INT_MAX};
+            if (lane < ctas * kWarps) best = S.best[round][lane];
+            if (lane + 32 < ctas * kWarps) best.meet(S.best[round][lane + 32].v, S.best[round][lane + 32].i);
+            best.join();
             next = best.i < V ? best.i : -1;
         }
     }
@@ -489,26 +567,26 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
 template <typename T, typename Q>
 cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
     // CTAs of a cluster: a piece for each warp, at most
-    int ctas = 1;
-    while (ctas < kMostCtas && static_cast<int64_t>(ctas) * kWarps * kUnits * 16 / static_cast<int>(sizeof(T)) < a.V) ctas *= 2;
+    int log_ctas = 0;
+    while ((1 << log_ctas) < kMostCtas && (static_cast<int64_t>(kWarps * kUnits * 16 / sizeof(T)) << log_ctas) < a.V) ++log_ctas;
     const int smem = seen_bytes(a.K + 1) + kRing;
-    if (smem > 40 * 1024) {
+    if (smem > 40 * 1024) {   // (a launch's first 48 KB hold `Shared` too)
         static std::atomic<uint64_t> allowed{0};
         const cudaError_t e = kv8::allow_smem(verify_kernel<T, Q>, seen_bytes(65) + kRing, allowed);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * ctas);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.batch) << log_ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.x = 1 << log_ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<T, Q>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<T, Q>, a, log_ctas);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return e;
 }
