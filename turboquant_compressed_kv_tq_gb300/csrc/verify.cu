@@ -65,13 +65,14 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float logit(float x) { return x == x ? fminf(x, FLT_MAX) : -INFINITY; }
 
 // log2(e) / T as c + lo, both positive, so that what is masked (-inf) stays -inf in either product: log2(e) = 1.442695 (rounded down)
-// + 1.9259630e-8, the quotient rounded down, and what the division leaves. To 2^-44.
+// + 1.9259630e-8; c is below the quotient, lo what it leaves. To 2^-40.
 struct Scale {
     float c, lo, near;   // near: c + lo in one number, off by 2^-25 of itself
     __device__ __forceinline__ explicit Scale(float T) {
         constexpr float hi = 0x1.715476p+0f, rest = 1.9259630e-8f;
-        c = __fdiv_rd(hi, T);
-        lo = __fdividef(fmaf(-c, T, hi) + rest, T);
+        const float r = rcp(T);
+        c = hi * r * (1.0f - 0x1p-21f);   // (the reciprocal is off by 2^-23, the products by 2^-24)
+        lo = (fmaf(-c, T, hi) + rest) * r;
         near = c + lo;
     }
     __device__ __forceinline__ float weight(float d) const { return ex2(fmaf(d, c, d * lo)); }   // d <= 0
@@ -99,26 +100,17 @@ __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(tc::smem_addr(p)), "r"(rank));
     return r;
 }
-// 16 or 8 bytes into another CTA's shared memory, counted on a barrier there.
-__device__ __forceinline__ void send(uint32_t to, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];\n" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
-                 : "memory");
+// 16 or 8 bytes into another CTA's shared memory.
+__device__ __forceinline__ void send(uint32_t to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-__device__ __forceinline__ void send(uint32_t to, uint32_t bar, uint32_t a, uint32_t b) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];\n" ::"r"(to), "r"(a), "r"(b), "r"(bar) : "memory");
+__device__ __forceinline__ void send(uint32_t to, uint32_t a, uint32_t b) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};\n" ::"r"(to), "r"(a), "r"(b) : "memory");
 }
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar) {   // for the barrier's first phase, and what other CTAs sent with it
-    const uint32_t a = tc::smem_addr(bar);
-    for (unsigned it = 0; it < tc::kSpinLimit; ++it) {
-        uint32_t done;
-        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n selp.u32 %0, 1, 0, p;\n}\n"
-                     : "=r"(done)
-                     : "r"(a)
-                     : "memory");
-        if (done) return true;
-    }
-    return false;
-}
+// The cluster's barrier: every thread of it arrives, and waits once for each arrival. What was written before an arrival is seen behind
+// the wait, in all CTAs. (The hardware's own: it ends as soon as all threads have arrived, or ended.)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory"); }
 
 // Values [i0, i1) of a row on their way into the L2 cache (one thread; whole units).
 template <typename T>
@@ -144,6 +136,12 @@ __device__ __forceinline__ Units units(const T* row, int V, int each, int rank) 
 }
 
 // What is known of a row, or a part of it: the largest value, the sum of weights relative to it, and where it is.
+// The largest of the warp's numbers (no NaN), as integers that are ordered as they are.
+__device__ __forceinline__ float warp_max(float x) {
+    const int i = __float_as_int(x), k = __reduce_max_sync(kAll, i ^ (i >> 31 & 0x7FFFFFFF));
+    return __int_as_float(k ^ (k >> 31 & 0x7FFFFFFF));
+}
+
 struct __align__(16) Seen {
     float top, sum;   // (nothing but masked values: sum 0)
     int at, piece;    // of a lane while it goes through a row: the piece (its first unit) in which the largest stood first, or -1
@@ -185,7 +183,7 @@ struct __align__(16) Seen {
                 s = __fadd2_rn(s, make_float2(ex2(e.x), ex2(e.y)));
             }
             sum = fmaf(s.x + s.y, fmaf(fmaf(top, S.near, -m), -kLn2, 1.0f), sum);
-        } else {   // seldom: one value after the other
+        } else if (t > -INFINITY) {   // seldom: one value after the other
 #pragma unroll 1
             for (int e = 0; e < kPer * kIn; ++e) sum += S.weight(number(reinterpret_cast<const T*>(from + e / kIn * 32)[e % kIn]) - top);
         }
@@ -195,9 +193,7 @@ struct __align__(16) Seen {
     template <typename T>
     __device__ __forceinline__ void find(const T* row, int end, int head) {
         constexpr int kIn = 16 / sizeof(T);
-        float t = top;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, o));
+        const float t = warp_max(top);
         if (top == t && piece >= 0) {
 #pragma unroll 1
             for (int v = kUnits / 32 - 1; v >= 0; --v) {
@@ -215,9 +211,7 @@ struct __align__(16) Seen {
     }
     // With what the warp's other lanes know, for all of them.
     __device__ __forceinline__ void join(const Scale& S) {
-        float t = top;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, o));
+        const float t = warp_max(top);
         sum *= S.weight(top - t);
         at = static_cast<int>(__reduce_min_sync(kAll, static_cast<unsigned>(top < t ? INT_MAX : at)));
         top = t;
@@ -243,7 +237,6 @@ constexpr int kParts = kWarps * kMostCtas;   // the cluster's warps
 
 struct Shared {
     uint64_t bars[kWarps][kStages];
-    uint64_t arrived[3];       // what the cluster's warps saw of the rows, and their best tokens of either round
     Best best[2][kParts];      // written by every warp of the cluster
     int odd[kWarps];           // a value of the warp's part of some row is +inf or NaN
     int kept;
@@ -269,15 +262,15 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     const bool probs = D.target_probs != 0;
     const T* target = static_cast<const T*>(D.target) + b * D.target_stride_batch;
     const Q* draft = static_cast<const Q*>(D.draft) + (D.draft ? b * D.draft_stride_batch : 0);
-    const int each = (V / kIn + ctas - 1) >> log_ctas;
-    if (tid < 3) tc::mbar_init(&S.arrived[tid], 1);
+    const int each = (V / kIn + ctas - 1) >> log_ctas, pieces = (each + kUnits - 1) / kUnits;
+    // a row's pieces go to the warps in turn, and on with the next row's
+    auto first_piece = [&](int i) { return ((warp - i * pieces) & (kWarps - 1)) * kUnits; };
     if (lane < kStages) tc::mbar_init(&S.bars[warp][lane], 1);
     if (lane == 0) S.odd[warp] = 0;
     if (tid == 0) S.kept = K;
     tc::mbar_fence_init();
     __syncwarp();
-    // (waited for before the first word to another CTA)
-    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+    cluster_arrive();   // (waited for before the first word to another CTA)
     // ---- a warp's pieces of the rows, one row behind the other (lane 0 asks for them, each as another has been taken)
     int last_row = 0, ask_row = 0, ask_u = 0, ask_end = 0, ask_st = 0, asked = 0;   // the first row is needed whatever k is
     const T* ask_from = target;   // of unit 0
@@ -285,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
         const T* r = target + ask_row * D.target_stride_row;
         const Units part = units(r, V, each, rank);
         ask_from = r + part.head;
-        ask_u = part.u0 + warp * kUnits;
+        ask_u = part.u0 + first_piece(ask_row);
         ask_end = part.u1;
     };
     auto ask = [&]() {
@@ -329,24 +322,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
 #pragma unroll 1
             while (asked < kStages && (ask_u < ask_end || ask_row < last_row)) ask();
         }
-        if (tid == 0) tc::mbar_expect_tx(&S.arrived[0], (k + 1) * ctas * kWarps * static_cast<int>(sizeof(Seen)));
     }
-    if (tid == 32 && !greedy) {
-        ahead(D.noise + b * D.noise_stride, i_begin, i_end);
-        tc::mbar_expect_tx(&S.arrived[1], ctas * kWarps * static_cast<int>(sizeof(Best)));
-    }
-    auto late = [&](auto&& wait) {   // a wait that may run out: once more then, so that nothing is on its way when the kernel ends
-        if (!wait()) {
-            atomicOr(A.err, TQ_DEVERR_TIMEOUT);
-            wait();
-        }
-    };
-    bool begun = false;   // all CTAs of the cluster have
-    auto begin = [&]() {
-        __syncwarp();
-        if (!begun) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-        begun = true;
-    };
+    if (tid == 32 && !greedy) ahead(D.noise + b * D.noise_stride, i_begin, i_end);
     // ---- each row's largest value, where it is, and its sum
     if (stats) {
         int st = 0, phase = 0;
@@ -357,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             // what lies outside whole units: before them the first CTA's, behind them the last one's
             int edge = -1;
             float x_edge = 0.0f;
-            if (warp == 0) {
+            if (warp == (i & (kWarps - 1))) {
                 if (rank == 0 && lane < part.head) edge = lane;
                 if (rank == ctas - 1 && lane >= 16 && part.tail + lane - 16 < V) edge = part.tail + lane - 16;
                 if (edge >= 0) x_edge = number(row[edge]);
@@ -365,8 +342,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             Seen s = nothing();
             auto where = [&](int u, int e) { return part.head + (u + e / kIn * 32 + lane) * kIn + e % kIn; };
 #pragma unroll 1
-            for (int u = part.u0 + warp * kUnits; u < part.u1; u += kWarps * kUnits) {
-                late([&]() { return tc::mbar_wait(&S.bars[warp][st], phase); });
+            for (int u = part.u0 + first_piece(i); u < part.u1; u += kWarps * kUnits) {
+                if (!tc::mbar_wait(&S.bars[warp][st], phase)) {   // once more, so that no copy is on its way when the kernel ends
+                    if (lane == 0) atomicOr(A.err, TQ_DEVERR_TIMEOUT);
+                    tc::mbar_wait(&S.bars[warp][st], phase);
+                }
                 uint4* from = ring + st * kUnits + lane;
                 if (u + kUnits > part.u1) {   // behind the last unit nothing can be
                     const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
@@ -386,28 +366,28 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
                 atomicOr(A.err, TQ_DEVERR_NONFINITE);
                 s = nothing();
 #pragma unroll 1
-                for (int u = part.u0 + warp * kUnits; u < part.u1; u += kWarps * kUnits)
+                for (int u = part.u0 + first_piece(i); u < part.u1; u += kWarps * kUnits)
 #pragma unroll 1
                     for (int e = 0; e < kPer * kIn; ++e)
                         if (u + e / kIn * 32 + lane < part.u1) s.take(logit(number(row[where(u, e)])), scale, where(u, e));
                 if (edge >= 0) s.take(logit(x_edge), scale, edge);
             }
-            if (greedy) s.find(row + part.head, part.u1, part.head);
-            s.join(scale);
-            begin();
+            if (__any_sync(kAll, s.sum > 0.0f)) {
+                if (greedy) s.find(row + part.head, part.u1, part.head);
+                s.join(scale);
+            }
+            if (i == 0) cluster_wait();
             if (lane < ctas)
-                send(remote(&seen_part[(i * kMostCtas + rank) * kWarps + warp], lane), remote(&S.arrived[0], lane), __float_as_uint(s.top), __float_as_uint(s.sum),
-                     static_cast<uint32_t>(s.at), 0u);
+                send(remote(&seen_part[(i * kMostCtas + rank) * kWarps + warp], lane), __float_as_uint(s.top), __float_as_uint(s.sum), static_cast<uint32_t>(s.at), 0u);
         }
     }
     if (lane < 8 && mine < k && d >= 0 && d < V) {
         x_d = number(target[mine * D.target_stride_row + d]);
         if (D.draft && !greedy) q_d = number(draft[mine * D.draft_stride_row + d]);
     }
-    begin();
-    __syncthreads();   // (S.kept, S.odd)
+    if (stats) cluster_arrive();
+    cluster_wait();
     // ---- how many drafts stand: row i is warp i % 8's
-    if (stats) late([&]() { return wait_cluster(&S.arrived[0]); });
 #pragma unroll 1
     for (int i = warp; i <= k; i += kWarps) {
         Seen s = nothing();
@@ -456,7 +436,6 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             const Q* q = minus && D.draft ? draft + n * D.draft_stride_row : nullptr;
             const int own = minus && !D.draft ? D.draft_tokens[static_cast<int64_t>(b) * K + n] : -1;
             if (tid == 0 && q) ahead(q, i_begin, i_end);
-            if (tid == 0 && round == 1) tc::mbar_expect_tx(&S.arrived[2], ctas * kWarps * static_cast<int>(sizeof(Best)));
             Best best{0.0f, INT_MAX};
             // 8 values, those that are none -inf (0 of probabilities)
             auto race = [&](float2 (&x)[4], float2 (&y)[4], const float2 (&e)[4], auto&& index) {
@@ -500,42 +479,42 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
                     best.meet(here, at);
                 }
             };
+            // rows that lie alike in chunks of 8, and what lies outside those (the first CTA's) one value at a time; others all so
             const bool alike = reinterpret_cast<uintptr_t>(noise + head) % 16 == 0 && (!q || reinterpret_cast<uintptr_t>(q + head) % 16 == 0);
-            if (alike) {
-                const int per = (chunks + ctas - 1) >> log_ctas, end = min(chunks, (rank + 1) * per);
+            const int per = (chunks + ctas - 1) >> log_ctas;
 #pragma unroll 1
-                for (int v = rank * per + tid; v < end; v += kThreads) {
-                    const int i0 = head + v * 8;
+            for (int job = 0; job < (alike && rank == 0 ? 3 : 1); ++job) {
+                const bool eight = alike && job == 0;
+                const int step = eight ? 1 : kThreads;   // between a thread's 8 values
+                const int begin = !alike ? i_begin : job == 0 ? head + rank * per * 8 : job == 1 ? 0 : head + chunks * 8;
+                const int end = !alike ? i_end : job == 0 ? head + min(chunks, (rank + 1) * per) * 8 : job == 1 ? head : V;
+#pragma unroll 1
+                for (int i0 = begin + (eight ? tid * 8 : tid); i0 < end; i0 += 8 * kThreads) {
                     float2 x[4], y[4] = {}, e[4];
-                    load8(row + i0, x);
-                    load8(noise + i0, e);
-                    if (q) load8(q + i0, y);
-                    race(x, y, e, [&](int i) { return i0 + i; });
-                }
-            }
-            // one value at a time: all of rows that do not lie alike, else what lies outside chunks (the first CTA's)
-            const int count = !alike ? i_end - i_begin : rank == 0 ? V - chunks * 8 : 0;
-            auto place = [&](int j) { return !alike ? i_begin + j : j < head ? j : j + chunks * 8; };
-#pragma unroll 1
-            for (int j0 = tid; j0 < count; j0 += 8 * kThreads) {
-                float2 x[4], y[4], e[4];
-                const float none = probs ? 0.0f : -INFINITY;
+                    if (eight) {
+                        load8(row + i0, x);
+                        load8(noise + i0, e);
+                        if (q) load8(q + i0, y);
+                    } else {
+                        const float none = probs ? 0.0f : -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float &xi = i % 2 ? x[i / 2].y : x[i / 2].x, &yi = i % 2 ? y[i / 2].y : y[i / 2].x, &ei = i % 2 ? e[i / 2].y : e[i / 2].x;
-                    xi = none, yi = 0.0f, ei = 1.0f;
-                    if (j0 + i * kThreads < count) {
-                        const int at = place(j0 + i * kThreads);
-                        xi = number(row[at]), ei = noise[at];
-                        if (q) yi = number(q[at]);
+                        for (int i = 0; i < 8; ++i) {
+                            float &xi = i % 2 ? x[i / 2].y : x[i / 2].x, &yi = i % 2 ? y[i / 2].y : y[i / 2].x, &ei = i % 2 ? e[i / 2].y : e[i / 2].x;
+                            const int at = i0 + i * kThreads;
+                            xi = none, ei = 1.0f;
+                            if (at < end) {
+                                xi = number(row[at]), ei = noise[at];
+                                if (q) yi = number(q[at]);
+                            }
+                        }
                     }
+                    race(x, y, e, [&](int i) { return i0 + i * step; });
                 }
-                race(x, y, e, [&](int i) { return place(j0 + i * kThreads); });
             }
             best.join();
-            if (lane < ctas)
-                send(remote(&S.best[round][rank * kWarps + warp], lane), remote(&S.arrived[1 + round], lane), __float_as_uint(best.v), static_cast<uint32_t>(best.i));
-            late([&]() { return wait_cluster(&S.arrived[1 + round]); });
+            if (lane < ctas) send(remote(&S.best[round][rank * kWarps + warp], lane), __float_as_uint(best.v), static_cast<uint32_t>(best.i));
+            cluster_arrive();
+            cluster_wait();
             best = Best{0.0f, INT_MAX};
             if (lane < ctas * kWarps) best = S.best[round][lane];
             if (lane + 32 < ctas * kWarps) best.meet(S.best[round][lane + 32].v, S.best[round][lane + 32].i);
