@@ -524,10 +524,48 @@ def test_verification_of_masked_rows(V):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("K,V", [(0, 40), (0, 30011), (2, 40), (2, 30011)])
+def test_verification_of_rows_of_one_value(dtype, K, V):
+    # the lowest number, the largest, zero: each token alike, the lowest of equals where nothing is drawn
+    B = 6
+    for value in (torch.finfo(dtype).min, torch.finfo(dtype).max, 0.0, -1000.0):
+        c = verify_case(V, B, K, V, dtype, F32, temps="mixed")
+        c["target"][:] = value
+        c["target"][:, :, 3] = -math.inf
+        check(c)
+        c["noise"] = None
+        got = check(c)
+        assert all(int(got.tokens[b, int(got.accepted[b])]) == 0 for b in range(B))
+        c["target"][:, :, :5] = -math.inf
+        assert check(c).tokens[:, 0].tolist() == [5] * B
+        c["noise"] = torch.ones((B, V), device=DEV)   # with equal noise the lowest too
+        c["temperatures"] = torch.full((B,), 0.7, device=DEV)
+        if K == 0:
+            assert check(c).tokens[:, 0].tolist() == [5] * B
+
+
+@pytest.mark.parametrize("B,V", [(1, 1), (3, 31), (700, 1000), (5, 4097), (300, 33000), (40, 131072), (2, 200003), (160, 20000)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_drawing_one_token(dtype, B, V):
+    check(verify_case(B + V, B, 0, V, dtype, None))
+    c = verify_case(B + V + 1, B, 0, V, dtype, None, temps=None, probs=True)
+    check(c)
+    check(c | {"noise": None})
+    # equals stand apart: the lowest of them, whatever the largest logit was when either came by
+    c = verify_case(B + V + 2, B, 0, V, dtype, None, temps=None)
+    if V > 30:
+        lo, hi = V // 5, V - 2
+        for at in (lo, hi):
+            c["target"][:, 0, at] = 12.25
+            c["noise"][:, at] = 2.0 ** -20
+        assert check(c).tokens[:, 0].tolist() == [lo] * B
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("V", [50, 9001])
 def test_verification_of_what_is_no_number(dtype, V):
-    B, K = 10, 2
-    for odd in (math.nan, math.inf):
+    B = 10
+    for K, odd in ((2, math.nan), (2, math.inf), (0, math.nan), (0, math.inf)):
         c = verify_case(V + 3, B, K, V, dtype, F32)
         c["target"][::2, 0, 11] = odd
         c["target"][::2, 0, V - 1] = odd
@@ -538,7 +576,7 @@ def test_verification_of_what_is_no_number(dtype, V):
         c["noise"] = None
         check(c)
         assert tq.tq_device_error() == 16
-    c = verify_case(V + 4, B, K, V, dtype, F32)
+    c = verify_case(V + 4, B, 2, V, dtype, F32)
     c["draft_probs"][0, 0, int(c["draft_tokens"][0, 0])] = math.nan   # not kept
     c["uniforms"][1, 0] = math.nan
     c["temperatures"][0:2] = 1.0

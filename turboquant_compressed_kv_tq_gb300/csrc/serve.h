@@ -41,7 +41,8 @@ struct VerifyArgs {
 cudaError_t launch_reserve(const BlocksArgs& a, cudaStream_t s);
 cudaError_t launch_release(const BlocksArgs& a, cudaStream_t s);
 cudaError_t launch_rope(const RopeArgs& a, int dtype, int sms, cudaStream_t s);
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
+cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_draw(const VerifyArgs& a, int sms, cudaStream_t s);   // no drafts: verification's form for single tokens
 #endif
 
 }  // namespace serve

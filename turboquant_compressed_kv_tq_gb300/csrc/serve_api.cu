@@ -133,7 +133,8 @@ tq_status tq_verify_drafts(const tq_drafts* drafts, int batch, int num_drafts, i
     auto off = [](const void* p, int t) { return !aligned(p, t == TQ_F32 ? 4 : 2); };
     if (off(drafts->target, drafts->target_dtype) || (drafts->draft && off(drafts->draft, drafts->draft_dtype))) return TQ_ERR_INVALID_ARG;
     VerifyArgs a{};
-    if (device_state(&a.err, nullptr) != TQ_OK) return TQ_ERR_CUDA;
+    int sms = 0;
+    if (device_state(&a.err, &sms) != TQ_OK) return TQ_ERR_CUDA;
     a.d = *drafts;
     a.batch = batch;
     a.K = num_drafts;
@@ -142,7 +143,7 @@ tq_status tq_verify_drafts(const tq_drafts* drafts, int batch, int num_drafts, i
     a.tokens = tokens;
     a.logprobs = logprobs;
     a.keep = keep_lens;
-    return launch_verify(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+    return launch_verify(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -9,115 +9,15 @@
 // (2 KB a piece) and goes through its pieces without waiting for other warps; what it saw of a row goes into every CTA of the cluster as soon
 // as the row is through. All find the same number of kept drafts then, and take the next token's row, again in parts.
 // One launch, no workspace, nothing that two calls share; no order of arrival changes a result.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include <algorithm>
 
-#include <cfloat>
-#include <climits>
-#include <type_traits>
-
-#include "kv8_device.cuh"
-#include "serve.h"
-#include "tc_ptx.cuh"
+#include "verify_device.cuh"
 
 namespace tq {
 namespace serve {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMostCtas = 8;
 constexpr int kUnits = 128, kStages = 2;   // a warp's pieces of a row: units of 16 bytes, and how many are on their way
-constexpr unsigned kAll = 0xffffffffu;
-constexpr float kLn2 = 0.69314718f;
-constexpr float kUsual = 8192.0f;   // exponents below which one product makes a weight
-
-__device__ __forceinline__ float number(float x) { return x; }
-__device__ __forceinline__ float number(__half x) { return __half2float(x); }
-__device__ __forceinline__ float number(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// The values of 16 bytes, in pairs.
-__device__ __forceinline__ void numbers(const uint4& u, float2* x, float) {
-    x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
-}
-__device__ __forceinline__ void numbers(const uint4& u, float2* x, __nv_bfloat16) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-}
-__device__ __forceinline__ void numbers(const uint4& u, float2* x, __half) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-}
-// 8 values at a 16-byte boundary.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float2 (&x)[4]) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) numbers(__ldg(reinterpret_cast<const uint4*>(p) + i), x + i * 8 / sizeof(T), T());
-}
-
-using kv8::ex2;
-using kv8::rcp;
-
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-
-// A logit as it counts: +inf the largest number, NaN -inf.
-__device__ __forceinline__ float logit(float x) { return x == x ? fminf(x, FLT_MAX) : -INFINITY; }
-
-// log2(e) / T as c + lo, both positive, so that what is masked (-inf) stays -inf in either product: log2(e) = 1.442695 (rounded down)
-// + 1.9259630e-8; c is below the quotient, lo what it leaves. To 2^-40.
-struct Scale {
-    float c, lo, near;   // near: c + lo in one number, off by 2^-25 of itself
-    __device__ __forceinline__ explicit Scale(float T) {
-        constexpr float hi = 0x1.715476p+0f, rest = 1.9259630e-8f;
-        const float r = rcp(T);
-        c = hi * r * (1.0f - 0x1p-21f);   // (the reciprocal is off by 2^-23, the products by 2^-24)
-        lo = (fmaf(-c, T, hi) + rest) * r;
-        near = c + lo;
-    }
-    __device__ __forceinline__ float weight(float d) const { return ex2(fmaf(d, c, d * lo)); }   // d <= 0
-    // The same with the exponent's rounding put back: to 2^-22. NaN of a masked value.
-    __device__ __forceinline__ float weight_near(float d) const {
-        const float t = d * c, w = ex2(t);
-        return fmaf(w, fmaf(d, lo, fmaf(d, c, -t)) * kLn2, w);
-    }
-    __device__ __forceinline__ float log(float d) const {   // d / T
-        const float t = d * c;
-        return fmaf(t, kLn2, fmaf(d, lo, fmaf(d, c, -t)) * kLn2 + t * -1.9046543e-9f);   // (ln 2 less kLn2)
-    }
-};
-
-// ------------------------------------------------------------------ the cluster
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-    return r;
-}
-// A shared-memory address of this CTA in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(tc::smem_addr(p)), "r"(rank));
-    return r;
-}
-// 16 or 8 bytes into another CTA's shared memory.
-__device__ __forceinline__ void send(uint32_t to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ void send(uint32_t to, uint32_t a, uint32_t b) {
-    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};\n" ::"r"(to), "r"(a), "r"(b) : "memory");
-}
-// The cluster's barrier: every thread of it arrives, and waits once for each arrival. What was written before an arrival is seen behind
-// the wait, in all CTAs. (The hardware's own: it ends as soon as all threads have arrived, or ended.)
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;\n" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory"); }
-
-// Values [i0, i1) of a row on their way into the L2 cache (one thread; whole units).
-template <typename T>
-__device__ __forceinline__ void ahead(const T* row, int i0, int i1) {
-    const uintptr_t a = (reinterpret_cast<uintptr_t>(row + i0) + 15) & ~static_cast<uintptr_t>(15), e = reinterpret_cast<uintptr_t>(row + i1) & ~static_cast<uintptr_t>(15);
-    if (i0 < i1 && a < e) tc::bulk_prefetch_l2(reinterpret_cast<const void*>(a), static_cast<unsigned>(e - a));
-}
 
 // A row as units of 16 bytes: the values before the first whole one, a CTA's units [u0, u1), the first value behind the last one.
 struct Units {
@@ -136,12 +36,6 @@ __device__ __forceinline__ Units units(const T* row, int V, int each, int rank) 
 }
 
 // What is known of a row, or a part of it: the largest value, the sum of weights relative to it, and where it is.
-// The largest of the warp's numbers (no NaN), as integers that are ordered as they are.
-__device__ __forceinline__ float warp_max(float x) {
-    const int i = __float_as_int(x), k = __reduce_max_sync(kAll, i ^ (i >> 31 & 0x7FFFFFFF));
-    return __int_as_float(k ^ (k >> 31 & 0x7FFFFFFF));
-}
-
 struct __align__(16) Seen {
     float top, sum;   // (nothing but masked values: sum 0)
     int at, piece;    // of a lane while it goes through a row: the piece (its first unit) in which the largest stood first, or -1
@@ -173,6 +67,7 @@ struct __align__(16) Seen {
 #pragma unroll
         for (int i = 1; i < N; ++i) t = fmaxf(fmaxf(t, x[i].x), x[i].y);
         rise(t, S, from_piece);
+        if (t == top && piece < 0) piece = from_piece;   // (a largest value of -FLT_MAX)
         const float m = top * S.near;
         if (fabsf(m) < kUsual) {
             const float2 c = both(S.near), off = both(-m);
@@ -220,20 +115,6 @@ struct __align__(16) Seen {
     }
 };
 __device__ __forceinline__ Seen nothing() { return Seen{-FLT_MAX, 0.0f, INT_MAX, -1}; }
-
-struct __align__(8) Best {
-    float v;   // a positive score
-    int i;
-    __device__ __forceinline__ void meet(float w, int j) {   // the larger, the lower index of equals
-        if (w > v || (w == v && j < i)) v = w, i = j;
-    }
-    __device__ __forceinline__ void join() {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) meet(__shfl_xor_sync(kAll, v, o), __shfl_xor_sync(kAll, i, o));
-    }
-};
-
-constexpr int kParts = kWarps * kMostCtas;   // the cluster's warps
 
 struct Shared {
     uint64_t bars[kWarps][kStages];
@@ -544,45 +425,35 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
 }
 
 template <typename T, typename Q>
-cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
-    // CTAs of a cluster: a piece for each warp, at most
+cudaError_t launch(const VerifyArgs& a, int sms, cudaStream_t s) {
+    // CTAs of a cluster: as many as fill the SMs once (four on each), and a piece for each warp, at most
     int log_ctas = 0;
-    while ((1 << log_ctas) < kMostCtas && (static_cast<int64_t>(kWarps * kUnits * 16 / sizeof(T)) << log_ctas) < a.V) ++log_ctas;
+    while ((1 << log_ctas) < kMostCtas && (static_cast<int64_t>(kWarps * kUnits * 16 / sizeof(T)) << log_ctas) < a.V &&
+           (static_cast<int64_t>(a.batch) << (log_ctas + 1)) <= 4 * sms)
+        ++log_ctas;
     const int smem = seen_bytes(a.K + 1) + kRing;
     if (smem > 40 * 1024) {   // (a launch's first 48 KB hold `Shared` too)
         static std::atomic<uint64_t> allowed{0};
         const cudaError_t e = kv8::allow_smem(verify_kernel<T, Q>, seen_bytes(65) + kRing, allowed);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.batch) << log_ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1 << log_ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<T, Q>, a, log_ctas);
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return e;
+    return launch_cluster(verify_kernel<T, Q>, a, log_ctas, smem, s);
 }
 
 template <typename T>
-cudaError_t launch_q(const VerifyArgs& a, cudaStream_t s) {
-    if (!a.d.draft || a.d.draft_dtype == TQ_F32) return launch<T, float>(a, s);
-    if (a.d.draft_dtype == TQ_F16) return launch<T, __half>(a, s);
-    return launch<T, __nv_bfloat16>(a, s);
+cudaError_t launch_q(const VerifyArgs& a, int sms, cudaStream_t s) {
+    if (!a.d.draft || a.d.draft_dtype == TQ_F32) return launch<T, float>(a, sms, s);
+    if (a.d.draft_dtype == TQ_F16) return launch<T, __half>(a, sms, s);
+    return launch<T, __nv_bfloat16>(a, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
-    if (a.d.target_dtype == TQ_F32) return launch_q<float>(a, s);
-    if (a.d.target_dtype == TQ_F16) return launch_q<__half>(a, s);
-    return launch_q<__nv_bfloat16>(a, s);
+cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t s) {
+    if (a.K == 0) return launch_draw(a, sms, s);
+    if (a.d.target_dtype == TQ_F32) return launch_q<float>(a, sms, s);
+    if (a.d.target_dtype == TQ_F16) return launch_q<__half>(a, sms, s);
+    return launch_q<__nv_bfloat16>(a, sms, s);
 }
 
 }  // namespace serve
