@@ -15,33 +15,53 @@ namespace tq {
 namespace serve {
 namespace {
 
-constexpr int kValues = 16;   // of a thread at a time
+constexpr int kResident = 3;                   // CTAs on an SM
+constexpr int kValues = 16;                    // of a thread at a time
+constexpr int kPiece = 32 * kValues, kStages = 2;   // values of a warp's piece, and how many pieces are on their way
 
 struct DrawShared {
+    uint64_t bars[kWarps][kStages];
     float2 seen[2][kParts];   // (largest, sum) of the cluster's warps, of either round
     Best best[kParts];
 };
+template <typename T>
+constexpr int kStageBytes = kPiece * (sizeof(T) + 4);   // logits, then noise
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) draw_kernel(const __grid_constant__ VerifyArgs A, int log_ctas) {
+__global__ void __launch_bounds__(kThreads, kResident) draw_kernel(const __grid_constant__ VerifyArgs A, int log_ctas) {
+    constexpr int kGroup = 16 / sizeof(T);   // values of a thread that lie together
     __shared__ __align__(16) DrawShared S;
+    extern __shared__ __align__(128) unsigned char s_ring[];
     const int ctas = 1 << log_ctas, rank = cluster_rank();
     const int b = blockIdx.x >> log_ctas, tid = threadIdx.x, lane = tid % 32, warp = tid / 32, V = A.V;
     const tq_drafts& D = A.d;
     const float asked_T = !D.noise ? 0.0f : D.temperatures ? D.temperatures[b] : 1.0f;
+    if (lane < kStages) tc::mbar_init(&S.bars[warp][lane], 1);
+    tc::mbar_fence_init();
+    __syncwarp();
     cluster_arrive();   // (waited for before the first word to another CTA)
     const T* row = static_cast<const T*>(D.target) + b * D.target_stride_batch;
     const float* noise = D.noise ? D.noise + b * D.noise_stride : nullptr;
-    const int share = (V + ctas - 1) >> log_ctas, i_begin = min(V, rank * share), i_end = min(V, i_begin + share);
-    if (tid == 0) ahead(row, i_begin, i_end);
     const bool probs = D.target_probs != 0, greedy = !(asked_T > 0.0f);
-    if (tid == 32 && !greedy) ahead(noise, i_begin, i_end);
     const Scale scale(greedy ? 1.0f : fminf(fmaxf(asked_T, 0x1p-120f), 0x1p100f));
-    // rows that lie alike in chunks of 8, and what lies outside those (the first CTA's) one value at a time; others all so
+    // A CTA's values: whole chunks of 8 through its warps' rings, where logits and noise lie alike, and what lies outside those (the
+    // first CTA's) one value at a time; else all so.
     const int head = min(V, static_cast<int>((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16 / sizeof(T))), chunks = (V - head) / 8;
     const bool alike = greedy || reinterpret_cast<uintptr_t>(noise + head) % 16 == 0;
-    const int per = (chunks + ctas - 1) >> log_ctas;
-    auto index = [](int i0, int step, int i) { return i0 + i / 8 * 8 * kThreads + i % 8 * step; };
+    const int per = alike ? ((chunks + ctas - 1) >> log_ctas) * 8 : (V + ctas - 1) >> log_ctas;
+    const int main_end = alike ? head + chunks * 8 : V, main_begin = min(main_end, (alike ? head : 0) + rank * per), my_end = min(main_end, main_begin + per);
+    unsigned char* const ring = s_ring + warp * kStages * kStageBytes<T>;
+    int asked = 0;   // of this round, by lane 0: the first value of the next piece
+    auto ask = [&](int st) {
+        const int at = asked, n = min(kPiece, my_end - at);
+        if (n <= 0) return;
+        asked = at + kWarps * kPiece;
+        uint64_t* bar = &S.bars[warp][st];
+        tc::mbar_expect_tx(bar, n * (greedy ? static_cast<int>(sizeof(T)) : static_cast<int>(sizeof(T)) + 4));
+        tc::bulk_g2s(ring + st * kStageBytes<T>, row + at, n * static_cast<int>(sizeof(T)), bar);
+        if (!greedy) tc::bulk_g2s(ring + st * kStageBytes<T> + kPiece * sizeof(T), noise + at, n * 4, bar);
+    };
+    int st = 0, phase = 0;
 
     float top, sum;
     Best best;
@@ -52,34 +72,52 @@ __global__ void __launch_bounds__(kThreads, 3) draw_kernel(const __grid_constant
         best = Best{0.0f, INT_MAX};       // relative to `top`
         float best_x = 0.0f, best_e = 1.0f;
         int piece = -1, piece_step = 1;   // where the largest stood first
+        if (alike && lane == 0) {
+            asked = main_begin + warp * kPiece;
+#pragma unroll 1
+            for (int i = 0; i < kStages; ++i) ask((st + i) % kStages);
+        }
 #pragma unroll 1
         for (int job = alike && rank == 0 ? 0 : 1; job < (alike && rank == 0 ? 3 : 2); ++job) {   // (in the order of their values)
-            const bool eight = alike && job == 1;
-            const int step = eight ? 1 : kThreads;   // between values of a chunk
-            const int begin = !alike ? i_begin : job == 0 ? 0 : job == 1 ? head + rank * per * 8 : head + chunks * 8;
-            const int end = !alike ? i_end : job == 0 ? head : job == 1 ? head + min(chunks, (rank + 1) * per) * 8 : V;
+            const bool piped = alike && job == 1;
+            const int begin = job == 0 ? 0 : job == 1 ? main_begin : main_end, end = job == 0 ? head : job == 1 ? my_end : V;
+            const int step = piped ? 1 : kThreads, far = piped ? 32 * kGroup : kGroup * kThreads;   // between values of a group, and groups
 #pragma unroll 1
-            for (int i0 = begin + (eight ? tid * 8 : tid); i0 < end; i0 += kValues * kThreads) {
+            for (int i0 = begin + (piped ? warp * kPiece : tid); i0 < end; i0 += piped ? kWarps * kPiece : kValues * kThreads) {
                 float2 x[kValues / 2], e[kValues / 2];
                 const float none = probs ? 0.0f : -INFINITY;
-                if (eight) {
+                const int mine = piped ? i0 + lane * kGroup : i0;   // the thread's first
+                if (piped) {
+                    if (!tc::mbar_wait(&S.bars[warp][st], phase)) {   // once more, so that no copy is on its way when the kernel ends
+                        if (lane == 0) atomicOr(A.err, TQ_DEVERR_TIMEOUT);
+                        tc::mbar_wait(&S.bars[warp][st], phase);
+                    }
+                    const uint4* xs = reinterpret_cast<const uint4*>(ring + st * kStageBytes<T>);
+                    const float4* es = reinterpret_cast<const float4*>(ring + st * kStageBytes<T> + kPiece * sizeof(T));
 #pragma unroll
-                    for (int c = 0; c < kValues / 8; ++c) {
-                        const int at = i0 + c * 8 * kThreads;
-                        float2 (&xc)[4] = reinterpret_cast<float2 (&)[4]>(x[4 * c]), (&ec)[4] = reinterpret_cast<float2 (&)[4]>(e[4 * c]);
-                        if (c == 0 || at < end) {
-                            load8(row + at, xc);
-                            if (!greedy) load8(noise + at, ec);
+                    for (int g = 0; g < kValues / kGroup; ++g) {
+                        if (mine + g * far < end) {
+                            numbers(xs[g * 32 + lane], x + g * kGroup / 2, T());
+                            if (!greedy) {
+#pragma unroll
+                                for (int i = 0; i < kGroup / 4; ++i) {
+                                    const float4 v = es[(g * 32 + lane) * (kGroup / 4) + i];
+                                    e[g * kGroup / 2 + 2 * i] = make_float2(v.x, v.y), e[g * kGroup / 2 + 2 * i + 1] = make_float2(v.z, v.w);
+                                }
+                            }
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) xc[i] = both(none), ec[i] = both(1.0f);
+                            for (int i = 0; i < kGroup / 2; ++i) x[g * kGroup / 2 + i] = both(none), e[g * kGroup / 2 + i] = both(1.0f);
                         }
                     }
+                    __syncwarp();
+                    if (lane == 0) ask(st);
+                    if (++st == kStages) st = 0, phase ^= 1;
                 } else {
 #pragma unroll
                     for (int i = 0; i < kValues; ++i) {
                         float &xi = i % 2 ? x[i / 2].y : x[i / 2].x, &ei = i % 2 ? e[i / 2].y : e[i / 2].x;
-                        const int at = index(i0, step, i);
+                        const int at = i0 + i * kThreads;
                         xi = none, ei = 1.0f;
                         if (at < end) {
                             xi = number(row[at]);
@@ -87,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 3) draw_kernel(const __grid_constant
                         }
                     }
                 }
+                auto index = [&](int i) { return mine + i / kGroup * far + i % kGroup * step; };
                 if (clean) {
                     bool odd = false;
 #pragma unroll
@@ -104,9 +143,9 @@ __global__ void __launch_bounds__(kThreads, 3) draw_kernel(const __grid_constant
                     sum *= f;
                     best.v = probs ? best.v : best.v * f;
                     top = t;
-                    piece = i0, piece_step = step;
+                    piece = mine, piece_step = step;
                 } else if (t == top && piece < 0) {   // (-FLT_MAX)
-                    piece = i0, piece_step = step;
+                    piece = mine, piece_step = step;
                 }
                 // weights as in Seen::take: relative to m, and a factor `exact` from m to the exact top
                 const float m = top * scale.near;
@@ -148,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 3) draw_kernel(const __grid_constant
 #pragma unroll
                     for (int i = kValues - 1; i >= 0; --i)
                         if ((i % 2 ? w[i / 2].y : w[i / 2].x) == here)
-                            at = index(i0, step, i), at_x = i % 2 ? x[i / 2].y : x[i / 2].x, at_e = i % 2 ? e[i / 2].y : e[i / 2].x;
+                            at = index(i), at_x = i % 2 ? x[i / 2].y : x[i / 2].x, at_e = i % 2 ? e[i / 2].y : e[i / 2].x;
                     // scores nearer to each other than what a change of `top` rounds: once more, against one top
                     const float was = (probs ? best_x : weight(best_x)) * rcp(fmaxf(best_e, 0x1p-100f));
                     if (best.i == INT_MAX || here > was || (here == was && at < best.i)) {
@@ -178,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 3) draw_kernel(const __grid_constant
             if (top == t && piece >= 0 && (probs ? t > 0.0f : s > 0.0f)) {
 #pragma unroll 1
                 for (int i = 0; i < kValues; ++i) {
-                    const int at = index(piece, piece_step, i);
+                    const int at = piece + i / kGroup * (piece_step == 1 ? 32 * kGroup : kGroup * kThreads) + i % kGroup * piece_step;
                     // (behind a share's end lies another's, or the row's: what is as large there is no lower)
                     if (at < V && (clean ? logit(number(row[at])) : number(row[at])) == t) {
                         best = Best{1.0f, at};
@@ -217,8 +256,11 @@ __global__ void __launch_bounds__(kThreads, 3) draw_kernel(const __grid_constant
 template <typename T>
 cudaError_t launch(const VerifyArgs& a, int sms, cudaStream_t s) {
     int log_ctas = 0;
-    while ((1 << log_ctas) < kMostCtas && (kValues * kThreads << log_ctas) < a.V && (static_cast<int64_t>(a.batch) << (log_ctas + 1)) <= 3 * sms) ++log_ctas;
-    return launch_cluster(draw_kernel<T>, a, log_ctas, 0, s);
+    while ((1 << log_ctas) < kMostCtas && (kWarps * kPiece << log_ctas) < a.V && (static_cast<int64_t>(a.batch) << (log_ctas + 1)) <= kResident * sms) ++log_ctas;
+    constexpr int smem = kWarps * kStages * kStageBytes<T>;
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = kv8::allow_smem(draw_kernel<T>, smem, allowed);
+    return e != cudaSuccess ? e : launch_cluster(draw_kernel<T>, a, log_ctas, smem, s);
 }
 
 }  // namespace
