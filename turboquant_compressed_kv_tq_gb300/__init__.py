@@ -7,6 +7,7 @@ library's CUDA kernels. PyTorch provides device memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import struct
 from typing import NamedTuple, Optional
@@ -512,6 +513,7 @@ class _KV8:
 
     def __init__(self):
         torch = _torch()
+        self.empty, self.zeros = torch.empty, torch.zeros
         self.codes = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
         self.i32, self.f32 = torch.int32, torch.float32
         self.device = torch._C._cuda_getDevice                # of torch.cuda.current_device
@@ -781,6 +783,7 @@ class KV8Cache:
 
 # ----------------------------------------------------------------- around the caches' calls
 
+_here = contextlib.nullcontext()   # the current stream, at once
 _pack_drafts = struct.Struct("@PqqPqqPPPPPqPiii4x").pack   # tq_drafts
 
 
@@ -813,8 +816,8 @@ def tq_rope_apply(rope: Rope, q, k=None, out=None, k_out=None, starts=None, posi
     elif k_out is not None:
         raise ValueError("k_out without k")
     if out is None or (k is not None and k_out is None):
-        make = _torch().empty if new_lens is None else _torch().zeros
-        with _on(stream):
+        make = t.empty if new_lens is None else t.zeros
+        with _on(stream) if stream is not None else _here:
             if out is None:
                 out = make(q.shape, dtype=dtype, device=q.device)
             if k is not None and k_out is None:
@@ -982,11 +985,10 @@ def tq_verify_drafts(target, draft_tokens=None, draft_probs=None, uniforms=None,
             raise TypeError(f"noise must be float32, not {noise.dtype}")
     per, each, full = (batch,), (batch, drafts), (batch, rows)
     if out is None:
-        torch = _torch()
-        with _on(stream):
-            out = Verified(torch.empty(batch, dtype=i32, device=target.device), torch.empty(full, dtype=i32, device=target.device),
-                           torch.empty(batch, dtype=i32, device=target.device) if seq_lens is not None else None,
-                           torch.empty(full, dtype=f32, device=target.device))
+        make, on = t.empty, target.device
+        with _on(stream) if stream is not None else _here:
+            out = Verified(make(per, dtype=i32, device=on), make(full, dtype=i32, device=on),
+                           make(per, dtype=i32, device=on) if seq_lens is not None else None, make(full, dtype=f32, device=on))
     elif (seq_lens is None) != (out.keep_lens is None):
         raise ValueError("keep_lens go with seq_lens")
     packed = _pack_drafts(
