@@ -24,6 +24,7 @@ struct RopeArgs {
     int heads[2];
     kv8::Rope rope;            // rot 0: nothing turns
     int back;                  // the opposite angle
+    int stream;                // outputs past the L2 cache (set by the launch)
     int batch, n, D;
     const int32_t *starts, *news;
     unsigned* err;
