@@ -143,51 +143,52 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     const bool probs = D.target_probs != 0;
     const T* target = static_cast<const T*>(D.target) + b * D.target_stride_batch;
     const Q* draft = static_cast<const Q*>(D.draft) + (D.draft ? b * D.draft_stride_batch : 0);
-    const int each = (V / kIn + ctas - 1) >> log_ctas, pieces = (each + kUnits - 1) / kUnits;
-    // a row's pieces go to the warps in turn, and on with the next row's
-    auto first_piece = [&](int i) { return ((warp - i * pieces) & (kWarps - 1)) * kUnits; };
+    const int each = (V / kIn + ctas - 1) >> log_ctas, pieces = max(1, (each + kUnits - 1) / kUnits);   // of this CTA's part of a row
     if (lane < kStages) tc::mbar_init(&S.bars[warp][lane], 1);
     if (lane == 0) S.odd[warp] = 0;
     if (tid == 0) S.kept = K;
     tc::mbar_fence_init();
     __syncwarp();
     cluster_arrive();   // (waited for before the first word to another CTA)
-    // ---- a warp's pieces of the rows, one row behind the other (lane 0 asks for them, each as another has been taken)
-    int last_row = 0, ask_row = 0, ask_u = 0, ask_end = 0, ask_st = 0, asked = 0;   // the first row is needed whatever k is
-    const T* ask_from = target;   // of unit 0
-    auto start_row = [&]() {
-        const T* r = target + ask_row * D.target_stride_row;
-        const Units part = units(r, V, each, rank);
-        ask_from = r + part.head;
-        ask_u = part.u0 + first_piece(ask_row);
-        ask_end = part.u1;
-    };
-    auto ask = [&]() {
-        while (ask_u >= ask_end) {
-            if (ask_row >= last_row) return;
-            ++ask_row;
-            start_row();
-        }
-        const unsigned bytes = min(kUnits, ask_end - ask_u) * 16;
-        uint64_t* bar = &S.bars[warp][ask_st];
-        tc::mbar_expect_tx(bar, bytes);
-        tc::bulk_g2s(ring + ask_st * kUnits, ask_from + static_cast<int64_t>(ask_u) * kIn, bytes, bar);
-        ask_u += kWarps * kUnits;
-        ask_st = ask_st + 1 < kStages ? ask_st + 1 : 0;
-        ++asked;
-    };
-    if (lane == 0 && !probs) {
-        start_row();
-#pragma unroll 1
-        for (int i = 0; i < kStages; ++i) ask();
-    }
     if (k < 0 || k > K) {
         if (rank == 0 && tid == 0) atomicOr(A.err, TQ_DEVERR_SEQLEN);
         k = min(max(k, 0), K);
     }
+    const bool greedy = !(asked_T > 0.0f), stats = !probs || greedy;   // (probabilities are as they are)
+    // ---- all rows' pieces, one row behind the other, are dealt to the warps in eight runs, so that a warp has few rows (lane 0 asks for
+    // them, each as another has been taken)
+    const int all = stats ? (k + 1) * pieces : 0;
+    auto run = [&](int w) { return all * w / kWarps; };   // where warp w's begins
+    const int g0 = run(warp), g1 = run(warp + 1);
+    int ask_g = g0, ask_row = g0 / pieces, ask_piece = g0 % pieces, ask_u0 = 0, ask_end = 0, ask_st = 0;
+    const T* ask_from = nullptr;   // of unit 0
+    auto ask = [&]() {
+        while (ask_g < g1) {
+            if (ask_piece == 0 || !ask_from) {
+                const T* r = target + ask_row * D.target_stride_row;
+                const Units part = units(r, V, each, rank);
+                ask_from = r + part.head;
+                ask_u0 = part.u0;
+                ask_end = part.u1;
+            }
+            const int u = ask_u0 + ask_piece * kUnits;
+            ++ask_g;
+            if (++ask_piece == pieces) ask_piece = 0, ++ask_row;
+            if (u >= ask_end) continue;   // (rows that begin elsewhere may have a unit less)
+            const unsigned bytes = min(kUnits, ask_end - u) * 16;
+            uint64_t* bar = &S.bars[warp][ask_st];
+            tc::mbar_expect_tx(bar, bytes);
+            tc::bulk_g2s(ring + ask_st * kUnits, ask_from + static_cast<int64_t>(u) * kIn, bytes, bar);
+            ask_st = ask_st + 1 < kStages ? ask_st + 1 : 0;
+            return;
+        }
+    };
+    if (lane == 0) {
+#pragma unroll 1
+        for (int i = 0; i < kStages; ++i) ask();
+    }
     // draft i is lane i / 8 of warp i % 8's
     const int mine = warp + kWarps * lane;
-    const bool greedy = !(asked_T > 0.0f), stats = !probs || greedy;   // (probabilities are as they are)
     int d = -1;
     float x_d = 0.0f, q_d = 1.0f, u_d = 0.0f;
     if (lane < 8 && mine < k) {
@@ -196,26 +197,20 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     }
     const Scale scale(greedy ? 1.0f : fminf(fmaxf(asked_T, 0x1p-120f), 0x1p100f));
     const int share = (V + ctas - 1) >> log_ctas, i_begin = min(V, rank * share), i_end = min(V, i_begin + share);
-    if (stats) {
-        last_row = k;
-        if (lane == 0) {
-            if (probs) start_row();
-#pragma unroll 1
-            while (asked < kStages && (ask_u < ask_end || ask_row < last_row)) ask();
-        }
-    }
     if (tid == 32 && !greedy) ahead(D.noise + b * D.noise_stride, i_begin, i_end);
     // ---- each row's largest value, where it is, and its sum
-    if (stats) {
+    bool begun = false;   // every CTA of the cluster has
+    if (g0 < g1) {
         int st = 0, phase = 0;
 #pragma unroll 1
-        for (int i = 0; i <= k; ++i) {
+        for (int i = g0 / pieces; i * pieces < g1; ++i) {
             const T* row = target + i * D.target_stride_row;
             const Units part = units(row, V, each, rank);
+            const int first = part.u0 + max(0, g0 - i * pieces) * kUnits, last = min(part.u1, part.u0 + (g1 - i * pieces) * kUnits);   // of this warp
             // what lies outside whole units: before them the first CTA's, behind them the last one's
             int edge = -1;
             float x_edge = 0.0f;
-            if (warp == (i & (kWarps - 1))) {
+            if (g0 <= i * pieces) {   // (the warp that has its first piece)
                 if (rank == 0 && lane < part.head) edge = lane;
                 if (rank == ctas - 1 && lane >= 16 && part.tail + lane - 16 < V) edge = part.tail + lane - 16;
                 if (edge >= 0) x_edge = number(row[edge]);
@@ -223,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             Seen s = nothing();
             auto where = [&](int u, int e) { return part.head + (u + e / kIn * 32 + lane) * kIn + e % kIn; };
 #pragma unroll 1
-            for (int u = part.u0 + first_piece(i); u < part.u1; u += kWarps * kUnits) {
+            for (int u = first; u < last; u += kUnits) {
                 if (!tc::mbar_wait(&S.bars[warp][st], phase)) {   // once more, so that no copy is on its way when the kernel ends
                     if (lane == 0) atomicOr(A.err, TQ_DEVERR_TIMEOUT);
                     tc::mbar_wait(&S.bars[warp][st], phase);
@@ -247,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
                 atomicOr(A.err, TQ_DEVERR_NONFINITE);
                 s = nothing();
 #pragma unroll 1
-                for (int u = part.u0 + first_piece(i); u < part.u1; u += kWarps * kUnits)
+                for (int u = first; u < last; u += kUnits)
 #pragma unroll 1
                     for (int e = 0; e < kPer * kIn; ++e)
                         if (u + e / kIn * 32 + lane < part.u1) s.take(logit(number(row[where(u, e)])), scale, where(u, e));
@@ -257,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
                 if (greedy) s.find(row + part.head, part.u1, part.head);
                 s.join(scale);
             }
-            if (i == 0) cluster_wait();
+            if (!begun) cluster_wait();
+            begun = true;
             if (lane < ctas)
                 send(remote(&seen_part[(i * kMostCtas + rank) * kWarps + warp], lane), __float_as_uint(s.top), __float_as_uint(s.sum), static_cast<uint32_t>(s.at), 0u);
         }
@@ -266,16 +262,24 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
         x_d = number(target[mine * D.target_stride_row + d]);
         if (D.draft && !greedy) q_d = number(draft[mine * D.draft_stride_row + d]);
     }
-    if (stats) cluster_arrive();
-    cluster_wait();
+    if (!begun) cluster_wait();
+    if (stats) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
     // ---- how many drafts stand: row i is warp i % 8's
 #pragma unroll 1
     for (int i = warp; i <= k; i += kWarps) {
         Seen s = nothing();
         if (stats) {
+            // (of each CTA the warps that have pieces of the row)
             const Seen* p = seen_part + i * kParts;
-            if (lane < ctas * kWarps) s = p[lane];
-            Seen more = lane + 32 < ctas * kWarps ? p[lane + 32] : nothing();
+            const int w = lane % kWarps;
+            const bool theirs = max(run(w), i * pieces) < min(run(w + 1), (i + 1) * pieces);
+            if (theirs && lane < ctas * kWarps) s = p[lane];
+            Seen more = theirs && lane + 32 < ctas * kWarps ? p[lane + 32] : nothing();
             if (more.top > s.top) { const Seen x = s; s = more; more = x; }
             s.sum += more.sum * scale.weight(more.top - s.top);
             if (more.top == s.top) s.at = min(s.at, more.at);
