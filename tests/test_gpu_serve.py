@@ -371,6 +371,31 @@ def test_blocks_of_no_sequences_or_maps():
             call()
 
 
+def test_blocks_of_far_rows():
+    # entries more than 2^31 behind the table's start, positions near 2^31, slots beyond it
+    width, BT, rows = (1 << 27) - 1, 16, 17
+    table = torch.full((rows, width), -1, dtype=torch.int32, device=DEV)
+    near_end = width * BT - 5
+    table[rows - 1, near_end // BT - 1] = 3
+    bt = tq.BlockTable.wrap(table, i32([(1 << 30) + 7, 9, 11]), i32([0]), BT, (1 << 30) + 9)
+    lens = torch.zeros(rows, dtype=torch.int32, device=DEV)
+    lens[rows - 1] = near_end - near_end % BT - 2
+    news = torch.zeros(rows, dtype=torch.int32, device=DEV)
+    news[rows - 1] = 20
+    places = tq.Places(rows, 21)
+    bt.reserve(lens, news, 20, places)
+    assert places.granted.tolist() == [0] * (rows - 1) + [18]          # what the row has left
+    at = int(lens[rows - 1])
+    id = (1 << 30) + 7
+    want = [(3 * BT + p % BT) if p // BT == near_end // BT - 1 else id * BT + p % BT for p in range(at, at + 18)]
+    assert places.slots.tolist() == want + [-1] * 3 and places.positions.tolist()[:18] == list(range(at, at + 18))
+    assert tq.tq_device_error() == tq.TQ_DEVERR_CAPACITY
+    lens[rows - 1] = at - BT + 2
+    bt.release(torch.where(torch.arange(rows, device=DEV) == rows - 1, lens, 0).to(torch.int32))
+    errors(["capacity"])   # block 3 was not taken from the list
+    assert bt.n_used.item() == 0 and bt.free_blocks.tolist() == [id, 9, 11] and int(table.max()) == -1
+
+
 def test_blocks_captured_and_replayed():
     B, width, BT = 5, 40, 16
     bt = tq.BlockTable(B, width, B * width, BT)
@@ -689,14 +714,59 @@ def test_verification_captured_and_on_two_streams():
             assert all(torch.equal(a, b) for a, b in zip(x, w))
 
 
-def test_verification_of_far_rows():
-    B, K, V = 2, 1, 999
+@pytest.mark.parametrize("K", [0, 1])
+def test_verification_of_far_rows(K):
+    B, V = 2, 999
     c = verify_case(41, B, K, V, BF16, F32)
     hold = torch.zeros((1 << 31) + 4 * V, dtype=BF16, device=DEV)
     x = torch.as_strided(hold, (B, K + 1, V), (1 << 31, V, 1))
     x.copy_(c["target"])
     c["target"] = x
     check(c)
+
+
+def test_verification_lengths_in_place():
+    c = verify_case(61, 6, 2, 700)
+    want = tq.tq_verify_drafts(**c)
+    lens = c["seq_lens"].clone()
+    out = tq.Verified(*(torch.zeros_like(x) for x in want))._replace(keep_lens=lens)
+    tq.tq_verify_drafts(**(c | {"seq_lens": lens}), out=out)
+    for x, y in zip(out, want):
+        assert torch.equal(x, y)
+    quiet = tq.tq_verify_drafts(**(c | {"seq_lens": None}), out=out._replace(keep_lens=None, logprobs=None))
+    assert quiet.keep_lens is None and torch.equal(quiet.tokens, want.tokens)
+
+
+FIRST_IN_A_GRAPH = """
+import torch, turboquant_compressed_kv_tq_gb300 as tq
+f = dict(device="cuda")
+bt, lens, places = tq.BlockTable(3, 4, 12, 16), torch.zeros(3, dtype=torch.int32, **f), tq.Places(3, 6)
+rope, q = tq.Rope.of_base(64), torch.randn(3, 4, 2, 64, **f)
+x, d, u, e = torch.randn(3, 9, 5000, **f), torch.zeros(3, 8, dtype=torch.int32, **f), torch.rand(3, 8, **f), torch.rand(3, 5000, **f) + 0.1
+def calls():
+    bt.reserve(lens, None, 2, places)
+    bt.release(lens)
+    return rope.apply(q, starts=lens)[0], tq.tq_verify_drafts(x, d, None, u, e), tq.tq_verify_drafts(x[:, :1], noise=e), tq.tq_verify_drafts(x[:, :1])
+s = torch.cuda.Stream()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=s):
+    got = calls()
+g.replay()
+torch.cuda.synchronize()
+want = calls()
+assert torch.equal(got[0], want[0]) and all(torch.equal(a.tokens, b.tokens) for a, b in zip(got[1:], want[1:])) and tq.tq_device_error() == 0
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_in_a_graph():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_A_GRAPH], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", (r.stdout[-500:], r.stderr[-2000:])
 
 
 def test_verification_refusals():
