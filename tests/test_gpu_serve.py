@@ -313,7 +313,7 @@ def check_release(bt, table, free, used, keeps, BT, num_blocks):
 @pytest.mark.parametrize("B,width,BT,n_new,most_len,spare", [
     (1, 1, 16, 1, 0, 0), (1, 4, 16, 1, 63, 5), (7, 9, 16, 5, 100, 0), (33, 20, 32, 100, 500, 3), (300, 8, 64, 9, 400, 11), (1025, 3, 16, 7, 30, 0),
     (2500, 6, 16, 40, 30, 100), (3, 700, 16, 11000, 50, 9), (64, 130, 16, 2000, 17, -40), (7, 9, 16, 5, 100, -2), (1500, 4, 32, 30, 90, -300), (5, 3, 256, 600, 100, 0),
-    (40, 10, 16, 0, 100, 4), (4097, 3, 16, 7, 30, 0), (9, 4, 16, 900, 60, -3), (20, 40, 16, 130, 500, -4)])
+    (40, 10, 16, 0, 100, 4), (4097, 3, 16, 7, 30, 0), (9001, 3, 16, 2, 30, 50), (20000, 8, 16, 100, 20, -5000), (33, 70, 16, 1000, 90, 20), (9, 4, 16, 900, 60, -3), (20, 40, 16, 130, 500, -4)])
 @pytest.mark.parametrize("ragged", [True, False])
 def test_blocks_reserve_and_release(B, width, BT, n_new, most_len, spare, ragged):
     table, free, lens, news, total = blocks_case(B * 31 + width, B, width, BT, n_new, min(most_len, width * BT), spare, ragged, missing=spare > 5)
@@ -712,6 +712,27 @@ def test_verification_captured_and_on_two_streams():
     for round_ in got:
         for x, w in zip(round_, want):
             assert all(torch.equal(a, b) for a, b in zip(x, w))
+
+
+@pytest.mark.parametrize("K", [0, 2])
+@pytest.mark.parametrize("dtype,V", [(BF16, 33003), (F32, 33003), (F16, 65536)])
+def test_verification_of_infinities_between_ctas(dtype, V, K):
+    # two tokens of +inf are equally likely, wherever one of them lies: the smaller noise decides
+    B = 48
+    c = verify_case(V + K, B, K, V, dtype, None, temps=None)
+    c["draft_tokens"] = None if K == 0 else torch.zeros((B, K), dtype=torch.int32, device=DEV)
+    at = torch.arange(B, device=DEV)
+    ends = [(i * V) // 8 + j for i in (1, 2, 3, 4, 5, 6) for j in range(-4, 4)]   # where the shares of eight CTAs may end
+    places = torch.tensor([ends[b % len(ends)] for b in range(B)], device=DEV)
+    c["target"][at, :, places] = math.inf
+    c["target"][:, :, 77] = math.inf
+    c["noise"][:, 77], c["noise"][at, places] = 0.5, 0.75
+    got = check(c)
+    errors_word = tq.tq_device_error()
+    assert errors_word == tq.TQ_DEVERR_NONFINITE and not got.accepted.any() and bool((got.tokens[:, 0] == 77).all())
+    c["noise"][:, 77] = 1.0
+    got = check(c)
+    assert tq.tq_device_error() == tq.TQ_DEVERR_NONFINITE and torch.equal(got.tokens[:, 0].long(), places)
 
 
 @pytest.mark.parametrize("K", [0, 1])

@@ -6,7 +6,10 @@
 // against the row's largest at the end, so that equals are equal wherever in the row they stand.
 //
 // A cluster of CTAs has a sequence, as many as fill the SMs once: a cluster's last steps (two barriers, its last threads' loads) are as
-// long for a short share of a row as for a long one.
+// long for a short share of a row as for a long one. Each warp has a ring of bulk copies of its own, as in verify.cu.
+//
+// Measured: 200 rows of 131,072, f32, a third of them greedy: 35 us (5.9 TB/s of what is read); 42 with the values loaded to registers, 47 in two
+// passes. Three CTAs an SM and two pieces a ring: two and three 41 us, four and one 38.
 #include <algorithm>
 
 #include "verify_device.cuh"

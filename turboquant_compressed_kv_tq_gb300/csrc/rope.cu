@@ -8,7 +8,11 @@
 //
 // A thread has two chunks of 8 coordinates that hold whole pairs; the lanes of a warp lie beside each other
 // in a row, then in neighbouring tokens, so that a warp reads and writes runs of 64 bytes at least whatever the order of the axes.
-// Chunks of several heads are on their way at once, the first ones while the angles are computed.
+// The first heads' chunks are on their way while the angles are computed.
+//
+// Measured: 8192 tokens, 64 + 8 heads of 128, bf16, out of a fused projection into contiguous heads: 51 us (5.9 TB/s); 6 x 1999 tokens, 12
+// heads of 256, f32: 47 us (6.2). Two heads ahead (one in fp32) at five CTAs an SM: with four and three CTAs 57 and 51, with one
+// and six 54 and 55.
 #include <algorithm>
 #include <type_traits>
 

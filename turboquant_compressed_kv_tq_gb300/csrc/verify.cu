@@ -9,6 +9,9 @@
 // (2 KB a piece) and goes through its pieces without waiting for other warps; what it saw of a row goes into every CTA of the cluster as soon
 // as the row is through. All find the same number of kept drafts then, and take the next token's row, again in parts.
 // One launch, no workspace, nothing that two calls share; no order of arrival changes a result.
+//
+// Measured: 64 sequences of 4 drafts, 131,072 tokens, bf16: 37.5 us (151 MB, 4.0 TB/s; the largest values alone, 84 MB, 24 us); one
+// sequence of a draft, 32,000 tokens: 8.4 us. Pieces of 2 KB, two on their way: with three or four, three CTAs fit an SM, and 43 to 56 us.
 #include <algorithm>
 
 #include "verify_device.cuh"
@@ -38,7 +41,9 @@ __device__ __forceinline__ Units units(const T* row, int V, int each, int rank) 
 // What is known of a row, or a part of it: the largest value, the sum of weights relative to it, and where it is.
 struct __align__(16) Seen {
     float top, sum;   // (nothing but masked values: sum 0)
-    int at, piece;    // of a lane while it goes through a row: the piece (its first unit) in which the largest stood first, or -1
+    int at;
+    int piece;        // of a lane while it goes through a row: the piece (its first unit) in which the largest stood first, or -1;
+                      // of what is joined: 1 where a value is +inf or NaN
 
     __device__ __forceinline__ void rise(float t, const Scale& S, int from_piece) {
         if (t > top) {
@@ -119,7 +124,6 @@ __device__ __forceinline__ Seen nothing() { return Seen{-FLT_MAX, 0.0f, INT_MAX,
 struct Shared {
     uint64_t bars[kWarps][kStages];
     Best best[2][kParts];      // written by every warp of the cluster
-    int odd[kWarps];           // a value of the warp's part of some row is +inf or NaN
     int kept;
 };
 
@@ -145,7 +149,6 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     const Q* draft = static_cast<const Q*>(D.draft) + (D.draft ? b * D.draft_stride_batch : 0);
     const int each = (V / kIn + ctas - 1) >> log_ctas, pieces = max(1, (each + kUnits - 1) / kUnits);   // of this CTA's part of a row
     if (lane < kStages) tc::mbar_init(&S.bars[warp][lane], 1);
-    if (lane == 0) S.odd[warp] = 0;
     if (tid == 0) S.kept = K;
     tc::mbar_fence_init();
     __syncwarp();
@@ -237,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
                 if (++st == kStages) st = 0, phase ^= 1;
             }
             if (edge >= 0) s.take(x_edge, scale, edge);
+            const bool odd = __any_sync(kAll, !(s.sum < INFINITY));
             if (!(s.sum < INFINITY)) {   // a NaN, or +inf (inf - inf): once more, as they count
-                S.odd[warp] = 1;
                 atomicOr(A.err, TQ_DEVERR_NONFINITE);
                 s = nothing();
 #pragma unroll 1
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             if (!begun) cluster_wait();
             begun = true;
             if (lane < ctas)
-                send(remote(&seen_part[(i * kMostCtas + rank) * kWarps + warp], lane), __float_as_uint(s.top), __float_as_uint(s.sum), static_cast<uint32_t>(s.at), 0u);
+                send(remote(&seen_part[(i * kMostCtas + rank) * kWarps + warp], lane), __float_as_uint(s.top), __float_as_uint(s.sum), static_cast<uint32_t>(s.at), odd ? 1u : 0u);
         }
     }
     if (lane < 8 && mine < k && d >= 0 && d < V) {
@@ -280,10 +283,12 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             const bool theirs = max(run(w), i * pieces) < min(run(w + 1), (i + 1) * pieces);
             if (theirs && lane < ctas * kWarps) s = p[lane];
             Seen more = theirs && lane + 32 < ctas * kWarps ? p[lane + 32] : nothing();
+            const bool odd = __any_sync(kAll, s.piece > 0 || more.piece > 0);
             if (more.top > s.top) { const Seen x = s; s = more; more = x; }
             s.sum += more.sum * scale.weight(more.top - s.top);
             if (more.top == s.top) s.at = min(s.at, more.at);
             s.join(scale);
+            s.piece = odd;
             if (lane == 0) seen[i] = s;
         }
         if (lane == i / kWarps && i < k) {
@@ -308,8 +313,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
         // drafts' probabilities
         const float* noise = D.noise + b * D.noise_stride;
         const float top = probs ? 0.0f : seen[n].top, sum = probs ? 1.0f : seen[n].sum;
-        bool odd = false;
-        for (int w = 0; w < kWarps; ++w) odd |= S.odd[w] != 0;
+        const bool odd = stats && seen[n].piece > 0;
         const float m = top * scale.near;
         const bool usual = fabsf(m) < kUsual;   // as in Seen::take: the weights are then relative to m, and so is their sum
         const float whole = usual && !probs ? fmaf(sum, fmaf(top, scale.near, -m) * kLn2, sum) : sum;
