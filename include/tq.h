@@ -862,8 +862,8 @@ typedef struct {
  * tokens' slots are -1. A length outside [0, max_blocks * block_tokens] counts as no
  * new tokens, new_lens outside [0, n_new] as the nearest (TQ_DEVERR_SEQLEN); an n_used outside [0,
  * n_free] as an empty list (TQ_DEVERR_CAPACITY).
- * Errors: TQ_ERR_INVALID_ARG (pointers, sizes; max_blocks * block_tokens or batch times the
- * most that a row can be given above 2^31 - 1), TQ_ERR_UNSUPPORTED (block_tokens).
+ * Errors: TQ_ERR_INVALID_ARG (pointers, sizes; batch above 2^24; max_blocks * block_tokens or
+ * batch times the most that a row can be given above 2^31 - 1), TQ_ERR_UNSUPPORTED (block_tokens).
  */
 tq_status tq_blocks_reserve(const tq_blocks *blocks, int batch, const int32_t *seq_lens, const int32_t *new_lens, int n_new,
                             const tq_places *places, tq_stream_t stream);
@@ -930,10 +930,11 @@ tq_status tq_rope_apply(const tq_rope *rope, int transposed, tq_dtype dtype, int
  *   logprobs    device float [batch][num_drafts + 1] or NULL: ln of each one's softmax(logits / temperature) (greedy: at
  *               temperature 1; with target_probs: ln p), 0 behind
  *   keep_lens   device int32 [batch] or NULL: seq_lens[b] + n + 1, the tokens whose keys and values stand
- * num_drafts = 0 draws one token for each sequence. -inf is a token that cannot be; +inf, the largest number; NaN counts as -inf.
- * A row that is looked at and holds +inf or a NaN sets TQ_DEVERR_NONFINITE, and so does one in which nothing
- * can be: its token is -1 (logprob 0). Sums are fp32, over weights to 2^-20; the weights that one token hangs on are good to
- * 2^-21; probabilities below 2^-100 (of the row's largest) count as 0. The same call gives the same bits every time. No workspace.
+ * num_drafts = 0 draws one token for each sequence. A logit of -inf is a token that cannot be; +inf counts as the largest
+ * number, NaN as -inf, and a row of logits that holds either sets TQ_DEVERR_NONFINITE. So does a next token's row in which nothing
+ * can be: the token is -1 (logprob 0). A probability that is NaN is never taken. Sums are fp32, over weights to 2^-20; the
+ * weights that a draft hangs on are good to 2^-21; probabilities below 2^-100 (of the row's largest) count as 0. The same call gives the same
+ * bits every time. No workspace. The outputs share no memory with the inputs, but keep_lens may be seq_lens.
  * Errors: TQ_ERR_INVALID_ARG (pointers, sizes, dtypes; batch above 2^24, vocab above 2^28), TQ_ERR_UNSUPPORTED (num_drafts above 64).
  */
 typedef struct {

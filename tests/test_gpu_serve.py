@@ -423,6 +423,38 @@ def test_blocks_captured_and_replayed():
         assert places.slots.tolist() == slots
 
 
+@pytest.mark.parametrize("cut", [0, 1, 2])
+def test_blocks_large_maps_captured(cut):
+    # maps of a launch of their own, into arrays that begin anywhere; every replay goes on from the last
+    B, width, BT, n = 70, 200, 16, 701
+    bt = tq.BlockTable(B, width, B * width, BT)
+    lens, places = torch.zeros(B, dtype=torch.int32, device=DEV), tq.Places(B, B * n + 8)
+    hold = [torch.zeros(B * n + 16, dtype=d, device=DEV) for d in (torch.int32, torch.int32, torch.int64)]
+    maps = [h[cut:cut + B * n + 8] for h in hold]
+    for name, m in zip(("seq_ids", "positions", "slots"), maps):
+        setattr(places, name, m)
+        setattr(places.desc, name, m.data_ptr())
+    news = i32([(37 * b) % (n + 1) for b in range(B)])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        bt.reserve(lens, news, n, places)
+        bt.release(lens)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        bt.reserve(lens, news, n, places)
+        lens += places.granted
+    table, free, used, host = bt.table.tolist(), bt.free_blocks.tolist(), 0, [0] * B
+    for _ in range(4):
+        graph.replay()
+        used, granted, starts, seqs, pos, slots, err = ref.reserve(table, free, used, host, news.tolist(), n, BT, B * width, B * n + 8)
+        assert not err and places.starts.tolist() == starts
+        assert [m.tolist() for m in maps] == [seqs, pos, slots]
+        host = [h + g for h, g in zip(host, granted)]
+    assert all(not h[:cut].any() and not h[cut + B * n + 8:].any() for h in hold)
+
+
 def test_blocks_share_the_batch_calls_free_list():
     kc, vc = tq.Codec(64, 3, tq.TQ_MODE_PROD, seed=0), tq.Codec(64, 3, tq.TQ_MODE_MSE, seed=1)
     cache, other = (tq.CompressedKVCache(kc, vc, 1, 32, 16, 1) for _ in "ab")

@@ -46,6 +46,7 @@ def test_blocks_calls(lib):
     assert reserve(lib, batch=-1) == INVALID and release(lib, batch=-1) == INVALID
     assert reserve(lib, seq=None) == INVALID and release(lib, keep=None) == INVALID
     assert reserve(lib, n=-1) == INVALID
+    assert reserve(lib, batch=(1 << 24) + 1, n=0) == INVALID and release(lib, batch=(1 << 24) + 1) == INVALID
     assert reserve(lib, places=_lib.tq_places(max_tokens=-1)) == INVALID
     assert reserve(lib, places=_lib.tq_places(slots=FAKE, max_tokens=4)) == INVALID          # maps without starts
     # 2^31 places: rows that can be given 2^20 each
@@ -119,7 +120,7 @@ def verify(lib, d=None, batch=1, K=2, V=100, acc=FAKE, tokens=FAKE, logs=None, k
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(batch=-1), INVALID), (dict(K=-1), INVALID), (dict(K=65), UNSUPPORTED), (dict(V=0), INVALID), (dict(acc=None), INVALID), (dict(tokens=None), INVALID),
+    (dict(batch=-1), INVALID), (dict(batch=(1 << 24) + 1), INVALID), (dict(V=(1 << 28) + 1), INVALID), (dict(K=-1), INVALID), (dict(K=65), UNSUPPORTED), (dict(V=0), INVALID), (dict(acc=None), INVALID), (dict(tokens=None), INVALID),
     (dict(keep=FAKE), INVALID), (dict(d=drafts(target=None)), INVALID), (dict(d=drafts(target=FAKE + 1)), INVALID), (dict(d=drafts(draft=FAKE + 2)), INVALID),
     (dict(d=drafts(target_dtype=3)), INVALID), (dict(d=drafts(draft_dtype=7)), INVALID), (dict(d=drafts(draft_tokens=None)), INVALID),
     (dict(d=drafts(uniforms=None)), INVALID),

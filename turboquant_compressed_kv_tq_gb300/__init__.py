@@ -989,16 +989,18 @@ def tq_verify_drafts(target, draft_tokens=None, draft_probs=None, uniforms=None,
         with _on(stream) if stream is not None else _here:
             out = Verified(make(per, dtype=i32, device=on), make(full, dtype=i32, device=on),
                            make(per, dtype=i32, device=on) if seq_lens is not None else None, make(full, dtype=f32, device=on))
-    elif (seq_lens is None) != (out.keep_lens is None):
-        raise ValueError("keep_lens go with seq_lens")
+        to = (out.accepted.data_ptr(), out.tokens.data_ptr(), out.logprobs.data_ptr(), out.keep_lens.data_ptr() if seq_lens is not None else None)
+    else:
+        if (seq_lens is None) != (out.keep_lens is None):
+            raise ValueError("keep_lens go with seq_lens")
+        to = (_array(out.accepted, "accepted", i32, device, per), _array(out.tokens, "tokens", i32, device, full),
+              _array(out.logprobs, "logprobs", f32, device, full), _array(out.keep_lens, "keep_lens", i32, device, per))
     packed = _pack_drafts(
         target.data_ptr(), tb, tr, draft, db, dr, (_array(draft_tokens, "draft_tokens", i32, device, each) or 0) if drafts else 0,
         _array(draft_lens, "draft_lens", i32, device, per) or 0, _array(temperatures, "temperatures", f32, device, per) or 0,
         (_array(uniforms, "uniforms", f32, device, each) or 0) if drafts else 0, noise.data_ptr() if noise is not None else 0, nb,
         _array(seq_lens, "seq_lens", i32, device, per) or 0, code, dcode, int(target_probs))
-    status = t.verify(packed, batch, drafts, vocab, _array(out.accepted, "accepted", i32, device, per),
-                      _array(out.tokens, "tokens", i32, device, full), _array(out.logprobs, "logprobs", f32, device, full),
-                      _array(out.keep_lens, "keep_lens", i32, device, per), _raw_stream(t, stream, device))
+    status = t.verify(packed, batch, drafts, vocab, *to, _raw_stream(t, stream, device))
     if status:
         check(status, "tq_verify_drafts")
     return out

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, kResident) draw_kernel(const __grid_
     const int per = alike ? ((chunks + ctas - 1) >> log_ctas) * 8 : (V + ctas - 1) >> log_ctas;
     const int main_end = alike ? head + chunks * 8 : V, main_begin = min(main_end, (alike ? head : 0) + rank * per), my_end = min(main_end, main_begin + per);
     unsigned char* const ring = s_ring + warp * kStages * kStageBytes<T>;
-    int asked = 0;   // of this round, by lane 0: the first value of the next piece
+    int asked = 0;   // by lane 0: the first value of the next piece
     auto ask = [&](int st) {
         const int at = asked, n = min(kPiece, my_end - at);
         if (n <= 0) return;

@@ -14,7 +14,7 @@ namespace {
 constexpr int64_t kMost = 2147483647;
 
 tq_status check_blocks(const tq_blocks* b, int batch) {
-    if (!b || !b->table || !b->n_used || b->n_free < 0 || (b->n_free > 0 && !b->free_blocks) || b->max_blocks <= 0 || b->num_blocks <= 0 || batch < 0)
+    if (!b || !b->table || !b->n_used || b->n_free < 0 || (b->n_free > 0 && !b->free_blocks) || b->max_blocks <= 0 || b->num_blocks <= 0 || batch < 0 || batch > (1 << 24))
         return TQ_ERR_INVALID_ARG;
     if (b->block_tokens < 16 || (b->block_tokens & (b->block_tokens - 1)) != 0) return TQ_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(b->max_blocks) * b->block_tokens > kMost) return TQ_ERR_INVALID_ARG;
