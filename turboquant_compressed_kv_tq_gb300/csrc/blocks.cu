@@ -21,6 +21,7 @@ namespace {
 constexpr int kRows = 1024;       // threads of a CTA at most: rows that it takes at once
 constexpr int kFewest = 128;      // threads of a CTA at least
 constexpr int kFew = 4;           // entries that a thread looks at by itself
+constexpr int kGroups = 4;        // groups of 32 entries that a warp looks up at once
 constexpr int kMostCtas = 8;
 constexpr int kFusedTokens = 16384;   // maps of up to so many tokens are written by the rows' own launch (a second one costs 2 us and more)
 constexpr unsigned kAll = 0xffffffffu;
@@ -161,9 +162,13 @@ __global__ void __launch_bounds__(kRows) reserve_kernel(const __grid_constant__ 
             const int i = S.longs[l];
             const int32_t* entries = A.table + static_cast<int64_t>(R.row(chunk, i)) * A.max_blocks;
             int count = 0;
-            for (int lb = S.first[i] + lane; lb < S.end[i]; lb += 128) {
+            const int last = S.end[i];
+            for (int lb = S.first[i] + lane; lb < last; lb += 32 * kGroups) {
+                int id[kGroups];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) count += lb + g * 32 < S.end[i] && entries[lb + g * 32] < 0;
+                for (int g = 0; g < kGroups; ++g) id[g] = lb + g * 32 < last ? entries[lb + g * 32] : 0;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) count += id[g] < 0;
             }
             count = __reduce_add_sync(kAll, count);
             if (lane == 0) S.value[i] = count;
@@ -207,14 +212,14 @@ __global__ void __launch_bounds__(kRows) reserve_kernel(const __grid_constant__ 
             int rank = static_cast<int>(S.start[i]);
             const int last = S.end[i];
             bool out = false;
-            for (int lb0 = S.first[i]; lb0 < last && !out; lb0 += 128) {
-                int id[4];
+            for (int lb0 = S.first[i]; lb0 < last && !out; lb0 += 32 * kGroups) {
+                int id[kGroups];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) id[g] = lb0 + g * 32 + lane < last ? entries[lb0 + g * 32 + lane] : 0;
-                unsigned lacking[4];
-                int mine[4];
+                for (int g = 0; g < kGroups; ++g) id[g] = lb0 + g * 32 + lane < last ? entries[lb0 + g * 32 + lane] : 0;
+                unsigned lacking[kGroups];
+                int mine[kGroups];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < kGroups; ++g) {
                     lacking[g] = __ballot_sync(kAll, id[g] < 0);
                     mine[g] = rank + __popc(lacking[g] & ((1u << lane) - 1));
                     rank += __popc(lacking[g]);
@@ -222,17 +227,17 @@ __global__ void __launch_bounds__(kRows) reserve_kernel(const __grid_constant__ 
                 // the first place without a block, and the blocks of those before it: all looked up at once
                 int stop = last;
 #pragma unroll
-                for (int g = 3; g >= 0; --g) {
+                for (int g = kGroups - 1; g >= 0; --g) {
                     const unsigned gone = __ballot_sync(kAll, id[g] < 0 && mine[g] >= left);
                     if (gone) stop = lb0 + g * 32 + __ffs(gone) - 1;
                 }
 #pragma unroll
-                for (int g = 0; g < 4; ++g) lacking[g] = lb0 + g * 32 + lane < stop && id[g] < 0;
+                for (int g = 0; g < kGroups; ++g) lacking[g] = lb0 + g * 32 + lane < stop && id[g] < 0;
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
+                for (int g = 0; g < kGroups; ++g)
                     if (lacking[g]) id[g] = A.free_blocks[used + mine[g]];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < kGroups; ++g) {
                     const int lb = lb0 + g * 32 + lane;
                     if (lacking[g]) entries[lb] = id[g];
                     if (lb < stop && (id[g] < 0 || id[g] >= A.num_blocks)) atomicOr(A.err, TQ_DEVERR_BLOCK);
@@ -368,15 +373,15 @@ __global__ void __launch_bounds__(kRows) release_kernel(const __grid_constant__ 
 #pragma unroll
             for (int e = 0; e < kFew; ++e) count += e < held && ids[e] < A.num_blocks;
             __syncthreads();
-            // f(entry, id) of a long row's entries up to the first negative one, a lane for each; four groups of 32 looked up at once
+            // f(entry, id) of a long row's entries up to the first negative one, a lane for each; kGroups x 32 looked up at once
             auto each = [&](int i, auto&& f) {
                 const int32_t* entries = A.table + static_cast<int64_t>(R.row(chunk, i)) * A.max_blocks;
-                for (int lb0 = S.first[i]; lb0 < A.max_blocks; lb0 += 128) {
-                    int id[4];
+                for (int lb0 = S.first[i]; lb0 < A.max_blocks; lb0 += 32 * kGroups) {
+                    int id[kGroups];
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) id[g] = lb0 + g * 32 + lane < A.max_blocks ? entries[lb0 + g * 32 + lane] : -1;
+                    for (int g = 0; g < kGroups; ++g) id[g] = lb0 + g * 32 + lane < A.max_blocks ? entries[lb0 + g * 32 + lane] : -1;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
+                    for (int g = 0; g < kGroups; ++g) {
                         const unsigned gone = __ballot_sync(kAll, id[g] < 0);
                         const int n = gone ? __ffs(gone) - 1 : 32;
                         f(lb0 + g * 32 + lane, id[g], lane < n);

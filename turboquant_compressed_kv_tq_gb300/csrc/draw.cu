@@ -38,13 +38,13 @@ __global__ void __launch_bounds__(kThreads, kResident) draw_kernel(const __grid_
     const int ctas = 1 << log_ctas, rank = cluster_rank();
     const int b = blockIdx.x >> log_ctas, tid = threadIdx.x, lane = tid % 32, warp = tid / 32, V = A.V;
     const tq_drafts& D = A.d;
-    const float asked_T = !D.noise ? 0.0f : D.temperatures ? D.temperatures[b] : 1.0f;
+    const float asked_T = D.temperatures ? D.temperatures[b] : 1.0f;
     if (lane < kStages) tc::mbar_init(&S.bars[warp][lane], 1);
     tc::mbar_fence_init();
     __syncwarp();
     cluster_arrive();   // (waited for before the first word to another CTA)
     const T* row = static_cast<const T*>(D.target) + b * D.target_stride_batch;
-    const float* noise = D.noise ? D.noise + b * D.noise_stride : nullptr;
+    const float* noise = D.noise + b * D.noise_stride;   // (without noise all rows are the other kernel's)
     const bool probs = D.target_probs != 0, greedy = !(asked_T > 0.0f);
     const Scale scale(greedy ? 1.0f : fminf(fmaxf(asked_T, 0x1p-120f), 0x1p100f));
     // A CTA's values: whole chunks of 8 through its warps' rings, where logits and noise lie alike, and what lies outside those (the
