@@ -697,6 +697,23 @@ def test_verification_temperatures(T):
             assert not 100 <= int(got.tokens[b, n]) < 200
 
 
+def test_verification_looks_at_no_row_behind_the_drafts():
+    B, K, V = 9, 4, 3001
+    c = verify_case(71, B, K, V, BF16, F32)
+    c["draft_lens"] = i32([b % (K + 1) for b in range(B)])
+    want = check(c)
+    spoilt = c | {name: c[name].clone() for name in ("target", "draft_probs", "draft_tokens", "uniforms")}
+    for b in range(B):
+        k = b % (K + 1)
+        spoilt["target"][b, k + 1:] = math.nan
+        for name in ("draft_probs", "uniforms"):
+            spoilt[name][b, k:] = math.nan
+        spoilt["draft_tokens"][b, k:] = 1 << 30
+    for x, y in zip(tq.tq_verify_drafts(**spoilt), want):
+        assert torch.equal(x, y)
+    errors([])
+
+
 def test_verification_draws_the_targets_distribution():
     # 60000 sequences of one draft over 6 tokens, one row of p and one of q for all: the first token is distributed as p, the
     # second as its row. A count is off by five deviations once in a million.
