@@ -1,0 +1,45 @@
+"""The calls around the caches' where they can go wrong: masked rows with a NaN in them, lengths where nothing is drafted, noise that
+leaves no token, the largest rotation."""
+import math
+
+import pytest
+import torch
+
+import serve_util as ref
+import turboquant_compressed_kv_tq_gb300 as tq
+from test_gpu_serve import BF16, DEV, F16, F32, check, check_rotation, errors, gen, i32, no_device_error, verify_case  # noqa: F401 (no_device_error: fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def nonfinite():
+    torch.cuda.synchronize()
+    return bool(tq.tq_device_error() & tq.TQ_DEVERR_NONFINITE)
+
+
+@pytest.mark.parametrize("form", ["drafts", "greedy", "draw"])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("V", [300, 50021, 131072])
+def test_nan_among_masked_tokens_is_told(dtype, V, form):
+    # few tokens allowed, one of them NaN; or a row that begins with NaNs: nothing else in the lanes that see them
+    B, K = 4, 2 if form == "drafts" else 0
+    rows = {"one": [V // 2 + 1], "first": list(range(min(V // 3, 9000))), "last": [V - 1]}
+    for name, at in rows.items():
+        c = verify_case(V + K, B, K, V, dtype, F32, temps=None)
+        x = c["target"]
+        if name == "first":
+            x[2, 0, at] = math.nan
+        else:
+            x[2, 0] = -math.inf
+            x[2, 0, V // 4] = 1.5
+            x[2, 0, at] = math.nan
+        if form == "greedy":
+            c["noise"] = None
+        got = check(c)
+        assert nonfinite(), name
+        if name != "first":
+            assert int(got.tokens[2, int(got.accepted[2])]) == V // 4 or int(got.accepted[2]) > 0
+        # masked alike without a NaN: nothing to tell
+        x[2, 0, at] = -math.inf
+        check(c)
+        assert not nonfinite(), name

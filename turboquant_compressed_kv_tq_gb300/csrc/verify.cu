@@ -86,6 +86,11 @@ struct __align__(16) Seen {
         } else if (t > -INFINITY) {   // seldom: one value after the other
 #pragma unroll 1
             for (int e = 0; e < kPer * kIn; ++e) sum += S.weight(number(reinterpret_cast<const T*>(from + e / kIn * 32)[e % kIn]) - top);
+        } else {   // masked tokens weigh nothing, but a NaN that the largest value (-inf, or NaN) does not show is to be seen in the sum
+            float2 s = x[0];
+#pragma unroll
+            for (int i = 1; i < N; ++i) s = __fadd2_rn(s, x[i]);
+            if (!(s.x + s.y == -INFINITY)) sum = s.x + s.y;
         }
     }
     // Where the largest value is, by another look at the piece (`row`: its first whole unit, of `end` units; value 0 of it is value
