@@ -43,3 +43,17 @@ def test_nan_among_masked_tokens_is_told(dtype, V, form):
         x[2, 0, at] = -math.inf
         check(c)
         assert not nonfinite(), name
+
+
+@pytest.mark.parametrize("noise", [True, False])
+def test_lengths_where_nothing_is_drafted(noise):
+    c = verify_case(3, 4, 0, 700, F32, None, temps=None)
+    if not noise:
+        c["noise"] = None
+    want = check(c)
+    for bad in ([0, 0, 1, 0], [0, -1, 0, 0]):
+        got = tq.tq_verify_drafts(**(c | {"draft_lens": i32(bad)}))
+        errors(["seqlen"])
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    check(c | {"draft_lens": i32([0] * 4)})
+    errors([])

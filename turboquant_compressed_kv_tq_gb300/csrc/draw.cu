@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kThreads, kResident) draw_kernel(const __grid_
     const int b = blockIdx.x >> log_ctas, tid = threadIdx.x, lane = tid % 32, warp = tid / 32, V = A.V;
     const tq_drafts& D = A.d;
     const float asked_T = D.temperatures ? D.temperatures[b] : 1.0f;
+    if (tid == 0 && rank == 0 && D.draft_lens && D.draft_lens[b] != 0) atomicOr(A.err, TQ_DEVERR_SEQLEN);   // (of no drafts)
     if (lane < kStages) tc::mbar_init(&S.bars[warp][lane], 1);
     tc::mbar_fence_init();
     __syncwarp();
