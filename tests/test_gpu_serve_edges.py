@@ -57,3 +57,20 @@ def test_lengths_where_nothing_is_drafted(noise):
         assert all(torch.equal(x, y) for x, y in zip(got, want))
     check(c | {"draft_lens": i32([0] * 4)})
     errors([])
+
+
+@pytest.mark.parametrize("V", [900, 40000])
+def test_noise_that_leaves_no_token(V):
+    # what is likely has infinite noise, what is left counts as 0: no token, whether or not the call has drafts
+    B = 3
+    for dtype in (F32, BF16):
+        x = torch.full((B, 2, V), -200.0, dtype=dtype, device=DEV)
+        x[:, :, :V // 2] = 0.0
+        e = torch.ones(B, V, device=DEV)
+        e[:, :V // 2] = math.inf
+        drawn = tq.tq_verify_drafts(x[:, :1], noise=e)
+        assert nonfinite()
+        drafted = tq.tq_verify_drafts(x, i32([[0]] * B), None, torch.zeros(B, 1, device=DEV), e, draft_lens=i32([0] * B))
+        assert nonfinite()
+        for got in (drawn, drafted):
+            assert got.tokens[:, 0].tolist() == [-1] * B and not got.logprobs.any() and not got.accepted.any()

@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, kResident) draw_kernel(const __grid_
         } else if (best.i != INT_MAX) {
             const float m = t * scale.near;
             best.v = (probs ? best_x : fabsf(m) < kUsual ? ex2(fmaf(best_x, scale.near, -m)) : scale.weight(best_x - t)) * rcp(fmaxf(best_e, 0x1p-100f));
+            if (!(best.v > 0.0f)) best = Best{0.0f, INT_MAX};   // (likely only beside what this thread saw)
         }
         top = t, sum = s;
         break;
