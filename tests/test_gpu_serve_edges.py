@@ -74,3 +74,19 @@ def test_noise_that_leaves_no_token(V):
         assert nonfinite()
         for got in (drawn, drafted):
             assert got.tokens[:, 0].tolist() == [-1] * B and not got.logprobs.any() and not got.accepted.any()
+
+
+@pytest.mark.parametrize("K", [0, 2])
+@pytest.mark.parametrize("noise", [True, False])
+def test_probabilities_that_are_no_numbers_are_not_taken(K, noise):
+    # greedy, of probabilities: no logits, nothing to tell
+    B, V = 4, 3001
+    c = verify_case(17, B, K, V, F32, F32, temps=None, probs=True)
+    if noise:
+        c["temperatures"] = torch.zeros(B, device=DEV)
+    else:
+        c["noise"] = None
+    c["target"][1, 0, 5:900] = math.nan
+    got = check(c)
+    errors([])
+    assert not bool(((got.tokens[1] >= 5) & (got.tokens[1] < 900))[0])

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             if (edge >= 0) s.take(x_edge, scale, edge);
             const bool odd = __any_sync(kAll, !(s.sum < INFINITY));
             if (!(s.sum < INFINITY)) {   // a NaN, or +inf (inf - inf): once more, as they count
-                atomicOr(A.err, TQ_DEVERR_NONFINITE);
+                if (!probs) atomicOr(A.err, TQ_DEVERR_NONFINITE);
                 s = nothing();
 #pragma unroll 1
                 for (int u = first; u < last; u += kUnits)
