@@ -90,3 +90,21 @@ def test_probabilities_that_are_no_numbers_are_not_taken(K, noise):
     got = check(c)
     errors([])
     assert not bool(((got.tokens[1] >= 5) & (got.tokens[1] < 900))[0])
+
+
+def test_the_largest_rotation():
+    # 2^31 - 1 tokens, the most that a call takes, in place
+    n, D = (1 << 31) - 1, 16
+    x = torch.zeros(1, 1, n, D, dtype=BF16, device=DEV)
+    ends = [slice(0, 40), slice(n // 2 - 20, n // 2 + 20), slice(n - 40, n)]
+    before = []
+    for i, s in enumerate(ends):
+        x[:, :, s] = torch.randn((1, 1, 40, D), generator=gen(i), device=DEV).to(BF16)
+        before.append(x[:, :, s].clone())
+    r = tq.Rope.of_base(D)
+    r.apply(x, out=x)
+    for s, y in zip(ends, before):
+        pos = torch.arange(s.start, s.stop, device=DEV)[None]
+        check_rotation(y, x[:, :, s], pos, r, r.inv_freq)
+    del x
+    torch.cuda.empty_cache()

@@ -154,7 +154,7 @@ cudaError_t launch(RopeArgs a, int sms, cudaStream_t s) {
     a.stream = static_cast<int64_t>(a.batch) * a.n * (a.heads[0] + a.heads[1]) * a.D * static_cast<int64_t>(sizeof(T)) > (64 << 20);
     const int J = a.D / 16, all = a.batch * a.n, heads = a.heads[0] + a.heads[1];
     const int tokens = std::min(all, std::max(1, 32 / J)), slots = std::max(1, std::min(heads, kThreads / (J * tokens)));
-    const int tiles = (all + tokens - 1) / tokens;
+    const int tiles = (all - 1) / tokens + 1;   // (all up to 2^31 - 1)
     // the heads in parts, as long as there are fewer CTAs than SMs
     const int parts = std::max(1, std::min((heads + slots - 1) / slots, sms / tiles));
     auto kernel = a.rope.inter ? rope_kernel<T, true> : rope_kernel<T, false>;
