@@ -108,3 +108,20 @@ def test_the_largest_rotation():
         check_rotation(y, x[:, :, s], pos, r, r.inv_freq)
     del x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("Hq,Hk", [(8, 1), (1, 4), (1, 1)])
+def test_rotation_of_a_single_head_in_place(Hq, Hk):
+    # queries or keys of one head in a fused projection: its stride says nothing
+    B, n, D = 3, 7, 64
+    whole = torch.randn((B, n, Hq + 2 * Hk, D), generator=gen(5), device=DEV).to(BF16).transpose(1, 2)
+    before = whole.clone()
+    q, k = whole[:, :Hq], whole[:, Hq:Hq + Hk]
+    r = tq.Rope.of_base(D)
+    r.apply(q, k, q, k)
+    pos = torch.arange(n, device=DEV).expand(B, n)
+    check_rotation(before[:, :Hq], q, pos, r, r.inv_freq)
+    check_rotation(before[:, Hq:Hq + Hk], k, pos, r, r.inv_freq)
+    assert torch.equal(whole[:, Hq + Hk:], before[:, Hq + Hk:])
+    with pytest.raises(tq.TQError):   # one head over the others
+        r.apply(q, k, out=q, k_out=whole[:, Hq - 1:Hq - 1 + Hk])

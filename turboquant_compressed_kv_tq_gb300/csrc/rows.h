@@ -66,10 +66,10 @@ inline bool rows_meet(const tq_rows* a, int64_t ha, const tq_rows* b, int64_t hb
     rows_span(b, nb, hb, nt, D, blo, bhi);
     const int64_t apart = (reinterpret_cast<intptr_t>(b->data) - reinterpret_cast<intptr_t>(a->data)) / elem;
     if (apart + blo >= ahi || alo >= apart + bhi) return false;
-    if (!same_layout(a, b, nb, std::max(ha, hb), nt)) return true;
+    if (!same_layout(a, b, nb, std::min(ha, hb), nt)) return true;   // (the stride of a single head says nothing)
     // steps (a's index less b's) along each axis, the largest stride first
     struct { int64_t stride, lo, hi; } axis[3] = {{nb > 1 ? a->stride_batch : 0, 1 - nb, nb - 1},
-                                                  {std::max(ha, hb) > 1 ? a->stride_head : 0, 1 - hb, ha - 1},
+                                                  {ha > 1 ? a->stride_head : hb > 1 ? b->stride_head : 0, 1 - hb, ha - 1},
                                                   {nt > 1 ? a->stride_token : 0, 1 - nt, nt - 1}};
     for (auto& x : axis)
         if (x.stride < 0) x = {-x.stride, -x.hi, -x.lo};
