@@ -892,7 +892,8 @@ tq_status tq_blocks_release(const tq_blocks *blocks, int batch, const int32_t *k
  *              the rows that went in; at scale 1 also the way back
  * Coordinates behind rot_dim pass as they are. An output is its input (in place), or shares no memory with the
  * inputs or the other output, and its rows share none with each other: TQ_ERR_INVALID_ARG where they do, and
- * also where two that lie in different layouts are not apart as a whole.
+ * also where two that lie in different layouts are not apart as a whole, or where strides that are shorter than what the
+ * smaller ones span leave more than a million combinations to look at.
  * head_dim a multiple of 16, at most 1024. Arithmetic is fp32, the angle exact (see tq_rope); one rounding.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, rot_dim).
  */

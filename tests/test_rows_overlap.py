@@ -48,3 +48,51 @@ def test_a_single_head_in_a_projection(tell):
     over = (BASE + 7 * D * 2, n * H * D, 0, H * D)
     got = tell([q + k + (nb, 8, 1, n, D), k + q + (nb, 1, 8, n, D), q + over + (nb, 8, 1, n, D), over + q + (nb, 1, 8, n, D), k + over + (nb, 1, 1, n, D)])
     assert [m for _, m in got] == [False, False, True, True, False]
+
+
+def starts(at, strides, n):
+    sb, sh, st = (s if k > 1 else 0 for s, k in zip(strides, n))
+    return [at + b * sb + h * sh + t * st for b in range(n[0]) for h in range(n[1]) for t in range(n[2])]
+
+
+def meet_themselves(rows, D):
+    rows = sorted(rows)
+    return any(y - x < D for x, y in zip(rows, rows[1:]))
+
+
+def test_any_strides(tell):
+    # strides of which none need be as long as what the others span; rows shifted against each other
+    rnd = random.Random(1)
+    cases, want = [], []
+    for _ in range(20000):
+        D = rnd.choice([1, 2, 8])
+        n = [rnd.randint(1, 5) for _ in range(3)]
+        hb = rnd.choice([n[1], n[1], 1, rnd.randint(1, 5)])
+        a = [rnd.randint(-12, 12) * rnd.choice([1, D]) for _ in range(3)]
+        b = list(a)
+        if n[1] == 1 or hb == 1:
+            b[1] = rnd.randint(-40, 40)
+        apart = rnd.randint(-60, 60)
+        ra, rb = starts(0, a, n), starts(apart, b, [n[0], hb, n[2]])
+        cases.append((BASE, *a, BASE + 2 * apart, *b, n[0], n[1], hb, n[2], D))
+        want.append((meet_themselves(ra, D), any(abs(x - y) < D for x in ra for y in rb)))
+    got = tell(cases)
+    assert [m for m, _ in got] == [m for m, _ in want]
+    assert [m for _, m in got] == [m for _, m in want]
+
+
+def test_strides_that_share_multiples(tell):
+    # heads 192 apart, tokens 128: the third head's first token is the first head's fourth
+    D = 64
+    alone = (BASE + (1 << 30), 1 << 20, 64, 512)
+    got = tell([(BASE, 4096, 192, 128) + alone + (1, 3, 3, 4, D), (BASE, 4096, 192, 128) + alone + (1, 3, 3, 3, D),
+                (BASE, 4096, 192, 128) + alone + (1, 2, 2, 64, D), (BASE, 4096, 64 * 101, 64 * 100) + alone + (1, 100, 100, 101, D),
+                (BASE, 4096, 64 * 101, 64 * 100) + alone + (1, 100, 100, 102, D), (BASE, 4096, 64 * 101, 64 * 100) + alone + (1, 101, 101, 102, D)])
+    assert [m for m, _ in got] == [True, False, False, False, False, True]
+
+
+def test_layouts_that_take_too_long_to_tell(tell):
+    # heads s + 1 apart, tokens s: apart as long as there are at most s of either; so many that it is not looked through are refused
+    def call(s, n):
+        return tell([(BASE, 0, s + 1, s, BASE + (1 << 60), 0, s + 1, s, 1, n, n, n, 1)])[0][0]
+    assert [call(1000, 1000), call(1000, 1002), call(10 ** 7, 10 ** 7)] == [False, True, True]

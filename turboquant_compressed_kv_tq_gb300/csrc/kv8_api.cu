@@ -48,7 +48,7 @@ bool out_overlaps(const tq_rows* q, const tq_rows* out, int64_t nb, int64_t nh, 
     if (o.meets_itself(D) || q->data == out->data) return true;
     if (!same_layout(q, out, nb, nh, nt)) return false;
     const int64_t apart = (reinterpret_cast<intptr_t>(out->data) - reinterpret_cast<intptr_t>(q->data)) / 2;
-    return o.meet(apart, 0, D);
+    return o.meet(apart, D);
 }
 
 tq_status make_rope(const tq_rope* r, int D, const int32_t* positions, Rope* out) {

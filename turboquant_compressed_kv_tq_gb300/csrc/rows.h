@@ -19,28 +19,47 @@ inline tq_status check_rows(const tq_rows* r, int elem) {
     return TQ_OK;
 }
 
-// The axes of rows of heads, in elements, the largest stride first; an axis of one element has none.
-struct Axes {
-    int64_t stride[3], n[3];
-    Axes(const tq_rows* r, int64_t nb, int64_t nh, int64_t nt) : stride{r->stride_batch, r->stride_head, r->stride_token}, n{nb, nh, nt} {
-        for (int i = 0; i < 3; ++i) stride[i] = n[i] > 1 ? std::abs(stride[i]) : 0;
+// Sums of steps along three axes: lo .. hi of each stride, the largest stride first.
+struct Steps {
+    int64_t stride[3], lo[3], hi[3];
+    int looks = 1 << 20;   // at most; a few where each stride is as long as what the smaller ones span
+    void sort() {
+        for (int i = 0; i < 3; ++i)
+            if (stride[i] < 0) stride[i] = -stride[i], std::swap(lo[i], hi[i]), lo[i] = -lo[i], hi[i] = -hi[i];
         for (int i = 0; i < 2; ++i)
             for (int k = 0; k < 2 - i; ++k)
-                if (stride[k] < stride[k + 1]) std::swap(stride[k], stride[k + 1]), std::swap(n[k], n[k + 1]);
+                if (stride[k] < stride[k + 1]) std::swap(stride[k], stride[k + 1]), std::swap(lo[k], lo[k + 1]), std::swap(hi[k], hi[k + 1]);
     }
-    // Whether two rows whose starts differ by a sum of steps along axes k.. lie within D elements of being `delta` apart. A
-    // yes has such rows to show; a no is sure where each stride is as long as what the smaller ones span.
-    bool meet(int64_t delta, int k, int D) const {
+    // Whether a sum along axes k.. lies within D elements of `delta`: exact, and yes where it cannot be told in so many looks.
+    bool meet(int64_t delta, int k, int D) {
         if (k == 3 || stride[k] == 0) return std::abs(delta) < D;
-        const int64_t d = delta / stride[k];
-        for (int64_t i = d - 1; i <= d + 1; ++i)
-            if (std::abs(i) < n[k] && meet(delta - i * stride[k], k + 1, D)) return true;
+        int64_t least = delta - D + 1, most = delta + D - 1;   // of the steps along axis k
+        for (int j = k + 1; j < 3; ++j) least -= stride[j] * hi[j], most -= stride[j] * lo[j];
+        auto down = [&](int64_t x) { return x / stride[k] - (x % stride[k] < 0); };
+        const int64_t end = std::min(hi[k], down(most));
+        for (int64_t i = std::max(lo[k], down(least + stride[k] - 1)); i <= end; ++i)
+            if (--looks < 0 || meet(delta - i * stride[k], k + 1, D)) return true;
         return false;
     }
+};
+
+// The axes of rows of heads, in elements; an axis of one element has none.
+struct Axes {
+    Steps steps;
+    Axes(const tq_rows* r, int64_t nb, int64_t nh, int64_t nt) {
+        const int64_t stride[3] = {r->stride_batch, r->stride_head, r->stride_token}, n[3] = {nb, nh, nt};
+        for (int i = 0; i < 3; ++i) steps.stride[i] = n[i] > 1 ? stride[i] : 0, steps.lo[i] = 1 - n[i], steps.hi[i] = n[i] - 1;
+        steps.sort();
+    }
+    // Whether two rows lie within D elements of being `delta` apart.
+    bool meet(int64_t delta, int D) const { return Steps(steps).meet(delta, 0, D); }
     // Whether the rows share memory with each other.
     bool meets_itself(int D) const {
-        for (int k = 0; k < 3; ++k)
-            if ((stride[k] > 0 && meet(stride[k], k + 1, D)) || (stride[k] == 0 && n[k] > 1)) return true;
+        Steps s = steps;
+        for (int k = 0; k < 3; ++k) {
+            s.lo[k] = 1;   // the first axis along which two rows lie apart
+            if (s.stride[k] == 0 ? s.hi[k] > 0 : s.meet(0, k, D)) return true;
+        }
         return false;
     }
 };
@@ -59,7 +78,7 @@ inline void rows_span(const tq_rows* r, int64_t nb, int64_t nh, int64_t nt, int 
 }
 
 // Whether a row of a ([nb][ha][nt] of them) shares memory with a row of b ([nb][hb][nt]). Sets in different layouts share where
-// their spans do; of sets that lie alike, a yes has two such rows to show, and a no is sure as in Axes::meet.
+// their spans do; sets that lie alike, where two rows do.
 inline bool rows_meet(const tq_rows* a, int64_t ha, const tq_rows* b, int64_t hb, int64_t nb, int64_t nt, int D, int elem) {
     int64_t alo, ahi, blo, bhi;
     rows_span(a, nb, ha, nt, D, alo, ahi);
@@ -67,23 +86,12 @@ inline bool rows_meet(const tq_rows* a, int64_t ha, const tq_rows* b, int64_t hb
     const int64_t apart = (reinterpret_cast<intptr_t>(b->data) - reinterpret_cast<intptr_t>(a->data)) / elem;
     if (apart + blo >= ahi || alo >= apart + bhi) return false;
     if (!same_layout(a, b, nb, std::min(ha, hb), nt)) return true;   // (the stride of a single head says nothing)
-    // steps (a's index less b's) along each axis, the largest stride first
-    struct { int64_t stride, lo, hi; } axis[3] = {{nb > 1 ? a->stride_batch : 0, 1 - nb, nb - 1},
-                                                  {ha > 1 ? a->stride_head : hb > 1 ? b->stride_head : 0, 1 - hb, ha - 1},
-                                                  {nt > 1 ? a->stride_token : 0, 1 - nt, nt - 1}};
-    for (auto& x : axis)
-        if (x.stride < 0) x = {-x.stride, -x.hi, -x.lo};
-    for (int i = 0; i < 2; ++i)
-        for (int k = 0; k < 2 - i; ++k)
-            if (axis[k].stride < axis[k + 1].stride) std::swap(axis[k], axis[k + 1]);
-    auto meet = [&](auto&& self, int64_t delta, int k) -> bool {
-        if (k == 3 || axis[k].stride == 0) return std::abs(delta) < D;
-        const int64_t d = delta / axis[k].stride;
-        for (int64_t i = d - 1; i <= d + 1; ++i)
-            if (i >= axis[k].lo && i <= axis[k].hi && self(self, delta - i * axis[k].stride, k + 1)) return true;
-        return false;
-    };
-    return meet(meet, apart, 0);
+    // steps: a's index less b's
+    Steps s{{nb > 1 ? a->stride_batch : 0, ha > 1 ? a->stride_head : hb > 1 ? b->stride_head : 0, nt > 1 ? a->stride_token : 0},
+            {1 - nb, 1 - hb, 1 - nt},
+            {nb - 1, ha - 1, nt - 1}};
+    s.sort();
+    return s.meet(apart, 0, D);
 }
 
 }  // namespace tq
