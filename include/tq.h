@@ -935,7 +935,8 @@ tq_status tq_rope_apply(const tq_rope *rope, int transposed, tq_dtype dtype, int
  * number, NaN as -inf, and a row of logits that holds either sets TQ_DEVERR_NONFINITE. So does a next token's row in which nothing
  * can be: the token is -1 (logprob 0). A probability that is NaN is never taken. Sums are fp32, over weights to 2^-20; the
  * weights that a draft hangs on are good to 2^-21; probabilities below 2^-100 (of the row's largest) count as 0. The same call gives the same
- * bits every time. No workspace. The outputs share no memory with the inputs, but keep_lens may be seq_lens.
+ * bits every time. No workspace. The outputs share no memory with each other or with what is read, but keep_lens may be seq_lens
+ * (TQ_ERR_INVALID_ARG).
  * Errors: TQ_ERR_INVALID_ARG (pointers, sizes, dtypes; batch above 2^24, vocab above 2^28), TQ_ERR_UNSUPPORTED (num_drafts above 64).
  */
 typedef struct {

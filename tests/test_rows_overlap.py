@@ -9,12 +9,19 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PROGRAM = r"""
 #include <cstdio>
 #include "rows.h"
-// lines of: address and three strides of two sets, batch, heads of each, tokens, D -> whether the first meets itself, and the second
+// "0" and lines of: address and three strides of two sets, batch, heads of each, tokens, D -> whether the first meets itself, and the second
+// "1" and lines of: an array's address and bytes; rows' address, stride, number, stride, number, bytes -> whether they meet
 int main() {
-    long long v[13];
-    for (;;) {
+    long long v[13], kind;
+    while (std::scanf("%lld", &kind) == 1) {
+        if (kind == 1) {
+            for (int i = 0; i < 8; ++i)
+                if (std::scanf("%lld", v + i) != 1) return 1;
+            std::printf("%d\n", tq::Span(reinterpret_cast<void*>(v[0]), v[1]).meets_rows(reinterpret_cast<void*>(v[2]), v[3], v[4], v[5], v[6], v[7]));
+            continue;
+        }
         for (long long& x : v)
-            if (std::scanf("%lld", &x) != 1) return 0;
+            if (std::scanf("%lld", &x) != 1) return 1;
         const tq_rows a{reinterpret_cast<void*>(v[0]), v[1], v[2], v[3]}, b{reinterpret_cast<void*>(v[4]), v[5], v[6], v[7]};
         const int D = static_cast<int>(v[12]);
         std::printf("%d %d\n", tq::Axes(&a, v[8], v[9], v[11]).meets_itself(D), tq::rows_meet(&a, v[9], &b, v[10], v[8], v[11], D, 2));
@@ -31,9 +38,11 @@ def tell(tmp_path_factory):
     subprocess.check_call(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "include"), "-I",
                            os.path.join(ROOT, "turboquant_compressed_kv_tq_gb300", "csrc"), str(d / "tell.cpp"), "-o", exe])
 
-    def call(cases):
-        text = "\n".join(" ".join(str(x) for x in c) for c in cases) + "\n"
+    def call(cases, kind=0):
+        text = "\n".join(" ".join(str(x) for x in (kind, *c)) for c in cases) + "\n"
         out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True, timeout=600).stdout.split()
+        if kind:
+            return [x == "1" for x in out]
         return [(out[2 * i] == "1", out[2 * i + 1] == "1") for i in range(len(cases))]
     return call
 
@@ -96,3 +105,15 @@ def test_layouts_that_take_too_long_to_tell(tell):
     def call(s, n):
         return tell([(BASE, 0, s + 1, s, BASE + (1 << 60), 0, s + 1, s, 1, n, n, n, 1)])[0][0]
     assert [call(1000, 1000), call(1000, 1002), call(10 ** 7, 10 ** 7)] == [False, True, True]
+
+
+def test_an_array_and_rows(tell):
+    rnd = random.Random(2)
+    cases, want = [], []
+    for _ in range(20000):
+        size, bytes_ = rnd.randint(0, 20), rnd.randint(1, 12)
+        sb, nb, sr, nr = rnd.randint(-40, 40), rnd.randint(0, 5), rnd.randint(-15, 15), rnd.randint(0, 5)
+        at = rnd.randint(-150, 150)
+        cases.append((BASE + at, size, BASE, sb, nb, sr, nr, bytes_))
+        want.append(size > 0 and any(at < b * sb + r * sr + bytes_ and b * sb + r * sr < at + size for b in range(nb) for r in range(nr)))
+    assert tell(cases, 1) == want

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cstddef>
 #include <cstdint>
 #include <cstdlib>
 #include <utility>
@@ -31,7 +32,7 @@ struct Steps {
                 if (stride[k] < stride[k + 1]) std::swap(stride[k], stride[k + 1]), std::swap(lo[k], lo[k + 1]), std::swap(hi[k], hi[k + 1]);
     }
     // Whether a sum along axes k.. lies within D elements of `delta`: exact, and yes where it cannot be told in so many looks.
-    bool meet(int64_t delta, int k, int D) {
+    bool meet(int64_t delta, int k, int64_t D) {
         if (k == 3 || stride[k] == 0) return std::abs(delta) < D;
         int64_t least = delta - D + 1, most = delta + D - 1;   // of the steps along axis k
         for (int j = k + 1; j < 3; ++j) least -= stride[j] * hi[j], most -= stride[j] * lo[j];
@@ -92,6 +93,34 @@ inline bool rows_meet(const tq_rows* a, int64_t ha, const tq_rows* b, int64_t hb
             {nb - 1, ha - 1, nt - 1}};
     s.sort();
     return s.meet(apart, 0, D);
+}
+
+// The bytes of an array (none of a null pointer's).
+struct Span {
+    intptr_t lo = 0, hi = 0;
+    Span(const void* p, int64_t bytes) {
+        if (p && bytes > 0) lo = reinterpret_cast<intptr_t>(p), hi = lo + bytes;
+    }
+    bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+    // A row of `bytes` of p + b * stride_b + r * stride_r (bytes), b < nb, r < nr.
+    bool meets_rows(const void* p, int64_t stride_b, int64_t nb, int64_t stride_r, int64_t nr, int64_t bytes) const {
+        if (!p || nb <= 0 || nr <= 0 || lo == hi) return false;
+        // a row's start lies in (lo - bytes, hi): twice that, about its middle
+        Steps s{{nb > 1 ? 2 * stride_b : 0, nr > 1 ? 2 * stride_r : 0, 0}, {0, 0, 0}, {nb - 1, nr - 1, 0}};
+        s.sort();
+        return s.meet(lo + hi - bytes - 2 * reinterpret_cast<intptr_t>(p), 0, hi - lo + bytes);
+    }
+};
+// Whether any of `written` shares memory with another, or with one of `read`.
+template <size_t W, size_t R>
+bool spans_meet(const Span (&written)[W], const Span (&read)[R]) {
+    for (size_t i = 0; i < W; ++i) {
+        for (size_t j = i + 1; j < W; ++j)
+            if (written[i].meets(written[j])) return true;
+        for (const Span& r : read)
+            if (written[i].meets(r)) return true;
+    }
+    return false;
 }
 
 }  // namespace tq

@@ -132,6 +132,21 @@ tq_status tq_verify_drafts(const tq_drafts* drafts, int batch, int num_drafts, i
         return TQ_ERR_INVALID_ARG;
     auto off = [](const void* p, int t) { return !aligned(p, t == TQ_F32 ? 4 : 2); };
     if (off(drafts->target, drafts->target_dtype) || (drafts->draft && off(drafts->draft, drafts->draft_dtype))) return TQ_ERR_INVALID_ARG;
+    const int64_t rows = num_drafts + 1, B = batch;
+    {
+        // an output in an input could change what the cluster's other CTAs have still to read
+        const bool drawn = drafts->noise != nullptr;
+        const Span written[] = {{accepted, 4 * B}, {tokens, 4 * B * rows}, {logprobs, 4 * B * rows}, {keep_lens, 4 * B}};
+        const Span read[] = {{drafts->draft_tokens, 4 * B * num_drafts}, {drafts->draft_lens, 4 * B}, {drawn ? drafts->temperatures : nullptr, 4 * B},
+                             {drawn ? drafts->uniforms : nullptr, 4 * B * num_drafts}, {keep_lens == drafts->seq_lens ? nullptr : drafts->seq_lens, keep_lens ? 4 * B : 0}};
+        if (spans_meet(written, read)) return TQ_ERR_INVALID_ARG;
+        const int size = drafts->target_dtype == TQ_F32 ? 4 : 2, q_size = drafts->draft_dtype == TQ_F32 ? 4 : 2;
+        for (const Span& w : written)
+            if (w.meets_rows(drafts->target, drafts->target_stride_batch * size, B, drafts->target_stride_row * size, rows, static_cast<int64_t>(vocab) * size) ||
+                w.meets_rows(drawn ? drafts->draft : nullptr, drafts->draft_stride_batch * q_size, B, drafts->draft_stride_row * q_size, num_drafts, static_cast<int64_t>(vocab) * q_size) ||
+                w.meets_rows(drafts->noise, drafts->noise_stride * 4, B, 0, 1, static_cast<int64_t>(vocab) * 4))
+                return TQ_ERR_INVALID_ARG;
+    }
     VerifyArgs a{};
     int sms = 0;
     if (device_state(&a.err, &sms) != TQ_OK) return TQ_ERR_CUDA;
