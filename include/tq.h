@@ -862,7 +862,9 @@ typedef struct {
  * tokens' slots are -1. A length outside [0, max_blocks * block_tokens] counts as no
  * new tokens, new_lens outside [0, n_new] as the nearest (TQ_DEVERR_SEQLEN); an n_used outside [0,
  * n_free] as an empty list (TQ_DEVERR_CAPACITY).
- * Errors: TQ_ERR_INVALID_ARG (pointers, sizes; batch above 2^24; max_blocks * block_tokens or
+ * The table's rows, the free list, n_used and the arrays of `places` share no memory with each other or with the
+ * lengths, but granted may be new_lens.
+ * Errors: TQ_ERR_INVALID_ARG (pointers, sizes, shared memory; batch above 2^24; max_blocks * block_tokens or
  * batch times the most that a row can be given above 2^31 - 1), TQ_ERR_UNSUPPORTED (block_tokens).
  */
 tq_status tq_blocks_reserve(const tq_blocks *blocks, int batch, const int32_t *seq_lens, const int32_t *new_lens, int n_new,

@@ -125,3 +125,19 @@ def test_rotation_of_a_single_head_in_place(Hq, Hk):
     assert torch.equal(whole[:, Hq + Hk:], before[:, Hq + Hk:])
     with pytest.raises(tq.TQError):   # one head over the others
         r.apply(q, k, out=q, k_out=whole[:, Hq - 1:Hq - 1 + Hk])
+
+
+@pytest.mark.parametrize("B,n", [(5, 7), (300, 40), (2500, 60)])
+def test_new_lengths_that_become_the_granted_ones(B, n):
+    width, BT = 6, 16
+    news = [(7 * b) % (n + 1) for b in range(B)]
+    lens = [(5 * b) % 50 for b in range(B)]
+    table, free = [[-1] * width for _ in range(B)], list(range(B * 2))
+    bt = tq.BlockTable.wrap(torch.tensor(table, dtype=torch.int32, device=DEV), i32(free), i32([0]), BT, B * 2)
+    places = tq.Places(B, sum(news))
+    places.granted.copy_(i32(news))
+    bt.reserve(i32(lens), places.granted, n, places)
+    used, granted, starts, seqs, pos, slots, err = ref.reserve(table, free, 0, lens, news, n, BT, B * 2, sum(news))
+    errors(err)
+    assert places.granted.tolist() == granted and places.starts.tolist() == starts and bt.table.tolist() == table and bt.n_used.item() == used
+    assert places.seq_ids.tolist() == seqs and places.positions.tolist() == pos and places.slots.tolist() == slots

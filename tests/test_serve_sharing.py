@@ -48,3 +48,45 @@ def test_verifications_that_share_nothing(lib):  # noqa: F811
                 assert verify(lib, **{out: AT[other] + BYTES[other]}) == passed and verify(lib, **{out: AT[other] - BYTES[out]}) == passed
     # what a greedy call does not look at
     assert verify(lib, noise=False, logprobs=AT["uniforms"], accepted=AT["temperatures"], tokens=AT["draft"]) == passed
+
+
+ROWS, WIDTH, FREE, MOST = 3, 4, 9, 12
+BLOCKS = ["table", "free_blocks", "n_used", "granted", "starts", "seq_ids", "positions", "slots", "lens", "news"]
+BLOCKS_AT = {name: (i + 1) << 20 for i, name in enumerate(BLOCKS)}
+BLOCKS_BYTES = {"table": 4 * ROWS * WIDTH, "free_blocks": 4 * FREE, "n_used": 4, "granted": 4 * ROWS, "starts": 4 * ROWS + 4, "seq_ids": 4 * MOST, "positions": 4 * MOST,
+                "slots": 8 * MOST, "lens": 4 * ROWS, "news": 4 * ROWS}
+
+
+def reserve(lib, release=False, **at):
+    a = BLOCKS_AT | at
+    b = _lib.tq_blocks(a["table"], a["free_blocks"], a["n_used"], FREE, WIDTH, 16, FREE)
+    p = _lib.tq_places(a["granted"], a["starts"], a["seq_ids"], a["positions"], a["slots"], MOST)
+    if release:
+        return lib.tq_blocks_release(ctypes.addressof(b), ROWS, a["lens"], None)
+    return lib.tq_blocks_reserve(ctypes.addressof(b), ROWS, a["lens"], a["news"], 4, ctypes.addressof(p), None)
+
+
+@pytest.mark.parametrize("out", BLOCKS[:8])
+@pytest.mark.parametrize("other", BLOCKS)
+def test_outputs_of_a_reservation(lib, out, other):  # noqa: F811
+    if out == other:
+        return
+    where = {BLOCKS_AT[other], BLOCKS_AT[other] + BLOCKS_BYTES[other] - 4, BLOCKS_AT[other] - BLOCKS_BYTES[out] + 4}
+    if (out, other) == ("granted", "news"):
+        where.remove(BLOCKS_AT[other])
+    for at in where:
+        assert reserve(lib, **{out: at}) == INVALID
+        if {out, other} <= {"table", "free_blocks", "n_used", "lens"}:
+            assert reserve(lib, release=True, **{out: at}) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="these calls pass the checks, and nothing is at their addresses")
+def test_reservations_that_share_nothing(lib):  # noqa: F811
+    passed = _lib.TQ_ERR_CUDA   # (no device)
+    assert reserve(lib) == passed and reserve(lib, release=True) == passed
+    assert reserve(lib, granted=BLOCKS_AT["news"]) == passed and reserve(lib, lens=BLOCKS_AT["news"]) == passed
+    for out in BLOCKS[:8]:
+        for other in BLOCKS:
+            if out != other:
+                assert reserve(lib, **{out: BLOCKS_AT[other] + BLOCKS_BYTES[other]}) == passed
+                assert reserve(lib, **{out: BLOCKS_AT[other] - BLOCKS_BYTES[out]}) == passed

@@ -58,6 +58,15 @@ tq_status tq_blocks_reserve(const tq_blocks* blocks, int batch, const int32_t* s
     if (!maps) a.places.max_tokens = 0;
     if (maps && a.places.max_tokens > 0 && !a.places.starts) return TQ_ERR_INVALID_ARG;
     if (batch == 0 && !a.places.starts) return TQ_OK;
+    {
+        // (the maps' launch looks lengths and entries up once more, behind the counts)
+        const tq_places& p = a.places;
+        const Span written[] = {{blocks->table, 4 * int64_t(batch) * blocks->max_blocks}, {blocks->free_blocks, 4 * int64_t(blocks->n_free)}, {blocks->n_used, 4},
+                                {p.granted, 4 * int64_t(batch)}, {p.starts, 4 * (int64_t(batch) + 1)}, {p.seq_ids, 4 * int64_t(p.max_tokens)},
+                                {p.positions, 4 * int64_t(p.max_tokens)}, {p.slots, 8 * int64_t(p.max_tokens)}};
+        const Span read[] = {{seq_lens, 4 * int64_t(batch)}, {new_lens == p.granted ? nullptr : new_lens, 4 * int64_t(batch)}};
+        if (spans_meet(written, read)) return TQ_ERR_INVALID_ARG;
+    }
     if ((st = blocks_args(blocks, batch, &a)) != TQ_OK) return st;
     a.seq = seq_lens;
     a.news = new_lens;
@@ -70,6 +79,9 @@ tq_status tq_blocks_release(const tq_blocks* blocks, int batch, const int32_t* k
     if (st != TQ_OK) return st;
     if (batch == 0) return TQ_OK;
     if (!keep_lens) return TQ_ERR_INVALID_ARG;
+    const Span written[] = {{blocks->table, 4 * int64_t(batch) * blocks->max_blocks}, {blocks->free_blocks, 4 * int64_t(blocks->n_free)}, {blocks->n_used, 4}};
+    const Span read[] = {{keep_lens, 4 * int64_t(batch)}};
+    if (spans_meet(written, read)) return TQ_ERR_INVALID_ARG;
     BlocksArgs a{};
     if ((st = blocks_args(blocks, batch, &a)) != TQ_OK) return st;
     a.seq = keep_lens;
