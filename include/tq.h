@@ -935,8 +935,11 @@ tq_status tq_rope_apply(const tq_rope *rope, int transposed, tq_dtype dtype, int
  *   keep_lens   device int32 [batch] or NULL: seq_lens[b] + n + 1, the tokens whose keys and values stand
  * num_drafts = 0 draws one token for each sequence. A logit of -inf is a token that cannot be; +inf counts as the largest
  * number, NaN as -inf, and a row of logits that holds either sets TQ_DEVERR_NONFINITE. So does a next token's row in which nothing
- * can be: the token is -1 (logprob 0). A probability that is NaN is never taken. Sums are fp32, over weights to 2^-20; the
- * weights that a draft hangs on are good to 2^-21; probabilities below 2^-100 (of the row's largest) count as 0. The same call gives the same
+ * can be: the token is -1 (logprob 0). A probability that is NaN is never taken.
+ * Arithmetic is fp32. What is off, at most, as a part of itself: a weight 2^-d, d = log2(e) (largest - x) / temperature, by 2^-22 + d 2^-23
+ * (below 2^-126 it counts as 0), the one that a draft hangs on by 2^-21 + d 2^-24; a row's sum of weights by S = 2^-18 + vocab 2^-33
+ * (2^-21 as a rule); a quotient by noise by 2^-22 more; max(p - q, 0) by as much of p as p (a weight by its sum) is; a logprob by 2^-22, and by S. (Rows with
+ * +inf or NaN apart.) Drafts and tokens that lie nearer to the border, or to one another, may go either way. The same call gives the same
  * bits every time. No workspace. The outputs share no memory with each other or with what is read, but keep_lens may be seq_lens
  * (TQ_ERR_INVALID_ARG).
  * Errors: TQ_ERR_INVALID_ARG (pointers, sizes, dtypes; batch above 2^24, vocab above 2^28), TQ_ERR_UNSUPPORTED (num_drafts above 64).

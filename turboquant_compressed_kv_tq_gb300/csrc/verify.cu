@@ -60,8 +60,8 @@ struct __align__(16) Seen {
     }
     // A lane's units of a piece, every 32nd from `from`. Usually the weights are
     // 2^(x c - m), m = top c rounded, so that each takes one product, and their sum is brought from m to the exact top c (a factor
-    // 1 - delta ln 2, |delta| < 2^-11) once; c's own error, 2^-25 of itself, is common to sum and weights but for what it does to
-    // (x - top) / T. Where m is large (temperatures near 0, rows of the lowest numbers) differences come first.
+    // 1 - delta ln 2, |delta| < 2^-11) once; c's own error, 2^-24 of itself, is common to sum and weights but for what it does to
+    // (x - top) / T: with the exponent's rounding, weights 2^-d are off by 2^-22 + d 2^-23. Where m is large (temperatures near 0, rows of the lowest numbers) differences come first.
     template <typename T>
     __device__ __forceinline__ void take(const uint4* from, const Scale& S, int from_piece) {
         constexpr int kIn = 16 / sizeof(T), kPer = kUnits / 32, N = kPer * kIn / 2;

@@ -58,7 +58,7 @@ __device__ __forceinline__ float logit(float x) { return x == x ? fminf(x, FLT_M
 // log2(e) / T as c + lo, both positive, so that what is masked (-inf) stays -inf in either product: log2(e) = 1.442695 (rounded down)
 // + 1.9259630e-8; c is below the quotient, lo what it leaves. To 2^-40.
 struct Scale {
-    float c, lo, near;   // near: c + lo in one number, off by 2^-25 of itself
+    float c, lo, near;   // near: c + lo in one number, off by 2^-24 of itself at most
     __device__ __forceinline__ explicit Scale(float T) {
         constexpr float hi = 0x1.715476p+0f, rest = 1.9259630e-8f;
         const float r = rcp(T);
@@ -67,7 +67,7 @@ struct Scale {
         near = c + lo;
     }
     __device__ __forceinline__ float weight(float d) const { return ex2(fmaf(d, c, d * lo)); }   // d <= 0
-    // The same with the exponent's rounding put back: to 2^-22. NaN of a masked value.
+    // The same with the exponent's rounding put back: to 2^-21, and d's own. NaN of a masked value.
     __device__ __forceinline__ float weight_near(float d) const {
         const float t = d * c, w = ex2(t);
         return fmaf(w, fmaf(d, lo, fmaf(d, c, -t)) * kLn2, w);
