@@ -68,9 +68,9 @@ struct __align__(16) Seen {
         float2 x[N];
 #pragma unroll
         for (int v = 0; v < kPer; ++v) numbers(from[v * 32], x + v * kIn / 2, T());
-        float t = fmaxf(x[0].x, x[0].y);
+        float t = largest(x[0].x, x[0].x, x[0].y);   // NaN if one is among them: top stays, and the sum becomes NaN
 #pragma unroll
-        for (int i = 1; i < N; ++i) t = fmaxf(fmaxf(t, x[i].x), x[i].y);
+        for (int i = 1; i < N; ++i) t = largest(t, x[i].x, x[i].y);
         rise(t, S, from_piece);
         if (t == top && piece < 0) piece = from_piece;   // (a largest value of -FLT_MAX)
         const float m = top * S.near;
@@ -86,11 +86,8 @@ struct __align__(16) Seen {
         } else if (t > -INFINITY) {   // seldom: one value after the other
 #pragma unroll 1
             for (int e = 0; e < kPer * kIn; ++e) sum += S.weight(number(reinterpret_cast<const T*>(from + e / kIn * 32)[e % kIn]) - top);
-        } else {   // masked tokens weigh nothing, but a NaN that the largest value (-inf, or NaN) does not show is to be seen in the sum
-            float2 s = x[0];
-#pragma unroll
-            for (int i = 1; i < N; ++i) s = __fadd2_rn(s, x[i]);
-            if (!(s.x + s.y == -INFINITY)) sum = s.x + s.y;
+        } else if (t != t) {   // among masked tokens only
+            sum = t;
         }
     }
     // Where the largest value is, by another look at the piece (`row`: its first whole unit, of `end` units; value 0 of it is value

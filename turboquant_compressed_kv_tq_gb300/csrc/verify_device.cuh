@@ -52,6 +52,13 @@ using kv8::rcp;
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
+// The largest of three numbers, NaN if one of them is.
+__device__ __forceinline__ float largest(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // A logit as it counts: +inf the largest number, NaN -inf.
 __device__ __forceinline__ float logit(float x) { return x == x ? fminf(x, FLT_MAX) : -INFINITY; }
 
