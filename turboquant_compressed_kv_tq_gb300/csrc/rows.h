@@ -105,10 +105,13 @@ struct Span {
     // A row of `bytes` of p + b * stride_b + r * stride_r (bytes), b < nb, r < nr.
     bool meets_rows(const void* p, int64_t stride_b, int64_t nb, int64_t stride_r, int64_t nr, int64_t bytes) const {
         if (!p || nb <= 0 || nr <= 0 || lo == hi) return false;
+        const intptr_t first = reinterpret_cast<intptr_t>(p);
+        const int64_t b = stride_b * (nb - 1), r = stride_r * (nr - 1);
+        if (first + std::min<int64_t>(b, 0) + std::min<int64_t>(r, 0) >= hi || first + std::max<int64_t>(b, 0) + std::max<int64_t>(r, 0) + bytes <= lo) return false;
         // a row's start lies in (lo - bytes, hi): twice that, about its middle
         Steps s{{nb > 1 ? 2 * stride_b : 0, nr > 1 ? 2 * stride_r : 0, 0}, {0, 0, 0}, {nb - 1, nr - 1, 0}};
         s.sort();
-        return s.meet(lo + hi - bytes - 2 * reinterpret_cast<intptr_t>(p), 0, hi - lo + bytes);
+        return s.meet(lo + hi - bytes - 2 * first, 0, hi - lo + bytes);
     }
 };
 // Whether any of `written` shares memory with another, or with one of `read`.
