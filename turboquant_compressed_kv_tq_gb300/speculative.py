@@ -35,17 +35,15 @@ class DraftedBatch:
         from . import Places
         self.blocks, self.seq_lens = blocks, seq_lens
         self.places = Places(seq_lens.numel(), device=seq_lens.device)
-        self.n_new = None                                            # of the step that has begun
-        self.short = torch.zeros_like(seq_lens, dtype=torch.bool)    # sequences that have not a place for each of its tokens
+        self.n_new = None   # of the step that has begun
+        # sequences that have not a place for each of its tokens
+        self._short = torch.zeros_like(seq_lens, dtype=torch.bool)
+        self._short_rows = self._short[:, None]
 
     def begin(self, n_new: int, stream=None):
         """Blocks for n_new tokens of each sequence; returns how many got a place (int32 [batch], on the device). A sequence
         with fewer than n_new takes no part in the step."""
-        import torch
-        from . import _on
         self.blocks.reserve(self.seq_lens, None, n_new, self.places, stream)
-        with _on(stream):
-            torch.ne(self.places.granted, n_new, out=self.short)
         self.n_new = n_new
         return self.places.granted
 
@@ -63,22 +61,26 @@ class DraftedBatch:
         """Verify the drafts against target [batch, drafts + 1, vocab], drafts + 1 at most the step's tokens; the sequences keep
         the tokens that stand. Returns tq_verify_drafts' Verified: its last token of each sequence is the next step's first
         (tokens of -1: the sequence stood still, and its first token is the one that it had)."""
-        import torch
-        from . import _on, tq_verify_drafts
+        from . import _here, _on, tq_verify_drafts
         if self.n_new is not None and target.dim() == 3 and target.shape[1] > self.n_new:
             raise ValueError(f"target has {target.shape[1]} rows a sequence, the step {self.n_new} tokens")
-        before = self.seq_lens
-        if out is not None and out.keep_lens is not None and out.keep_lens.data_ptr() == before.data_ptr():   # (in place)
-            with _on(stream):
+        with _on(stream) if stream is not None else _here:
+            before = self.seq_lens
+            if out is not None and out.keep_lens is not None and out.keep_lens.data_ptr() == before.data_ptr():   # (in place)
                 before = before.clone()
-        verified = tq_verify_drafts(target, draft_tokens, draft_probs, uniforms, noise, temperatures, draft_lens, self.seq_lens,
-                                    target_probs, out, stream)
-        with _on(stream):
-            torch.where(self.short, before, verified.keep_lens, out=verified.keep_lens)
+            verified = tq_verify_drafts(target, draft_tokens, draft_probs, uniforms, noise, temperatures, draft_lens, self.seq_lens,
+                                        target_probs, out, stream)
+            if self.n_new is not None:
+                self._stand_still(verified, before)
             self.blocks.release(verified.keep_lens, stream)
             self.seq_lens.copy_(verified.keep_lens)   # (what is returned stays as it is in the next step)
-            verified.accepted.masked_fill_(self.short, 0)
-            verified.tokens.masked_fill_(self.short[:, None], -1)
-            if verified.logprobs is not None:
-                verified.logprobs.masked_fill_(self.short[:, None], 0.0)
         return verified
+
+    def _stand_still(self, verified, before):
+        import torch
+        torch.ne(self.places.granted, self.n_new, out=self._short)
+        torch.where(self._short, before, verified.keep_lens, out=verified.keep_lens)
+        verified.accepted.masked_fill_(self._short, 0)
+        verified.tokens.masked_fill_(self._short_rows, -1)
+        if verified.logprobs is not None:
+            verified.logprobs.masked_fill_(self._short_rows, 0.0)
