@@ -595,7 +595,6 @@ class Rope:
     @classmethod
     def of_base(cls, rot_dim: int, base: float = 10000.0, device="cuda", interleaved: bool = False, scale: float = 1.0):
         """inv_freq[i] = base ** (-2 i / rot_dim)."""
-        torch = _torch()
         return cls(cls._frequencies(rot_dim, base, device), interleaved, scale)
 
     # Forms for contexts longer than the trained one, as frequencies of their own.

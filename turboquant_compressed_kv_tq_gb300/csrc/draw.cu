@@ -8,8 +8,8 @@
 // A cluster of CTAs has a sequence, as many as fill the SMs once: a cluster's last steps (two barriers, its last threads' loads) are as
 // long for a short share of a row as for a long one. Each warp has a ring of bulk copies of its own, as in verify.cu.
 //
-// Measured: 200 rows of 131,072, f32, a third of them greedy: 35 us (5.9 TB/s of what is read); 42 with the values loaded to registers, 47 in two
-// passes. Three CTAs an SM and two pieces a ring: two and three 41 us, four and one 38.
+// Measured: 200 rows of 131,072, f32, a third of them greedy (whose noise is not read: 175 MB): 36 us (4.8 TB/s); 42 with the values loaded to
+// registers, 47 in two passes. Three CTAs an SM and two pieces a ring: two and three 41 us, four and one 38.
 #include <algorithm>
 
 #include "verify_device.cuh"
