@@ -42,11 +42,18 @@ class Run:
             self.cache.append(0, k, v, i32([0]), self.bt.table[b:b + 1], self.width)
             self.plain.append(0, k, v, i32([0]), torch.arange(self.width, device=DEV, dtype=torch.int32)[None] + b * self.width, self.width)
 
-    def step(self):
+    def step(self, stream=None):
         q, k, v = (x.transpose(1, 2) for x in self.qkv.split((self.Hq, self.Hk, self.Hk), dim=2))
-        self.loop.begin(self.n)
-        self.loop.attend(self.cache, 0, k.contiguous(), v.contiguous(), q.contiguous(), self.width * self.BT, self.out, self.ws)
-        return self.loop.finish(self.logits, self.drafts, None, self.uniforms, self.noise, out=self.seen)
+        k, v, q = (x.contiguous() for x in (k, v, q))
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+            torch.cuda._sleep(1 << 22)   # 2 ms of the current stream: what is not on the named one comes late
+        self.loop.begin(self.n, stream)
+        self.loop.attend(self.cache, 0, k, v, q, self.width * self.BT, self.out, self.ws, stream=stream)
+        seen = self.loop.finish(self.logits, self.drafts, None, self.uniforms, self.noise, out=self.seen, stream=stream)
+        if stream is not None:
+            stream.synchronize()   # (q, k and v are the other stream's)
+        return seen
 
     def draw(self, seed):
         g = gen(seed)
@@ -158,6 +165,14 @@ def test_steps_at_the_end_of_a_row():
     torch.cuda.synchronize()
     tq.tq_device_error()
     assert torch.equal(seen[0].keep_lens, kept)   # what was returned stays
+
+
+def test_steps_on_a_named_stream():
+    r = Run([14, 30, 5, 33], 8)
+    s = torch.cuda.Stream()
+    for i in range(3):
+        r.draw(400 + i)
+        assert 1 in r.check(lambda: r.step(s))
 
 
 def test_steps_whose_kept_lengths_go_in_place():
